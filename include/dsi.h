@@ -385,6 +385,79 @@ dsi_status dsi_latent_fp8_append(const void* x, int64_t n_rows, int64_t ld_x,
                                  void* stream);
 
 /*
+ * dsi_norm_rope — head norms and position rotation of new tokens' queries and
+ * keys in one pass, the keys written straight into their cache rows (the
+ * pages have no counterpart: they start at normed, rotated queries and keys).
+ *
+ * A vector x of d dims is one head of one token.  Norm over dims [0, norm_dim):
+ *   DSI_NORM_RMS    y_i = x_i / sqrt(mean x^2 + eps) * weight_i
+ *   DSI_NORM_LAYER  y_i = (x_i - mean x) / sqrt(mean (x - mean x)^2 + eps) * weight_i + bias_i
+ *   DSI_NORM_NONE   y = x        (and y_i = x_i for i >= norm_dim)
+ * then the rotation of dims [rope_offset, rope_offset + rope_dim) by the
+ * token's position p: for pair i (0 <= i < rope_dim / 2) with
+ * c = rope_table[p, i], s = rope_table[p, rope_dim / 2 + i]
+ *   z_a = y_a c - y_b s,  z_b = y_a s + y_b c
+ *   a, b = rope_offset + i, rope_offset + i + rope_dim / 2   (interleaved == 0)
+ *   a, b = rope_offset + 2i, rope_offset + 2i + 1            (interleaved != 0)
+ * The other dims pass through.  Index keys: norm_dim = d, rotation of 64 of
+ * the dims; latent rows: d = 576, norm_dim = 512, rope_offset = 512.
+ * All arithmetic is fp32 with one rounding at the end, into out_dtype:
+ *   DSI_BF16        bf16 [out_rows, n_heads, d] with pitches ld_out_row, ld_out_head
+ *   DSI_MXFP8_E4M3  E4M3 codes [out_rows, n_heads, d] and E8M0 bytes
+ *                   [out_rows, n_heads, d / out_group], packed: the scale and
+ *                   rounding rules of dsi_mxfp8_quantize on z
+ *   DSI_FP8_E4M3    E4M3 codes [out_rows, n_heads, d] and fp32 scales
+ *                   [out_rows, n_heads, ceil(d / 128)], packed, one per tile of
+ *                   128 dims: the rules of dsi_latent_fp8_append on z
+ * The quantised forms start from the fp32 z; a bf16 result that is quantised
+ * by a second call is rounded twice and can differ in single codes.
+ * Row i goes to out row dst_rows[i] (i when dst_rows is NULL).  A negative
+ * entry skips the row; one >= out_rows, or a position outside
+ * 0 .. table_rows - 1, skips it and sets the device status to DSI_ERR_BOUNDS.
+ * Rows that share an out row leave it undefined.  A bf16 out may be x itself
+ * (same pitches, no dst_rows); outputs must not overlap anything else.
+ *   queries, keys  either may be NULL (then only the other is computed);
+ *             n_heads == 0 counts as NULL
+ *   x         bf16 [n_rows, n_heads, d] with pitches ld_row, ld_head, contiguous dims
+ *   weight    fp32 [norm_dim] or NULL (all ones);  bias fp32 [norm_dim] or NULL
+ *             (DSI_NORM_LAYER only)
+ *   rope_table fp32 [table_rows, rope_dim], cosines then sines
+ *   positions int64 [n_rows]
+ * x, out, weight, bias and rope_table 16-byte aligned; pitches multiples of 8.
+ * Errors: DSI_ERR_INVALID_ARG (null pointer, negative size, misalignment,
+ * a pitch below the vector's width, eps < 0 or NaN, bias without
+ * DSI_NORM_LAYER), DSI_ERR_UNSUPPORTED (d not a multiple of 8 or outside
+ * 8..1024, norm_dim not a multiple of 8 or outside 8..d, rope_dim not a
+ * multiple of 16, rope_offset not a multiple of 8, out_group not 32, 64 or
+ * 128 or not dividing d, unknown norm or out_dtype).
+ */
+typedef enum { DSI_NORM_NONE = 0, DSI_NORM_RMS = 1, DSI_NORM_LAYER = 2 } dsi_norm;
+
+typedef struct dsi_heads {
+  const void*    x;           /* bf16 [n_rows, n_heads, d] */
+  int64_t        ld_row;      /* elements from one row of x to the next */
+  int64_t        ld_head;     /* elements from one head of x to the next */
+  int32_t        n_heads;
+  int32_t        norm;        /* dsi_norm */
+  int32_t        norm_dim;    /* dims [0, norm_dim) are normed (unused for DSI_NORM_NONE) */
+  int32_t        out_dtype;   /* dsi_dtype of out */
+  const float*   weight;      /* fp32 [norm_dim] or NULL */
+  const float*   bias;        /* fp32 [norm_dim] or NULL */
+  void*          out;
+  int64_t        ld_out_row;  /* bf16 out: elements from one row to the next */
+  int64_t        ld_out_head; /* bf16 out: elements from one head to the next */
+  void*          out_scale;   /* scales of a quantised out, else NULL */
+  const int64_t* dst_rows;    /* [n_rows] out row of each row, or NULL */
+  int64_t        out_rows;    /* rows of out (entries of dst_rows are checked against it) */
+  int32_t        out_group;   /* MXFP8 out: 32, 64 or 128 (0 = 32); else unused */
+} dsi_heads;
+
+dsi_status dsi_norm_rope(const dsi_heads* queries, const dsi_heads* keys, int64_t n_rows,
+                         int32_t d, float eps, const float* rope_table, int64_t table_rows,
+                         const int64_t* positions, int32_t rope_offset, int32_t rope_dim,
+                         int32_t interleaved, void* stream);
+
+/*
  * dsi_selftest_wait_timeout — exercises the failure-detection path.  The
  * pages have no counterpart: every wait inside the library's kernels is
  * bounded, and a wait that runs out sets the device status word to

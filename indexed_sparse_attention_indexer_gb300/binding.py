@@ -7,6 +7,7 @@ fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -19,6 +20,7 @@ _LIBS = {}
 DSI_OK, DSI_ERR_INVALID_ARG, DSI_ERR_UNSUPPORTED, DSI_ERR_CUDA = 0, 1, 2, 3
 DSI_ERR_TIMEOUT, DSI_ERR_BOUNDS, DSI_ERR_WORKSPACE = 4, 5, 6
 DSI_BF16, DSI_FP8_E4M3, DSI_MXFP8_E4M3 = 0, 1, 2
+NORMS = {None: 0, "rms": 1, "layer": 2}
 D_QK, D_LATENT = 576, 512
 
 c_void_p, c_int32, c_int64, c_float, c_size_t = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
@@ -32,6 +34,15 @@ class DsiCache(ctypes.Structure):
                 ("max_pages", c_int32), ("seq_lens", c_void_p), ("batch", c_int32),
                 ("s_max", c_int64), ("num_pages", c_int64), ("k_group", c_int32),
                 ("latent_dtype", c_int32), ("latent_scale", c_void_p)]
+
+
+class DsiHeads(ctypes.Structure):
+    """Mirror of ``struct dsi_heads``."""
+    _fields_ = [("x", c_void_p), ("ld_row", c_int64), ("ld_head", c_int64), ("n_heads", c_int32),
+                ("norm", c_int32), ("norm_dim", c_int32), ("out_dtype", c_int32),
+                ("weight", c_void_p), ("bias", c_void_p), ("out", c_void_p),
+                ("ld_out_row", c_int64), ("ld_out_head", c_int64), ("out_scale", c_void_p),
+                ("dst_rows", c_void_p), ("out_rows", c_int64), ("out_group", c_int32)]
 
 
 # name -> (restype, argtypes); the exported surface of include/dsi.h
@@ -65,6 +76,9 @@ SIGNATURES = {
                                      c_void_p, c_void_p, c_void_p]),
     "dsi_latent_fp8_append": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
                                         c_void_p]),
+    "dsi_norm_rope": (c_int32, [ctypes.POINTER(DsiHeads), ctypes.POINTER(DsiHeads), c_int64,
+                                c_int32, c_float, c_void_p, c_int64, c_void_p, c_int32, c_int32,
+                                c_int32, c_void_p]),
     "dsi_workspace_size": (c_size_t, [c_int32, c_int32, c_int32, c_int32, c_int64, c_int32]),
     "dsi_layer_workspace_size": (c_size_t, [ctypes.POINTER(DsiCache), c_int32, c_int32, c_int32,
                                             c_int32, c_int64, c_int32]),
@@ -180,6 +194,98 @@ class Cache:
         return ctypes.byref(self.struct)
 
 
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on(device: torch.device):
+    """The tensors' device made current for a call (kernels launch on the current device)."""
+    if device.type != "cuda" or device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+class Heads:
+    """Queries or keys of ``norm_rope``: the tensors plus the ``dsi_heads`` struct that points
+    at them (it can be kept and used again while the tensors live).
+
+    ``x [n, heads, d]`` bf16 (any row and head strides); ``norm`` None, "rms" or "layer" over
+    the first ``norm_dim`` dims (all of them unless given) with fp32 ``weight`` / ``bias``.
+    ``out`` is a bf16 tensor ``[rows, heads, d]`` (``x`` itself for in place; a new one unless
+    given) or an E4M3 one, packed, with ``out_scale``: uint8 ``[rows, heads, d / group]`` makes it
+    MXFP8, fp32 ``[rows, heads, ceil(d / 128)]`` FP8 with tile scales.  The ``heads`` dim may be
+    left out of ``out`` and ``out_scale`` when there is one head, and page pools
+    ``[pages, page_size, ...]`` may stand for their rows.  ``dst_rows`` (int64 ``[n]``): the out
+    row of each row; negative skips it.
+    """
+
+    def __init__(self, x: torch.Tensor, norm: Optional[str] = None,
+                 weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                 norm_dim: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                 out_scale: Optional[torch.Tensor] = None, dst_rows: Optional[torch.Tensor] = None):
+        _need(x.dim() == 3 and x.dtype == torch.bfloat16, "x is a bf16 [n, heads, d] tensor")
+        n, heads, d = (int(v) for v in x.shape)
+        _need(x.stride(2) == 1 or d == 1 or x.numel() == 0, "the dims of x must be contiguous")
+        _need(norm in NORMS, f"norm is one of {list(NORMS)}")
+        nd = d if norm_dim is None else int(norm_dim)
+        for t, name in ((weight, "weight"), (bias, "bias")):
+            _need(t is None or (t.dtype == torch.float32 and t.is_contiguous() and t.numel() == nd),
+                  f"{name} is a contiguous fp32 [norm_dim] tensor")
+        _need(dst_rows is None or (dst_rows.dtype == torch.int64 and dst_rows.is_contiguous()
+                                   and dst_rows.numel() == n), "dst_rows is an int64 [n] tensor")
+        if out is None:
+            out = torch.empty((n, heads, d), dtype=torch.bfloat16, device=x.device)
+        for t in (weight, bias, out, out_scale, dst_rows):
+            _need(t is None or t.device == x.device, "all tensors must be on one device")
+        s = DsiHeads()
+        s.x, s.n_heads, s.norm, s.norm_dim = x.data_ptr() or None, heads, NORMS[norm], nd
+        # a dim of size one has no pitch that matters
+        s.ld_head = int(x.stride(1)) if heads > 1 else d
+        s.ld_row = int(x.stride(0)) if n > 1 else d
+        s.weight = weight.data_ptr() if weight is not None else None
+        s.bias = bias.data_ptr() if bias is not None else None
+        s.dst_rows = dst_rows.data_ptr() if dst_rows is not None else None
+        s.out = out.data_ptr() or None
+        _need(int(out.shape[-1]) == d, "out has the dims of x")
+        if out.dtype == torch.bfloat16 and out.dim() == 3 and int(out.shape[1]) == heads:
+            _need(out_scale is None, "a bf16 out has no scales")
+            _need(out.stride(2) == 1 or d == 1 or out.numel() == 0, "the dims of out must be contiguous")
+            rows = int(out.shape[0])
+            s.ld_out_head = int(out.stride(1)) if heads > 1 else d
+            s.ld_out_row = int(out.stride(0)) if rows > 1 else d
+            s.out_dtype = DSI_BF16
+        else:
+            _need(out.is_contiguous(), "a page pool or E4M3 codes must be contiguous")
+            _need(heads <= 1 or int(out.shape[-2]) == heads, "out has the heads of x")
+            rows = out.numel() // (heads * d) if heads else 0
+            s.ld_out_row, s.ld_out_head = max(1, heads) * d, d
+            if out.dtype == torch.bfloat16:
+                _need(out_scale is None, "a bf16 out has no scales")
+                s.out_dtype = DSI_BF16
+            else:
+                _need(out.dtype == torch.float8_e4m3fn, "out is bf16 or E4M3 codes")
+                _need(out_scale is not None and out_scale.is_contiguous(),
+                      "E4M3 codes need a contiguous out_scale")
+                per = int(out_scale.shape[-1])
+                _need(out_scale.numel() == rows * heads * per,
+                      "out_scale has a row for every vector of out")
+                if out_scale.dtype == torch.uint8:
+                    _need(per > 0 and d % per == 0, "MXFP8 scales are [rows, heads, d / group]")
+                    s.out_dtype, s.out_group = DSI_MXFP8_E4M3, d // per
+                else:
+                    _need(out_scale.dtype == torch.float32 and per == (d + 127) // 128,
+                          "FP8 scales are fp32 [rows, heads, ceil(d / 128)]")
+                    s.out_dtype = DSI_FP8_E4M3
+                s.out_scale = out_scale.data_ptr() or None
+        s.out_rows = rows
+        self.x, self.weight, self.bias, self.out = x, weight, bias, out
+        self.out_scale, self.dst_rows, self.n, self.d, self.struct = out_scale, dst_rows, n, d, s
+
+    def ref(self):
+        return ctypes.byref(self.struct)
+
+
 # ----------------------------------------------------------------------------
 # entry points (same names as the C ABI)
 # ----------------------------------------------------------------------------
@@ -250,6 +356,43 @@ def latent_fp8_append(x, dst_rows=None, codes=None, scales=None, stream=None,
                                    _ptr(scales), _stream(stream))
     _check(lib, "dsi_latent_fp8_append", st)
     return codes, scales
+
+
+def rope_table(n_positions: int, rope_dim: int, theta: float = 10000.0, device="cuda"):
+    """fp32 ``[n_positions, rope_dim]`` table of ``norm_rope``: cosines, then sines, of
+    position * theta^(-2 i / rope_dim), the angles in fp64."""
+    i = torch.arange(0, rope_dim, 2, dtype=torch.float64, device=device)
+    ang = torch.arange(n_positions, dtype=torch.float64, device=device)[:, None] * theta ** (-i / rope_dim)
+    return torch.cat([ang.cos(), ang.sin()], dim=1).to(torch.float32)
+
+
+def norm_rope(queries: Optional[Heads], keys: Optional[Heads], table, positions,
+              rope_offset: int = 0, interleaved: bool = False, eps: float = 1e-6, stream=None,
+              checked: bool = False):
+    """Head norms and position rotation of new tokens' queries and keys in one launch (keys
+    into their cache rows): ``dsi_norm_rope``.  ``table`` fp32 ``[positions, rope_dim]`` (see
+    ``rope_table``), ``positions`` int64 ``[n]``.  Returns the two sides' outs."""
+    lib = load(checked)
+    side = queries if queries is not None else keys
+    _need(side is not None, "queries, keys or both")
+    _need(queries is None or keys is None or
+          (queries.n, queries.d, queries.x.device) == (keys.n, keys.d, keys.x.device),
+          "queries and keys have the same rows, dims and device")
+    _need(table.dtype == torch.float32 and table.dim() == 2 and table.is_contiguous(),
+          "table is a contiguous fp32 [positions, rope_dim] tensor")
+    _need(positions.dtype == torch.int64 and positions.is_contiguous() and positions.numel() == side.n,
+          "positions is an int64 [n] tensor")
+    _need(table.device == side.x.device and positions.device == side.x.device,
+          "all tensors must be on one device")
+    if side.n:
+        with _on(side.x.device):
+            st = lib.dsi_norm_rope(queries.ref() if queries is not None else None,
+                                   keys.ref() if keys is not None else None, side.n, side.d, eps,
+                                   table.data_ptr(), table.shape[0], positions.data_ptr(),
+                                   int(rope_offset), table.shape[1], int(bool(interleaved)),
+                                   _stream(stream))
+        _check(lib, "dsi_norm_rope", st)
+    return (queries.out if queries is not None else None), (keys.out if keys is not None else None)
 
 
 def topk(scores, K: int, row_len=None, q_offset: int = 0, idx=None, count=None, stream=None,

@@ -7,6 +7,7 @@
 
 #include "kernels.h"
 #include "latent_fp8.h"
+#include "norm_rope.h"
 
 using namespace dsi;
 
@@ -163,6 +164,39 @@ WsPlan layer_plan(const dsi_cache* c, int rows, int Hi, int H, int K, int64_t q_
                   bool fused_prefill) {
   const int64_t span = decode ? c->s_max : q_offset + rows;
   return plan_workspace(rows, Hi, H, K, span, (size_t)-1, !fused_prefill, true);
+}
+
+// One side (queries or keys) of dsi_norm_rope; a side that is not there has
+// n_heads == 0 in `out`.
+dsi_status check_heads(const dsi_heads* h, int64_t n_rows, int d, dsi_heads* out) {
+  memset(out, 0, sizeof(*out));
+  if (!h || h->n_heads == 0) return DSI_OK;
+  if (h->n_heads < 0 || !h->x || !h->out) return DSI_ERR_INVALID_ARG;
+  if (!aligned(h->x, 16) || !aligned(h->out, 16) || !aligned(h->weight, 16) || !aligned(h->bias, 16))
+    return DSI_ERR_INVALID_ARG;
+  if (h->ld_head < d || h->ld_row < d || h->ld_row % 8 != 0 || h->ld_head % 8 != 0)
+    return DSI_ERR_INVALID_ARG;
+  if (h->norm != DSI_NORM_NONE && h->norm != DSI_NORM_RMS && h->norm != DSI_NORM_LAYER)
+    return DSI_ERR_UNSUPPORTED;
+  if (h->bias && h->norm != DSI_NORM_LAYER) return DSI_ERR_INVALID_ARG;
+  if (h->norm != DSI_NORM_NONE && (h->norm_dim < 8 || h->norm_dim > d || h->norm_dim % 8 != 0))
+    return DSI_ERR_UNSUPPORTED;
+  if (h->out_rows < 0 || (!h->dst_rows && h->out_rows < n_rows)) return DSI_ERR_INVALID_ARG;
+  *out = *h;
+  if (h->out_dtype == DSI_BF16) {
+    if (h->ld_out_head < d || h->ld_out_row < d || h->ld_out_row % 8 != 0 || h->ld_out_head % 8 != 0)
+      return DSI_ERR_INVALID_ARG;
+    return DSI_OK;
+  }
+  if (!h->out_scale) return DSI_ERR_INVALID_ARG;
+  if (h->out_dtype == DSI_MXFP8_E4M3) {
+    out->out_group = h->out_group ? h->out_group : 32;
+    if (out->out_group != 32 && out->out_group != 64 && out->out_group != 128)
+      return DSI_ERR_UNSUPPORTED;
+    return d % out->out_group == 0 ? DSI_OK : DSI_ERR_UNSUPPORTED;
+  }
+  if (h->out_dtype != DSI_FP8_E4M3) return DSI_ERR_UNSUPPORTED;
+  return aligned(h->out_scale, 4) ? DSI_OK : DSI_ERR_INVALID_ARG;
 }
 
 }  // namespace
@@ -387,6 +421,36 @@ dsi_status dsi_latent_fp8_append(const void* x, int64_t n_rows, int64_t ld_x,
   return from_cuda(launch_latent_fp8_append(reinterpret_cast<const bf16*>(x), n_rows, ld_x,
                                             dst_rows, static_cast<uint8_t*>(codes), scales,
                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dsi_status dsi_norm_rope(const dsi_heads* queries, const dsi_heads* keys, int64_t n_rows,
+                         int32_t d, float eps, const float* rope_table, int64_t table_rows,
+                         const int64_t* positions, int32_t rope_offset, int32_t rope_dim,
+                         int32_t interleaved, void* stream) {
+  if (n_rows < 0 || !rope_table || !positions || table_rows < 1 || !(eps >= 0.f))
+    return DSI_ERR_INVALID_ARG;
+  if (d < 8 || d > 1024 || d % 8 != 0) return DSI_ERR_UNSUPPORTED;
+  if (rope_dim < 0 || rope_offset < 0 || rope_offset > d - rope_dim) return DSI_ERR_INVALID_ARG;
+  if (rope_dim < 16 || rope_dim % 16 != 0 || rope_offset % 8 != 0) return DSI_ERR_UNSUPPORTED;
+  if (!aligned(rope_table, 16) || !aligned(positions, 8)) return DSI_ERR_INVALID_ARG;
+  dsi_heads q, k;
+  dsi_status s = check_heads(queries, n_rows, d, &q);
+  if (s != DSI_OK) return s;
+  s = check_heads(keys, n_rows, d, &k);
+  if (s != DSI_OK) return s;
+  if (n_rows > (1ll << 40)) return DSI_ERR_UNSUPPORTED;   // vector counts stay in 64 bits
+  if (n_rows == 0 || q.n_heads + (int64_t)k.n_heads == 0) return DSI_OK;
+  RopeArgs a;
+  a.table = rope_table;
+  a.positions = positions;
+  a.table_rows = table_rows;
+  a.n_rows = n_rows;
+  a.eps = eps;
+  a.d = d;
+  a.rope_offset = rope_offset;
+  a.rope_dim = rope_dim;
+  a.interleaved = interleaved;
+  return from_cuda(launch_norm_rope(q, k, a, status_ptr(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 dsi_status dsi_selftest_wait_timeout(uint64_t limit_ns, void* stream) {
