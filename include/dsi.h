@@ -385,6 +385,70 @@ dsi_status dsi_latent_fp8_append(const void* x, int64_t n_rows, int64_t ld_x,
                                  void* stream);
 
 /*
+ * dsi_dense_mla_decode — attention of the newest tokens over the whole latent
+ * cache: no indexer, every position of the history takes part ("Day 0
+ * Inference Adaptation and Performance Optimization for New Models" §1: the
+ * dense attention that index selection replaces).
+ *
+ * The T = tokens_per_seq newest tokens of every sequence (their rows are the
+ * last T cached positions; query rows come T to a sequence, as in
+ * dsi_indexed_attention_multi): candidate t sees positions
+ * 0 .. seq_lens[b] - T + t.  For head h of query row r over the visible s:
+ *   l_s = scale * q[r, h, :] . c_s   (576 dims)
+ *   out[r, h, :] = sum_s softmax(l)_s * c_s[0:512];  lse[r, h] = ln sum_s exp(l_s)
+ * With an FP8 latent cache c_s is code * tile scale, the fp32 product rounded
+ * to bf16 (what the tensor cores multiply).
+ *   q    bf16 [batch*T, n_heads, 576], n_heads 1..128
+ *   out  bf16 [batch*T, n_heads, 512]
+ *   lse  fp32 [batch*T, n_heads] or NULL
+ *   A row that sees nothing gives out = 0 and lse = -inf.
+ *   workspace / workspace_bytes: NULL and 0, or 256-byte aligned with at least
+ *        dsi_dense_mla_workspace_size() bytes: then long histories are split
+ *        over the device and joined (without it a sequence stays on one pair
+ *        of SMs).  Calls that may run at once need a workspace each.
+ * Cache rows outside the visible range of a sequence are never used: they may
+ * hold anything, as may block_table entries of pages past the history.  The
+ * page ids of visible positions are checked on the device: one outside the
+ * pool reads as rows of zeros and sets the device status to DSI_ERR_BOUNDS.
+ * Results do not depend on the split beyond rounding, and are the same from
+ * one call to the next.
+ * Errors: DSI_ERR_INVALID_ARG (null pointer, misaligned q, out or workspace,
+ * T < 1, NaN scale, inconsistent cache), DSI_ERR_UNSUPPORTED (n_heads outside
+ * 1..128, page_size not a multiple of 8, 2^31 cache rows or more),
+ * DSI_ERR_WORKSPACE (workspace too small).
+ */
+dsi_status dsi_dense_mla_decode(const void* q, const dsi_cache* cache, int32_t tokens_per_seq,
+                                int32_t n_heads, float scale, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dsi_window_mla_decode / dsi_window_mla_prefill — the same attention over a
+ * sliding window, with the first positions of the sequence always visible
+ * (sinks): a token that sees n positions causally attends to
+ *   { s < n : s >= n - window or s < n_sink }.
+ * Decode: rows as in dsi_dense_mla_decode.  Prefill: T tokens of one sequence
+ * (batch == 1), token t at position q_offset + t, n = q_offset + t + 1
+ * (a window of q_offset + T or more makes it dense causal attention).
+ *   window  >= 1;  n_sink >= 0
+ * Everything else, and the errors, as for dsi_dense_mla_decode;
+ * DSI_ERR_INVALID_ARG also for window < 1, n_sink < 0 and, in the prefill,
+ * q_offset + T > s_max.
+ */
+dsi_status dsi_window_mla_decode(const void* q, const dsi_cache* cache, int32_t tokens_per_seq,
+                                 int32_t n_heads, int64_t window, int64_t n_sink, float scale,
+                                 void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+dsi_status dsi_window_mla_prefill(const void* q, const dsi_cache* cache, int32_t T,
+                                  int32_t n_heads, int64_t q_offset, int64_t window,
+                                  int64_t n_sink, float scale, void* out, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace with which the dense and window calls split their work
+ * over the current device (the same for every shape; 256 when rows or n_heads
+ * is not positive). */
+size_t dsi_dense_mla_workspace_size(int32_t rows, int32_t n_heads);
+
+/*
  * dsi_norm_rope — head norms and position rotation of new tokens' queries and
  * keys in one pass, the keys written straight into their cache rows (the
  * pages have no counterpart: they start at normed, rotated queries and keys).

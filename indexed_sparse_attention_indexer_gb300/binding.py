@@ -76,6 +76,15 @@ SIGNATURES = {
                                      c_void_p, c_void_p, c_void_p]),
     "dsi_latent_fp8_append": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
                                         c_void_p]),
+    "dsi_dense_mla_decode": (c_int32, [c_void_p, ctypes.POINTER(DsiCache), c_int32, c_int32,
+                                       c_float, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "dsi_window_mla_decode": (c_int32, [c_void_p, ctypes.POINTER(DsiCache), c_int32, c_int32,
+                                        c_int64, c_int64, c_float, c_void_p, c_void_p, c_void_p,
+                                        c_size_t, c_void_p]),
+    "dsi_window_mla_prefill": (c_int32, [c_void_p, ctypes.POINTER(DsiCache), c_int32, c_int32,
+                                         c_int64, c_int64, c_int64, c_float, c_void_p, c_void_p,
+                                         c_void_p, c_size_t, c_void_p]),
+    "dsi_dense_mla_workspace_size": (c_size_t, [c_int32, c_int32]),
     "dsi_norm_rope": (c_int32, [ctypes.POINTER(DsiHeads), ctypes.POINTER(DsiHeads), c_int64,
                                 c_int32, c_float, c_void_p, c_int64, c_void_p, c_int32, c_int32,
                                 c_int32, c_void_p]),
@@ -356,6 +365,79 @@ def latent_fp8_append(x, dst_rows=None, codes=None, scales=None, stream=None,
                                    _ptr(scales), _stream(stream))
     _check(lib, "dsi_latent_fp8_append", st)
     return codes, scales
+
+
+def dense_mla_workspace_size(rows: int, n_heads: int, checked: bool = False) -> int:
+    """Bytes of workspace with which the dense and window calls split long histories."""
+    return int(load(checked).dsi_dense_mla_workspace_size(rows, n_heads))
+
+
+def _dense(fn: str, q, cache: Cache, args, rows: int, scale, out, lse, want_lse, workspace, stream,
+           checked):
+    """Checks and buffers shared by the dense and window calls; the new buffers belong to the
+    stream that the kernels run on."""
+    lib = load(checked)
+    _need(q.dtype == torch.bfloat16 and q.dim() == 3 and q.is_contiguous() and int(q.shape[2]) == D_QK,
+          f"q is a contiguous bf16 [rows, heads, {D_QK}] tensor")
+    _need(cache.latent is not None and cache.latent.device == q.device, "the cache has no latent rows on q's device")
+    n, H = int(q.shape[0]), int(q.shape[1])
+    _need(n == rows, f"q has {n} rows, the call {rows}")
+    if out is not None:
+        _need(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == (n, H, D_LATENT)
+              and out.device == q.device, f"out is a contiguous bf16 [rows, heads, {D_LATENT}] tensor")
+    if lse is not None:
+        _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (n, H)
+              and lse.device == q.device, "lse is a contiguous fp32 [rows, heads] tensor")
+    if n == 0 or H == 0:
+        return (out if out is not None else q.new_empty((n, H, D_LATENT)),
+                lse if lse is not None or not want_lse else q.new_empty((n, H), dtype=torch.float32))
+    with _on(q.device):
+        if out is None or workspace is None or (lse is None and want_lse):
+            on = stream
+            if on is not None and not hasattr(on, "cuda_stream"):
+                on = torch.cuda.ExternalStream(int(on), device=q.device)
+            with torch.cuda.stream(on):
+                if workspace is None:
+                    workspace = alloc_workspace(lib.dsi_dense_mla_workspace_size(n, H), q.device)
+                if out is None:
+                    out = torch.empty((n, H, D_LATENT), dtype=torch.bfloat16, device=q.device)
+                if lse is None and want_lse:
+                    lse = torch.empty((n, H), dtype=torch.float32, device=q.device)
+        st = getattr(lib, fn)(q.data_ptr(), cache.ref(), *args, scale, out.data_ptr(),
+                              lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(lib, fn, st)
+    return out, lse
+
+
+def dense_mla_decode(q, cache: Cache, scale: float, tokens_per_seq: int = 1, out=None, lse=None,
+                     want_lse=True, workspace=None, stream=None, checked: bool = False):
+    """Attention of the newest tokens over the whole latent cache: ``dsi_dense_mla_decode``.
+    ``q`` bf16 ``[batch * tokens_per_seq, heads, 576]``; returns (out, lse)."""
+    T = int(tokens_per_seq)
+    return _dense("dsi_dense_mla_decode", q, cache, (T, int(q.shape[1])), cache.struct.batch * T, scale,
+                  out, lse, want_lse, workspace, stream, checked)
+
+
+def window_mla_decode(q, cache: Cache, window: int, n_sink: int, scale: float,
+                      tokens_per_seq: int = 1, out=None, lse=None, want_lse=True, workspace=None,
+                      stream=None, checked: bool = False):
+    """The newest tokens over their last ``window`` positions and the first ``n_sink``:
+    ``dsi_window_mla_decode``."""
+    T = int(tokens_per_seq)
+    return _dense("dsi_window_mla_decode", q, cache, (T, int(q.shape[1]), int(window), int(n_sink)),
+                  cache.struct.batch * T, scale, out, lse, want_lse, workspace, stream, checked)
+
+
+def window_mla_prefill(q, cache: Cache, q_offset: int, window: int, n_sink: int, scale: float,
+                       out=None, lse=None, want_lse=True, workspace=None, stream=None,
+                       checked: bool = False):
+    """Tokens ``q_offset ...`` of one sequence, each over its last ``window`` positions and the
+    first ``n_sink``: ``dsi_window_mla_prefill``."""
+    T = int(q.shape[0])
+    return _dense("dsi_window_mla_prefill", q, cache, (T, int(q.shape[1]), int(q_offset), int(window),
+                                                       int(n_sink)),
+                  T, scale, out, lse, want_lse, workspace, stream, checked)
 
 
 def rope_table(n_positions: int, rope_dim: int, theta: float = 10000.0, device="cuda"):

@@ -5,6 +5,7 @@
 
 #include <atomic>
 
+#include "dense_mla.h"
 #include "kernels.h"
 #include "latent_fp8.h"
 #include "norm_rope.h"
@@ -421,6 +422,77 @@ dsi_status dsi_latent_fp8_append(const void* x, int64_t n_rows, int64_t ld_x,
   return from_cuda(launch_latent_fp8_append(reinterpret_cast<const bf16*>(x), n_rows, ld_x,
                                             dst_rows, static_cast<uint8_t*>(codes), scales,
                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t dsi_dense_mla_workspace_size(int32_t rows, int32_t n_heads) {
+  if (rows <= 0 || n_heads <= 0) return 256;
+  return dense_mla_workspace();
+}
+
+// The dense and window calls: rows of a decode batch or of a prefill.
+static dsi_status dense_common(const void* q, const dsi_cache* cache, int64_t rows, int T, int H,
+                               int decode, int64_t q_offset, int64_t window, int64_t n_sink,
+                               float scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                               void* stream) {
+  if (!q || !out || rows < 0 || window < 1 || n_sink < 0 || !(scale == scale))
+    return DSI_ERR_INVALID_ARG;
+  if (rows > 0x7fffffff) return DSI_ERR_UNSUPPORTED;
+  if (H < 1 || H > 128) return DSI_ERR_UNSUPPORTED;
+  const dsi_status s = check_cache(cache, (int)rows, decode, q_offset, false, true, decode ? T : 1);
+  if (s != DSI_OK) return s;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSI_ERR_INVALID_ARG;
+  if (cache->s_max >= (1ll << 31) ||
+      (cache->block_table ? cache->num_pages > ((1ll << 31) - 1) / cache->page_size
+                          : cache->batch > 0 && cache->s_max > ((1ll << 31) - 1) / cache->batch))
+    return DSI_ERR_UNSUPPORTED;
+  if (ws) {
+    if (!aligned(ws, 256)) return DSI_ERR_INVALID_ARG;
+    if (ws_bytes < dense_mla_workspace()) return DSI_ERR_WORKSPACE;
+  }
+  if (rows == 0) return DSI_OK;
+  DenseArgs a;
+  a.q = reinterpret_cast<const bf16*>(q);
+  a.c = view_of(cache);
+  a.c.tokens_per_seq = decode ? T : 1;
+  a.latent_scale = cache->latent_dtype == DSI_FP8_E4M3 ? cache->latent_scale : nullptr;
+  a.rows = (int)rows;
+  a.T = decode ? T : (int)rows;
+  a.H = H;
+  a.decode = decode;
+  a.q_offset = q_offset;
+  // nothing lies past s_max: larger windows and sink counts are the same ones
+  a.window = window < cache->s_max ? window : cache->s_max;
+  a.n_sink = n_sink < cache->s_max ? n_sink : cache->s_max;
+  a.scale = scale;
+  a.out = reinterpret_cast<bf16*>(out);
+  a.lse = lse;
+  a.ws = ws;
+  a.err = status_ptr();
+  return from_cuda(launch_dense_mla(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dsi_status dsi_dense_mla_decode(const void* q, const dsi_cache* cache, int32_t tokens_per_seq,
+                                int32_t n_heads, float scale, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  return dsi_window_mla_decode(q, cache, tokens_per_seq, n_heads, INT64_MAX, 0, scale, out, lse,
+                               workspace, workspace_bytes, stream);
+}
+
+dsi_status dsi_window_mla_decode(const void* q, const dsi_cache* cache, int32_t tokens_per_seq,
+                                 int32_t n_heads, int64_t window, int64_t n_sink, float scale,
+                                 void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  if (!cache || tokens_per_seq < 1 || cache->batch < 0) return DSI_ERR_INVALID_ARG;
+  return dense_common(q, cache, (int64_t)cache->batch * tokens_per_seq, tokens_per_seq, n_heads, 1,
+                      0, window, n_sink, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+dsi_status dsi_window_mla_prefill(const void* q, const dsi_cache* cache, int32_t T,
+                                  int32_t n_heads, int64_t q_offset, int64_t window,
+                                  int64_t n_sink, float scale, void* out, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  return dense_common(q, cache, T, T, n_heads, 0, q_offset, window, n_sink, scale, out, lse,
+                      workspace, workspace_bytes, stream);
 }
 
 dsi_status dsi_norm_rope(const dsi_heads* queries, const dsi_heads* keys, int64_t n_rows,

@@ -124,3 +124,78 @@ def test_rope_table():
     assert t.shape == (70000, 64) and t.dtype == torch.float32
     a = torch.tensor(69999.0, dtype=torch.float64) * 10000.0 ** (-2.0 * 5 / 64)
     assert abs(float(t[69999, 5]) - float(a.cos())) < 1e-6 and abs(float(t[69999, 37]) - float(a.sin())) < 1e-6
+
+
+def _cache(**kw):
+    c = binding.DsiCache()
+    c.k_idx, c.latent, c.seq_lens, c.batch, c.s_max = None, FAKE, FAKE, 4, 1024
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def _dense(L, c, q=FAKE, T=1, H=128, scale=0.04, out=FAKE, lse=None, ws=None, wsb=0):
+    return L.dsi_dense_mla_decode(q, ctypes.byref(c) if c is not None else None, T, H, scale, out, lse, ws, wsb, None)
+
+
+def test_dense_and_window_refusals(L):
+    need = L.dsi_dense_mla_workspace_size(4, 128)
+    assert need >= 256 and L.dsi_dense_mla_workspace_size(0, 128) == 256
+    calls = [
+        lambda c, window=100, sink=4, T=1, off=0, **kw: _dense(L, c, T=T, **kw),
+        lambda c, window=100, sink=4, T=1, off=0, q=FAKE, H=128, scale=0.04, out=FAKE, lse=None, ws=None, wsb=0:
+            L.dsi_window_mla_decode(q, ctypes.byref(c) if c is not None else None, T, H, window, sink, scale,
+                                    out, lse, ws, wsb, None),
+        lambda c, window=100, sink=4, T=1, off=0, q=FAKE, H=128, scale=0.04, out=FAKE, lse=None, ws=None, wsb=0:
+            L.dsi_window_mla_prefill(q, ctypes.byref(c) if c is not None else None, T, H, off, window, sink,
+                                     scale, out, lse, ws, wsb, None),
+    ]
+    for i, f in enumerate(calls):
+        base = dict(batch=1) if i == 2 else {}
+        mk = lambda **kw: _cache(**dict(base, **kw))
+        assert f(None) == E
+        for kw in (dict(q=None), dict(out=None), dict(q=FAKE + 8), dict(out=FAKE + 2), dict(lse=FAKE + 2),
+                   dict(scale=float("nan")), dict(ws=FAKE + 16, wsb=need), dict(T=-1)):
+            assert f(mk(), **kw) == E, (i, kw)
+        for kw in (dict(H=0), dict(H=129), dict(H=-1)):
+            assert f(mk(), **kw) == U, (i, kw)
+        assert f(mk(), ws=FAKE, wsb=need - 1) == binding.DSI_ERR_WORKSPACE
+        for kw in (dict(latent=None), dict(latent=FAKE + 8), dict(batch=-1), dict(s_max=0),
+                   dict(latent_dtype=1), dict(latent_dtype=1, latent_scale=FAKE + 2),
+                   dict(block_table=FAKE, page_size=0, max_pages=16, num_pages=9),
+                   dict(block_table=FAKE, page_size=64, max_pages=15, num_pages=9)):
+            assert f(mk(**kw)) == E, (i, kw)
+        for kw in (dict(latent_dtype=2), dict(s_max=1 << 31),
+                   dict(block_table=FAKE, page_size=12, max_pages=1, s_max=12, num_pages=9),
+                   dict(block_table=FAKE, page_size=64, max_pages=16, num_pages=1 << 25)):
+            assert f(mk(**kw)) == U, (i, kw)
+    dec, pre = calls[1], calls[2]
+    assert _dense(L, _cache(), T=0) == E and _dense(L, _cache(seq_lens=None)) == E
+    assert _dense(L, _cache(batch=1 << 30), T=4) == U                # 2^32 query rows
+    assert _dense(L, _cache(batch=1 << 21, s_max=1 << 10)) == U       # 2^31 cache rows
+    for f in (dec, pre):
+        c = _cache(batch=1)
+        assert f(c, window=0) == E and f(c, window=-5) == E and f(c, sink=-1) == E
+    assert pre(_cache(batch=2)) == E and pre(_cache(batch=1), off=-1) == E
+    assert pre(_cache(batch=1), T=8, off=1020) == E                   # beyond s_max
+    assert _dense(L, _cache(batch=0)) == OK and pre(_cache(batch=1), T=0) == OK
+
+
+def test_dense_binding_checks(L):
+    lat = torch.zeros((2, 64, 576), dtype=torch.bfloat16)
+    cache = binding.Cache(None, lat, torch.zeros(2, dtype=torch.int32))
+    q = torch.zeros((2, 8, 576), dtype=torch.bfloat16)
+    for bad in (q.float(), q[:, :, :512], q.transpose(0, 1), q[:1]):
+        with pytest.raises(ValueError):
+            binding.dense_mla_decode(bad, cache, 0.04)
+        with pytest.raises(ValueError):
+            binding.window_mla_decode(bad, cache, 10, 1, 0.04)
+    for kw in (dict(out=torch.zeros((2, 8, 512))), dict(out=torch.zeros((2, 8, 576), dtype=torch.bfloat16)),
+               dict(lse=torch.zeros((2, 7))), dict(lse=torch.zeros((2, 8), dtype=torch.float64)),
+               dict(tokens_per_seq=2)):
+        with pytest.raises(ValueError):
+            binding.dense_mla_decode(q, cache, 0.04, **kw)
+    with pytest.raises(ValueError):
+        binding.dense_mla_decode(q, binding.Cache(torch.zeros((2, 64, 64), dtype=torch.bfloat16), None), 0.04)
+    with pytest.raises(ValueError):
+        binding.window_mla_prefill(q.float(), cache, 0, 10, 1, 0.04)
