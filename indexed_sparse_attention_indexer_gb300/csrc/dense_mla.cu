@@ -1,86 +1,917 @@
 // Attention over the whole latent cache, or over a sliding window of it with
-// the first positions visible.
+// the first positions visible, on the tcgen05 tensor cores.
 //
-// One warp takes one head of one query row: 18 query dims and 16 output dims
-// a lane, the visible positions one after the other (a coalesced 1152-byte
-// row, a shuffle sum for the logit, an online softmax step).  The eight heads
-// of a block read the same rows through L1.  Bound by instruction issue.
+// The rows of the MMA's M dimension are 128 (query token, head) pairs: as many
+// consecutive tokens of one sequence as fit (a group; 128 heads: one token).
+// One group's fp32 output (128 x 512) alone would fill a CTA's tensor memory,
+// so a cluster of two CTAs shares a group by dimension:
+//   CTA 0: logits over key dims   0..255 and 512..543, output dims   0..255
+//   CTA 1: logits over key dims 256..511 and 544..575, output dims 256..511
+// and the two partial logit tiles (128 x 64 positions, fp32) are swapped
+// through distributed shared memory, so that both take the same softmax
+// decisions.  Every cache row is read once from HBM for a group.
+//
+// A group's positions are cut into tiles of 64 aligned positions: those that
+// hold sinks, then those from the window's start to the end of the history.
+// The tiles of all groups, laid end to end, are dealt out in equal contiguous
+// runs to the clusters (one resident per SM pair): a run may end inside a
+// group, whose pieces are then joined by a second kernel from their running
+// maxima and sums.  Where dealing out whole groups costs at most
+// kWholeSlack tiles more, groups stay whole and nothing is joined.
+//
+// Roles in a CTA (12 warps), each walking the same list of pieces; the tile
+// pipeline runs on across pieces:
+//   producers (warps 0-1): a tile's rows into a 128-byte-swizzled stage (ring
+//     of 4) by TMA boxes; tiles at an edge (not wholly visible to every token
+//     of the group) and FP8 rows with plain loads, rows that nobody sees as
+//     zeros, so that what they hold never meets the tensor core;
+//   logit issuer (warp 3): S = Qslice . C^T into one of two TMEM tiles;
+//   exchange (warps 4-7): the group's query slice into TMEM (rope half: shared
+//     memory); this CTA's partial logits out of TMEM into the peer's buffer;
+//   softmax (warps 8-11, one row per thread): own partial plus the peer's,
+//     mask, online softmax in log2 units with a lazily moved reference max
+//     (the accumulator is rescaled only when the max grows by more than 2^8),
+//     P in bf16 to shared memory, and the epilogue;
+//   value issuer (warp 2): O += P . V from the same stage.
+// Every wait is bounded; the cluster syncs after set-up and before exit.
 #include "dense_mla.h"
 
+#include <string.h>
+
+#include <atomic>
+
 #include "kernels.h"
+#include "tc_common.cuh"
+#include "tma_host.h"
 
 namespace dsi {
+using namespace tc;
+
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kM = 128;                        // rows of a group: (token, head) pairs
+constexpr int kNp = 64;                        // positions per tile
+constexpr int kBlocks = 5;                     // stage blocks: four 64-dim blocks and the rope dims
+constexpr int kStages = 4;
+constexpr int kBlockBytes = kNp * 128;         // 64 dims of a tile
+constexpr int kStageBytes = kBlocks * kBlockBytes;
+constexpr int kRopeHalf = 32;                  // rope dims of each CTA
+// 12 warps (three per SM sub-partition): at most 168 registers a thread
+constexpr int kProducers = 2;                  // warps 0-1
+constexpr int kPvWarp = 2;
+constexpr int kQkWarp = 3;                     // then exchange: warps 4-7
+constexpr int kSmWarp0 = 8;                    // softmax: warps 8-11
+constexpr int kThreads = 12 * 32;
+constexpr int kProdThreads = kProducers * 32;
+constexpr int kMaxClusters = 128;
+constexpr int kWholeSlack = 8;
+constexpr int kPoison = 8;                     // tiles whose poisoned rows are remembered
 
-// Physical row of position p of sequence b; -1 (reported) for a bad page id.
-__device__ __forceinline__ int64_t row_of(const CacheView& c, int b, int64_t p, int* err) {
-  if (!c.block_table) return (int64_t)b * c.s_max + p;
-  const int64_t pg = p / c.page_size;
-  const int page = __ldg(c.block_table + (int64_t)b * c.max_pages + pg);
-  if (page < 0 || page >= c.num_pages) { report(err, kErrBounds); return -1; }
-  return (int64_t)page * c.page_size + (p - pg * c.page_size);
+constexpr int OFF_C = 0;
+constexpr int OFF_P = OFF_C + kStages * kStageBytes;      // P [128 x 64] bf16
+constexpr int OFF_X = OFF_P + kM * kNp * 2;               // the peer's partial logits, fp32
+constexpr int OFF_QR = OFF_X + kM * kNp * 4;              // query rope half, rows of 128 bytes
+constexpr int OFF_BAR = OFF_QR + kM * 128;
+constexpr int kBars = 2 * kStages + 10;
+constexpr int OFF_ROWS = OFF_BAR + kBars * 8;             // [2][64] cache rows of a tile (generic path)
+constexpr int OFF_POISON = OFF_ROWS + 2 * kNp * 4;
+constexpr int OFF_MISC = OFF_POISON + kPoison * 8;
+constexpr int OFF_SCAN = OFF_MISC + 64;                   // 40 ints
+constexpr int SMEM = OFF_SCAN + 160 + 1024;
+static_assert(SMEM <= 227 * 1024, "shared memory");
+static_assert(kProdThreads == kNp, "a producer thread looks up one row of a tile");
+static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 8 == 0, "alignment");
+
+constexpr uint32_t TM_S = 0;      // two logit tiles of 64 columns
+constexpr uint32_t TM_Q = 128;    // query slice: four 64-dim blocks, 128 columns
+constexpr uint32_t TM_O = 256;    // output half, 256 columns
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t IDESC_S = idesc_f32(1, kM, kNp);
+constexpr uint32_t IDESC_O = idesc_f32_bmn(1, kM, 256);
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleLog2 = 8.f;
+constexpr uint32_t kXBytes = kM * kNp * 4;
+
+// What a cluster leaves for the join: the group that its last piece starts and
+// does not finish (or -1), the group that its first piece continues (or -1),
+// and whether it finishes it.
+struct Record { int starts, continues, finishes, pad; };
+struct Workspace {
+  float* o;        // [2 * clusters][128][512] unnormalised outputs
+  float4* ml;      // [2 * clusters][128] reference max, rounded sum, exact sum
+  Record* rec;     // [clusters]
+};
+
+struct Plan {
+  int tokens;      // tokens of a group
+  int per_seq;     // groups of a sequence
+  int groups;
+  int split;       // a workspace is there
+};
+
+struct Group {
+  int b, row0, nt;             // sequence, first query row, tokens
+  int n_first, n_last;         // visible lengths of the first and last token
+  int lo, main0, sink_tiles, tiles;
+};
+
+__device__ __forceinline__ Group group_of(const DenseArgs& a, const Plan& p, int g) {
+  Group r;
+  r.b = p.per_seq == 1 ? g : g / p.per_seq;
+  const int t0 = (g - r.b * p.per_seq) * p.tokens;
+  r.nt = min(p.tokens, a.T - t0);
+  r.row0 = r.b * a.T + t0;
+  r.n_first = (int)visible_len(a.c, r.row0, a.decode, a.q_offset);
+  r.n_last = r.nt == 1 ? r.n_first
+                       : (int)visible_len(a.c, r.row0 + r.nt - 1, a.decode, a.q_offset);
+  r.lo = max(0, r.n_first - (int)a.window);
+  r.main0 = r.lo / kNp;
+  r.sink_tiles = min((min((int)a.n_sink, r.lo) + kNp - 1) / kNp, r.main0);
+  // a group that sees nothing still has a (wholly masked) tile: its output is written
+  r.tiles = max(1, r.sink_tiles + max(0, (r.n_last + kNp - 1) / kNp - r.main0));
+  return r;
+}
+__device__ __forceinline__ int tile_pos(const Group& g, int t) {
+  return (t < g.sink_tiles ? t : g.main0 + t - g.sink_tiles) * kNp;
+}
+// Every token of the group sees all positions p0 .. p0 + len - 1.
+__device__ __forceinline__ bool all_see(const DenseArgs& a, const Group& g, int p0, int len) {
+  return p0 + len <= g.n_first && (p0 >= g.n_last - (int)a.window || p0 + len <= (int)a.n_sink);
+}
+__device__ __forceinline__ bool any_sees(const DenseArgs& a, const Group& g, int p) {
+  return p < g.n_last && (p >= g.lo || p < (int)a.n_sink);
 }
 
-__global__ void __launch_bounds__(256)
-dense_mla_simt(DenseArgs a) {
-  const int r = blockIdx.x, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (h >= a.H) return;
-  const int b = seq_of_row(a.c, r, a.decode);
-  const int64_t n = visible_len(a.c, r, a.decode, a.q_offset);
-  const int64_t lo = n > a.window ? n - a.window : 0;
-  const int64_t sinks = a.n_sink < lo ? a.n_sink : lo;
-  float q[18], o[16];
-  const bf16* qrow = a.q + ((int64_t)r * a.H + h) * DSI_D_QK;
+// A cluster's pieces: whole groups g, g + stride, ..., or the groups of a run
+// of `left` tiles that starts at tile t of group g.
+struct Walk {
+  int g, t, left, stride;      // stride > 0: whole groups
+};
+struct Piece {
+  Group grp;
+  int g, t0, t1;
+  bool last;                   // the cluster's last
+};
+__device__ __forceinline__ bool next_piece(const DenseArgs& a, const Plan& p, Walk& w, Piece& x) {
+  if (w.g >= p.groups || w.left <= 0) return false;
+  x.g = w.g;
+  x.grp = group_of(a, p, w.g);
+  x.t0 = w.t;
+  if (w.stride > 0) {
+    x.t1 = x.grp.tiles;
+    w.g += w.stride;
+    x.last = w.g >= p.groups;
+  } else {
+    x.t1 = min(x.grp.tiles, w.t + w.left);
+    w.left -= x.t1 - x.t0;
+    w.t = 0;
+    if (x.t1 == x.grp.tiles) ++w.g;
+    x.last = w.left <= 0 || w.g >= p.groups;
+  }
+  return true;
+}
+
+// Cache row of position p of sequence b; -1 (reported) for a bad page id.
+__device__ __forceinline__ int row_of(const CacheView& c, int b, int p, int* err) {
+  if (!c.block_table) return (int)((int64_t)b * c.s_max + p);
+  const int pg = p / c.page_size;
+  const int page = __ldg(c.block_table + (int64_t)b * c.max_pages + pg);
+  if (page < 0 || page >= c.num_pages) { report(err, kErrBounds); return -1; }
+  return page * c.page_size + (p - pg * c.page_size);
+}
+
+__device__ __forceinline__ void producers_sync() { asm volatile("bar.sync 1, 64;\n" ::: "memory"); }
+
+// 16 E4M3 codes times their tile scale, rounded to bf16 (lo = codes 0..7).
+__device__ __forceinline__ void e4m3x16_scaled(const uint4& v, float sc, uint4& lo, uint4& hi) {
+  float f[16];
+  fp8x16_to_f32(v, f);
+  uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 18; ++i) q[i] = __bfloat162float(qrow[i * 32 + lane]);
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i] * sc, f[2 * i + 1] * sc);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  lo = make_uint4(w[0], w[1], w[2], w[3]);
+  hi = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ bool bf16x8_finite(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool ok = true;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  for (int64_t j = 0; j < sinks + (n - lo); ++j) {
-    const int64_t p = j < sinks ? j : lo + (j - sinks);
-    const int64_t row = row_of(a.c, b, p, a.err);
-    float c[18], dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < 18; ++i) {
-      const int d = i * 32 + lane;
-      if (row < 0) {
-        c[i] = 0.f;
-      } else if (a.latent_scale) {
-        __nv_fp8_e4m3 v;
-        v.__x = reinterpret_cast<const uint8_t*>(a.c.latent)[row * DSI_D_QK + d];
-        c[i] = __bfloat162float(__float2bfloat16(static_cast<float>(v) * a.latent_scale[row * 5 + d / 128]));
-      } else {
-        c[i] = __bfloat162float(a.c.latent[row * DSI_D_QK + d]);
-      }
-      dot = fmaf(q[i], c[i], dot);
+  for (int i = 0; i < 4; ++i)
+    ok = ok && (w[i] & 0x7F80u) != 0x7F80u && (w[i] & 0x7F800000u) != 0x7F800000u;
+  return ok;
+}
+
+// Bits 0 .. k-1 of 64.
+__device__ __forceinline__ uint64_t low_bits(int k) {
+  return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1ull;
+}
+
+template <bool F8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, Workspace ws,
+             int box) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);   // [kStages] tile landed
+  uint64_t* empty = full + kStages;            // [kStages] stage free (value MMAs done)
+  uint64_t* s_full = empty + kStages;          // [2] logits in TMEM
+  uint64_t* s_empty = s_full + 2;              // [2] logits read out (exchange and softmax)
+  uint64_t* p_full = s_full + 4;               // P written
+  uint64_t* p_empty = s_full + 5;              // P.V done
+  uint64_t* q_ready = s_full + 6;              // query slice in place
+  uint64_t* o_done = s_full + 7;               // a piece's last P.V done
+  uint64_t* x_full = s_full + 8;               // the peer's partial logits landed
+  uint64_t* x_empty = s_full + 9;              // the peer has read what we sent
+  int* rows_s = reinterpret_cast<int*>(smem + OFF_ROWS);
+  unsigned int* poison = reinterpret_cast<unsigned int*>(smem + OFF_POISON);   // [kPoison][2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  int* start_s = reinterpret_cast<int*>(smem + OFF_MISC + 8);                   // group, tile
+  int* widest_s = reinterpret_cast<int*>(smem + OFF_MISC + 16);
+  unsigned long long* total_s = reinterpret_cast<unsigned long long*>(smem + OFF_MISC + 24);
+  int* scan_s = reinterpret_cast<int*>(smem + OFF_SCAN);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rho = cluster_ctarank();
+  const uint32_t peer = rho ^ 1u;
+  const int k = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  int* err = a.err;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], kProducers);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 256);
+    }
+    mbar_init(p_full, 128);
+    mbar_init(p_empty, 1);
+    mbar_init(q_ready, 128);
+    mbar_init(o_done, 1);
+    mbar_init(x_full, 1);
+    mbar_init(x_empty, 4);
+    *abort_flag = 0;
+    start_s[0] = plan.groups;
+    start_s[1] = 0;
+    *widest_s = 0;
+    *total_s = 0ull;
+    fence_barrier_init();
+  }
+  if (warp == kQkWarp) tmem_alloc(tmem_slot, TMEM_COLS);
+  if (warp == 0 && lane == 0) prefetch_tmap(&lmap);
+  grid_dep_wait();     // lengths, queries and cache rows may come from the kernel before
+  __syncthreads();
+
+  // ---- the cluster's share of the tiles (every CTA computes the same split) ----
+  {
+    unsigned long long sum = 0;
+    int widest = 0;
+    for (int g = tid; g < plan.groups; g += kThreads) {
+      const int n = group_of(a, plan, g).tiles;
+      sum += (unsigned)n;
+      widest = max(widest, n);
     }
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, w);
-    const float v = dot * a.scale * kLog2e;
-    const float m_new = fmaxf(m, v);
-    const float f = m == -INFINITY ? 0.f : exp2f(m - m_new), pr = exp2f(v - m_new);
-    m = m_new;
-    l = l * f + pr;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = fmaf(pr, c[i], o[i] * f);
+    for (int o = 16; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      widest = max(widest, __shfl_xor_sync(0xffffffffu, widest, o));
+    }
+    if (lane == 0) {
+      atomicAdd(total_s, sum);
+      atomicMax(widest_s, widest);
+    }
   }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  bf16* out = a.out + ((int64_t)r * a.H + h) * DSI_D_LATENT;
+  __syncthreads();
+  const unsigned long long total = *total_s;
+  const unsigned long long even = (total + clusters - 1) / clusters;
+  const unsigned long long whole =
+      (unsigned long long)((plan.groups + clusters - 1) / clusters) * (unsigned)*widest_s;
+  Walk walk;
+  if (!plan.split || total >= (1ull << 30) || whole <= even + kWholeSlack) {
+    walk.g = k;
+    walk.t = 0;
+    walk.left = 1;
+    walk.stride = clusters;
+  } else {
+    const int share = (int)even;
+    const long long start = (long long)share * k;
+    long long before = 0;
+    for (int g0 = 0; g0 < plan.groups && start < (long long)total; g0 += kThreads) {
+      const int g = g0 + tid;
+      const int n = g < plan.groups ? group_of(a, plan, g).tiles : 0;
+      int chunk;
+      const int at = block_exclusive_scan(n, scan_s, chunk);
+      if (n > 0 && start >= before + at && start < before + at + n) {
+        start_s[0] = g;
+        start_s[1] = (int)(start - before - at);
+      }
+      before += chunk;
+      if (start < before) break;               // uniform: found in this chunk
+    }
+    __syncthreads();
+    walk.g = start_s[0];
+    walk.t = start_s[1];
+    walk.left = share;
+    walk.stride = 0;
+  }
+  if (tid == 0) mbar_arrive_expect_tx(x_full, kXBytes);   // the peer's first tile
+  tc_fence_before();
+  cluster_sync();      // the peer's barriers exist (and are armed) before anyone uses them
+  tc_fence_after();
+  grid_dep_launch();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < kProducers) {
+    // ======================= producers ==========================================
+    Piece x;
+    int tg = 0, loaded = 0;                    // tiles; tiles by plain loads
+    bool ok = true;
+    uint32_t issued = 0;                       // stages with a TMA tile (lane 0 of warp 0)
+    while (ok && next_piece(a, plan, walk, x)) {
+      for (int t = x.t0; t < x.t1; ++t, ++tg) {
+        const int stage = tg % kStages;
+        const uint32_t ph = (uint32_t)(tg / kStages) & 1u;
+        const int p0 = tile_pos(x.grp, t);
+        uint8_t* st = smem + OFF_C + stage * kStageBytes;
+        unsigned int* pz = poison + (tg & (kPoison - 1)) * 2;
+        const bool whole = all_see(a, x.grp, p0, kNp);
+        if (!F8 && whole) {
+          // whole tile by TMA: boxes of `box` rows (a page or a part of one) x 64 dims
+          if (!(ok = warp_wait(&empty[stage], ph ^ 1, abort_flag, err))) break;
+          if (warp == 0) {
+            if (lane == 0) {
+              pz[0] = pz[1] = 0u;
+              mbar_arrive_expect_tx(&full[stage], kStageBytes);
+              issued |= 1u << stage;
+            }
+            __syncwarp();
+            const int boxes = kNp / box;
+            for (int i = lane; i < boxes * kBlocks; i += 32) {
+              const int bx = i / kBlocks, blk = i - bx * kBlocks;
+              const int row = row_of(a.c, x.grp.b, p0 + bx * box, err);
+              // a bad page id: the box past the tensor's last row, which reads as zeros
+              const int y = row < 0 ? (int)a.c.num_pages * a.c.page_size : row;
+              tma_load_2d(st + blk * kBlockBytes + bx * box * 128, &lmap,
+                          blk < 4 ? (int)rho * 256 + blk * 64 : DSI_D_LATENT, y, &full[stage]);
+            }
+          } else if (lane == 0) {
+            mbar_arrive(&full[stage]);
+          }
+          continue;
+        }
+        // plain loads: rows that no token sees become zeros; a row that only
+        // some tokens see is searched for NaN and infinities, which are taken
+        // out and remembered (its logits become NaN where it is seen)
+        int* rows = rows_s + (loaded++ & 1) * kNp;   // (the barrier below keeps its readers apart)
+        rows[tid] = any_sees(a, x.grp, p0 + tid) ? row_of(a.c, x.grp.b, p0 + tid, err) : -1;
+        if (tid == 0) pz[0] = pz[1] = 0u;
+        producers_sync();
+        if constexpr (F8) {
+          constexpr int kPieces = 18;          // 16 codes each: 256 latent and 32 rope dims
+          constexpr int kPer = kNp * kPieces / kProdThreads;
+          static_assert(kPer * kProdThreads == kNp * kPieces, "whole rounds");
+          const uint8_t* codes = reinterpret_cast<const uint8_t*>(a.c.latent);
+          uint4 cv[kPer];
+          float sc[kPer];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) out[i * 32 + lane] = __float2bfloat16(o[i] * inv);
-  if (a.lse && lane == 0) a.lse[(int64_t)r * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) / kLog2e;
+          for (int i = 0; i < kPer; ++i) {
+            const int q = tid + i * kProdThreads, rr = q / kPieces, u = q - rr * kPieces;
+            const int64_t row = rows[rr];
+            const int d0 = u < 16 ? (int)rho * 256 + u * 16
+                                  : DSI_D_LATENT + (int)rho * kRopeHalf + (u - 16) * 16;
+            cv[i] = make_uint4(0, 0, 0, 0);
+            sc[i] = 0.f;
+            if (row >= 0) {
+              cv[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * DSI_D_QK + d0));
+              sc[i] = __ldg(a.latent_scale + row * 5 + (d0 >> 7));
+            }
+          }
+          if (!(ok = warp_wait(&empty[stage], ph ^ 1, abort_flag, err))) break;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int q = tid + i * kProdThreads, rr = q / kPieces, u = q - rr * kPieces;
+            uint4 lo, hi;
+            e4m3x16_scaled(cv[i], sc[i], lo, hi);
+            if (!whole && !all_see(a, x.grp, p0 + rr, 1) && !(bf16x8_finite(lo) && bf16x8_finite(hi))) {
+              lo = hi = make_uint4(0, 0, 0, 0);
+              atomicOr(pz + (rr >> 5), 1u << (rr & 31));
+            }
+            uint8_t* blk = st + (u >> 2) * kBlockBytes;
+            const uint32_t ch = u < 16 ? (uint32_t)(u & 3) * 2 : rho * 4 + (uint32_t)(u - 16) * 2;
+            *reinterpret_cast<uint4*>(blk + sw128_offset(rr, ch)) = lo;
+            *reinterpret_cast<uint4*>(blk + sw128_offset(rr, ch + 1)) = hi;
+          }
+        } else {
+          constexpr int kPieces = 36;          // 16 bytes each: 256 latent and 32 rope dims
+          constexpr int kBatch = 12, kRounds = kNp * kPieces / (kProdThreads * kBatch);
+          static_assert(kRounds * kBatch * kProdThreads == kNp * kPieces, "whole rounds");
+          if (!(ok = warp_wait(&empty[stage], ph ^ 1, abort_flag, err))) break;
+          for (int b0 = 0; b0 < kRounds; ++b0) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int q = tid + (b0 * kBatch + i) * kProdThreads, rr = q / kPieces, u = q - rr * kPieces;
+              const int64_t row = rows[rr];
+              const int d0 = u < 32 ? (int)rho * 256 + u * 8
+                                    : DSI_D_LATENT + (int)rho * kRopeHalf + (u - 32) * 8;
+              v[i] = make_uint4(0, 0, 0, 0);
+              if (row >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(a.c.latent + row * DSI_D_QK + d0));
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int q = tid + (b0 * kBatch + i) * kProdThreads, rr = q / kPieces, u = q - rr * kPieces;
+              if (!all_see(a, x.grp, p0 + rr, 1) && !bf16x8_finite(v[i])) {
+                v[i] = make_uint4(0, 0, 0, 0);
+                atomicOr(pz + (rr >> 5), 1u << (rr & 31));
+              }
+              const uint32_t ch = u < 32 ? (uint32_t)(u & 7) : rho * 4 + (uint32_t)(u - 32);
+              *reinterpret_cast<uint4*>(st + (u >> 3) * kBlockBytes + sw128_offset(rr, ch)) = v[i];
+            }
+          }
+        }
+        fence_proxy_async_smem();   // the tensor core reads the stage through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[stage]);
+      }
+    }
+    // never leave the CTA with a copy still landing in shared memory
+    if (warp == 0 && lane == 0 && *abort_flag) {
+      volatile int no_abort = 0;    // the drain is bounded by time only
+      for (int s = 0; s < kStages; ++s) {
+        if (!((issued >> s) & 1u)) continue;
+        int last = tg - 1;          // the last tile that used stage s
+        while (last >= 0 && last % kStages != s) --last;
+        if (last >= 0)
+          mbar_wait(&full[s], (uint32_t)(last / kStages) & 1u, &no_abort, err, 100000000ull);
+      }
+    }
+  } else if (warp == kQkWarp) {
+    // ======================= logit issuer =======================================
+    if (lane == 0) {
+      Piece x;
+      int tg = 0, pieces = 0;
+      bool ok = true;
+      const uint64_t qr = desc_sw128(smem_u32(smem + OFF_QR));
+      while (ok && next_piece(a, plan, walk, x)) {
+        if (!(ok = mbar_wait(q_ready, (uint32_t)pieces & 1u, abort_flag, err))) break;
+        ++pieces;
+        for (int t = x.t0; t < x.t1; ++t, ++tg) {
+          const int stage = tg % kStages, sb = tg & 1;
+          if (!(ok = mbar_wait(&full[stage], (uint32_t)(tg / kStages) & 1u, abort_flag, err))) break;
+          if (!(ok = mbar_wait(&s_empty[sb], ((uint32_t)(tg >> 1) & 1u) ^ 1u, abort_flag, err))) break;
+          tc_fence_after();
+          const uint32_t t_s = tmem + TM_S + sb * kNp;
+          const uint32_t base = smem_u32(smem + OFF_C + stage * kStageBytes);
+          const uint64_t d0 = desc_sw128(base);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            mma_bf16_tmem_a(t_s, tmem + TM_Q + i * 8,
+                            d0 + (uint64_t)(((i >> 2) * kBlockBytes + (i & 3) * 32) >> 4), IDESC_S,
+                            i > 0 ? 1u : 0u);
+          const uint64_t dr = d0 + (uint64_t)((4 * kBlockBytes + rho * 64) >> 4);
+#pragma unroll
+          for (int i = 0; i < kRopeHalf / 16; ++i)
+            mma_bf16(t_s, qr + (uint64_t)((i * 32) >> 4), dr + (uint64_t)((i * 32) >> 4), IDESC_S, 1u);
+          mma_commit(&s_full[sb]);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kPvWarp) {
+    // ======================= value issuer =======================================
+    if (lane == 0) {
+      Piece x;
+      int tg = 0;
+      bool ok = true;
+      const uint64_t pd = desc_sw128(smem_u32(smem + OFF_P));
+      while (ok && next_piece(a, plan, walk, x)) {
+        for (int t = x.t0; t < x.t1; ++t, ++tg) {
+          const int stage = tg % kStages;
+          if (!(ok = mbar_wait(p_full, (uint32_t)tg & 1u, abort_flag, err))) break;
+          tc_fence_after();
+          const uint64_t vd = desc_sw128_mn(smem_u32(smem + OFF_C + stage * kStageBytes), kBlockBytes);
+#pragma unroll
+          for (int i = 0; i < kNp / 16; ++i)
+            mma_bf16(tmem + TM_O, pd + (uint64_t)((i * 32) >> 4), vd + (uint64_t)((i * 2048) >> 4),
+                     IDESC_O, (t > x.t0 || i > 0) ? 1u : 0u);
+          mma_commit(p_empty);
+          mma_commit(&empty[stage]);
+          if (t + 1 == x.t1) mma_commit(o_done);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp < kSmWarp0) {
+    // ======================= exchange ===========================================
+    const int m = (warp & 3) * 32 + lane;              // row = TMEM lane
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    // exchange buffer [4-position group][row] x float4: a warp's stores of one
+    // group are 512 contiguous bytes
+    const uint32_t x_remote = map_to_rank(smem_u32(smem + OFF_X), peer) + m * 16;
+    const uint32_t xfull_remote = map_to_rank(smem_u32(x_full), peer);
+    Piece x;
+    int tg = 0;
+    bool ok = true;
+    while (ok && next_piece(a, plan, walk, x)) {
+      // the query slice: the logit MMAs of the piece before are done (this warp
+      // has seen all of its logit tiles)
+      const bool live = m < x.grp.nt * a.H;
+      const uint4* qrow = reinterpret_cast<const uint4*>(
+          a.q + ((int64_t)x.grp.row0 * a.H + (live ? m : 0)) * DSI_D_QK);
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint4 v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = live ? __ldg(qrow + rho * 32 + half * 16 + i) : zero;
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 y = v[8 * ch + i];
+            w[4 * i] = y.x; w[4 * i + 1] = y.y; w[4 * i + 2] = y.z; w[4 * i + 3] = y.w;
+          }
+          tmem_st32(tmem + lane_base + TM_Q + (half * 2 + ch) * 32, w);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kRopeHalf / 8; ++i) {
+        const uint4 y = live ? __ldg(qrow + DSI_D_LATENT / 8 + rho * (kRopeHalf / 8) + i) : zero;
+        *reinterpret_cast<uint4*>(smem + OFF_QR + sw128_offset(m, i)) = y;
+      }
+      tmem_st_wait();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(q_ready);
+      for (int t = x.t0; t < x.t1; ++t, ++tg) {
+        const int sb = tg & 1;
+        float v[kNp];
+        if (!(ok = warp_wait(&s_full[sb], (uint32_t)(tg >> 1) & 1u, abort_flag, err))) break;
+        tc_fence_after();
+        tmem_ld32(tmem + lane_base + TM_S + sb * kNp, v);
+        tmem_ld32(tmem + lane_base + TM_S + sb * kNp + 32, v + 32);
+        const unsigned int z0 = poison[(tg & (kPoison - 1)) * 2], z1 = poison[(tg & (kPoison - 1)) * 2 + 1];
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(&s_empty[sb]);
+        if (z0 | z1) {
+#pragma unroll
+          for (int j = 0; j < kNp; ++j)
+            if (((j < 32 ? z0 >> j : z1 >> (j - 32)) & 1u)) v[j] = __int_as_float(0x7fffffff);
+        }
+        // once the peer has read the tile before
+        if (!(ok = warp_wait_cluster(x_empty, ((uint32_t)tg & 1u) ^ 1u, abort_flag, err))) break;
+#pragma unroll
+        for (int q4 = 0; q4 < kNp / 4; ++q4)
+          st_async_v4(x_remote + q4 * (kM * 16),
+                      make_float4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]),
+                      xfull_remote);
+      }
+    }
+  } else {
+    // ======================= softmax + epilogue ==================================
+    const int quarter = warp & 3, m = quarter * 32 + lane;   // row = TMEM lane
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    uint8_t* const pbuf = smem + OFF_P;
+    const uint8_t* xrow = smem + OFF_X + m * 16;
+    const uint32_t xempty_remote = map_to_rank(smem_u32(x_empty), peer);
+    // a scale of 0 becomes the smallest normal one: logits of 0, and "masked" times it stays -inf
+    const float sl2 = a.scale == 0.f ? 1.17549435e-38f : a.scale * kLog2e;
+    Record rec = {-1, -1, 0, 0};
+    Piece x;
+    int tg = 0, pieces = 0;
+    bool ok = true;
+    while (ok && next_piece(a, plan, walk, x)) {
+      const int tok = min(m / a.H, x.grp.nt - 1);
+      const int n_row = tok == 0 ? x.grp.n_first
+                                 : (int)visible_len(a.c, x.grp.row0 + tok, a.decode, a.q_offset);
+      const int lo_row = n_row - (int)a.window;
+      float m_ref = -INFINITY, l_r = 0.f, l_u = 0.f;   // sums of the rounded and the exact weights
+      for (int t = x.t0; t < x.t1; ++t, ++tg) {
+        const int sb = tg & 1, p0 = tile_pos(x.grp, t);
+        float v[kNp];
+        if (!(ok = warp_wait(&s_full[sb], (uint32_t)(tg >> 1) & 1u, abort_flag, err))) break;
+        tc_fence_after();
+        tmem_ld32(tmem + lane_base + TM_S + sb * kNp, v);
+        tmem_ld32(tmem + lane_base + TM_S + sb * kNp + 32, v + 32);
+        const unsigned int z0 = poison[(tg & (kPoison - 1)) * 2], z1 = poison[(tg & (kPoison - 1)) * 2 + 1];
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(&s_empty[sb]);
+        if (!(ok = warp_wait_cluster(x_full, (uint32_t)tg & 1u, abort_flag, err))) break;
+#pragma unroll
+        for (int q4 = 0; q4 < kNp / 4; ++q4) {
+          const float4 y = *reinterpret_cast<const float4*>(xrow + q4 * (kM * 16));
+          v[4 * q4] += y.x; v[4 * q4 + 1] += y.y; v[4 * q4 + 2] += y.z; v[4 * q4 + 3] += y.w;
+        }
+        __syncwarp();
+        if (lane == 0 && !(x.last && t + 1 == x.t1)) {   // buffer credit; warp 0 re-arms first
+          if (quarter == 0) mbar_arrive_expect_tx_relaxed(x_full, kXBytes);
+          mbar_arrive_remote_relaxed(xempty_remote);
+        }
+        if (z0 | z1) {
+#pragma unroll
+          for (int j = 0; j < kNp; ++j)
+            if (((j < 32 ? z0 >> j : z1 >> (j - 32)) & 1u)) v[j] = __int_as_float(0x7fffffff);
+        }
+        // what "masked" must be so that its weight is 2^-inf = 0, whatever the scale's sign
+        const bool flip = sl2 < 0.f;
+        if (!all_see(a, x.grp, p0, kNp)) {
+          const uint64_t see = low_bits(n_row - p0) &
+                               (~low_bits(lo_row - p0) | low_bits((int)a.n_sink - p0));
+#pragma unroll
+          for (int j = 0; j < kNp; ++j)
+            if (!((see >> j) & 1ull)) v[j] = flip ? INFINITY : -INFINITY;
+        }
+        // largest logit: the largest sum (the smallest for a negative scale)
+        float mx[8];
+        if (!flip) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mx[j] = v[j];
+#pragma unroll
+          for (int j = 8; j < kNp; ++j) mx[j & 7] = fmaxf(mx[j & 7], v[j]);
+#pragma unroll
+          for (int w2 = 4; w2 >= 1; w2 >>= 1)
+#pragma unroll
+            for (int j = 0; j < w2; ++j) mx[j] = fmaxf(mx[j], mx[j + w2]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mx[j] = v[j];
+#pragma unroll
+          for (int j = 8; j < kNp; ++j) mx[j & 7] = fminf(mx[j & 7], v[j]);
+#pragma unroll
+          for (int w2 = 4; w2 >= 1; w2 >>= 1)
+#pragma unroll
+            for (int j = 0; j < w2; ++j) mx[j] = fminf(mx[j], mx[j + w2]);
+        }
+        // (an infinite sum is a masked or an overflowed one: not scaled, 0 * inf is no logit)
+        const bool none = mx[0] == (flip ? INFINITY : -INFINITY);
+        const float tmax = none ? -INFINITY : mx[0] * sl2;
+        float alpha = 1.f;
+        bool rescale = false;
+        if (m_ref == -INFINITY) {
+          m_ref = tmax;                        // nothing in the accumulator yet
+        } else if (tmax > m_ref + kRescaleLog2) {
+          alpha = exp2f(m_ref - tmax);
+          m_ref = tmax;
+          rescale = true;
+        }
+        // the P tile is free, and P.V(t-1) has landed in the accumulator
+        if (!(ok = warp_wait(p_empty, ((uint32_t)tg & 1u) ^ 1u, abort_flag, err))) break;
+        tc_fence_after();
+        // weights 2^(logit * sl2 - reference); the bf16 values that P.V multiplies
+        // are summed for the output's denominator, the exact ones for the lse
+        float pr[4] = {0.f, 0.f, 0.f, 0.f}, pu[4] = {0.f, 0.f, 0.f, 0.f};
+        const float nmr = (m_ref == -INFINITY) ? 0.f : -m_ref;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          uint32_t w4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = 8 * u + 2 * e;
+            const float e0 = ex2_approx(fmaf(v[j], sl2, nmr));
+            const float e1 = ex2_approx(fmaf(v[j + 1], sl2, nmr));
+            const __nv_bfloat162 p2 = __floats2bfloat162_rn(e0, e1);
+            const float2 f2 = __bfloat1622float2(p2);
+            pr[e] += f2.x + f2.y;
+            pu[e] += e0 + e1;
+            w4[e] = *reinterpret_cast<const uint32_t*>(&p2);
+          }
+          *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, u)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        }
+        l_r = l_r * alpha + ((pr[0] + pr[1]) + (pr[2] + pr[3]));
+        l_u = l_u * alpha + ((pu[0] + pu[1]) + (pu[2] + pu[3]));
+        // TMEM loads and stores are warp-collective: rescale when any row of the
+        // warp needs it (the others multiply by 1)
+        if (__any_sync(0xffffffffu, rescale)) {
+          for (int c0 = 0; c0 < 256; c0 += 32) {
+            float o[32];
+            uint32_t w[32];
+            tmem_ld32(tmem + lane_base + TM_O + c0, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * alpha);
+            tmem_st32(tmem + lane_base + TM_O + c0, w);
+          }
+          tmem_st_wait();
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(p_full);
+      }
+      if (!ok || !(ok = warp_wait(o_done, (uint32_t)pieces & 1u, abort_flag, err))) break;
+      ++pieces;
+      tc_fence_after();
+      // ---- the piece's output: this CTA's 256 dims ------------------------------
+      const bool entire = x.t0 == 0 && x.t1 == x.grp.tiles;
+      const int slot = 2 * k + (x.t0 == 0 ? 1 : 0);
+      if (!entire) {
+        if (x.t0 == 0) {
+          rec.starts = x.g;
+        } else {
+          rec.continues = x.g;
+          rec.finishes = x.t1 == x.grp.tiles;
+        }
+      }
+      const bool live = m < x.grp.nt * a.H;
+      const int64_t orow = (int64_t)x.grp.row0 * a.H + m;
+      // nothing visible: 0; NaN stays NaN
+      const float inv = l_r == 0.f ? 0.f : 1.f / l_r;
+      for (int c0 = 0; c0 < 256; c0 += 32) {
+        float o[32];
+        __syncwarp();        // rows without an output skip the stores of the round before
+        tmem_ld32(tmem + lane_base + TM_O + c0, o);
+        tmem_ld_wait();
+        if (!live) {
+        } else if (entire) {
+          bf16* dst = a.out + orow * DSI_D_LATENT + rho * 256 + c0;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            __align__(16) bf16 o8[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o8[e] = __float2bfloat16(o[i + e] * inv);
+            *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(o8);
+          }
+        } else {
+          float* dst = ws.o + ((int64_t)slot * kM + m) * DSI_D_LATENT + rho * 256 + c0;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        }
+      }
+      if (live && rho == 0) {
+        if (!entire) ws.ml[slot * kM + m] = make_float4(m_ref, l_r, l_u, 0.f);
+        else if (a.lse) a.lse[orow] = l_u == 0.f ? -INFINITY : (m_ref + log2f(l_u)) / kLog2e;
+      }
+      tc_fence_before();
+    }
+    if (plan.split && rho == 0 && m == 0) ws.rec[k] = rec;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kQkWarp) tmem_dealloc(tmem, TMEM_COLS);
+  cluster_sync();      // the peer may still arrive on / write into this CTA until here
+}
+
+// Joins the pieces of a split group: block (k, m) takes row m of the group that
+// cluster k started and did not finish; its other pieces are the first ones of
+// clusters k + 1, k + 2, ... up to the one that finishes it.
+__global__ void __launch_bounds__(128)
+dense_mla_join(DenseArgs a, Plan plan, Workspace ws, int clusters) {
+  __shared__ float weight[kMaxClusters];
+  __shared__ float red[3][4];
+  __shared__ int end_s;
+  const int k = blockIdx.x, m = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_wait();     // the pieces come from the kernel launched just before
+  grid_dep_launch();
+  const int g = ws.rec[k].starts;
+  if (g < 0) return;
+  const int b = g / plan.per_seq, t0 = (g - b * plan.per_seq) * plan.tokens;
+  if (m >= min(plan.tokens, a.T - t0) * a.H) return;
+  if (tid == 0) end_s = clusters;
+  __syncthreads();
+  const int j = k + 1 + tid;
+  if (j < clusters) {
+    const Record r = ws.rec[j];
+    if (r.continues == g && r.finishes) atomicMin(&end_s, j);
+  }
+  __syncthreads();
+  const int pieces = min(end_s, clusters - 1) - k + 1;      // <= kMaxClusters
+  // piece 0: the last of cluster k; piece i: the first of cluster k + i
+  float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  if (tid < pieces) ml = ws.ml[(2 * (k + tid) + (tid == 0 ? 1 : 0)) * kM + m];
+  float top = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) red[0][warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+  weight[tid] = f;
+  float sr = f * ml.y, su = f * ml.z;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sr += __shfl_xor_sync(0xffffffffu, sr, o);
+    su += __shfl_xor_sync(0xffffffffu, su, o);
+  }
+  if (lane == 0) { red[1][warp] = sr; red[2][warp] = su; }
+  __syncthreads();
+  sr = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  su = (red[2][0] + red[2][1]) + (red[2][2] + red[2][3]);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = 0; i < pieces; ++i) {
+    const int64_t slot = 2 * (k + i) + (i == 0 ? 1 : 0);
+    const float4 v = reinterpret_cast<const float4*>(ws.o + (slot * kM + m) * DSI_D_LATENT)[tid];
+    const float w = weight[i];
+    o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+  }
+  const float inv = sr == 0.f ? 0.f : 1.f / sr;
+  const int64_t row = ((int64_t)b * a.T + t0) * a.H + m;
+  __align__(8) bf16 o4[4] = {__float2bfloat16(o.x * inv), __float2bfloat16(o.y * inv),
+                             __float2bfloat16(o.z * inv), __float2bfloat16(o.w * inv)};
+  *reinterpret_cast<uint2*>(a.out + row * DSI_D_LATENT + tid * 4) = *reinterpret_cast<const uint2*>(o4);
+  if (a.lse && tid == 0) a.lse[row] = su == 0.f ? -INFINITY : (top + log2f(su)) / kLog2e;
+}
+
+// Two-CTA clusters that fit on the current device at once (queried once per
+// device and form); half the SMs when the query fails (no device).
+template <bool F8>
+int cluster_slots() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) { cudaGetLastError(); return 76; }
+  int v = cached[dev].load(std::memory_order_relaxed);
+  if (v) return v;
+  if (cudaFuncSetAttribute(dense_mla_tc<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) {
+    cudaGetLastError();
+    return 76;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = SMEM;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&v, dense_mla_tc<F8>, &cfg) != cudaSuccess || v < 1) {
+    cudaGetLastError();
+    return 76;
+  }
+  v = v < kMaxClusters ? v : kMaxClusters;
+  cached[dev].store(v, std::memory_order_relaxed);
+  return v;
+}
+
+constexpr size_t kSlotBytes = (size_t)kM * (DSI_D_LATENT * sizeof(float) + sizeof(float4));
+
+template <bool F8>
+cudaError_t launch(const CUtensorMap& map, const DenseArgs& a, const Plan& plan, const Workspace& ws,
+                   int box, int clusters, cudaStream_t st) {
+  // per device: the current one's attribute, whatever was set before
+  cudaError_t e = cudaFuncSetAttribute(dense_mla_tc<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e != cudaSuccess) return e;
+  e = launch_overlapped(dense_mla_tc<F8>, dim3(2u * (unsigned)clusters), dim3(kThreads), SMEM, st,
+                        map, a, plan, ws, box);
+  note_launch();
+  return e;
 }
 
 }  // namespace
 
-size_t dense_mla_workspace() { return 256; }
+size_t dense_mla_workspace() {
+  const int n = cluster_slots<false>() > cluster_slots<true>() ? cluster_slots<false>() : cluster_slots<true>();
+  return (size_t)n * (2 * kSlotBytes + sizeof(Record));
+}
 
 cudaError_t launch_dense_mla(const DenseArgs& a, cudaStream_t st) {
-  dense_mla_simt<<<dim3((unsigned)a.rows, (unsigned)((a.H + 7) / 8)), 256, 0, st>>>(a);
+  const bool f8 = a.latent_scale != nullptr;
+  Plan plan;
+  plan.tokens = kM / a.H < a.T ? kM / a.H : a.T;
+  plan.per_seq = (a.T + plan.tokens - 1) / plan.tokens;
+  const int64_t groups = (int64_t)plan.per_seq * (a.rows / a.T);
+  plan.groups = (int)groups;                     // <= rows
+  const int slots = f8 ? cluster_slots<true>() : cluster_slots<false>();
+  // at most a cluster a tile
+  const int64_t span = a.window + a.n_sink < a.c.s_max ? a.window + a.n_sink + plan.tokens + 2 * kNp : a.c.s_max;
+  const int64_t tiles = groups * ((span + kNp - 1) / kNp + 1);
+  const int clusters = (int)(tiles < slots ? tiles : slots);
+  plan.split = a.ws != nullptr && clusters > 1;
+  Workspace ws = {nullptr, nullptr, nullptr};
+  if (plan.split) {
+    ws.o = static_cast<float*>(a.ws);
+    ws.ml = reinterpret_cast<float4*>(ws.o + (size_t)2 * clusters * kM * DSI_D_LATENT);
+    ws.rec = reinterpret_cast<Record*>(ws.ml + (size_t)2 * clusters * kM);
+  }
+  // TMA boxes: the largest part of 64 rows that pages are made of
+  int box = kNp;
+  if (a.c.block_table)
+    while (a.c.page_size % box != 0) box /= 2;   // page sizes are multiples of 8
+  CUtensorMap map;
+  memset(&map, 0, sizeof(map));
+  const uint64_t rows = a.c.block_table ? (uint64_t)a.c.num_pages * a.c.page_size
+                                        : (uint64_t)a.c.batch * a.c.s_max;
+  if (!f8 && !tma_map_2d(&map, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, DSI_D_QK, 64,
+                         (uint32_t)box))
+    return cudaErrorInvalidValue;
+  cudaError_t e = f8 ? launch<true>(map, a, plan, ws, box, clusters, st)
+                     : launch<false>(map, a, plan, ws, box, clusters, st);
+  if (e != cudaSuccess || !plan.split) return e;
+  e = launch_overlapped(dense_mla_join, dim3((unsigned)clusters, (unsigned)(plan.tokens * a.H)), dim3(128),
+                        0, st, a, plan, ws, clusters);
   note_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace dsi
