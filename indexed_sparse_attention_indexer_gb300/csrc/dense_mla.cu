@@ -98,7 +98,7 @@ constexpr uint32_t kXBytes = kM * kNp * 4;
 struct Record { int starts, continues, finishes, pad; };
 struct Workspace {
   float* o;        // [2 * clusters][128][512] unnormalised outputs
-  float4* ml;      // [2 * clusters][128] reference max, rounded sum, exact sum
+  float2* ml;      // [2 * clusters][128] reference max, sum of weights
   Record* rec;     // [clusters]
 };
 
@@ -204,9 +204,26 @@ __device__ __forceinline__ bool bf16x8_finite(const uint4& v) {
   return ok;
 }
 
-// Bits 0 .. k-1 of 64.
-__device__ __forceinline__ uint64_t low_bits(int k) {
-  return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1ull;
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 template <bool F8>
@@ -564,7 +581,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
         if (z0 | z1) {
 #pragma unroll
           for (int j = 0; j < kNp; ++j)
-            if (((j < 32 ? z0 >> j : z1 >> (j - 32)) & 1u)) v[j] = __int_as_float(0x7fffffff);
+            v[j] = ((j < 32 ? z0 >> j : z1 >> (j - 32)) & 1u) ? __int_as_float(0x7fffffff) : v[j];
         }
         // once the peer has read the tile before
         if (!(ok = warp_wait_cluster(x_empty, ((uint32_t)tg & 1u) ^ 1u, abort_flag, err))) break;
@@ -593,7 +610,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
       const int n_row = tok == 0 ? x.grp.n_first
                                  : (int)visible_len(a.c, x.grp.row0 + tok, a.decode, a.q_offset);
       const int lo_row = n_row - (int)a.window;
-      float m_ref = -INFINITY, l_r = 0.f, l_u = 0.f;   // sums of the rounded and the exact weights
+      float m_ref = -INFINITY, l_sum = 0.f;
       for (int t = x.t0; t < x.t1; ++t, ++tg) {
         const int sb = tg & 1, p0 = tile_pos(x.grp, t);
         float v[kNp];
@@ -609,7 +626,9 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
 #pragma unroll
         for (int q4 = 0; q4 < kNp / 4; ++q4) {
           const float4 y = *reinterpret_cast<const float4*>(xrow + q4 * (kM * 16));
-          v[4 * q4] += y.x; v[4 * q4 + 1] += y.y; v[4 * q4 + 2] += y.z; v[4 * q4 + 3] += y.w;
+          const float2 s0 = unpack2(add2(pack2(v[4 * q4], v[4 * q4 + 1]), pack2(y.x, y.y)));
+          const float2 s1 = unpack2(add2(pack2(v[4 * q4 + 2], v[4 * q4 + 3]), pack2(y.z, y.w)));
+          v[4 * q4] = s0.x; v[4 * q4 + 1] = s0.y; v[4 * q4 + 2] = s1.x; v[4 * q4 + 3] = s1.y;
         }
         __syncwarp();
         if (lane == 0 && !(x.last && t + 1 == x.t1)) {   // buffer credit; warp 0 re-arms first
@@ -619,16 +638,16 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
         if (z0 | z1) {
 #pragma unroll
           for (int j = 0; j < kNp; ++j)
-            if (((j < 32 ? z0 >> j : z1 >> (j - 32)) & 1u)) v[j] = __int_as_float(0x7fffffff);
+            v[j] = ((j < 32 ? z0 >> j : z1 >> (j - 32)) & 1u) ? __int_as_float(0x7fffffff) : v[j];
         }
         // what "masked" must be so that its weight is 2^-inf = 0, whatever the scale's sign
         const bool flip = sl2 < 0.f;
         if (!all_see(a, x.grp, p0, kNp)) {
-          const uint64_t see = low_bits(n_row - p0) &
-                               (~low_bits(lo_row - p0) | low_bits((int)a.n_sink - p0));
+          const int end = n_row - p0, from = lo_row - p0, sinks = (int)a.n_sink - p0;
+          const float out_of_sight = flip ? INFINITY : -INFINITY;
 #pragma unroll
           for (int j = 0; j < kNp; ++j)
-            if (!((see >> j) & 1ull)) v[j] = flip ? INFINITY : -INFINITY;
+            v[j] = (j < end) & ((j >= from) | (j < sinks)) ? v[j] : out_of_sight;
         }
         // largest logit: the largest sum (the smallest for a negative scale)
         float mx[8];
@@ -666,28 +685,28 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
         // the P tile is free, and P.V(t-1) has landed in the accumulator
         if (!(ok = warp_wait(p_empty, ((uint32_t)tg & 1u) ^ 1u, abort_flag, err))) break;
         tc_fence_after();
-        // weights 2^(logit * sl2 - reference); the bf16 values that P.V multiplies
-        // are summed for the output's denominator, the exact ones for the lse
-        float pr[4] = {0.f, 0.f, 0.f, 0.f}, pu[4] = {0.f, 0.f, 0.f, 0.f};
+        // weights 2^(logit * sl2 - reference), rounded to bf16 for P.V (half a step,
+        // to nearest: the errors of a row's weights average out) and summed in
+        // fp32 before the rounding, which keeps the lse exact to fp32
+        uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
         const float nmr = (m_ref == -INFINITY) ? 0.f : -m_ref;
+        const uint64_t scale2 = pack2(sl2, sl2), nmr2 = pack2(nmr, nmr);
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           uint32_t w4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = 8 * u + 2 * e;
-            const float e0 = ex2_approx(fmaf(v[j], sl2, nmr));
-            const float e1 = ex2_approx(fmaf(v[j + 1], sl2, nmr));
+            const float2 x2 = unpack2(fma2(pack2(v[j], v[j + 1]), scale2, nmr2));
+            const float e0 = ex2_approx(x2.x), e1 = ex2_approx(x2.y);
+            sum2[e] = add2(sum2[e], pack2(e0, e1));
             const __nv_bfloat162 p2 = __floats2bfloat162_rn(e0, e1);
-            const float2 f2 = __bfloat1622float2(p2);
-            pr[e] += f2.x + f2.y;
-            pu[e] += e0 + e1;
             w4[e] = *reinterpret_cast<const uint32_t*>(&p2);
           }
           *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, u)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
-        l_r = l_r * alpha + ((pr[0] + pr[1]) + (pr[2] + pr[3]));
-        l_u = l_u * alpha + ((pu[0] + pu[1]) + (pu[2] + pu[3]));
+        const float2 tot = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
+        l_sum = l_sum * alpha + (tot.x + tot.y);
         // TMEM loads and stores are warp-collective: rescale when any row of the
         // warp needs it (the others multiply by 1)
         if (__any_sync(0xffffffffu, rescale)) {
@@ -722,33 +741,45 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
       }
       const bool live = m < x.grp.nt * a.H;
       const int64_t orow = (int64_t)x.grp.row0 * a.H + m;
-      // nothing visible: 0; NaN stays NaN
-      const float inv = l_r == 0.f ? 0.f : 1.f / l_r;
-      for (int c0 = 0; c0 < 256; c0 += 32) {
-        float o[32];
-        __syncwarp();        // rows without an output skip the stores of the round before
+      // nothing visible: 0; NaN stays NaN.  A direct output goes through the P
+      // tile (free: the piece's last P.V is done), a warp's 32 rows in its own 4 KB,
+      // so that a store instruction writes four rows of 128 bytes instead of 32
+      // rows of 16
+      const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+      const int rows_here = min(32, x.grp.nt * a.H - quarter * 32);
+      for (int c0 = 0; c0 < 256; c0 += 64) {
+        float o[64];
+        __syncwarp();
         tmem_ld32(tmem + lane_base + TM_O + c0, o);
+        tmem_ld32(tmem + lane_base + TM_O + c0 + 32, o + 32);
         tmem_ld_wait();
-        if (!live) {
-        } else if (entire) {
-          bf16* dst = a.out + orow * DSI_D_LATENT + rho * 256 + c0;
+        if (entire) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
+          for (int i = 0; i < 8; ++i) {
             __align__(16) bf16 o8[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o8[e] = __float2bfloat16(o[i + e] * inv);
-            *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(o8);
+            for (int e = 0; e < 8; ++e) o8[e] = __float2bfloat16(o[8 * i + e] * inv);
+            *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, i)) = *reinterpret_cast<const uint4*>(o8);
           }
-        } else {
+          __syncwarp();
+          bf16* dst = a.out + ((int64_t)x.grp.row0 * a.H + quarter * 32) * DSI_D_LATENT + rho * 256 + c0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = i * 4 + (lane >> 3);
+            const uint4 y = *reinterpret_cast<const uint4*>(pbuf + sw128_offset(quarter * 32 + rr, lane & 7));
+            if (rr < rows_here)
+              *reinterpret_cast<uint4*>(dst + (int64_t)rr * DSI_D_LATENT + (lane & 7) * 8) = y;
+          }
+        } else if (live) {
           float* dst = ws.o + ((int64_t)slot * kM + m) * DSI_D_LATENT + rho * 256 + c0;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
+          for (int i = 0; i < 64; i += 4)
             *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         }
       }
       if (live && rho == 0) {
-        if (!entire) ws.ml[slot * kM + m] = make_float4(m_ref, l_r, l_u, 0.f);
-        else if (a.lse) a.lse[orow] = l_u == 0.f ? -INFINITY : (m_ref + log2f(l_u)) / kLog2e;
+        if (!entire) ws.ml[slot * kM + m] = make_float2(m_ref, l_sum);
+        else if (a.lse) a.lse[orow] = l_sum == 0.f ? -INFINITY : (m_ref + log2f(l_sum)) / kLog2e;
       }
       tc_fence_before();
     }
@@ -767,7 +798,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
 __global__ void __launch_bounds__(128)
 dense_mla_join(DenseArgs a, Plan plan, Workspace ws, int clusters) {
   __shared__ float weight[kMaxClusters];
-  __shared__ float red[3][4];
+  __shared__ float red[2][4];
   __shared__ int end_s;
   const int k = blockIdx.x, m = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_wait();     // the pieces come from the kernel launched just before
@@ -786,7 +817,7 @@ dense_mla_join(DenseArgs a, Plan plan, Workspace ws, int clusters) {
   __syncthreads();
   const int pieces = min(end_s, clusters - 1) - k + 1;      // <= kMaxClusters
   // piece 0: the last of cluster k; piece i: the first of cluster k + i
-  float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  float2 ml = make_float2(-INFINITY, 0.f);
   if (tid < pieces) ml = ws.ml[(2 * (k + tid) + (tid == 0 ? 1 : 0)) * kM + m];
   float top = ml.x;
 #pragma unroll
@@ -796,16 +827,12 @@ dense_mla_join(DenseArgs a, Plan plan, Workspace ws, int clusters) {
   top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
   const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
   weight[tid] = f;
-  float sr = f * ml.y, su = f * ml.z;
+  float sum = f * ml.y;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    sr += __shfl_xor_sync(0xffffffffu, sr, o);
-    su += __shfl_xor_sync(0xffffffffu, su, o);
-  }
-  if (lane == 0) { red[1][warp] = sr; red[2][warp] = su; }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) red[1][warp] = sum;
   __syncthreads();
-  sr = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-  su = (red[2][0] + red[2][1]) + (red[2][2] + red[2][3]);
+  sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int i = 0; i < pieces; ++i) {
@@ -814,12 +841,12 @@ dense_mla_join(DenseArgs a, Plan plan, Workspace ws, int clusters) {
     const float w = weight[i];
     o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
   }
-  const float inv = sr == 0.f ? 0.f : 1.f / sr;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t row = ((int64_t)b * a.T + t0) * a.H + m;
   __align__(8) bf16 o4[4] = {__float2bfloat16(o.x * inv), __float2bfloat16(o.y * inv),
                              __float2bfloat16(o.z * inv), __float2bfloat16(o.w * inv)};
   *reinterpret_cast<uint2*>(a.out + row * DSI_D_LATENT + tid * 4) = *reinterpret_cast<const uint2*>(o4);
-  if (a.lse && tid == 0) a.lse[row] = su == 0.f ? -INFINITY : (top + log2f(su)) / kLog2e;
+  if (a.lse && tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) / kLog2e;
 }
 
 // Two-CTA clusters that fit on the current device at once (queried once per
@@ -854,7 +881,7 @@ int cluster_slots() {
   return v;
 }
 
-constexpr size_t kSlotBytes = (size_t)kM * (DSI_D_LATENT * sizeof(float) + sizeof(float4));
+constexpr size_t kSlotBytes = (size_t)kM * (DSI_D_LATENT * sizeof(float) + sizeof(float2));
 
 template <bool F8>
 cudaError_t launch(const CUtensorMap& map, const DenseArgs& a, const Plan& plan, const Workspace& ws,
@@ -891,7 +918,7 @@ cudaError_t launch_dense_mla(const DenseArgs& a, cudaStream_t st) {
   Workspace ws = {nullptr, nullptr, nullptr};
   if (plan.split) {
     ws.o = static_cast<float*>(a.ws);
-    ws.ml = reinterpret_cast<float4*>(ws.o + (size_t)2 * clusters * kM * DSI_D_LATENT);
+    ws.ml = reinterpret_cast<float2*>(ws.o + (size_t)2 * clusters * kM * DSI_D_LATENT);
     ws.rec = reinterpret_cast<Record*>(ws.ml + (size_t)2 * clusters * kM);
   }
   // TMA boxes: the largest part of 64 rows that pages are made of
