@@ -414,7 +414,8 @@ dsi_status dsi_latent_fp8_append(const void* x, int64_t n_rows, int64_t ld_x,
  * one call to the next.
  * Errors: DSI_ERR_INVALID_ARG (null pointer, misaligned q, out or workspace,
  * T < 1, NaN scale, inconsistent cache), DSI_ERR_UNSUPPORTED (n_heads outside
- * 1..128, page_size not a multiple of 8, 2^31 cache rows or more),
+ * 1..128, page_size not a multiple of 8, 2^31 cache rows or query heads
+ * (batch * T * n_heads) or more),
  * DSI_ERR_WORKSPACE (workspace too small).
  */
 dsi_status dsi_dense_mla_decode(const void* q, const dsi_cache* cache, int32_t tokens_per_seq,

@@ -72,7 +72,7 @@ constexpr int OFF_P = OFF_C + kStages * kStageBytes;      // P [128 x 64] bf16
 constexpr int OFF_X = OFF_P + kM * kNp * 2;               // the peer's partial logits, fp32
 constexpr int OFF_QR = OFF_X + kM * kNp * 4;              // query rope half, rows of 128 bytes
 constexpr int OFF_BAR = OFF_QR + kM * 128;
-constexpr int kBars = 2 * kStages + 10;
+constexpr int kBars = 3 * kStages + 11;
 constexpr int OFF_ROWS = OFF_BAR + kBars * 8;             // [2][64] cache rows of a tile (generic path)
 constexpr int OFF_POISON = OFF_ROWS + 2 * kNp * 4;
 constexpr int OFF_MISC = OFF_POISON + kPoison * 8;
@@ -180,8 +180,6 @@ __device__ __forceinline__ int row_of(const CacheView& c, int b, int p, int* err
   return page * c.page_size + (p - pg * c.page_size);
 }
 
-__device__ __forceinline__ void producers_sync() { asm volatile("bar.sync 1, 64;\n" ::: "memory"); }
-
 // 16 E4M3 codes times their tile scale, rounded to bf16 (lo = codes 0..7).
 __device__ __forceinline__ void e4m3x16_scaled(const uint4& v, float sc, uint4& lo, uint4& hi) {
   float f[16];
@@ -228,7 +226,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 
 template <bool F8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, Workspace ws,
+dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap qmap, DenseArgs a, Plan plan, Workspace ws,
              int box) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -243,6 +241,8 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
   uint64_t* o_done = s_full + 7;               // a piece's last P.V done
   uint64_t* x_full = s_full + 8;               // the peer's partial logits landed
   uint64_t* x_empty = s_full + 9;              // the peer has read what we sent
+  uint64_t* landed = s_full + 10;              // [kStages] an edge tile's copies landed
+  uint64_t* looked_up = landed + kStages;      // FP8: a tile's cache rows looked up
   int* rows_s = reinterpret_cast<int*>(smem + OFF_ROWS);
   unsigned int* poison = reinterpret_cast<unsigned int*>(smem + OFF_POISON);   // [kPoison][2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
@@ -250,6 +250,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
   int* start_s = reinterpret_cast<int*>(smem + OFF_MISC + 8);                   // group, tile
   int* widest_s = reinterpret_cast<int*>(smem + OFF_MISC + 16);
   unsigned long long* total_s = reinterpret_cast<unsigned long long*>(smem + OFF_MISC + 24);
+  unsigned int* taken_s = reinterpret_cast<unsigned int*>(smem + OFF_MISC + 32);
   int* scan_s = reinterpret_cast<int*>(smem + OFF_SCAN);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -262,6 +263,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], kProducers);
       mbar_init(&empty[s], 1);
+      mbar_init(&landed[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -273,6 +275,8 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
     mbar_init(o_done, 1);
     mbar_init(x_full, 1);
     mbar_init(x_empty, 4);
+    mbar_init(looked_up, kProducers);
+    taken_s[0] = taken_s[1] = 0u;
     *abort_flag = 0;
     start_s[0] = plan.groups;
     start_s[1] = 0;
@@ -281,7 +285,10 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
     fence_barrier_init();
   }
   if (warp == kQkWarp) tmem_alloc(tmem_slot, TMEM_COLS);
-  if (warp == 0 && lane == 0) prefetch_tmap(&lmap);
+  if (warp == 0 && lane == 0) {
+    if (!F8) prefetch_tmap(&lmap);
+    prefetch_tmap(&qmap);
+  }
   grid_dep_wait();     // lengths, queries and cache rows may come from the kernel before
   __syncthreads();
 
@@ -346,50 +353,114 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
 
   if (warp < kProducers) {
     // ======================= producers ==========================================
+    // A piece takes two ring slots for its query slice, then one a tile.
     Piece x;
-    int tg = 0, loaded = 0;                    // tiles; tiles by plain loads
+    int slot = 0, tg = 0;                      // ring slots; tiles
+    [[maybe_unused]] int loaded = 0;           // tiles by plain loads
+    uint32_t edge_ph = 0;                      // parities of landed[]
+    uint32_t issued = 0, issued_edge = 0;      // stages with a copy in flight; into an edge tile
     bool ok = true;
-    uint32_t issued = 0;                       // stages with a TMA tile (lane 0 of warp 0)
     while (ok && next_piece(a, plan, walk, x)) {
-      for (int t = x.t0; t < x.t1; ++t, ++tg) {
-        const int stage = tg % kStages;
-        const uint32_t ph = (uint32_t)(tg / kStages) & 1u;
+      for (int i = 0; i < 2; ++i, ++slot) {
+        const int stage = slot % kStages;
+        if (!(ok = warp_wait(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u, abort_flag, err))) break;
+        if (lane == 0) {
+          if (warp == 0) {
+            uint8_t* st = smem + OFF_C + stage * kStageBytes;
+            mbar_arrive_expect_tx(&full[stage], 2 * kM * 128);
+            issued |= 1u << stage;
+            issued_edge &= ~(1u << stage);
+            for (int bx = 0; bx < 2; ++bx)
+              tma_load_2d(st + bx * kM * 128, &qmap, (int)rho * 256 + (2 * i + bx) * 64,
+                          x.grp.row0 * a.H, &full[stage]);
+          } else {
+            mbar_arrive(&full[stage]);
+          }
+        }
+      }
+      if (!ok) break;
+      for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
+        const int stage = slot % kStages;
+        const uint32_t ph = (uint32_t)(slot / kStages) & 1u;
         const int p0 = tile_pos(x.grp, t);
         uint8_t* st = smem + OFF_C + stage * kStageBytes;
         unsigned int* pz = poison + (tg & (kPoison - 1)) * 2;
         const bool whole = all_see(a, x.grp, p0, kNp);
-        if (!F8 && whole) {
-          // whole tile by TMA: boxes of `box` rows (a page or a part of one) x 64 dims
-          if (!(ok = warp_wait(&empty[stage], ph ^ 1, abort_flag, err))) break;
+        if constexpr (!F8) {
+          // warp 0: the tile by TMA, boxes of `box` rows (a page or a part of one) x
+          // 64 dims; warp 1 passes a whole tile on and cleans one at an edge first
           if (warp == 0) {
+            if (!(ok = warp_wait(&empty[stage], ph ^ 1, abort_flag, err))) break;
+            const int boxes = kNp / box;
+            const int pb = p0 + lane * box;        // lane's box, if it has one
+            const bool seen = lane < boxes && pb < x.grp.n_last && (pb + box > x.grp.lo || pb < (int)a.n_sink);
+            const int n = __popc(__ballot_sync(0xffffffffu, seen));
+            uint64_t* bar = whole ? &full[stage] : &landed[stage];
             if (lane == 0) {
-              pz[0] = pz[1] = 0u;
-              mbar_arrive_expect_tx(&full[stage], kStageBytes);
+              mbar_arrive_expect_tx(bar, (uint32_t)(n * box * 128 * kBlocks));
+              if (!whole) mbar_arrive(&full[stage]);
               issued |= 1u << stage;
+              issued_edge = whole ? issued_edge & ~(1u << stage) : issued_edge | (1u << stage);
+              edge_ph ^= whole ? 0u : 1u << stage;
             }
             __syncwarp();
-            const int boxes = kNp / box;
             for (int i = lane; i < boxes * kBlocks; i += 32) {
-              const int bx = i / kBlocks, blk = i - bx * kBlocks;
-              const int row = row_of(a.c, x.grp.b, p0 + bx * box, err);
+              const int bx = i / kBlocks, blk = i - bx * kBlocks, p = p0 + bx * box;
+              if (!(p < x.grp.n_last && (p + box > x.grp.lo || p < (int)a.n_sink))) continue;
+              const int row = row_of(a.c, x.grp.b, p, err);
               // a bad page id: the box past the tensor's last row, which reads as zeros
               const int y = row < 0 ? (int)a.c.num_pages * a.c.page_size : row;
               tma_load_2d(st + blk * kBlockBytes + bx * box * 128, &lmap,
-                          blk < 4 ? (int)rho * 256 + blk * 64 : DSI_D_LATENT, y, &full[stage]);
+                          blk < 4 ? (int)rho * 256 + blk * 64 : DSI_D_LATENT, y, bar);
             }
-          } else if (lane == 0) {
-            mbar_arrive(&full[stage]);
+            __syncwarp();
+          } else {
+            unsigned int z[2] = {0u, 0u};
+            if (!whole) {
+              // rows that no token sees become zeros (weight 0 times what they hold must
+              // be 0); a row that only some tokens see is searched for NaN and infinities:
+              // it is taken out and remembered, and its logits become NaN where it is seen
+              if (!(ok = warp_wait(&landed[stage], (edge_ph >> stage) & 1u, abort_flag, err))) break;
+              edge_ph ^= 1u << stage;
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const int p = p0 + w * 32 + lane;
+                const unsigned int none = __ballot_sync(0xffffffffu, !any_sees(a, x.grp, p));
+                unsigned int some = ~none & ~__ballot_sync(0xffffffffu, all_see(a, x.grp, p, 1));
+                for (unsigned int todo = none | some; todo; todo &= todo - 1) {
+                  const int bit = __ffs(todo) - 1, rr = w * 32 + bit;
+                  uint4* at = reinterpret_cast<uint4*>(st + (lane >> 3) * kBlockBytes + sw128_offset(rr, lane & 7));
+                  uint4* rope = reinterpret_cast<uint4*>(st + 4 * kBlockBytes + sw128_offset(rr, rho * 4 + (lane & 3)));
+                  bool clear = (none >> bit) & 1u;
+                  if (!clear) {
+                    clear = __any_sync(0xffffffffu, !(bf16x8_finite(*at) && bf16x8_finite(*rope)));
+                    if (clear) z[w] |= 1u << bit;
+                  }
+                  if (clear) {
+                    *at = make_uint4(0, 0, 0, 0);
+                    if (lane < 4) *rope = make_uint4(0, 0, 0, 0);
+                  }
+                }
+              }
+              fence_proxy_async_smem();   // the tensor core reads the stage through the async proxy
+              __syncwarp();
+            } else if (!(ok = warp_wait(&empty[stage], ph ^ 1, abort_flag, err))) {
+              break;
+            }
+            if (lane == 0) {
+              pz[0] = z[0];
+              pz[1] = z[1];
+              mbar_arrive(&full[stage]);
+            }
           }
-          continue;
-        }
-        // plain loads: rows that no token sees become zeros; a row that only
-        // some tokens see is searched for NaN and infinities, which are taken
-        // out and remembered (its logits become NaN where it is seen)
-        int* rows = rows_s + (loaded++ & 1) * kNp;   // (the barrier below keeps its readers apart)
-        rows[tid] = any_sees(a, x.grp, p0 + tid) ? row_of(a.c, x.grp.b, p0 + tid, err) : -1;
-        if (tid == 0) pz[0] = pz[1] = 0u;
-        producers_sync();
-        if constexpr (F8) {
+        } else {
+          // plain loads, converted to bf16 on the way (edges: as above)
+          int* rows = rows_s + (loaded & 1) * kNp;     // (the barrier below keeps its readers apart)
+          rows[tid] = any_sees(a, x.grp, p0 + tid) ? row_of(a.c, x.grp.b, p0 + tid, err) : -1;
+          if (tid == 0) pz[0] = pz[1] = 0u;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(looked_up);
+          if (!(ok = warp_wait(looked_up, (uint32_t)loaded++ & 1u, abort_flag, err))) break;
           constexpr int kPieces = 18;          // 16 codes each: 256 latent and 32 rope dims
           constexpr int kPer = kNp * kPieces / kProdThreads;
           static_assert(kPer * kProdThreads == kNp * kPieces, "whole rounds");
@@ -424,37 +495,10 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
             *reinterpret_cast<uint4*>(blk + sw128_offset(rr, ch)) = lo;
             *reinterpret_cast<uint4*>(blk + sw128_offset(rr, ch + 1)) = hi;
           }
-        } else {
-          constexpr int kPieces = 36;          // 16 bytes each: 256 latent and 32 rope dims
-          constexpr int kBatch = 12, kRounds = kNp * kPieces / (kProdThreads * kBatch);
-          static_assert(kRounds * kBatch * kProdThreads == kNp * kPieces, "whole rounds");
-          if (!(ok = warp_wait(&empty[stage], ph ^ 1, abort_flag, err))) break;
-          for (int b0 = 0; b0 < kRounds; ++b0) {
-            uint4 v[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const int q = tid + (b0 * kBatch + i) * kProdThreads, rr = q / kPieces, u = q - rr * kPieces;
-              const int64_t row = rows[rr];
-              const int d0 = u < 32 ? (int)rho * 256 + u * 8
-                                    : DSI_D_LATENT + (int)rho * kRopeHalf + (u - 32) * 8;
-              v[i] = make_uint4(0, 0, 0, 0);
-              if (row >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(a.c.latent + row * DSI_D_QK + d0));
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const int q = tid + (b0 * kBatch + i) * kProdThreads, rr = q / kPieces, u = q - rr * kPieces;
-              if (!all_see(a, x.grp, p0 + rr, 1) && !bf16x8_finite(v[i])) {
-                v[i] = make_uint4(0, 0, 0, 0);
-                atomicOr(pz + (rr >> 5), 1u << (rr & 31));
-              }
-              const uint32_t ch = u < 32 ? (uint32_t)(u & 7) : rho * 4 + (uint32_t)(u - 32);
-              *reinterpret_cast<uint4*>(st + (u >> 3) * kBlockBytes + sw128_offset(rr, ch)) = v[i];
-            }
-          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[stage]);
         }
-        fence_proxy_async_smem();   // the tensor core reads the stage through the async proxy
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[stage]);
       }
     }
     // never leave the CTA with a copy still landing in shared memory
@@ -462,25 +506,26 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
       volatile int no_abort = 0;    // the drain is bounded by time only
       for (int s = 0; s < kStages; ++s) {
         if (!((issued >> s) & 1u)) continue;
-        int last = tg - 1;          // the last tile that used stage s
-        while (last >= 0 && last % kStages != s) --last;
-        if (last >= 0)
-          mbar_wait(&full[s], (uint32_t)(last / kStages) & 1u, &no_abort, err, 100000000ull);
+        int last = slot;            // the last slot that used stage s
+        while (last > 0 && last % kStages != s) --last;
+        if ((issued_edge >> s) & 1u) mbar_wait(&landed[s], ((edge_ph >> s) & 1u) ^ 1u, &no_abort, err, 100000000ull);
+        else mbar_wait(&full[s], (uint32_t)(last / kStages) & 1u, &no_abort, err, 100000000ull);
       }
     }
   } else if (warp == kQkWarp) {
     // ======================= logit issuer =======================================
     if (lane == 0) {
       Piece x;
-      int tg = 0, pieces = 0;
+      int slot = 0, tg = 0, pieces = 0;
       bool ok = true;
       const uint64_t qr = desc_sw128(smem_u32(smem + OFF_QR));
       while (ok && next_piece(a, plan, walk, x)) {
         if (!(ok = mbar_wait(q_ready, (uint32_t)pieces & 1u, abort_flag, err))) break;
         ++pieces;
-        for (int t = x.t0; t < x.t1; ++t, ++tg) {
-          const int stage = tg % kStages, sb = tg & 1;
-          if (!(ok = mbar_wait(&full[stage], (uint32_t)(tg / kStages) & 1u, abort_flag, err))) break;
+        slot += 2;                               // the query slice
+        for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
+          const int stage = slot % kStages, sb = tg & 1;
+          if (!(ok = mbar_wait(&full[stage], (uint32_t)(slot / kStages) & 1u, abort_flag, err))) break;
           if (!(ok = mbar_wait(&s_empty[sb], ((uint32_t)(tg >> 1) & 1u) ^ 1u, abort_flag, err))) break;
           tc_fence_after();
           const uint32_t t_s = tmem + TM_S + sb * kNp;
@@ -504,12 +549,13 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
     // ======================= value issuer =======================================
     if (lane == 0) {
       Piece x;
-      int tg = 0;
+      int slot = 0, tg = 0;
       bool ok = true;
       const uint64_t pd = desc_sw128(smem_u32(smem + OFF_P));
       while (ok && next_piece(a, plan, walk, x)) {
-        for (int t = x.t0; t < x.t1; ++t, ++tg) {
-          const int stage = tg % kStages;
+        slot += 2;                               // the query slice
+        for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
+          const int stage = slot % kStages;
           if (!(ok = mbar_wait(p_full, (uint32_t)tg & 1u, abort_flag, err))) break;
           tc_fence_after();
           const uint64_t vd = desc_sw128_mn(smem_u32(smem + OFF_C + stage * kStageBytes), kBlockBytes);
@@ -533,36 +579,48 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, DenseArgs a, Plan plan, W
     const uint32_t x_remote = map_to_rank(smem_u32(smem + OFF_X), peer) + m * 16;
     const uint32_t xfull_remote = map_to_rank(smem_u32(x_full), peer);
     Piece x;
-    int tg = 0;
+    int slot = 0, tg = 0;
     bool ok = true;
     while (ok && next_piece(a, plan, walk, x)) {
-      // the query slice: the logit MMAs of the piece before are done (this warp
-      // has seen all of its logit tiles)
+      // The query slice: the rope half by plain loads (begun first), the four 64-dim
+      // blocks out of the two ring slots that the producers filled ahead.  The
+      // logit MMAs of the piece before are done: this warp has seen all its tiles.
       const bool live = m < x.grp.nt * a.H;
-      const uint4* qrow = reinterpret_cast<const uint4*>(
-          a.q + ((int64_t)x.grp.row0 * a.H + (live ? m : 0)) * DSI_D_QK);
-      const uint4 zero = make_uint4(0, 0, 0, 0);
+      uint4 rope[kRopeHalf / 8];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint4 v[16];
+      for (int i = 0; i < kRopeHalf / 8; ++i)
+        rope[i] = live ? __ldg(reinterpret_cast<const uint4*>(
+                             a.q + ((int64_t)x.grp.row0 * a.H + m) * DSI_D_QK + DSI_D_LATENT + rho * kRopeHalf) + i)
+                       : make_uint4(0, 0, 0, 0);
+      for (int half = 0; half < 2; ++half, ++slot) {
+        const int stage = slot % kStages;
+        if (!(ok = warp_wait(&full[stage], (uint32_t)(slot / kStages) & 1u, abort_flag, err))) break;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = live ? __ldg(qrow + rho * 32 + half * 16 + i) : zero;
-#pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
+        for (int bx = 0; bx < 2; ++bx) {
+          const uint8_t* src = smem + OFF_C + stage * kStageBytes + bx * kM * 128;
           uint32_t w[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint4 y = v[8 * ch + i];
+            const uint4 y = *reinterpret_cast<const uint4*>(src + sw128_offset(m, i));
             w[4 * i] = y.x; w[4 * i + 1] = y.y; w[4 * i + 2] = y.z; w[4 * i + 3] = y.w;
           }
-          tmem_st32(tmem + lane_base + TM_Q + (half * 2 + ch) * 32, w);
+          tmem_st32(tmem + lane_base + TM_Q + (half * 2 + bx) * 32, w);
+        }
+        tmem_st_wait();
+        // the last of the four warps returns the slot (no barrier between them: a
+        // warp that has given up must not leave the others waiting); a warp can be a
+        // slot ahead of another but not a piece, so each half has its own count
+        __syncwarp();
+        if (lane == 0) {
+          __threadfence_block();
+          if ((atomicAdd(taken_s + half, 1u) & 3u) == 3u) mbar_arrive(&empty[stage]);
         }
       }
+      if (!ok) break;
 #pragma unroll
-      for (int i = 0; i < kRopeHalf / 8; ++i) {
-        const uint4 y = live ? __ldg(qrow + DSI_D_LATENT / 8 + rho * (kRopeHalf / 8) + i) : zero;
-        *reinterpret_cast<uint4*>(smem + OFF_QR + sw128_offset(m, i)) = y;
-      }
+      for (int i = 0; i < kRopeHalf / 8; ++i)
+        *reinterpret_cast<uint4*>(smem + OFF_QR + sw128_offset(m, i)) = rope[i];
+      slot += x.t1 - x.t0;
       tmem_st_wait();
       fence_proxy_async_smem();
       tc_fence_before();
@@ -884,13 +942,13 @@ int cluster_slots() {
 constexpr size_t kSlotBytes = (size_t)kM * (DSI_D_LATENT * sizeof(float) + sizeof(float2));
 
 template <bool F8>
-cudaError_t launch(const CUtensorMap& map, const DenseArgs& a, const Plan& plan, const Workspace& ws,
+cudaError_t launch(const CUtensorMap& map, const CUtensorMap& qmap, const DenseArgs& a, const Plan& plan, const Workspace& ws,
                    int box, int clusters, cudaStream_t st) {
   // per device: the current one's attribute, whatever was set before
   cudaError_t e = cudaFuncSetAttribute(dense_mla_tc<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   e = launch_overlapped(dense_mla_tc<F8>, dim3(2u * (unsigned)clusters), dim3(kThreads), SMEM, st,
-                        map, a, plan, ws, box);
+                        map, qmap, a, plan, ws, box);
   note_launch();
   return e;
 }
@@ -932,8 +990,11 @@ cudaError_t launch_dense_mla(const DenseArgs& a, cudaStream_t st) {
   if (!f8 && !tma_map_2d(&map, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, DSI_D_QK, 64,
                          (uint32_t)box))
     return cudaErrorInvalidValue;
-  cudaError_t e = f8 ? launch<true>(map, a, plan, ws, box, clusters, st)
-                     : launch<false>(map, a, plan, ws, box, clusters, st);
+  CUtensorMap qmap;
+  if (!tma_map_2d(&qmap, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)a.rows * a.H, DSI_D_QK, 64, kM))
+    return cudaErrorInvalidValue;
+  cudaError_t e = f8 ? launch<true>(map, qmap, a, plan, ws, box, clusters, st)
+                     : launch<false>(map, qmap, a, plan, ws, box, clusters, st);
   if (e != cudaSuccess || !plan.split) return e;
   e = launch_overlapped(dense_mla_join, dim3((unsigned)clusters, (unsigned)(plan.tokens * a.H)), dim3(128),
                         0, st, a, plan, ws, clusters);

@@ -436,8 +436,7 @@ static dsi_status dense_common(const void* q, const dsi_cache* cache, int64_t ro
                                void* stream) {
   if (!q || !out || rows < 0 || window < 1 || n_sink < 0 || !(scale == scale))
     return DSI_ERR_INVALID_ARG;
-  if (rows > 0x7fffffff) return DSI_ERR_UNSUPPORTED;
-  if (H < 1 || H > 128) return DSI_ERR_UNSUPPORTED;
+  if (H < 1 || H > 128 || rows > 0x7fffffff / H) return DSI_ERR_UNSUPPORTED;
   const dsi_status s = check_cache(cache, (int)rows, decode, q_offset, false, true, decode ? T : 1);
   if (s != DSI_OK) return s;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSI_ERR_INVALID_ARG;
