@@ -19,7 +19,7 @@
 // maxima and sums.  Where dealing out whole groups costs at most
 // kWholeSlack tiles more, groups stay whole and nothing is joined.
 //
-// Roles in a CTA (12 warps), each walking the same list of pieces; the tile
+// Roles in a CTA (16 warps), each walking the same list of pieces; the tile
 // pipeline runs on across pieces:
 //   producers (warps 0-1): a tile's rows into a 128-byte-swizzled stage (ring
 //     of 4) by TMA boxes; tiles at an edge (not wholly visible to every token
@@ -28,8 +28,8 @@
 //   logit issuer (warp 3): S = Qslice . C^T into one of two TMEM tiles;
 //   exchange (warps 4-7): the group's query slice into TMEM (rope half: shared
 //     memory); this CTA's partial logits out of TMEM into the peer's buffer;
-//   softmax (warps 8-11, one row per thread): own partial plus the peer's,
-//     mask, online softmax in log2 units with a lazily moved reference max
+//   softmax (warps 8-15, one row per thread, two sets of four warps on alternate
+//     tiles): own partial plus the peer's, mask, online softmax in log2 units with a lazily moved reference max
 //     (the accumulator is rescaled only when the max grows by more than 2^8),
 //     P in bf16 to shared memory, and the epilogue;
 //   value issuer (warp 2): O += P . V from the same stage.
@@ -51,28 +51,37 @@ namespace {
 
 constexpr int kM = 128;                        // rows of a group: (token, head) pairs
 constexpr int kNp = 64;                        // positions per tile
-constexpr int kBlocks = 5;                     // stage blocks: four 64-dim blocks and the rope dims
 constexpr int kStages = 4;
 constexpr int kBlockBytes = kNp * 128;         // 64 dims of a tile
-constexpr int kStageBytes = kBlocks * kBlockBytes;
 constexpr int kRopeHalf = 32;                  // rope dims of each CTA
-// 12 warps (three per SM sub-partition): at most 168 registers a thread
+constexpr int kRopeOff = 4 * kBlockBytes;      // stage: four 64-dim blocks, then 64 rows of rope dims
+constexpr int kRowBytes = 4 * 128 + kRopeHalf * 2;
+constexpr int kStageBytes = kNp * kRowBytes;   // 36 KB
+// 16 warps (four per SM sub-partition): at most 128 registers a thread
 constexpr int kProducers = 2;                  // warps 0-1
 constexpr int kPvWarp = 2;
 constexpr int kQkWarp = 3;                     // then exchange: warps 4-7
-constexpr int kSmWarp0 = 8;                    // softmax: warps 8-11
-constexpr int kThreads = 12 * 32;
+constexpr int kSmWarp0 = 8;                    // softmax: warps 8-11 even tiles, 12-15 odd ones
+constexpr int kThreads = 16 * 32;
 constexpr int kProdThreads = kProducers * 32;
 constexpr int kMaxClusters = 128;
 constexpr int kWholeSlack = 8;
+constexpr int kAhead = 8;                      // tiles between L2 prefetch and copy
+// partial logits travel in quarters of a tile (16 positions): three in flight for
+// each softmax set hide the round trip of a buffer (credit, stores, landing)
+constexpr int kQuarter = 16;
+constexpr int kXRing = 3;
+constexpr int kXBytes = kM * kQuarter * 4;
 constexpr int kPoison = 8;                     // tiles whose poisoned rows are remembered
 
 constexpr int OFF_C = 0;
 constexpr int OFF_P = OFF_C + kStages * kStageBytes;      // P [128 x 64] bf16
-constexpr int OFF_X = OFF_P + kM * kNp * 2;               // the peer's partial logits, fp32
-constexpr int OFF_QR = OFF_X + kM * kNp * 4;              // query rope half, rows of 128 bytes
-constexpr int OFF_BAR = OFF_QR + kM * 128;
-constexpr int kBars = 3 * kStages + 11;
+constexpr int OFF_X = OFF_P + kM * kNp * 2;               // [2 sets][kXRing] the peer's partial logits
+constexpr int OFF_QR = OFF_X + 2 * kXRing * kXBytes;     // query rope half
+constexpr int OFF_REF = OFF_QR + kM * kRopeHalf * 2;      // reference maxima of the rows
+constexpr int OFF_SUMS = OFF_REF + kM * 4;                // [2][2][128] (reference, sum) of both sets
+constexpr int OFF_BAR = OFF_SUMS + 4 * kM * 8;
+constexpr int kBars = 3 * kStages + 16 + 4 * kXRing;
 constexpr int OFF_ROWS = OFF_BAR + kBars * 8;             // [2][64] cache rows of a tile (generic path)
 constexpr int OFF_POISON = OFF_ROWS + 2 * kNp * 4;
 constexpr int OFF_MISC = OFF_POISON + kPoison * 8;
@@ -90,7 +99,6 @@ constexpr uint32_t IDESC_S = idesc_f32(1, kM, kNp);
 constexpr uint32_t IDESC_O = idesc_f32_bmn(1, kM, 256);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.f;
-constexpr uint32_t kXBytes = kM * kNp * 4;
 
 // What a cluster leaves for the join: the group that its last piece starts and
 // does not finish (or -1), the group that its first piece continues (or -1),
@@ -202,6 +210,39 @@ __device__ __forceinline__ bool bf16x8_finite(const uint4& v) {
   return ok;
 }
 
+// Bounded waits whose slow path is out of line: the roles' loops together have
+// to stay small enough for the instruction cache.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 1;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    if (ok) return true;
+    if ((i & 255u) == 0) {
+      if (*abort) return false;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        *abort = 1;
+        report(err, kErrTimeout);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  return mbar_try_wait(bar, parity) || wait_on(smem_u32(bar), parity, abort, err);
+}
+// The same for whole warps: all lanes proceed or none.
+__device__ __forceinline__ bool wait32(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  return __all_sync(0xffffffffu, wait1(bar, parity, abort, err));
+}
+// ... for phases that the other CTA's arrivals and stores complete
+__device__ __forceinline__ bool wait32_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  return __all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity) || wait_on(smem_u32(bar), parity, abort, err));
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
@@ -226,7 +267,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 
 template <bool F8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap qmap, DenseArgs a, Plan plan, Workspace ws,
+dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
+             const __grid_constant__ CUtensorMap qmap, DenseArgs a, Plan plan, Workspace ws,
              int box) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -235,14 +277,19 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
   uint64_t* empty = full + kStages;            // [kStages] stage free (value MMAs done)
   uint64_t* s_full = empty + kStages;          // [2] logits in TMEM
   uint64_t* s_empty = s_full + 2;              // [2] logits read out (exchange and softmax)
-  uint64_t* p_full = s_full + 4;               // P written
-  uint64_t* p_empty = s_full + 5;              // P.V done
-  uint64_t* q_ready = s_full + 6;              // query slice in place
-  uint64_t* o_done = s_full + 7;               // a piece's last P.V done
-  uint64_t* x_full = s_full + 8;               // the peer's partial logits landed
-  uint64_t* x_empty = s_full + 9;              // the peer has read what we sent
-  uint64_t* landed = s_full + 10;              // [kStages] an edge tile's copies landed
+  // barriers that only one softmax set waits for at a tile come in pairs, one for
+  // even and one for odd tiles: a set that skips a phase could not tell it apart
+  uint64_t* p_empty = s_full + 4;              // [2] P.V done
+  uint64_t* p_full = s_full + 6;               // P written
+  uint64_t* q_ready = s_full + 7;              // query slice in place
+  uint64_t* o_done = s_full + 8;               // a piece's last P.V done
+  uint64_t* landed = s_full + 9;               // [kStages] an edge tile's copies landed
   uint64_t* looked_up = landed + kStages;      // FP8: a tile's cache rows looked up
+  uint64_t* ref_set = looked_up + 1;           // [4] a tile's reference maxima (per lane quarter)
+  uint64_t* sums_set = ref_set + 4;            // both softmax sets' sums of a piece
+  uint64_t* o_free = ref_set + 5;              // a piece's output read out
+  uint64_t* x_full = o_free + 1;               // [2][kXRing] the peer's partial logits landed
+  uint64_t* x_empty = x_full + 2 * kXRing;     // [2][kXRing] the peer has read what we sent
   int* rows_s = reinterpret_cast<int*>(smem + OFF_ROWS);
   unsigned int* poison = reinterpret_cast<unsigned int*>(smem + OFF_POISON);   // [kPoison][2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
@@ -268,14 +315,19 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 256);
+      mbar_init(&p_empty[i], 1);
     }
     mbar_init(p_full, 128);
-    mbar_init(p_empty, 1);
     mbar_init(q_ready, 128);
     mbar_init(o_done, 1);
-    mbar_init(x_full, 1);
-    mbar_init(x_empty, 4);
+    for (int i = 0; i < 2 * kXRing; ++i) {
+      mbar_init(&x_full[i], 1);
+      mbar_init(&x_empty[i], 4);
+    }
     mbar_init(looked_up, kProducers);
+    for (int i = 0; i < 4; ++i) mbar_init(&ref_set[i], 1);
+    mbar_init(sums_set, 8);
+    mbar_init(o_free, 8);
     taken_s[0] = taken_s[1] = 0u;
     *abort_flag = 0;
     start_s[0] = plan.groups;
@@ -286,7 +338,10 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
   }
   if (warp == kQkWarp) tmem_alloc(tmem_slot, TMEM_COLS);
   if (warp == 0 && lane == 0) {
-    if (!F8) prefetch_tmap(&lmap);
+    if (!F8) {
+      prefetch_tmap(&lmap);
+      prefetch_tmap(&rmap);
+    }
     prefetch_tmap(&qmap);
   }
   grid_dep_wait();     // lengths, queries and cache rows may come from the kernel before
@@ -344,7 +399,8 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     walk.left = share;
     walk.stride = 0;
   }
-  if (tid == 0) mbar_arrive_expect_tx(x_full, kXBytes);   // the peer's first tile
+  if (tid == 0)                                // the peer's first quarters
+    for (int i = 0; i < 2 * kXRing; ++i) mbar_arrive_expect_tx(&x_full[i], kXBytes);
   tc_fence_before();
   cluster_sync();      // the peer's barriers exist (and are armed) before anyone uses them
   tc_fence_after();
@@ -363,7 +419,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     while (ok && next_piece(a, plan, walk, x)) {
       for (int i = 0; i < 2; ++i, ++slot) {
         const int stage = slot % kStages;
-        if (!(ok = warp_wait(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u, abort_flag, err))) break;
+        if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u, abort_flag, err))) break;
         if (lane == 0) {
           if (warp == 0) {
             uint8_t* st = smem + OFF_C + stage * kStageBytes;
@@ -390,28 +446,46 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           // warp 0: the tile by TMA, boxes of `box` rows (a page or a part of one) x
           // 64 dims; warp 1 passes a whole tile on and cleans one at an edge first
           if (warp == 0) {
-            if (!(ok = warp_wait(&empty[stage], ph ^ 1, abort_flag, err))) break;
+            if (!(ok = wait32(&empty[stage], ph ^ 1, abort_flag, err))) break;
             const int boxes = kNp / box;
             const int pb = p0 + lane * box;        // lane's box, if it has one
             const bool seen = lane < boxes && pb < x.grp.n_last && (pb + box > x.grp.lo || pb < (int)a.n_sink);
             const int n = __popc(__ballot_sync(0xffffffffu, seen));
             uint64_t* bar = whole ? &full[stage] : &landed[stage];
             if (lane == 0) {
-              mbar_arrive_expect_tx(bar, (uint32_t)(n * box * 128 * kBlocks));
+              mbar_arrive_expect_tx(bar, (uint32_t)(n * box * kRowBytes));
               if (!whole) mbar_arrive(&full[stage]);
               issued |= 1u << stage;
               issued_edge = whole ? issued_edge & ~(1u << stage) : issued_edge | (1u << stage);
               edge_ph ^= whole ? 0u : 1u << stage;
             }
             __syncwarp();
-            for (int i = lane; i < boxes * kBlocks; i += 32) {
-              const int bx = i / kBlocks, blk = i - bx * kBlocks, p = p0 + bx * box;
+            for (int i = lane; i < boxes * 5; i += 32) {
+              const int bx = i / 5, blk = i - bx * 5, p = p0 + bx * box;
               if (!(p < x.grp.n_last && (p + box > x.grp.lo || p < (int)a.n_sink))) continue;
               const int row = row_of(a.c, x.grp.b, p, err);
               // a bad page id: the box past the tensor's last row, which reads as zeros
               const int y = row < 0 ? (int)a.c.num_pages * a.c.page_size : row;
-              tma_load_2d(st + blk * kBlockBytes + bx * box * 128, &lmap,
-                          blk < 4 ? (int)rho * 256 + blk * 64 : DSI_D_LATENT, y, bar);
+              if (blk < 4)
+                tma_load_2d(st + blk * kBlockBytes + bx * box * 128, &lmap, (int)rho * 256 + blk * 64, y, bar);
+              else
+                tma_load_2d(st + kRopeOff + bx * box * kRopeHalf * 2, &rmap,
+                            DSI_D_LATENT + (int)rho * kRopeHalf, y, bar);
+            }
+            // decode: the caches come from HBM; a tile is asked for into L2 kAhead tiles
+            // before its copy, so that the copy holds its stage only as long as L2 takes
+            if (a.decode) {
+              for (int u = t == x.t0 ? t + 1 : t + kAhead; u < min(x.t1, t + kAhead + 1); ++u) {
+                const int pu = tile_pos(x.grp, u);
+                for (int i = lane; i < boxes * 5; i += 32) {
+                  const int bx = i / 5, blk = i - bx * 5, p = pu + bx * box;
+                  if (!(p < x.grp.n_last && (p + box > x.grp.lo || p < (int)a.n_sink))) continue;
+                  const int row = row_of(a.c, x.grp.b, p, err);
+                  if (row < 0) continue;
+                  if (blk < 4) tma_prefetch_2d(&lmap, (int)rho * 256 + blk * 64, row);
+                  else tma_prefetch_2d(&rmap, DSI_D_LATENT + (int)rho * kRopeHalf, row);
+                }
+              }
             }
             __syncwarp();
           } else {
@@ -420,7 +494,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
               // rows that no token sees become zeros (weight 0 times what they hold must
               // be 0); a row that only some tokens see is searched for NaN and infinities:
               // it is taken out and remembered, and its logits become NaN where it is seen
-              if (!(ok = warp_wait(&landed[stage], (edge_ph >> stage) & 1u, abort_flag, err))) break;
+              if (!(ok = wait32(&landed[stage], (edge_ph >> stage) & 1u, abort_flag, err))) break;
               edge_ph ^= 1u << stage;
 #pragma unroll
               for (int w = 0; w < 2; ++w) {
@@ -430,7 +504,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
                 for (unsigned int todo = none | some; todo; todo &= todo - 1) {
                   const int bit = __ffs(todo) - 1, rr = w * 32 + bit;
                   uint4* at = reinterpret_cast<uint4*>(st + (lane >> 3) * kBlockBytes + sw128_offset(rr, lane & 7));
-                  uint4* rope = reinterpret_cast<uint4*>(st + 4 * kBlockBytes + sw128_offset(rr, rho * 4 + (lane & 3)));
+                  uint4* rope = reinterpret_cast<uint4*>(st + kRopeOff + sw64_offset(rr, lane & 3));
                   bool clear = (none >> bit) & 1u;
                   if (!clear) {
                     clear = __any_sync(0xffffffffu, !(bf16x8_finite(*at) && bf16x8_finite(*rope)));
@@ -444,7 +518,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
               }
               fence_proxy_async_smem();   // the tensor core reads the stage through the async proxy
               __syncwarp();
-            } else if (!(ok = warp_wait(&empty[stage], ph ^ 1, abort_flag, err))) {
+            } else if (!(ok = wait32(&empty[stage], ph ^ 1, abort_flag, err))) {
               break;
             }
             if (lane == 0) {
@@ -460,7 +534,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           if (tid == 0) pz[0] = pz[1] = 0u;
           __syncwarp();
           if (lane == 0) mbar_arrive(looked_up);
-          if (!(ok = warp_wait(looked_up, (uint32_t)loaded++ & 1u, abort_flag, err))) break;
+          if (!(ok = wait32(looked_up, (uint32_t)loaded++ & 1u, abort_flag, err))) break;
           constexpr int kPieces = 18;          // 16 codes each: 256 latent and 32 rope dims
           constexpr int kPer = kNp * kPieces / kProdThreads;
           static_assert(kPer * kProdThreads == kNp * kPieces, "whole rounds");
@@ -480,7 +554,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
               sc[i] = __ldg(a.latent_scale + row * 5 + (d0 >> 7));
             }
           }
-          if (!(ok = warp_wait(&empty[stage], ph ^ 1, abort_flag, err))) break;
+          if (!(ok = wait32(&empty[stage], ph ^ 1, abort_flag, err))) break;
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
             const int q = tid + i * kProdThreads, rr = q / kPieces, u = q - rr * kPieces;
@@ -490,10 +564,10 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
               lo = hi = make_uint4(0, 0, 0, 0);
               atomicOr(pz + (rr >> 5), 1u << (rr & 31));
             }
-            uint8_t* blk = st + (u >> 2) * kBlockBytes;
-            const uint32_t ch = u < 16 ? (uint32_t)(u & 3) * 2 : rho * 4 + (uint32_t)(u - 16) * 2;
-            *reinterpret_cast<uint4*>(blk + sw128_offset(rr, ch)) = lo;
-            *reinterpret_cast<uint4*>(blk + sw128_offset(rr, ch + 1)) = hi;
+            const uint32_t ch = (uint32_t)(u & 3) * 2;
+            uint8_t* blk = u < 16 ? st + (u >> 2) * kBlockBytes : st + kRopeOff;
+            *reinterpret_cast<uint4*>(blk + (u < 16 ? sw128_offset(rr, ch) : sw64_offset(rr, ch))) = lo;
+            *reinterpret_cast<uint4*>(blk + (u < 16 ? sw128_offset(rr, ch + 1) : sw64_offset(rr, ch + 1))) = hi;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -518,15 +592,15 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       Piece x;
       int slot = 0, tg = 0, pieces = 0;
       bool ok = true;
-      const uint64_t qr = desc_sw128(smem_u32(smem + OFF_QR));
+      const uint64_t qr = desc_sw64(smem_u32(smem + OFF_QR));
       while (ok && next_piece(a, plan, walk, x)) {
-        if (!(ok = mbar_wait(q_ready, (uint32_t)pieces & 1u, abort_flag, err))) break;
+        if (!(ok = wait1(q_ready, (uint32_t)pieces & 1u, abort_flag, err))) break;
         ++pieces;
         slot += 2;                               // the query slice
         for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
           const int stage = slot % kStages, sb = tg & 1;
-          if (!(ok = mbar_wait(&full[stage], (uint32_t)(slot / kStages) & 1u, abort_flag, err))) break;
-          if (!(ok = mbar_wait(&s_empty[sb], ((uint32_t)(tg >> 1) & 1u) ^ 1u, abort_flag, err))) break;
+          if (!(ok = wait1(&full[stage], (uint32_t)(slot / kStages) & 1u, abort_flag, err))) break;
+          if (!(ok = wait1(&s_empty[sb], ((uint32_t)(tg >> 1) & 1u) ^ 1u, abort_flag, err))) break;
           tc_fence_after();
           const uint32_t t_s = tmem + TM_S + sb * kNp;
           const uint32_t base = smem_u32(smem + OFF_C + stage * kStageBytes);
@@ -536,7 +610,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
             mma_bf16_tmem_a(t_s, tmem + TM_Q + i * 8,
                             d0 + (uint64_t)(((i >> 2) * kBlockBytes + (i & 3) * 32) >> 4), IDESC_S,
                             i > 0 ? 1u : 0u);
-          const uint64_t dr = d0 + (uint64_t)((4 * kBlockBytes + rho * 64) >> 4);
+          const uint64_t dr = desc_sw64(base + kRopeOff);
 #pragma unroll
           for (int i = 0; i < kRopeHalf / 16; ++i)
             mma_bf16(t_s, qr + (uint64_t)((i * 32) >> 4), dr + (uint64_t)((i * 32) >> 4), IDESC_S, 1u);
@@ -556,14 +630,14 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         slot += 2;                               // the query slice
         for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
           const int stage = slot % kStages;
-          if (!(ok = mbar_wait(p_full, (uint32_t)tg & 1u, abort_flag, err))) break;
+          if (!(ok = wait1(p_full, (uint32_t)tg & 1u, abort_flag, err))) break;
           tc_fence_after();
           const uint64_t vd = desc_sw128_mn(smem_u32(smem + OFF_C + stage * kStageBytes), kBlockBytes);
 #pragma unroll
           for (int i = 0; i < kNp / 16; ++i)
             mma_bf16(tmem + TM_O, pd + (uint64_t)((i * 32) >> 4), vd + (uint64_t)((i * 2048) >> 4),
                      IDESC_O, (t > x.t0 || i > 0) ? 1u : 0u);
-          mma_commit(p_empty);
+          mma_commit(&p_empty[tg & 1]);
           mma_commit(&empty[stage]);
           if (t + 1 == x.t1) mma_commit(o_done);
         }
@@ -574,10 +648,11 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     // ======================= exchange ===========================================
     const int m = (warp & 3) * 32 + lane;              // row = TMEM lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    // exchange buffer [4-position group][row] x float4: a warp's stores of one
+    // exchange buffers [4-position group][row] x float4: a warp's stores of one
     // group are 512 contiguous bytes
     const uint32_t x_remote = map_to_rank(smem_u32(smem + OFF_X), peer) + m * 16;
     const uint32_t xfull_remote = map_to_rank(smem_u32(x_full), peer);
+    const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;   // a negative scale turns the queries' signs
     Piece x;
     int slot = 0, tg = 0;
     bool ok = true;
@@ -594,7 +669,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
                        : make_uint4(0, 0, 0, 0);
       for (int half = 0; half < 2; ++half, ++slot) {
         const int stage = slot % kStages;
-        if (!(ok = warp_wait(&full[stage], (uint32_t)(slot / kStages) & 1u, abort_flag, err))) break;
+        if (!(ok = wait32(&full[stage], (uint32_t)(slot / kStages) & 1u, abort_flag, err))) break;
 #pragma unroll
         for (int bx = 0; bx < 2; ++bx) {
           const uint8_t* src = smem + OFF_C + stage * kStageBytes + bx * kM * 128;
@@ -602,7 +677,8 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint4 y = *reinterpret_cast<const uint4*>(src + sw128_offset(m, i));
-            w[4 * i] = y.x; w[4 * i + 1] = y.y; w[4 * i + 2] = y.z; w[4 * i + 3] = y.w;
+            w[4 * i] = y.x ^ sign; w[4 * i + 1] = y.y ^ sign;
+            w[4 * i + 2] = y.z ^ sign; w[4 * i + 3] = y.w ^ sign;
           }
           tmem_st32(tmem + lane_base + TM_Q + (half * 2 + bx) * 32, w);
         }
@@ -619,7 +695,8 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       if (!ok) break;
 #pragma unroll
       for (int i = 0; i < kRopeHalf / 8; ++i)
-        *reinterpret_cast<uint4*>(smem + OFF_QR + sw128_offset(m, i)) = rope[i];
+        *reinterpret_cast<uint4*>(smem + OFF_QR + sw64_offset(m, i)) =
+            make_uint4(rope[i].x ^ sign, rope[i].y ^ sign, rope[i].z ^ sign, rope[i].w ^ sign);
       slot += x.t1 - x.t0;
       tmem_st_wait();
       fence_proxy_async_smem();
@@ -627,38 +704,50 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       mbar_arrive(q_ready);
       for (int t = x.t0; t < x.t1; ++t, ++tg) {
         const int sb = tg & 1;
-        float v[kNp];
-        if (!(ok = warp_wait(&s_full[sb], (uint32_t)(tg >> 1) & 1u, abort_flag, err))) break;
+        if (!(ok = wait32(&s_full[sb], (uint32_t)(tg >> 1) & 1u, abort_flag, err))) break;
         tc_fence_after();
+        float v[kNp];
         tmem_ld32(tmem + lane_base + TM_S + sb * kNp, v);
         tmem_ld32(tmem + lane_base + TM_S + sb * kNp + 32, v + 32);
         const unsigned int z0 = poison[(tg & (kPoison - 1)) * 2], z1 = poison[(tg & (kPoison - 1)) * 2 + 1];
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(&s_empty[sb]);
-        if (z0 | z1) {
+        if (__builtin_expect(z0 | z1, 0)) {
 #pragma unroll
           for (int j = 0; j < kNp; ++j)
             v[j] = ((j < 32 ? z0 >> j : z1 >> (j - 32)) & 1u) ? __int_as_float(0x7fffffff) : v[j];
         }
-        // once the peer has read the tile before
-        if (!(ok = warp_wait_cluster(x_empty, ((uint32_t)tg & 1u) ^ 1u, abort_flag, err))) break;
+        // each quarter once the peer has read what was in its buffer
+        const int q0 = (tg >> 1) * 4;            // quarters sent to this set so far
 #pragma unroll
-        for (int q4 = 0; q4 < kNp / 4; ++q4)
-          st_async_v4(x_remote + q4 * (kM * 16),
-                      make_float4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]),
-                      xfull_remote);
+        for (int i = 0; i < 4; ++i) {
+          const int buf = sb * kXRing + (q0 + i) % kXRing;
+          if (!(ok = wait32_cluster(&x_empty[buf], ((uint32_t)((q0 + i) / kXRing) & 1u) ^ 1u, abort_flag, err))) break;
+#pragma unroll
+          for (int g4 = 0; g4 < kQuarter / 4; ++g4) {
+            const int j = i * kQuarter + 4 * g4;
+            st_async_v4(x_remote + buf * kXBytes + g4 * (kM * 16),
+                        make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]), xfull_remote + buf * 8);
+          }
+        }
+        if (!ok) break;
       }
     }
   } else {
     // ======================= softmax + epilogue ==================================
+    // Two sets of four warps take alternate tiles: a tile is in its set's hands for
+    // two tile periods.  The reference maximum passes from set to set as soon as a
+    // tile's maximum is known; each set sums its own tiles' weights.
+    const int set = (warp - kSmWarp0) >> 2;
     const int quarter = warp & 3, m = quarter * 32 + lane;   // row = TMEM lane
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     uint8_t* const pbuf = smem + OFF_P;
     const uint8_t* xrow = smem + OFF_X + m * 16;
+    volatile float* const ref_s = reinterpret_cast<float*>(smem + OFF_REF) + m;
     const uint32_t xempty_remote = map_to_rank(smem_u32(x_empty), peer);
     // a scale of 0 becomes the smallest normal one: logits of 0, and "masked" times it stays -inf
-    const float sl2 = a.scale == 0.f ? 1.17549435e-38f : a.scale * kLog2e;
+    const float sl2 = a.scale == 0.f ? 1.17549435e-38f : fabsf(a.scale) * kLog2e;
     Record rec = {-1, -1, 0, 0};
     Piece x;
     int tg = 0, pieces = 0;
@@ -668,114 +757,117 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       const int n_row = tok == 0 ? x.grp.n_first
                                  : (int)visible_len(a.c, x.grp.row0 + tok, a.decode, a.q_offset);
       const int lo_row = n_row - (int)a.window;
-      float m_ref = -INFINITY, l_sum = 0.f;
+      float m_mine = -INFINITY, l_mine = 0.f;
       for (int t = x.t0; t < x.t1; ++t, ++tg) {
-        const int sb = tg & 1, p0 = tile_pos(x.grp, t);
-        float v[kNp];
-        if (!(ok = warp_wait(&s_full[sb], (uint32_t)(tg >> 1) & 1u, abort_flag, err))) break;
+        if ((tg & 1) != set) continue;
+        const int p0 = tile_pos(x.grp, t);
+        if (!(ok = wait32(&s_full[set], (uint32_t)(tg >> 1) & 1u, abort_flag, err))) break;
         tc_fence_after();
-        tmem_ld32(tmem + lane_base + TM_S + sb * kNp, v);
-        tmem_ld32(tmem + lane_base + TM_S + sb * kNp + 32, v + 32);
+        float v[kNp];
+        tmem_ld32(tmem + lane_base + TM_S + set * kNp, v);
+        tmem_ld32(tmem + lane_base + TM_S + set * kNp + 32, v + 32);
         const unsigned int z0 = poison[(tg & (kPoison - 1)) * 2], z1 = poison[(tg & (kPoison - 1)) * 2 + 1];
         tmem_ld_wait();
         tc_fence_before();
-        mbar_arrive(&s_empty[sb]);
-        if (!(ok = warp_wait_cluster(x_full, (uint32_t)tg & 1u, abort_flag, err))) break;
+        mbar_arrive(&s_empty[set]);
+        // the peer's partial logits
+        const int q0 = (tg >> 1) * 4;            // quarters that this set has received so far
 #pragma unroll
-        for (int q4 = 0; q4 < kNp / 4; ++q4) {
-          const float4 y = *reinterpret_cast<const float4*>(xrow + q4 * (kM * 16));
-          const float2 s0 = unpack2(add2(pack2(v[4 * q4], v[4 * q4 + 1]), pack2(y.x, y.y)));
-          const float2 s1 = unpack2(add2(pack2(v[4 * q4 + 2], v[4 * q4 + 3]), pack2(y.z, y.w)));
-          v[4 * q4] = s0.x; v[4 * q4 + 1] = s0.y; v[4 * q4 + 2] = s1.x; v[4 * q4 + 3] = s1.y;
-        }
-        __syncwarp();
-        if (lane == 0 && !(x.last && t + 1 == x.t1)) {   // buffer credit; warp 0 re-arms first
-          if (quarter == 0) mbar_arrive_expect_tx_relaxed(x_full, kXBytes);
-          mbar_arrive_remote_relaxed(xempty_remote);
-        }
-        if (z0 | z1) {
+        for (int i = 0; i < 4; ++i) {
+          const int buf = set * kXRing + (q0 + i) % kXRing;
+          if (!(ok = wait32_cluster(&x_full[buf], (uint32_t)((q0 + i) / kXRing) & 1u, abort_flag, err))) break;
 #pragma unroll
-          for (int j = 0; j < kNp; ++j)
-            v[j] = ((j < 32 ? z0 >> j : z1 >> (j - 32)) & 1u) ? __int_as_float(0x7fffffff) : v[j];
+          for (int g4 = 0; g4 < kQuarter / 4; ++g4) {
+            const int j = i * kQuarter + 4 * g4;
+            const float4 y = *reinterpret_cast<const float4*>(xrow + buf * kXBytes + g4 * (kM * 16));
+            const float2 s0 = unpack2(add2(pack2(v[j], v[j + 1]), pack2(y.x, y.y)));
+            const float2 s1 = unpack2(add2(pack2(v[j + 2], v[j + 3]), pack2(y.z, y.w)));
+            v[j] = s0.x; v[j + 1] = s0.y; v[j + 2] = s1.x; v[j + 3] = s1.y;
+          }
+          __syncwarp();
+          if (lane == 0) {                       // buffer credit; lane quarter 0 re-arms first
+            if (quarter == 0) mbar_arrive_expect_tx_relaxed(&x_full[buf], kXBytes);
+            mbar_arrive_remote_relaxed(xempty_remote + buf * 8);
+          }
         }
-        // what "masked" must be so that its weight is 2^-inf = 0, whatever the scale's sign
-        const bool flip = sl2 < 0.f;
-        if (!all_see(a, x.grp, p0, kNp)) {
+        if (!ok) break;
+        // NaN for poisoned and -inf for masked positions
+        if (__builtin_expect(!all_see(a, x.grp, p0, kNp), 0)) {
           const int end = n_row - p0, from = lo_row - p0, sinks = (int)a.n_sink - p0;
-          const float out_of_sight = flip ? INFINITY : -INFINITY;
 #pragma unroll
-          for (int j = 0; j < kNp; ++j)
-            v[j] = (j < end) & ((j >= from) | (j < sinks)) ? v[j] : out_of_sight;
+          for (int j = 0; j < kNp; ++j) {
+            v[j] = ((j < 32 ? z0 >> j : z1 >> (j - 32)) & 1u) ? __int_as_float(0x7fffffff) : v[j];
+            v[j] = (j < end) & ((j >= from) | (j < sinks)) ? v[j] : -INFINITY;
+          }
         }
-        // largest logit: the largest sum (the smallest for a negative scale)
-        float mx[8];
-        if (!flip) {
+        float mx[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) mx[j] = v[j];
+        for (int j = 0; j < 4; ++j) mx[j] = v[j];
 #pragma unroll
-          for (int j = 8; j < kNp; ++j) mx[j & 7] = fmaxf(mx[j & 7], v[j]);
+        for (int j = 4; j < kNp; j += 8) {       // (three-operand maxima)
 #pragma unroll
-          for (int w2 = 4; w2 >= 1; w2 >>= 1)
-#pragma unroll
-            for (int j = 0; j < w2; ++j) mx[j] = fmaxf(mx[j], mx[j + w2]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) mx[j] = v[j];
-#pragma unroll
-          for (int j = 8; j < kNp; ++j) mx[j & 7] = fminf(mx[j & 7], v[j]);
-#pragma unroll
-          for (int w2 = 4; w2 >= 1; w2 >>= 1)
-#pragma unroll
-            for (int j = 0; j < w2; ++j) mx[j] = fminf(mx[j], mx[j + w2]);
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], v[j + e]), j + 4 + e < kNp ? v[j + 4 + e] : v[j + e]);
         }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         // (an infinite sum is a masked or an overflowed one: not scaled, 0 * inf is no logit)
-        const bool none = mx[0] == (flip ? INFINITY : -INFINITY);
-        const float tmax = none ? -INFINITY : mx[0] * sl2;
-        float alpha = 1.f;
+        const float tmax = top == -INFINITY ? -INFINITY : top * sl2;
+        // the reference after the tile before (set by the other set), moved when
+        // this tile's maximum exceeds it by far; what is in the accumulator moves
+        // with it
+        if (tg > 0 && !(ok = wait32(&ref_set[quarter], (uint32_t)(tg - 1) & 1u, abort_flag, err))) break;
+        const float m_prev = t == x.t0 ? -INFINITY : ref_s[0];
+        float m_ref = m_prev, alpha = 1.f;
         bool rescale = false;
-        if (m_ref == -INFINITY) {
+        if (m_prev == -INFINITY) {
           m_ref = tmax;                        // nothing in the accumulator yet
-        } else if (tmax > m_ref + kRescaleLog2) {
-          alpha = exp2f(m_ref - tmax);
+        } else if (tmax > m_prev + kRescaleLog2) {
+          alpha = exp2f(m_prev - tmax);
           m_ref = tmax;
           rescale = true;
         }
-        // the P tile is free, and P.V(t-1) has landed in the accumulator
-        if (!(ok = warp_wait(p_empty, ((uint32_t)tg & 1u) ^ 1u, abort_flag, err))) break;
-        tc_fence_after();
-        // weights 2^(logit * sl2 - reference), rounded to bf16 for P.V (half a step,
-        // to nearest: the errors of a row's weights average out) and summed in
-        // fp32 before the rounding, which keeps the lse exact to fp32
+        ref_s[0] = m_ref;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ref_set[quarter]);
+        // weights 2^(logit * sl2 - reference), rounded to bf16 for P.V (half a step, to
+        // nearest: the errors of a row's weights average out) and summed in fp32
+        // before the rounding, which keeps the lse exact to fp32
         uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t pk[kNp / 2];
         const float nmr = (m_ref == -INFINITY) ? 0.f : -m_ref;
         const uint64_t scale2 = pack2(sl2, sl2), nmr2 = pack2(nmr, nmr);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          uint32_t w4[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = 8 * u + 2 * e;
-            const float2 x2 = unpack2(fma2(pack2(v[j], v[j + 1]), scale2, nmr2));
-            const float e0 = ex2_approx(x2.x), e1 = ex2_approx(x2.y);
-            sum2[e] = add2(sum2[e], pack2(e0, e1));
-            const __nv_bfloat162 p2 = __floats2bfloat162_rn(e0, e1);
-            w4[e] = *reinterpret_cast<const uint32_t*>(&p2);
-          }
-          *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, u)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        for (int j = 0; j < kNp / 2; ++j) {
+          const float2 x2 = unpack2(fma2(pack2(v[2 * j], v[2 * j + 1]), scale2, nmr2));
+          const float e0 = ex2_approx(x2.x), e1 = ex2_approx(x2.y);
+          sum2[j & 3] = add2(sum2[j & 3], pack2(e0, e1));
+          const __nv_bfloat162 p2 = __floats2bfloat162_rn(e0, e1);
+          pk[j] = *reinterpret_cast<const uint32_t*>(&p2);
         }
         const float2 tot = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
-        l_sum = l_sum * alpha + (tot.x + tot.y);
+        if (m_mine != m_ref) l_mine *= m_mine == -INFINITY ? 0.f : exp2f(m_mine - m_ref);
+        m_mine = m_ref;
+        l_mine += tot.x + tot.y;
+        // the P tile is free, and P.V(t-1) has landed in the accumulator; a piece's
+        // first P also waits until both sets have read out the output before
+        if (tg > 0 && !(ok = wait32(&p_empty[set ^ 1], (uint32_t)((tg - 1) >> 1) & 1u, abort_flag, err))) break;
+        if (t == x.t0 && pieces > 0 &&
+            !(ok = wait32(o_free, (uint32_t)(pieces - 1) & 1u, abort_flag, err))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, u)) =
+              make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
         // TMEM loads and stores are warp-collective: rescale when any row of the
         // warp needs it (the others multiply by 1)
-        if (__any_sync(0xffffffffu, rescale)) {
-          for (int c0 = 0; c0 < 256; c0 += 32) {
-            float o[32];
-            uint32_t w[32];
-            tmem_ld32(tmem + lane_base + TM_O + c0, o);
+        if (__builtin_expect(__any_sync(0xffffffffu, rescale), 0)) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < 256; c0 += 16) {
+            float o[16];
+            tmem_ld16(tmem + lane_base + TM_O + c0, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * alpha);
-            tmem_st32(tmem + lane_base + TM_O + c0, w);
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tmem_st16(tmem + lane_base + TM_O + c0, o);
           }
           tmem_st_wait();
         }
@@ -783,10 +875,22 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         tc_fence_before();
         mbar_arrive(p_full);
       }
-      if (!ok || !(ok = warp_wait(o_done, (uint32_t)pieces & 1u, abort_flag, err))) break;
+      if (!ok) break;
+      // ---- the piece's sum over both sets (a set without tiles has none) --------
+      volatile float2* const sums = reinterpret_cast<float2*>(smem + OFF_SUMS) + (pieces & 1) * 2 * kM + m;
+      sums[set * kM].x = m_mine;
+      sums[set * kM].y = l_mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sums_set);
+      if (!(ok = wait32(sums_set, (uint32_t)pieces & 1u, abort_flag, err))) break;
+      const float2 other = make_float2(sums[(set ^ 1) * kM].x, sums[(set ^ 1) * kM].y);
+      const float m_ref = fmaxf(m_mine, other.x);
+      float l_sum = m_mine == -INFINITY ? 0.f : l_mine * exp2f(m_mine - m_ref);
+      if (other.x != -INFINITY) l_sum += other.y * exp2f(other.x - m_ref);
+      if (!(ok = wait32(o_done, (uint32_t)pieces & 1u, abort_flag, err))) break;
       ++pieces;
       tc_fence_after();
-      // ---- the piece's output: this CTA's 256 dims ------------------------------
+      // ---- the piece's output: this CTA's 256 dims, 128 of them by each set ------
       const bool entire = x.t0 == 0 && x.t1 == x.grp.tiles;
       const int slot = 2 * k + (x.t0 == 0 ? 1 : 0);
       if (!entire) {
@@ -800,48 +904,51 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       const bool live = m < x.grp.nt * a.H;
       const int64_t orow = (int64_t)x.grp.row0 * a.H + m;
       // nothing visible: 0; NaN stays NaN.  A direct output goes through the P
-      // tile (free: the piece's last P.V is done), a warp's 32 rows in its own 4 KB,
-      // so that a store instruction writes four rows of 128 bytes instead of 32
-      // rows of 16
+      // tile (free: the piece's last P.V is done), each warp's 32 rows in its half
+      // of their 128 bytes, so that a store instruction writes eight rows of 64
+      // bytes instead of 32 rows of 16
       const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
       const int rows_here = min(32, x.grp.nt * a.H - quarter * 32);
-      for (int c0 = 0; c0 < 256; c0 += 64) {
-        float o[64];
+#pragma unroll 1
+      for (int c0 = set * 128; c0 < set * 128 + 128; c0 += 32) {
+        float o[32];
         __syncwarp();
         tmem_ld32(tmem + lane_base + TM_O + c0, o);
-        tmem_ld32(tmem + lane_base + TM_O + c0 + 32, o + 32);
         tmem_ld_wait();
         if (entire) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
             __align__(16) bf16 o8[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) o8[e] = __float2bfloat16(o[8 * i + e] * inv);
-            *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, i)) = *reinterpret_cast<const uint4*>(o8);
+            *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, set * 4 + i)) = *reinterpret_cast<const uint4*>(o8);
           }
           __syncwarp();
           bf16* dst = a.out + ((int64_t)x.grp.row0 * a.H + quarter * 32) * DSI_D_LATENT + rho * 256 + c0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = i * 4 + (lane >> 3);
-            const uint4 y = *reinterpret_cast<const uint4*>(pbuf + sw128_offset(quarter * 32 + rr, lane & 7));
+          for (int i = 0; i < 4; ++i) {
+            const int rr = i * 8 + (lane >> 2);
+            const uint4 y = *reinterpret_cast<const uint4*>(
+                pbuf + sw128_offset(quarter * 32 + rr, set * 4 + (lane & 3)));
             if (rr < rows_here)
-              *reinterpret_cast<uint4*>(dst + (int64_t)rr * DSI_D_LATENT + (lane & 7) * 8) = y;
+              *reinterpret_cast<uint4*>(dst + (int64_t)rr * DSI_D_LATENT + (lane & 3) * 8) = y;
           }
         } else if (live) {
           float* dst = ws.o + ((int64_t)slot * kM + m) * DSI_D_LATENT + rho * 256 + c0;
 #pragma unroll
-          for (int i = 0; i < 64; i += 4)
+          for (int i = 0; i < 32; i += 4)
             *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         }
       }
-      if (live && rho == 0) {
+      if (live && rho == 0 && set == 0) {
         if (!entire) ws.ml[slot * kM + m] = make_float2(m_ref, l_sum);
         else if (a.lse) a.lse[orow] = l_sum == 0.f ? -INFINITY : (m_ref + log2f(l_sum)) / kLog2e;
       }
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
     }
-    if (plan.split && rho == 0 && m == 0) ws.rec[k] = rec;
+    if (plan.split && rho == 0 && set == 0 && m == 0) ws.rec[k] = rec;
   }
   tc_fence_before();
   __syncthreads();
@@ -942,13 +1049,13 @@ int cluster_slots() {
 constexpr size_t kSlotBytes = (size_t)kM * (DSI_D_LATENT * sizeof(float) + sizeof(float2));
 
 template <bool F8>
-cudaError_t launch(const CUtensorMap& map, const CUtensorMap& qmap, const DenseArgs& a, const Plan& plan, const Workspace& ws,
+cudaError_t launch(const CUtensorMap& map, const CUtensorMap& rmap, const CUtensorMap& qmap, const DenseArgs& a, const Plan& plan, const Workspace& ws,
                    int box, int clusters, cudaStream_t st) {
   // per device: the current one's attribute, whatever was set before
   cudaError_t e = cudaFuncSetAttribute(dense_mla_tc<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   e = launch_overlapped(dense_mla_tc<F8>, dim3(2u * (unsigned)clusters), dim3(kThreads), SMEM, st,
-                        map, qmap, a, plan, ws, box);
+                        map, rmap, qmap, a, plan, ws, box);
   note_launch();
   return e;
 }
@@ -983,18 +1090,21 @@ cudaError_t launch_dense_mla(const DenseArgs& a, cudaStream_t st) {
   int box = kNp;
   if (a.c.block_table)
     while (a.c.page_size % box != 0) box /= 2;   // page sizes are multiples of 8
-  CUtensorMap map;
+  CUtensorMap map, rmap;
   memset(&map, 0, sizeof(map));
+  memset(&rmap, 0, sizeof(rmap));
   const uint64_t rows = a.c.block_table ? (uint64_t)a.c.num_pages * a.c.page_size
                                         : (uint64_t)a.c.batch * a.c.s_max;
-  if (!f8 && !tma_map_2d(&map, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, DSI_D_QK, 64,
-                         (uint32_t)box))
+  if (!f8 && (!tma_map_2d(&map, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, DSI_D_QK, 64,
+                          (uint32_t)box) ||
+              !tma_map_2d(&rmap, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, DSI_D_QK,
+                          kRopeHalf, (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_64B)))
     return cudaErrorInvalidValue;
   CUtensorMap qmap;
   if (!tma_map_2d(&qmap, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)a.rows * a.H, DSI_D_QK, 64, kM))
     return cudaErrorInvalidValue;
-  cudaError_t e = f8 ? launch<true>(map, qmap, a, plan, ws, box, clusters, st)
-                     : launch<false>(map, qmap, a, plan, ws, box, clusters, st);
+  cudaError_t e = f8 ? launch<true>(map, rmap, qmap, a, plan, ws, box, clusters, st)
+                     : launch<false>(map, rmap, qmap, a, plan, ws, box, clusters, st);
   if (e != cudaSuccess || !plan.split) return e;
   e = launch_overlapped(dense_mla_join, dim3((unsigned)clusters, (unsigned)(plan.tokens * a.H)), dim3(128),
                         0, st, a, plan, ws, clusters);
