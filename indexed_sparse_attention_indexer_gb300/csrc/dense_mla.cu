@@ -51,7 +51,6 @@ namespace {
 
 constexpr int kM = 128;                        // rows of a group: (token, head) pairs
 constexpr int kNp = 64;                        // positions per tile
-constexpr int kStages = 4;
 constexpr int kBlockBytes = kNp * 128;         // 64 dims of a tile
 constexpr int kRopeHalf = 32;                  // rope dims of each CTA
 constexpr int kRopeOff = 4 * kBlockBytes;      // stage: four 64-dim blocks, then 64 rows of rope dims
@@ -63,7 +62,6 @@ constexpr int kPvWarp = 2;
 constexpr int kQkWarp = 3;                     // then exchange: warps 4-7
 constexpr int kSmWarp0 = 8;                    // softmax: warps 8-11 even tiles, 12-15 odd ones
 constexpr int kThreads = 16 * 32;
-constexpr int kProdThreads = kProducers * 32;
 constexpr int kMaxClusters = 128;
 constexpr int kWholeSlack = 8;
 constexpr int kAhead = 8;                      // tiles between L2 prefetch and copy
@@ -74,22 +72,33 @@ constexpr int kXRing = 3;
 constexpr int kXBytes = kM * kQuarter * 4;
 constexpr int kPoison = 8;                     // tiles whose poisoned rows are remembered
 
-constexpr int OFF_C = 0;
-constexpr int OFF_P = OFF_C + kStages * kStageBytes;      // P [128 x 64] bf16
-constexpr int OFF_X = OFF_P + kM * kNp * 2;               // [2 sets][kXRing] the peer's partial logits
-constexpr int OFF_QR = OFF_X + 2 * kXRing * kXBytes;     // query rope half
-constexpr int OFF_REF = OFF_QR + kM * kRopeHalf * 2;      // reference maxima of the rows
-constexpr int OFF_SUMS = OFF_REF + kM * 4;                // [2][2][128] (reference, sum) of both sets
-constexpr int OFF_BAR = OFF_SUMS + 4 * kM * 8;
-constexpr int kBars = 3 * kStages + 16 + 4 * kXRing;
-constexpr int OFF_ROWS = OFF_BAR + kBars * 8;             // [2][64] cache rows of a tile (generic path)
-constexpr int OFF_POISON = OFF_ROWS + 2 * kNp * 4;
-constexpr int OFF_MISC = OFF_POISON + kPoison * 8;
-constexpr int OFF_SCAN = OFF_MISC + 64;                   // 40 ints
-constexpr int SMEM = OFF_SCAN + 160 + 1024;
-static_assert(SMEM <= 227 * 1024, "shared memory");
-static_assert(kProdThreads == kNp, "a producer thread looks up one row of a tile");
-static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 8 == 0, "alignment");
+// FP8 rows: raw tiles of codes land beside the ring and are converted into it
+// by the warps that are the second softmax set of bf16 rows.
+constexpr int kRawStages = 2;
+constexpr int kRawRope = 2 * kNp * 128;        // two blocks of 128 dims, then 64 rows of 32 rope dims
+constexpr int kRawBytes = kNp * (256 + kRopeHalf);
+
+template <bool F8>
+struct Layout {                                // shared memory, bytes
+  static constexpr int stages = F8 ? 3 : 4;
+  static constexpr int sets = F8 ? 1 : 2;      // softmax sets
+  static constexpr int fill_warps = F8 ? 4 : 2;   // warps that hand a tile to the tensor core
+  static constexpr int c = 0;
+  static constexpr int raw = c + stages * kStageBytes;
+  static constexpr int p = raw + (F8 ? kRawStages * kRawBytes : 0);   // P [128 x 64] bf16
+  static constexpr int x = p + kM * kNp * 2;   // [2][kXRing] the peer's partial logits
+  static constexpr int qr = x + 2 * kXRing * kXBytes;                 // query rope half
+  static constexpr int ref = qr + kM * kRopeHalf * 2;                 // reference maxima of the rows
+  static constexpr int sums = ref + kM * 4;    // [2][2][128] (reference, sum) of both sets
+  static constexpr int bar = sums + 4 * kM * 8;
+  static constexpr int bars = 3 * stages + 15 + 4 * kXRing + 2 * kRawStages;
+  static constexpr int poison = bar + bars * 8;
+  static constexpr int misc = poison + kPoison * 8;
+  static constexpr int scan = misc + 64;       // 40 ints
+  static constexpr int bytes = scan + 160 + 1024;
+  static_assert(bytes <= 227 * 1024, "shared memory");
+  static_assert(raw % 1024 == 0 && p % 1024 == 0 && qr % 512 == 0 && misc % 8 == 0, "alignment");
+};
 
 constexpr uint32_t TM_S = 0;      // two logit tiles of 64 columns
 constexpr uint32_t TM_Q = 128;    // query slice: four 64-dim blocks, 128 columns
@@ -273,9 +282,12 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);   // [kStages] tile landed
+  using Y = Layout<F8>;
+  constexpr int kStages = Y::stages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Y::bar);   // [kStages] tile in place
   uint64_t* empty = full + kStages;            // [kStages] stage free (value MMAs done)
-  uint64_t* s_full = empty + kStages;          // [2] logits in TMEM
+  uint64_t* landed = empty + kStages;          // [kStages] an edge tile's copies landed
+  uint64_t* s_full = landed + kStages;         // [2] logits in TMEM
   uint64_t* s_empty = s_full + 2;              // [2] logits read out (exchange and softmax)
   // barriers that only one softmax set waits for at a tile come in pairs, one for
   // even and one for odd tiles: a set that skips a phase could not tell it apart
@@ -283,22 +295,21 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
   uint64_t* p_full = s_full + 6;               // P written
   uint64_t* q_ready = s_full + 7;              // query slice in place
   uint64_t* o_done = s_full + 8;               // a piece's last P.V done
-  uint64_t* landed = s_full + 9;               // [kStages] an edge tile's copies landed
-  uint64_t* looked_up = landed + kStages;      // FP8: a tile's cache rows looked up
-  uint64_t* ref_set = looked_up + 1;           // [4] a tile's reference maxima (per lane quarter)
-  uint64_t* sums_set = ref_set + 4;            // both softmax sets' sums of a piece
-  uint64_t* o_free = ref_set + 5;              // a piece's output read out
-  uint64_t* x_full = o_free + 1;               // [2][kXRing] the peer's partial logits landed
+  uint64_t* ref_set = s_full + 9;              // [4] a tile's reference maxima (per lane quarter)
+  uint64_t* sums_set = s_full + 13;            // both softmax sets' sums of a piece
+  uint64_t* o_free = s_full + 14;              // a piece's output read out
+  uint64_t* x_full = s_full + 15;              // [2][kXRing] the peer's partial logits landed
   uint64_t* x_empty = x_full + 2 * kXRing;     // [2][kXRing] the peer has read what we sent
-  int* rows_s = reinterpret_cast<int*>(smem + OFF_ROWS);
-  unsigned int* poison = reinterpret_cast<unsigned int*>(smem + OFF_POISON);   // [kPoison][2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
-  int* start_s = reinterpret_cast<int*>(smem + OFF_MISC + 8);                   // group, tile
-  int* widest_s = reinterpret_cast<int*>(smem + OFF_MISC + 16);
-  unsigned long long* total_s = reinterpret_cast<unsigned long long*>(smem + OFF_MISC + 24);
-  unsigned int* taken_s = reinterpret_cast<unsigned int*>(smem + OFF_MISC + 32);
-  int* scan_s = reinterpret_cast<int*>(smem + OFF_SCAN);
+  uint64_t* raw_full = x_empty + 2 * kXRing;   // [kRawStages] FP8: codes landed
+  uint64_t* raw_empty = raw_full + kRawStages; // [kRawStages] FP8: codes converted
+  unsigned int* poison = reinterpret_cast<unsigned int*>(smem + Y::poison);   // [kPoison][2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Y::misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Y::misc + 4);
+  int* start_s = reinterpret_cast<int*>(smem + Y::misc + 8);                   // group, tile
+  int* widest_s = reinterpret_cast<int*>(smem + Y::misc + 16);
+  unsigned long long* total_s = reinterpret_cast<unsigned long long*>(smem + Y::misc + 24);
+  unsigned int* taken_s = reinterpret_cast<unsigned int*>(smem + Y::misc + 32);
+  int* scan_s = reinterpret_cast<int*>(smem + Y::scan);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rho = cluster_ctarank();
@@ -308,7 +319,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], kProducers);
+      mbar_init(&full[s], Y::fill_warps);
       mbar_init(&empty[s], 1);
       mbar_init(&landed[s], 1);
     }
@@ -324,10 +335,13 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       mbar_init(&x_full[i], 1);
       mbar_init(&x_empty[i], 4);
     }
-    mbar_init(looked_up, kProducers);
+    for (int i = 0; i < kRawStages; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
     for (int i = 0; i < 4; ++i) mbar_init(&ref_set[i], 1);
-    mbar_init(sums_set, 8);
-    mbar_init(o_free, 8);
+    mbar_init(sums_set, 4 * Y::sets);
+    mbar_init(o_free, 4 * Y::sets);
     taken_s[0] = taken_s[1] = 0u;
     *abort_flag = 0;
     start_s[0] = plan.groups;
@@ -338,10 +352,8 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
   }
   if (warp == kQkWarp) tmem_alloc(tmem_slot, TMEM_COLS);
   if (warp == 0 && lane == 0) {
-    if (!F8) {
-      prefetch_tmap(&lmap);
-      prefetch_tmap(&rmap);
-    }
+    prefetch_tmap(&lmap);
+    prefetch_tmap(&rmap);
     prefetch_tmap(&qmap);
   }
   grid_dep_wait();     // lengths, queries and cache rows may come from the kernel before
@@ -412,23 +424,25 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     // A piece takes two ring slots for its query slice, then one a tile.
     Piece x;
     int slot = 0, tg = 0;                      // ring slots; tiles
-    [[maybe_unused]] int loaded = 0;           // tiles by plain loads
     uint32_t edge_ph = 0;                      // parities of landed[]
     uint32_t issued = 0, issued_edge = 0;      // stages with a copy in flight; into an edge tile
     bool ok = true;
-    while (ok && next_piece(a, plan, walk, x)) {
+    // (FP8 rows: warp 0 alone, the tiles' copies go to the raw stages)
+    while (ok && (!F8 || warp == 0) && next_piece(a, plan, walk, x)) {
       for (int i = 0; i < 2; ++i, ++slot) {
         const int stage = slot % kStages;
         if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u, abort_flag, err))) break;
         if (lane == 0) {
           if (warp == 0) {
-            uint8_t* st = smem + OFF_C + stage * kStageBytes;
+            uint8_t* st = smem + Y::c + stage * kStageBytes;
             mbar_arrive_expect_tx(&full[stage], 2 * kM * 128);
             issued |= 1u << stage;
             issued_edge &= ~(1u << stage);
             for (int bx = 0; bx < 2; ++bx)
               tma_load_2d(st + bx * kM * 128, &qmap, (int)rho * 256 + (2 * i + bx) * 64,
                           x.grp.row0 * a.H, &full[stage]);
+            if (F8)
+              for (int w = 1; w < Y::fill_warps; ++w) mbar_arrive(&full[stage]);
           } else {
             mbar_arrive(&full[stage]);
           }
@@ -436,142 +450,101 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       }
       if (!ok) break;
       for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
-        const int stage = slot % kStages;
-        const uint32_t ph = (uint32_t)(slot / kStages) & 1u;
+        const int stage = F8 ? tg % kRawStages : slot % kStages;
+        const uint32_t ph = (uint32_t)(F8 ? tg / kRawStages : slot / kStages) & 1u;
         const int p0 = tile_pos(x.grp, t);
-        uint8_t* st = smem + OFF_C + stage * kStageBytes;
+        uint8_t* st = smem + (F8 ? Y::raw + stage * kRawBytes : Y::c + stage * kStageBytes);
         unsigned int* pz = poison + (tg & (kPoison - 1)) * 2;
-        const bool whole = all_see(a, x.grp, p0, kNp);
-        if constexpr (!F8) {
-          // warp 0: the tile by TMA, boxes of `box` rows (a page or a part of one) x
-          // 64 dims; warp 1 passes a whole tile on and cleans one at an edge first
-          if (warp == 0) {
-            if (!(ok = wait32(&empty[stage], ph ^ 1, abort_flag, err))) break;
-            const int boxes = kNp / box;
-            const int pb = p0 + lane * box;        // lane's box, if it has one
-            const bool seen = lane < boxes && pb < x.grp.n_last && (pb + box > x.grp.lo || pb < (int)a.n_sink);
-            const int n = __popc(__ballot_sync(0xffffffffu, seen));
-            uint64_t* bar = whole ? &full[stage] : &landed[stage];
-            if (lane == 0) {
-              mbar_arrive_expect_tx(bar, (uint32_t)(n * box * kRowBytes));
-              if (!whole) mbar_arrive(&full[stage]);
+        const bool whole = F8 || all_see(a, x.grp, p0, kNp);
+        if (warp == 0) {
+          // the tile by TMA, boxes of `box` rows (a page or a part of one) by 128 bytes of
+          // dims; boxes that no token sees are left out
+          uint64_t* bar = F8 ? &raw_full[stage] : whole ? &full[stage] : &landed[stage];
+          if (!(ok = wait32(F8 ? &raw_empty[stage] : &empty[stage], ph ^ 1, abort_flag, err))) break;
+          constexpr int kBlks = F8 ? 3 : 5;      // blocks of 128 bytes a row, the last the rope half
+          const int boxes = kNp / box;
+          const int pb = p0 + lane * box;        // lane's box, if it has one
+          const bool seen = lane < boxes && pb < x.grp.n_last && (pb + box > x.grp.lo || pb < (int)a.n_sink);
+          const int n = __popc(__ballot_sync(0xffffffffu, seen));
+          if (lane == 0) {
+            if (F8) pz[0] = pz[1] = 0u;
+            mbar_arrive_expect_tx(bar, (uint32_t)(n * box * (F8 ? kRawBytes / kNp : kRowBytes)));
+            if (!whole) mbar_arrive(&full[stage]);
+            if (!F8) {
               issued |= 1u << stage;
               issued_edge = whole ? issued_edge & ~(1u << stage) : issued_edge | (1u << stage);
               edge_ph ^= whole ? 0u : 1u << stage;
             }
-            __syncwarp();
-            for (int i = lane; i < boxes * 5; i += 32) {
-              const int bx = i / 5, blk = i - bx * 5, p = p0 + bx * box;
-              if (!(p < x.grp.n_last && (p + box > x.grp.lo || p < (int)a.n_sink))) continue;
-              const int row = row_of(a.c, x.grp.b, p, err);
-              // a bad page id: the box past the tensor's last row, which reads as zeros
-              const int y = row < 0 ? (int)a.c.num_pages * a.c.page_size : row;
-              if (blk < 4)
-                tma_load_2d(st + blk * kBlockBytes + bx * box * 128, &lmap, (int)rho * 256 + blk * 64, y, bar);
-              else
-                tma_load_2d(st + kRopeOff + bx * box * kRopeHalf * 2, &rmap,
-                            DSI_D_LATENT + (int)rho * kRopeHalf, y, bar);
-            }
-            // decode: the caches come from HBM; a tile is asked for into L2 kAhead tiles
-            // before its copy, so that the copy holds its stage only as long as L2 takes
-            if (a.decode) {
-              for (int u = t == x.t0 ? t + 1 : t + kAhead; u < min(x.t1, t + kAhead + 1); ++u) {
-                const int pu = tile_pos(x.grp, u);
-                for (int i = lane; i < boxes * 5; i += 32) {
-                  const int bx = i / 5, blk = i - bx * 5, p = pu + bx * box;
-                  if (!(p < x.grp.n_last && (p + box > x.grp.lo || p < (int)a.n_sink))) continue;
-                  const int row = row_of(a.c, x.grp.b, p, err);
-                  if (row < 0) continue;
-                  if (blk < 4) tma_prefetch_2d(&lmap, (int)rho * 256 + blk * 64, row);
-                  else tma_prefetch_2d(&rmap, DSI_D_LATENT + (int)rho * kRopeHalf, row);
-                }
+          }
+          __syncwarp();
+          for (int i = lane; i < boxes * kBlks; i += 32) {
+            const int bx = i / kBlks, blk = i - bx * kBlks, p = p0 + bx * box;
+            if (!(p < x.grp.n_last && (p + box > x.grp.lo || p < (int)a.n_sink))) continue;
+            const int row = row_of(a.c, x.grp.b, p, err);
+            // a bad page id: the box past the tensor's last row, which reads as zeros
+            const int y = row < 0 ? (int)a.c.num_pages * a.c.page_size : row;
+            if (blk < kBlks - 1)
+              tma_load_2d(st + blk * kBlockBytes + bx * box * 128, &lmap,
+                          (int)rho * 256 + blk * (256 / (kBlks - 1)), y, bar);
+            else
+              tma_load_2d(st + (F8 ? kRawRope + bx * box * kRopeHalf : kRopeOff + bx * box * kRopeHalf * 2),
+                          &rmap, DSI_D_LATENT + (int)rho * kRopeHalf, y, bar);
+          }
+          // decode: the caches come from HBM; a tile is asked for into L2 kAhead tiles
+          // before its copy, so that the copy holds its stage only as long as L2 takes
+          if (a.decode) {
+            for (int u = t == x.t0 ? t + 1 : t + kAhead; u < min(x.t1, t + kAhead + 1); ++u) {
+              const int pu = tile_pos(x.grp, u);
+              for (int i = lane; i < boxes * kBlks; i += 32) {
+                const int bx = i / kBlks, blk = i - bx * kBlks, p = pu + bx * box;
+                if (!(p < x.grp.n_last && (p + box > x.grp.lo || p < (int)a.n_sink))) continue;
+                const int row = row_of(a.c, x.grp.b, p, err);
+                if (row < 0) continue;
+                if (blk < kBlks - 1) tma_prefetch_2d(&lmap, (int)rho * 256 + blk * (256 / (kBlks - 1)), row);
+                else tma_prefetch_2d(&rmap, DSI_D_LATENT + (int)rho * kRopeHalf, row);
               }
-            }
-            __syncwarp();
-          } else {
-            unsigned int z[2] = {0u, 0u};
-            if (!whole) {
-              // rows that no token sees become zeros (weight 0 times what they hold must
-              // be 0); a row that only some tokens see is searched for NaN and infinities:
-              // it is taken out and remembered, and its logits become NaN where it is seen
-              if (!(ok = wait32(&landed[stage], (edge_ph >> stage) & 1u, abort_flag, err))) break;
-              edge_ph ^= 1u << stage;
-#pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                const int p = p0 + w * 32 + lane;
-                const unsigned int none = __ballot_sync(0xffffffffu, !any_sees(a, x.grp, p));
-                unsigned int some = ~none & ~__ballot_sync(0xffffffffu, all_see(a, x.grp, p, 1));
-                for (unsigned int todo = none | some; todo; todo &= todo - 1) {
-                  const int bit = __ffs(todo) - 1, rr = w * 32 + bit;
-                  uint4* at = reinterpret_cast<uint4*>(st + (lane >> 3) * kBlockBytes + sw128_offset(rr, lane & 7));
-                  uint4* rope = reinterpret_cast<uint4*>(st + kRopeOff + sw64_offset(rr, lane & 3));
-                  bool clear = (none >> bit) & 1u;
-                  if (!clear) {
-                    clear = __any_sync(0xffffffffu, !(bf16x8_finite(*at) && bf16x8_finite(*rope)));
-                    if (clear) z[w] |= 1u << bit;
-                  }
-                  if (clear) {
-                    *at = make_uint4(0, 0, 0, 0);
-                    if (lane < 4) *rope = make_uint4(0, 0, 0, 0);
-                  }
-                }
-              }
-              fence_proxy_async_smem();   // the tensor core reads the stage through the async proxy
-              __syncwarp();
-            } else if (!(ok = wait32(&empty[stage], ph ^ 1, abort_flag, err))) {
-              break;
-            }
-            if (lane == 0) {
-              pz[0] = z[0];
-              pz[1] = z[1];
-              mbar_arrive(&full[stage]);
             }
           }
+          __syncwarp();
         } else {
-          // plain loads, converted to bf16 on the way (edges: as above)
-          int* rows = rows_s + (loaded & 1) * kNp;     // (the barrier below keeps its readers apart)
-          rows[tid] = any_sees(a, x.grp, p0 + tid) ? row_of(a.c, x.grp.b, p0 + tid, err) : -1;
-          if (tid == 0) pz[0] = pz[1] = 0u;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(looked_up);
-          if (!(ok = wait32(looked_up, (uint32_t)loaded++ & 1u, abort_flag, err))) break;
-          constexpr int kPieces = 18;          // 16 codes each: 256 latent and 32 rope dims
-          constexpr int kPer = kNp * kPieces / kProdThreads;
-          static_assert(kPer * kProdThreads == kNp * kPieces, "whole rounds");
-          const uint8_t* codes = reinterpret_cast<const uint8_t*>(a.c.latent);
-          uint4 cv[kPer];
-          float sc[kPer];
+          // bf16 rows, warp 1: passes a whole tile on and cleans one at an edge first
+          unsigned int z[2] = {0u, 0u};
+          if (!whole) {
+            // rows that no token sees become zeros (weight 0 times what they hold must
+            // be 0); a row that only some tokens see is searched for NaN and infinities:
+            // it is taken out and remembered, and its logits become NaN where it is seen
+            if (!(ok = wait32(&landed[stage], (edge_ph >> stage) & 1u, abort_flag, err))) break;
+            edge_ph ^= 1u << stage;
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int q = tid + i * kProdThreads, rr = q / kPieces, u = q - rr * kPieces;
-            const int64_t row = rows[rr];
-            const int d0 = u < 16 ? (int)rho * 256 + u * 16
-                                  : DSI_D_LATENT + (int)rho * kRopeHalf + (u - 16) * 16;
-            cv[i] = make_uint4(0, 0, 0, 0);
-            sc[i] = 0.f;
-            if (row >= 0) {
-              cv[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * DSI_D_QK + d0));
-              sc[i] = __ldg(a.latent_scale + row * 5 + (d0 >> 7));
+            for (int w = 0; w < 2; ++w) {
+              const int p = p0 + w * 32 + lane;
+              const unsigned int none = __ballot_sync(0xffffffffu, !any_sees(a, x.grp, p));
+              unsigned int some = ~none & ~__ballot_sync(0xffffffffu, all_see(a, x.grp, p, 1));
+              for (unsigned int todo = none | some; todo; todo &= todo - 1) {
+                const int bit = __ffs(todo) - 1, rr = w * 32 + bit;
+                uint4* at = reinterpret_cast<uint4*>(st + (lane >> 3) * kBlockBytes + sw128_offset(rr, lane & 7));
+                uint4* rope = reinterpret_cast<uint4*>(st + kRopeOff + sw64_offset(rr, lane & 3));
+                bool clear = (none >> bit) & 1u;
+                if (!clear) {
+                  clear = __any_sync(0xffffffffu, !(bf16x8_finite(*at) && bf16x8_finite(*rope)));
+                  if (clear) z[w] |= 1u << bit;
+                }
+                if (clear) {
+                  *at = make_uint4(0, 0, 0, 0);
+                  if (lane < 4) *rope = make_uint4(0, 0, 0, 0);
+                }
+              }
             }
+            fence_proxy_async_smem();   // the tensor core reads the stage through the async proxy
+            __syncwarp();
+          } else if (!(ok = wait32(&empty[stage], ph ^ 1, abort_flag, err))) {
+            break;
           }
-          if (!(ok = wait32(&empty[stage], ph ^ 1, abort_flag, err))) break;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int q = tid + i * kProdThreads, rr = q / kPieces, u = q - rr * kPieces;
-            uint4 lo, hi;
-            e4m3x16_scaled(cv[i], sc[i], lo, hi);
-            if (!whole && !all_see(a, x.grp, p0 + rr, 1) && !(bf16x8_finite(lo) && bf16x8_finite(hi))) {
-              lo = hi = make_uint4(0, 0, 0, 0);
-              atomicOr(pz + (rr >> 5), 1u << (rr & 31));
-            }
-            const uint32_t ch = (uint32_t)(u & 3) * 2;
-            uint8_t* blk = u < 16 ? st + (u >> 2) * kBlockBytes : st + kRopeOff;
-            *reinterpret_cast<uint4*>(blk + (u < 16 ? sw128_offset(rr, ch) : sw64_offset(rr, ch))) = lo;
-            *reinterpret_cast<uint4*>(blk + (u < 16 ? sw128_offset(rr, ch + 1) : sw64_offset(rr, ch + 1))) = hi;
+          if (lane == 0) {
+            pz[0] = z[0];
+            pz[1] = z[1];
+            mbar_arrive(&full[stage]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[stage]);
         }
       }
     }
@@ -585,6 +558,73 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         if ((issued_edge >> s) & 1u) mbar_wait(&landed[s], ((edge_ph >> s) & 1u) ^ 1u, &no_abort, err, 100000000ull);
         else mbar_wait(&full[s], (uint32_t)(last / kStages) & 1u, &no_abort, err, 100000000ull);
       }
+      if (F8)
+        for (int i = max(0, tg - kRawStages); i < tg; ++i)
+          mbar_wait(&raw_full[i % kRawStages], (uint32_t)(i / kRawStages) & 1u, &no_abort, err, 100000000ull);
+    }
+  } else if (F8 && warp >= kSmWarp0 + 4) {
+    // ======================= FP8: conversion ======================================
+    // Two threads a row, nine pieces of 16 codes each: code * tile scale, rounded to
+    // bf16, into the ring stage.  The page is looked up two tiles ahead and the scales
+    // are loaded one ahead, within a piece.
+    const int c_thread = tid - (kSmWarp0 + 4) * 32, rr = c_thread & 63, hh = c_thread >> 6;
+    const int s0 = (int)rho * 2 + hh;            // tile of this thread's 128 latent dims
+    Piece x = {};
+    int slot = 0, tg = 0;
+    bool ok = true;
+    auto lookup = [&](int t) {                    // cache row of this thread's row of tile t
+      const int p = t < x.t1 ? tile_pos(x.grp, t) + rr : -1;
+      return p >= 0 && any_sees(a, x.grp, p) ? row_of(a.c, x.grp.b, p, err) : -1;
+    };
+    auto scales = [&](int row) {                  // of the latent dims and of the rope dims
+      return row < 0 ? make_float2(0.f, 0.f)
+                     : make_float2(__ldg(a.latent_scale + (int64_t)row * 5 + s0),
+                                   __ldg(a.latent_scale + (int64_t)row * 5 + 4));
+    };
+    while (ok && next_piece(a, plan, walk, x)) {
+      // (the query slots are waited for too: a skipped phase could not be told apart)
+      for (int i = 0; i < 2 && ok; ++i, ++slot)
+        ok = wait32(&empty[slot % kStages], ((uint32_t)(slot / kStages) & 1u) ^ 1u, abort_flag, err);
+      if (!ok) break;
+      int row_next = lookup(x.t0);
+      float2 sc = scales(row_next);
+      row_next = lookup(x.t0 + 1);
+      for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
+        const int stage = slot % kStages, rs = tg % kRawStages, p = tile_pos(x.grp, t) + rr;
+        const float2 sc_next = scales(row_next);
+        row_next = lookup(t + 2);
+        const bool seen = any_sees(a, x.grp, p), partly = seen && !all_see(a, x.grp, p, 1);
+        const uint8_t* raw = smem + Y::raw + rs * kRawBytes;
+        uint8_t* st = smem + Y::c + stage * kStageBytes;
+        if (!(ok = wait32(&raw_full[rs], (uint32_t)(tg / kRawStages) & 1u, abort_flag, err))) break;
+        if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u, abort_flag, err))) break;
+#pragma unroll
+        for (int u = 0; u < 9; ++u) {
+          const bool rope = u == 8;
+          uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+          if (seen) {
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                rope ? raw + kRawRope + rr * kRopeHalf + hh * 16 : raw + hh * kBlockBytes + sw128_offset(rr, u));
+            e4m3x16_scaled(v, rope ? sc.y : sc.x, lo, hi);
+          }
+          // (edges: as for bf16 rows)
+          if (partly && !(bf16x8_finite(lo) && bf16x8_finite(hi))) {
+            lo = hi = make_uint4(0, 0, 0, 0);
+            atomicOr(poison + (tg & (kPoison - 1)) * 2 + (rr >> 5), 1u << (rr & 31));
+          }
+          uint8_t* blk = rope ? st + kRopeOff : st + (hh * 2 + (u >> 2)) * kBlockBytes;
+          const uint32_t ch = rope ? (uint32_t)hh * 2 : (uint32_t)(u & 3) * 2;
+          *reinterpret_cast<uint4*>(blk + (rope ? sw64_offset(rr, ch) : sw128_offset(rr, ch))) = lo;
+          *reinterpret_cast<uint4*>(blk + (rope ? sw64_offset(rr, ch + 1) : sw128_offset(rr, ch + 1))) = hi;
+        }
+        sc = sc_next;
+        fence_proxy_async_smem();   // the tensor core reads the stage through the async proxy
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[rs]);
+          mbar_arrive(&full[stage]);
+        }
+      }
     }
   } else if (warp == kQkWarp) {
     // ======================= logit issuer =======================================
@@ -592,7 +632,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       Piece x;
       int slot = 0, tg = 0, pieces = 0;
       bool ok = true;
-      const uint64_t qr = desc_sw64(smem_u32(smem + OFF_QR));
+      const uint64_t qr = desc_sw64(smem_u32(smem + Y::qr));
       while (ok && next_piece(a, plan, walk, x)) {
         if (!(ok = wait1(q_ready, (uint32_t)pieces & 1u, abort_flag, err))) break;
         ++pieces;
@@ -603,7 +643,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           if (!(ok = wait1(&s_empty[sb], ((uint32_t)(tg >> 1) & 1u) ^ 1u, abort_flag, err))) break;
           tc_fence_after();
           const uint32_t t_s = tmem + TM_S + sb * kNp;
-          const uint32_t base = smem_u32(smem + OFF_C + stage * kStageBytes);
+          const uint32_t base = smem_u32(smem + Y::c + stage * kStageBytes);
           const uint64_t d0 = desc_sw128(base);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -625,14 +665,14 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       Piece x;
       int slot = 0, tg = 0;
       bool ok = true;
-      const uint64_t pd = desc_sw128(smem_u32(smem + OFF_P));
+      const uint64_t pd = desc_sw128(smem_u32(smem + Y::p));
       while (ok && next_piece(a, plan, walk, x)) {
         slot += 2;                               // the query slice
         for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
           const int stage = slot % kStages;
           if (!(ok = wait1(p_full, (uint32_t)tg & 1u, abort_flag, err))) break;
           tc_fence_after();
-          const uint64_t vd = desc_sw128_mn(smem_u32(smem + OFF_C + stage * kStageBytes), kBlockBytes);
+          const uint64_t vd = desc_sw128_mn(smem_u32(smem + Y::c + stage * kStageBytes), kBlockBytes);
 #pragma unroll
           for (int i = 0; i < kNp / 16; ++i)
             mma_bf16(tmem + TM_O, pd + (uint64_t)((i * 32) >> 4), vd + (uint64_t)((i * 2048) >> 4),
@@ -650,7 +690,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     // exchange buffers [4-position group][row] x float4: a warp's stores of one
     // group are 512 contiguous bytes
-    const uint32_t x_remote = map_to_rank(smem_u32(smem + OFF_X), peer) + m * 16;
+    const uint32_t x_remote = map_to_rank(smem_u32(smem + Y::x), peer) + m * 16;
     const uint32_t xfull_remote = map_to_rank(smem_u32(x_full), peer);
     const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;   // a negative scale turns the queries' signs
     Piece x;
@@ -672,7 +712,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         if (!(ok = wait32(&full[stage], (uint32_t)(slot / kStages) & 1u, abort_flag, err))) break;
 #pragma unroll
         for (int bx = 0; bx < 2; ++bx) {
-          const uint8_t* src = smem + OFF_C + stage * kStageBytes + bx * kM * 128;
+          const uint8_t* src = smem + Y::c + stage * kStageBytes + bx * kM * 128;
           uint32_t w[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -695,7 +735,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       if (!ok) break;
 #pragma unroll
       for (int i = 0; i < kRopeHalf / 8; ++i)
-        *reinterpret_cast<uint4*>(smem + OFF_QR + sw64_offset(m, i)) =
+        *reinterpret_cast<uint4*>(smem + Y::qr + sw64_offset(m, i)) =
             make_uint4(rope[i].x ^ sign, rope[i].y ^ sign, rope[i].z ^ sign, rope[i].w ^ sign);
       slot += x.t1 - x.t0;
       tmem_st_wait();
@@ -739,12 +779,12 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     // Two sets of four warps take alternate tiles: a tile is in its set's hands for
     // two tile periods.  The reference maximum passes from set to set as soon as a
     // tile's maximum is known; each set sums its own tiles' weights.
-    const int set = (warp - kSmWarp0) >> 2;
+    const int set = Y::sets == 2 ? (warp - kSmWarp0) >> 2 : 0;
     const int quarter = warp & 3, m = quarter * 32 + lane;   // row = TMEM lane
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    uint8_t* const pbuf = smem + OFF_P;
-    const uint8_t* xrow = smem + OFF_X + m * 16;
-    volatile float* const ref_s = reinterpret_cast<float*>(smem + OFF_REF) + m;
+    uint8_t* const pbuf = smem + Y::p;
+    const uint8_t* xrow = smem + Y::x + m * 16;
+    volatile float* const ref_s = reinterpret_cast<float*>(smem + Y::ref) + m;
     const uint32_t xempty_remote = map_to_rank(smem_u32(x_empty), peer);
     // a scale of 0 becomes the smallest normal one: logits of 0, and "masked" times it stays -inf
     const float sl2 = a.scale == 0.f ? 1.17549435e-38f : fabsf(a.scale) * kLog2e;
@@ -759,22 +799,23 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       const int lo_row = n_row - (int)a.window;
       float m_mine = -INFINITY, l_mine = 0.f;
       for (int t = x.t0; t < x.t1; ++t, ++tg) {
-        if ((tg & 1) != set) continue;
+        if (Y::sets == 2 && (tg & 1) != set) continue;
+        const int sb = tg & 1;
         const int p0 = tile_pos(x.grp, t);
-        if (!(ok = wait32(&s_full[set], (uint32_t)(tg >> 1) & 1u, abort_flag, err))) break;
+        if (!(ok = wait32(&s_full[sb], (uint32_t)(tg >> 1) & 1u, abort_flag, err))) break;
         tc_fence_after();
         float v[kNp];
-        tmem_ld32(tmem + lane_base + TM_S + set * kNp, v);
-        tmem_ld32(tmem + lane_base + TM_S + set * kNp + 32, v + 32);
+        tmem_ld32(tmem + lane_base + TM_S + sb * kNp, v);
+        tmem_ld32(tmem + lane_base + TM_S + sb * kNp + 32, v + 32);
         const unsigned int z0 = poison[(tg & (kPoison - 1)) * 2], z1 = poison[(tg & (kPoison - 1)) * 2 + 1];
         tmem_ld_wait();
         tc_fence_before();
-        mbar_arrive(&s_empty[set]);
+        mbar_arrive(&s_empty[sb]);
         // the peer's partial logits
-        const int q0 = (tg >> 1) * 4;            // quarters that this set has received so far
+        const int q0 = (tg >> 1) * 4;            // quarters received for even or odd tiles so far
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int buf = set * kXRing + (q0 + i) % kXRing;
+          const int buf = sb * kXRing + (q0 + i) % kXRing;
           if (!(ok = wait32_cluster(&x_full[buf], (uint32_t)((q0 + i) / kXRing) & 1u, abort_flag, err))) break;
 #pragma unroll
           for (int g4 = 0; g4 < kQuarter / 4; ++g4) {
@@ -814,8 +855,9 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         // the reference after the tile before (set by the other set), moved when
         // this tile's maximum exceeds it by far; what is in the accumulator moves
         // with it
-        if (tg > 0 && !(ok = wait32(&ref_set[quarter], (uint32_t)(tg - 1) & 1u, abort_flag, err))) break;
-        const float m_prev = t == x.t0 ? -INFINITY : ref_s[0];
+        if (Y::sets == 2 && tg > 0 &&
+            !(ok = wait32(&ref_set[quarter], (uint32_t)(tg - 1) & 1u, abort_flag, err))) break;
+        const float m_prev = t == x.t0 ? -INFINITY : Y::sets == 2 ? ref_s[0] : m_mine;
         float m_ref = m_prev, alpha = 1.f;
         bool rescale = false;
         if (m_prev == -INFINITY) {
@@ -825,9 +867,11 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           m_ref = tmax;
           rescale = true;
         }
-        ref_s[0] = m_ref;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ref_set[quarter]);
+        if (Y::sets == 2) {
+          ref_s[0] = m_ref;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ref_set[quarter]);
+        }
         // weights 2^(logit * sl2 - reference), rounded to bf16 for P.V (half a step, to
         // nearest: the errors of a row's weights average out) and summed in fp32
         // before the rounding, which keeps the lse exact to fp32
@@ -849,7 +893,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         l_mine += tot.x + tot.y;
         // the P tile is free, and P.V(t-1) has landed in the accumulator; a piece's
         // first P also waits until both sets have read out the output before
-        if (tg > 0 && !(ok = wait32(&p_empty[set ^ 1], (uint32_t)((tg - 1) >> 1) & 1u, abort_flag, err))) break;
+        if (tg > 0 && !(ok = wait32(&p_empty[sb ^ 1], (uint32_t)((tg - 1) >> 1) & 1u, abort_flag, err))) break;
         if (t == x.t0 && pieces > 0 &&
             !(ok = wait32(o_free, (uint32_t)(pieces - 1) & 1u, abort_flag, err))) break;
         tc_fence_after();
@@ -877,16 +921,19 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       }
       if (!ok) break;
       // ---- the piece's sum over both sets (a set without tiles has none) --------
-      volatile float2* const sums = reinterpret_cast<float2*>(smem + OFF_SUMS) + (pieces & 1) * 2 * kM + m;
-      sums[set * kM].x = m_mine;
-      sums[set * kM].y = l_mine;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sums_set);
-      if (!(ok = wait32(sums_set, (uint32_t)pieces & 1u, abort_flag, err))) break;
-      const float2 other = make_float2(sums[(set ^ 1) * kM].x, sums[(set ^ 1) * kM].y);
-      const float m_ref = fmaxf(m_mine, other.x);
-      float l_sum = m_mine == -INFINITY ? 0.f : l_mine * exp2f(m_mine - m_ref);
-      if (other.x != -INFINITY) l_sum += other.y * exp2f(other.x - m_ref);
+      float m_ref = m_mine, l_sum = l_mine;
+      if (Y::sets == 2) {
+        volatile float2* const sums = reinterpret_cast<float2*>(smem + Y::sums) + (pieces & 1) * 2 * kM + m;
+        sums[set * kM].x = m_mine;
+        sums[set * kM].y = l_mine;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sums_set);
+        if (!(ok = wait32(sums_set, (uint32_t)pieces & 1u, abort_flag, err))) break;
+        const float2 other = make_float2(sums[(set ^ 1) * kM].x, sums[(set ^ 1) * kM].y);
+        m_ref = fmaxf(m_mine, other.x);
+        l_sum = m_mine == -INFINITY ? 0.f : l_mine * exp2f(m_mine - m_ref);
+        if (other.x != -INFINITY) l_sum += other.y * exp2f(other.x - m_ref);
+      }
       if (!(ok = wait32(o_done, (uint32_t)pieces & 1u, abort_flag, err))) break;
       ++pieces;
       tc_fence_after();
@@ -910,7 +957,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
       const int rows_here = min(32, x.grp.nt * a.H - quarter * 32);
 #pragma unroll 1
-      for (int c0 = set * 128; c0 < set * 128 + 128; c0 += 32) {
+      for (int c0 = set * 128; c0 < set * 128 + 256 / Y::sets; c0 += 32) {
         float o[32];
         __syncwarp();
         tmem_ld32(tmem + lane_base + TM_O + c0, o);
@@ -1023,14 +1070,14 @@ int cluster_slots() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) { cudaGetLastError(); return 76; }
   int v = cached[dev].load(std::memory_order_relaxed);
   if (v) return v;
-  if (cudaFuncSetAttribute(dense_mla_tc<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) {
+  if (cudaFuncSetAttribute(dense_mla_tc<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<F8>::bytes) != cudaSuccess) {
     cudaGetLastError();
     return 76;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = SMEM;
+  cfg.dynamicSmemBytes = Layout<F8>::bytes;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = 2;
@@ -1052,9 +1099,9 @@ template <bool F8>
 cudaError_t launch(const CUtensorMap& map, const CUtensorMap& rmap, const CUtensorMap& qmap, const DenseArgs& a, const Plan& plan, const Workspace& ws,
                    int box, int clusters, cudaStream_t st) {
   // per device: the current one's attribute, whatever was set before
-  cudaError_t e = cudaFuncSetAttribute(dense_mla_tc<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  cudaError_t e = cudaFuncSetAttribute(dense_mla_tc<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<F8>::bytes);
   if (e != cudaSuccess) return e;
-  e = launch_overlapped(dense_mla_tc<F8>, dim3(2u * (unsigned)clusters), dim3(kThreads), SMEM, st,
+  e = launch_overlapped(dense_mla_tc<F8>, dim3(2u * (unsigned)clusters), dim3(kThreads), Layout<F8>::bytes, st,
                         map, rmap, qmap, a, plan, ws, box);
   note_launch();
   return e;
@@ -1091,15 +1138,17 @@ cudaError_t launch_dense_mla(const DenseArgs& a, cudaStream_t st) {
   if (a.c.block_table)
     while (a.c.page_size % box != 0) box /= 2;   // page sizes are multiples of 8
   CUtensorMap map, rmap;
-  memset(&map, 0, sizeof(map));
-  memset(&rmap, 0, sizeof(rmap));
   const uint64_t rows = a.c.block_table ? (uint64_t)a.c.num_pages * a.c.page_size
                                         : (uint64_t)a.c.batch * a.c.s_max;
-  if (!f8 && (!tma_map_2d(&map, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, DSI_D_QK, 64,
-                          (uint32_t)box) ||
-              !tma_map_2d(&rmap, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, DSI_D_QK,
-                          kRopeHalf, (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_64B)))
-    return cudaErrorInvalidValue;
+  const bool mapped =
+      f8 ? tma_map_2d(&map, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, DSI_D_QK, 128, (uint32_t)box) &&
+               tma_map_2d(&rmap, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, DSI_D_QK, kRopeHalf,
+                          (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_NONE)
+         : tma_map_2d(&map, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, DSI_D_QK, 64,
+                      (uint32_t)box) &&
+               tma_map_2d(&rmap, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, DSI_D_QK,
+                          kRopeHalf, (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (!mapped) return cudaErrorInvalidValue;
   CUtensorMap qmap;
   if (!tma_map_2d(&qmap, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)a.rows * a.H, DSI_D_QK, 64, kM))
     return cudaErrorInvalidValue;
