@@ -70,7 +70,6 @@ constexpr int kAhead = 8;                      // tiles between L2 prefetch and 
 constexpr int kQuarter = 16;
 constexpr int kXRing = 3;
 constexpr int kXBytes = kM * kQuarter * 4;
-constexpr int kPoison = 8;                     // tiles whose poisoned rows are remembered
 
 // FP8 rows: raw tiles of codes land beside the ring and are converted into it
 // by the warps that are the second softmax set of bf16 rows.
@@ -92,8 +91,7 @@ struct Layout {                                // shared memory, bytes
   static constexpr int sums = ref + kM * 4;    // [2][2][128] (reference, sum) of both sets
   static constexpr int bar = sums + 4 * kM * 8;
   static constexpr int bars = 3 * stages + 15 + 4 * kXRing + 2 * kRawStages;
-  static constexpr int poison = bar + bars * 8;
-  static constexpr int misc = poison + kPoison * 8;
+  static constexpr int misc = bar + bars * 8;
   static constexpr int scan = misc + 64;       // 40 ints
   static constexpr int bytes = scan + 160 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory");
@@ -219,9 +217,12 @@ __device__ __forceinline__ bool bf16x8_finite(const uint4& v) {
   return ok;
 }
 
-// Bounded waits whose slow path is out of line: the roles' loops together have
-// to stay small enough for the instruction cache.
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
+// Bounded waits whose slow path is out of line and takes few arguments: the
+// roles' loops together have to stay small enough for the instruction cache.
+__shared__ volatile int s_abort;               // a role has given up: the others follow
+__shared__ int* s_err;                         // device status word
+
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_ns();
   for (uint32_t i = 1;; ++i) {
     uint32_t ok;
@@ -231,25 +232,30 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     if (ok) return true;
     if ((i & 255u) == 0) {
-      if (*abort) return false;
+      if (s_abort) return false;
       if (global_ns() - t0 > kWaitLimitNs) {
-        *abort = 1;
-        report(err, kErrTimeout);
+        s_abort = 1;
+        report(s_err, kErrTimeout);
         return false;
       }
     }
   }
 }
-__device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  return mbar_try_wait(bar, parity) || wait_on(smem_u32(bar), parity, abort, err);
+__device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity) {
+  return mbar_try_wait(bar, parity) || wait_on(smem_u32(bar), parity);
 }
-// The same for whole warps: all lanes proceed or none.
-__device__ __forceinline__ bool wait32(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  return __all_sync(0xffffffffu, wait1(bar, parity, abort, err));
+// Whole warps: all lanes proceed or none.
+__device__ __forceinline__ bool wait32(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait1(bar, parity));
 }
 // ... for phases that the other CTA's arrivals and stores complete
-__device__ __forceinline__ bool wait32_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  return __all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity) || wait_on(smem_u32(bar), parity, abort, err));
+__device__ __forceinline__ bool wait32_cluster(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity) || wait_on(smem_u32(bar), parity));
+}
+
+// Bits 0 .. k-1 of 64.
+__device__ __forceinline__ uint64_t low_bits(int k) {
+  return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1ull;
 }
 
 // Two fp32 operations in one instruction.
@@ -277,8 +283,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 template <bool F8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
-             const __grid_constant__ CUtensorMap qmap, DenseArgs a, Plan plan, Workspace ws,
-             int box) {
+             const __grid_constant__ CUtensorMap qmap, const __grid_constant__ DenseArgs a,
+             const __grid_constant__ Plan plan, Workspace ws, int box) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -302,9 +308,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
   uint64_t* x_empty = x_full + 2 * kXRing;     // [2][kXRing] the peer has read what we sent
   uint64_t* raw_full = x_empty + 2 * kXRing;   // [kRawStages] FP8: codes landed
   uint64_t* raw_empty = raw_full + kRawStages; // [kRawStages] FP8: codes converted
-  unsigned int* poison = reinterpret_cast<unsigned int*>(smem + Y::poison);   // [kPoison][2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Y::misc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Y::misc + 4);
   int* start_s = reinterpret_cast<int*>(smem + Y::misc + 8);                   // group, tile
   int* widest_s = reinterpret_cast<int*>(smem + Y::misc + 16);
   unsigned long long* total_s = reinterpret_cast<unsigned long long*>(smem + Y::misc + 24);
@@ -343,7 +347,8 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     mbar_init(sums_set, 4 * Y::sets);
     mbar_init(o_free, 4 * Y::sets);
     taken_s[0] = taken_s[1] = 0u;
-    *abort_flag = 0;
+    s_abort = 0;
+    s_err = err;
     start_s[0] = plan.groups;
     start_s[1] = 0;
     *widest_s = 0;
@@ -426,12 +431,15 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     int slot = 0, tg = 0;                      // ring slots; tiles
     uint32_t edge_ph = 0;                      // parities of landed[]
     uint32_t issued = 0, issued_edge = 0;      // stages with a copy in flight; into an edge tile
+    const int64_t cache_rows = a.c.block_table ? a.c.num_pages * a.c.page_size : a.c.batch * a.c.s_max;
     bool ok = true;
     // (FP8 rows: warp 0 alone, the tiles' copies go to the raw stages)
+#pragma unroll 1
     while (ok && (!F8 || warp == 0) && next_piece(a, plan, walk, x)) {
+#pragma unroll 1
       for (int i = 0; i < 2; ++i, ++slot) {
         const int stage = slot % kStages;
-        if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u, abort_flag, err))) break;
+        if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u))) break;
         if (lane == 0) {
           if (warp == 0) {
             uint8_t* st = smem + Y::c + stage * kStageBytes;
@@ -449,25 +457,25 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         }
       }
       if (!ok) break;
+      int asked = x.t0;
+#pragma unroll 1
       for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
         const int stage = F8 ? tg % kRawStages : slot % kStages;
         const uint32_t ph = (uint32_t)(F8 ? tg / kRawStages : slot / kStages) & 1u;
         const int p0 = tile_pos(x.grp, t);
         uint8_t* st = smem + (F8 ? Y::raw + stage * kRawBytes : Y::c + stage * kStageBytes);
-        unsigned int* pz = poison + (tg & (kPoison - 1)) * 2;
         const bool whole = F8 || all_see(a, x.grp, p0, kNp);
         if (warp == 0) {
           // the tile by TMA, boxes of `box` rows (a page or a part of one) by 128 bytes of
           // dims; boxes that no token sees are left out
           uint64_t* bar = F8 ? &raw_full[stage] : whole ? &full[stage] : &landed[stage];
-          if (!(ok = wait32(F8 ? &raw_empty[stage] : &empty[stage], ph ^ 1, abort_flag, err))) break;
+          if (!(ok = wait32(F8 ? &raw_empty[stage] : &empty[stage], ph ^ 1))) break;
           constexpr int kBlks = F8 ? 3 : 5;      // blocks of 128 bytes a row, the last the rope half
           const int boxes = kNp / box;
           const int pb = p0 + lane * box;        // lane's box, if it has one
           const bool seen = lane < boxes && pb < x.grp.n_last && (pb + box > x.grp.lo || pb < (int)a.n_sink);
           const int n = __popc(__ballot_sync(0xffffffffu, seen));
           if (lane == 0) {
-            if (F8) pz[0] = pz[1] = 0u;
             mbar_arrive_expect_tx(bar, (uint32_t)(n * box * (F8 ? kRawBytes / kNp : kRowBytes)));
             if (!whole) mbar_arrive(&full[stage]);
             if (!F8) {
@@ -477,6 +485,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
             }
           }
           __syncwarp();
+#pragma unroll 1
           for (int i = lane; i < boxes * kBlks; i += 32) {
             const int bx = i / kBlks, blk = i - bx * kBlks, p = p0 + bx * box;
             if (!(p < x.grp.n_last && (p + box > x.grp.lo || p < (int)a.n_sink))) continue;
@@ -490,67 +499,68 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
               tma_load_2d(st + (F8 ? kRawRope + bx * box * kRopeHalf : kRopeOff + bx * box * kRopeHalf * 2),
                           &rmap, DSI_D_LATENT + (int)rho * kRopeHalf, y, bar);
           }
-          // decode: the caches come from HBM; a tile is asked for into L2 kAhead tiles
-          // before its copy, so that the copy holds its stage only as long as L2 takes
+          // decode: the caches come from HBM; tiles are asked for into L2 kAhead tiles
+          // before their copies (two a step until that far ahead, each CTA every other
+          // tile, whole rows), so that a copy holds its stage only as long as L2 takes
           if (a.decode) {
-            for (int u = t == x.t0 ? t + 1 : t + kAhead; u < min(x.t1, t + kAhead + 1); ++u) {
-              const int pu = tile_pos(x.grp, u);
-              for (int i = lane; i < boxes * kBlks; i += 32) {
-                const int bx = i / kBlks, blk = i - bx * kBlks, p = pu + bx * box;
-                if (!(p < x.grp.n_last && (p + box > x.grp.lo || p < (int)a.n_sink))) continue;
+            asked = max(asked, t + 2);
+            for (int n2 = 0; n2 < 2 && asked < min(x.t1, t + kAhead); ++n2, ++asked) {
+              const int p = tile_pos(x.grp, asked) + lane * box;
+              if ((asked & 1) == (int)rho && lane < boxes && p < x.grp.n_last &&
+                  (p + box > x.grp.lo || p < (int)a.n_sink)) {
                 const int row = row_of(a.c, x.grp.b, p, err);
-                if (row < 0) continue;
-                if (blk < kBlks - 1) tma_prefetch_2d(&lmap, (int)rho * 256 + blk * (256 / (kBlks - 1)), row);
-                else tma_prefetch_2d(&rmap, DSI_D_LATENT + (int)rho * kRopeHalf, row);
+                constexpr int kPitch = F8 ? DSI_D_QK : 2 * DSI_D_QK;
+                if (row >= 0 && (int64_t)row + box <= cache_rows)
+                  bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(a.c.latent) + (int64_t)row * kPitch,
+                                   (uint32_t)(box * kPitch));
               }
             }
           }
           __syncwarp();
         } else {
           // bf16 rows, warp 1: passes a whole tile on and cleans one at an edge first
-          unsigned int z[2] = {0u, 0u};
           if (!whole) {
             // rows that no token sees become zeros (weight 0 times what they hold must
-            // be 0); a row that only some tokens see is searched for NaN and infinities:
-            // it is taken out and remembered, and its logits become NaN where it is seen
-            if (!(ok = wait32(&landed[stage], (edge_ph >> stage) & 1u, abort_flag, err))) break;
+            // be 0); a row that only some tokens see and that holds NaN or an infinity
+            // becomes zeros as a value and NaN in its rope dims: its logits are NaN, for
+            // those that see it
+            if (!(ok = wait32(&landed[stage], (edge_ph >> stage) & 1u))) break;
             edge_ph ^= 1u << stage;
+#pragma unroll 1
+            for (int rr = lane; rr < kNp; rr += 32) {        // a lane clears whole rows
+              const bool none = !any_sees(a, x.grp, p0 + rr);
+              bool bad = false;
+              if (!none && !all_see(a, x.grp, p0 + rr, 1)) {
+#pragma unroll 1
+                for (int u = 0; u < 36; ++u)
+                  bad |= !bf16x8_finite(*reinterpret_cast<const uint4*>(
+                      u < 32 ? st + (u >> 3) * kBlockBytes + sw128_offset(rr, u & 7)
+                             : st + kRopeOff + sw64_offset(rr, u & 3)));
+              }
+              if (none || bad) {
+#pragma unroll 4
+                for (int u = 0; u < 32; ++u)
+                  *reinterpret_cast<uint4*>(st + (u >> 3) * kBlockBytes + sw128_offset(rr, u & 7)) =
+                      make_uint4(0, 0, 0, 0);
+                const uint32_t y = bad ? 0x7FFF7FFFu : 0u;
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const int p = p0 + w * 32 + lane;
-              const unsigned int none = __ballot_sync(0xffffffffu, !any_sees(a, x.grp, p));
-              unsigned int some = ~none & ~__ballot_sync(0xffffffffu, all_see(a, x.grp, p, 1));
-              for (unsigned int todo = none | some; todo; todo &= todo - 1) {
-                const int bit = __ffs(todo) - 1, rr = w * 32 + bit;
-                uint4* at = reinterpret_cast<uint4*>(st + (lane >> 3) * kBlockBytes + sw128_offset(rr, lane & 7));
-                uint4* rope = reinterpret_cast<uint4*>(st + kRopeOff + sw64_offset(rr, lane & 3));
-                bool clear = (none >> bit) & 1u;
-                if (!clear) {
-                  clear = __any_sync(0xffffffffu, !(bf16x8_finite(*at) && bf16x8_finite(*rope)));
-                  if (clear) z[w] |= 1u << bit;
-                }
-                if (clear) {
-                  *at = make_uint4(0, 0, 0, 0);
-                  if (lane < 4) *rope = make_uint4(0, 0, 0, 0);
-                }
+                for (int u = 0; u < 4; ++u)
+                  *reinterpret_cast<uint4*>(st + kRopeOff + sw64_offset(rr, u)) = make_uint4(y, y, y, y);
               }
             }
             fence_proxy_async_smem();   // the tensor core reads the stage through the async proxy
             __syncwarp();
-          } else if (!(ok = wait32(&empty[stage], ph ^ 1, abort_flag, err))) {
+          } else if (!(ok = wait32(&empty[stage], ph ^ 1))) {
             break;
           }
-          if (lane == 0) {
-            pz[0] = z[0];
-            pz[1] = z[1];
-            mbar_arrive(&full[stage]);
-          }
+          if (lane == 0) mbar_arrive(&full[stage]);
         }
       }
     }
     // never leave the CTA with a copy still landing in shared memory
-    if (warp == 0 && lane == 0 && *abort_flag) {
+    if (warp == 0 && lane == 0 && s_abort) {
       volatile int no_abort = 0;    // the drain is bounded by time only
+#pragma unroll 1
       for (int s = 0; s < kStages; ++s) {
         if (!((issued >> s) & 1u)) continue;
         int last = slot;            // the last slot that used stage s
@@ -581,14 +591,16 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
                      : make_float2(__ldg(a.latent_scale + (int64_t)row * 5 + s0),
                                    __ldg(a.latent_scale + (int64_t)row * 5 + 4));
     };
+#pragma unroll 1
     while (ok && next_piece(a, plan, walk, x)) {
       // (the query slots are waited for too: a skipped phase could not be told apart)
       for (int i = 0; i < 2 && ok; ++i, ++slot)
-        ok = wait32(&empty[slot % kStages], ((uint32_t)(slot / kStages) & 1u) ^ 1u, abort_flag, err);
+        ok = wait32(&empty[slot % kStages], ((uint32_t)(slot / kStages) & 1u) ^ 1u);
       if (!ok) break;
       int row_next = lookup(x.t0);
       float2 sc = scales(row_next);
       row_next = lookup(x.t0 + 1);
+#pragma unroll 1
       for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
         const int stage = slot % kStages, rs = tg % kRawStages, p = tile_pos(x.grp, t) + rr;
         const float2 sc_next = scales(row_next);
@@ -596,11 +608,12 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         const bool seen = any_sees(a, x.grp, p), partly = seen && !all_see(a, x.grp, p, 1);
         const uint8_t* raw = smem + Y::raw + rs * kRawBytes;
         uint8_t* st = smem + Y::c + stage * kStageBytes;
-        if (!(ok = wait32(&raw_full[rs], (uint32_t)(tg / kRawStages) & 1u, abort_flag, err))) break;
-        if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u, abort_flag, err))) break;
+        if (!(ok = wait32(&raw_full[rs], (uint32_t)(tg / kRawStages) & 1u))) break;
+        if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u))) break;
+        bool bad = false;
 #pragma unroll
         for (int u = 0; u < 9; ++u) {
-          const bool rope = u == 8;
+          const bool rope = u == 8;              // (last: it takes the row's NaN)
           uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
           if (seen) {
             const uint4 v = *reinterpret_cast<const uint4*>(
@@ -609,9 +622,10 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           }
           // (edges: as for bf16 rows)
           if (partly && !(bf16x8_finite(lo) && bf16x8_finite(hi))) {
+            bad = true;
             lo = hi = make_uint4(0, 0, 0, 0);
-            atomicOr(poison + (tg & (kPoison - 1)) * 2 + (rr >> 5), 1u << (rr & 31));
           }
+          if (rope && bad) lo = hi = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
           uint8_t* blk = rope ? st + kRopeOff : st + (hh * 2 + (u >> 2)) * kBlockBytes;
           const uint32_t ch = rope ? (uint32_t)hh * 2 : (uint32_t)(u & 3) * 2;
           *reinterpret_cast<uint4*>(blk + (rope ? sw64_offset(rr, ch) : sw128_offset(rr, ch))) = lo;
@@ -633,14 +647,16 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       int slot = 0, tg = 0, pieces = 0;
       bool ok = true;
       const uint64_t qr = desc_sw64(smem_u32(smem + Y::qr));
+#pragma unroll 1
       while (ok && next_piece(a, plan, walk, x)) {
-        if (!(ok = wait1(q_ready, (uint32_t)pieces & 1u, abort_flag, err))) break;
+        if (!(ok = wait1(q_ready, (uint32_t)pieces & 1u))) break;
         ++pieces;
         slot += 2;                               // the query slice
+#pragma unroll 1
         for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
           const int stage = slot % kStages, sb = tg & 1;
-          if (!(ok = wait1(&full[stage], (uint32_t)(slot / kStages) & 1u, abort_flag, err))) break;
-          if (!(ok = wait1(&s_empty[sb], ((uint32_t)(tg >> 1) & 1u) ^ 1u, abort_flag, err))) break;
+          if (!(ok = wait1(&full[stage], (uint32_t)(slot / kStages) & 1u))) break;
+          if (!(ok = wait1(&s_empty[sb], ((uint32_t)(tg >> 1) & 1u) ^ 1u))) break;
           tc_fence_after();
           const uint32_t t_s = tmem + TM_S + sb * kNp;
           const uint32_t base = smem_u32(smem + Y::c + stage * kStageBytes);
@@ -666,11 +682,13 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       int slot = 0, tg = 0;
       bool ok = true;
       const uint64_t pd = desc_sw128(smem_u32(smem + Y::p));
+#pragma unroll 1
       while (ok && next_piece(a, plan, walk, x)) {
         slot += 2;                               // the query slice
+#pragma unroll 1
         for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
           const int stage = slot % kStages;
-          if (!(ok = wait1(p_full, (uint32_t)tg & 1u, abort_flag, err))) break;
+          if (!(ok = wait1(p_full, (uint32_t)tg & 1u))) break;
           tc_fence_after();
           const uint64_t vd = desc_sw128_mn(smem_u32(smem + Y::c + stage * kStageBytes), kBlockBytes);
 #pragma unroll
@@ -696,6 +714,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     Piece x;
     int slot = 0, tg = 0;
     bool ok = true;
+#pragma unroll 1
     while (ok && next_piece(a, plan, walk, x)) {
       // The query slice: the rope half by plain loads (begun first), the four 64-dim
       // blocks out of the two ring slots that the producers filled ahead.  The
@@ -707,9 +726,10 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         rope[i] = live ? __ldg(reinterpret_cast<const uint4*>(
                              a.q + ((int64_t)x.grp.row0 * a.H + m) * DSI_D_QK + DSI_D_LATENT + rho * kRopeHalf) + i)
                        : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
       for (int half = 0; half < 2; ++half, ++slot) {
         const int stage = slot % kStages;
-        if (!(ok = wait32(&full[stage], (uint32_t)(slot / kStages) & 1u, abort_flag, err))) break;
+        if (!(ok = wait32(&full[stage], (uint32_t)(slot / kStages) & 1u))) break;
 #pragma unroll
         for (int bx = 0; bx < 2; ++bx) {
           const uint8_t* src = smem + Y::c + stage * kStageBytes + bx * kM * 128;
@@ -742,28 +762,23 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(q_ready);
+#pragma unroll 1
       for (int t = x.t0; t < x.t1; ++t, ++tg) {
         const int sb = tg & 1;
-        if (!(ok = wait32(&s_full[sb], (uint32_t)(tg >> 1) & 1u, abort_flag, err))) break;
+        if (!(ok = wait32(&s_full[sb], (uint32_t)(tg >> 1) & 1u))) break;
         tc_fence_after();
         float v[kNp];
         tmem_ld32(tmem + lane_base + TM_S + sb * kNp, v);
         tmem_ld32(tmem + lane_base + TM_S + sb * kNp + 32, v + 32);
-        const unsigned int z0 = poison[(tg & (kPoison - 1)) * 2], z1 = poison[(tg & (kPoison - 1)) * 2 + 1];
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(&s_empty[sb]);
-        if (__builtin_expect(z0 | z1, 0)) {
-#pragma unroll
-          for (int j = 0; j < kNp; ++j)
-            v[j] = ((j < 32 ? z0 >> j : z1 >> (j - 32)) & 1u) ? __int_as_float(0x7fffffff) : v[j];
-        }
         // each quarter once the peer has read what was in its buffer
         const int q0 = (tg >> 1) * 4;            // quarters sent to this set so far
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int buf = sb * kXRing + (q0 + i) % kXRing;
-          if (!(ok = wait32_cluster(&x_empty[buf], ((uint32_t)((q0 + i) / kXRing) & 1u) ^ 1u, abort_flag, err))) break;
+          if (!(ok = wait32_cluster(&x_empty[buf], ((uint32_t)((q0 + i) / kXRing) & 1u) ^ 1u))) break;
 #pragma unroll
           for (int g4 = 0; g4 < kQuarter / 4; ++g4) {
             const int j = i * kQuarter + 4 * g4;
@@ -792,22 +807,23 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     Piece x;
     int tg = 0, pieces = 0;
     bool ok = true;
+#pragma unroll 1
     while (ok && next_piece(a, plan, walk, x)) {
       const int tok = min(m / a.H, x.grp.nt - 1);
       const int n_row = tok == 0 ? x.grp.n_first
                                  : (int)visible_len(a.c, x.grp.row0 + tok, a.decode, a.q_offset);
       const int lo_row = n_row - (int)a.window;
       float m_mine = -INFINITY, l_mine = 0.f;
+#pragma unroll 1
       for (int t = x.t0; t < x.t1; ++t, ++tg) {
         if (Y::sets == 2 && (tg & 1) != set) continue;
         const int sb = tg & 1;
         const int p0 = tile_pos(x.grp, t);
-        if (!(ok = wait32(&s_full[sb], (uint32_t)(tg >> 1) & 1u, abort_flag, err))) break;
+        if (!(ok = wait32(&s_full[sb], (uint32_t)(tg >> 1) & 1u))) break;
         tc_fence_after();
         float v[kNp];
         tmem_ld32(tmem + lane_base + TM_S + sb * kNp, v);
         tmem_ld32(tmem + lane_base + TM_S + sb * kNp + 32, v + 32);
-        const unsigned int z0 = poison[(tg & (kPoison - 1)) * 2], z1 = poison[(tg & (kPoison - 1)) * 2 + 1];
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(&s_empty[sb]);
@@ -816,7 +832,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int buf = sb * kXRing + (q0 + i) % kXRing;
-          if (!(ok = wait32_cluster(&x_full[buf], (uint32_t)((q0 + i) / kXRing) & 1u, abort_flag, err))) break;
+          if (!(ok = wait32_cluster(&x_full[buf], (uint32_t)((q0 + i) / kXRing) & 1u))) break;
 #pragma unroll
           for (int g4 = 0; g4 < kQuarter / 4; ++g4) {
             const int j = i * kQuarter + 4 * g4;
@@ -832,14 +848,12 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           }
         }
         if (!ok) break;
-        // NaN for poisoned and -inf for masked positions
+        // masked positions: -inf
         if (__builtin_expect(!all_see(a, x.grp, p0, kNp), 0)) {
-          const int end = n_row - p0, from = lo_row - p0, sinks = (int)a.n_sink - p0;
+          const uint64_t see = low_bits(n_row - p0) & (~low_bits(lo_row - p0) | low_bits((int)a.n_sink - p0));
+          const uint32_t half[2] = {(uint32_t)see, (uint32_t)(see >> 32)};
 #pragma unroll
-          for (int j = 0; j < kNp; ++j) {
-            v[j] = ((j < 32 ? z0 >> j : z1 >> (j - 32)) & 1u) ? __int_as_float(0x7fffffff) : v[j];
-            v[j] = (j < end) & ((j >= from) | (j < sinks)) ? v[j] : -INFINITY;
-          }
+          for (int j = 0; j < kNp; ++j) v[j] = (half[j >> 5] >> (j & 31)) & 1u ? v[j] : -INFINITY;
         }
         float mx[4];
 #pragma unroll
@@ -856,14 +870,14 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         // this tile's maximum exceeds it by far; what is in the accumulator moves
         // with it
         if (Y::sets == 2 && tg > 0 &&
-            !(ok = wait32(&ref_set[quarter], (uint32_t)(tg - 1) & 1u, abort_flag, err))) break;
+            !(ok = wait32(&ref_set[quarter], (uint32_t)(tg - 1) & 1u))) break;
         const float m_prev = t == x.t0 ? -INFINITY : Y::sets == 2 ? ref_s[0] : m_mine;
         float m_ref = m_prev, alpha = 1.f;
         bool rescale = false;
         if (m_prev == -INFINITY) {
           m_ref = tmax;                        // nothing in the accumulator yet
         } else if (tmax > m_prev + kRescaleLog2) {
-          alpha = exp2f(m_prev - tmax);
+          alpha = ex2_approx(m_prev - tmax);
           m_ref = tmax;
           rescale = true;
         }
@@ -888,14 +902,14 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           pk[j] = *reinterpret_cast<const uint32_t*>(&p2);
         }
         const float2 tot = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
-        if (m_mine != m_ref) l_mine *= m_mine == -INFINITY ? 0.f : exp2f(m_mine - m_ref);
+        if (m_mine != m_ref) l_mine *= m_mine == -INFINITY ? 0.f : ex2_approx(m_mine - m_ref);
         m_mine = m_ref;
         l_mine += tot.x + tot.y;
         // the P tile is free, and P.V(t-1) has landed in the accumulator; a piece's
         // first P also waits until both sets have read out the output before
-        if (tg > 0 && !(ok = wait32(&p_empty[sb ^ 1], (uint32_t)((tg - 1) >> 1) & 1u, abort_flag, err))) break;
+        if (tg > 0 && !(ok = wait32(&p_empty[sb ^ 1], (uint32_t)((tg - 1) >> 1) & 1u))) break;
         if (t == x.t0 && pieces > 0 &&
-            !(ok = wait32(o_free, (uint32_t)(pieces - 1) & 1u, abort_flag, err))) break;
+            !(ok = wait32(o_free, (uint32_t)(pieces - 1) & 1u))) break;
         tc_fence_after();
 #pragma unroll
         for (int u = 0; u < 8; ++u)
@@ -928,13 +942,13 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         sums[set * kM].y = l_mine;
         __syncwarp();
         if (lane == 0) mbar_arrive(sums_set);
-        if (!(ok = wait32(sums_set, (uint32_t)pieces & 1u, abort_flag, err))) break;
+        if (!(ok = wait32(sums_set, (uint32_t)pieces & 1u))) break;
         const float2 other = make_float2(sums[(set ^ 1) * kM].x, sums[(set ^ 1) * kM].y);
         m_ref = fmaxf(m_mine, other.x);
         l_sum = m_mine == -INFINITY ? 0.f : l_mine * exp2f(m_mine - m_ref);
         if (other.x != -INFINITY) l_sum += other.y * exp2f(other.x - m_ref);
       }
-      if (!(ok = wait32(o_done, (uint32_t)pieces & 1u, abort_flag, err))) break;
+      if (!(ok = wait32(o_done, (uint32_t)pieces & 1u))) break;
       ++pieces;
       tc_fence_after();
       // ---- the piece's output: this CTA's 256 dims, 128 of them by each set ------
