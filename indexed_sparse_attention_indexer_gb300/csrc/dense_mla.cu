@@ -1018,61 +1018,78 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
   cluster_sync();      // the peer may still arrive on / write into this CTA until here
 }
 
-// Joins the pieces of a split group: block (k, m) takes row m of the group that
-// cluster k started and did not finish; its other pieces are the first ones of
-// clusters k + 1, k + 2, ... up to the one that finishes it.
-__global__ void __launch_bounds__(128)
-dense_mla_join(DenseArgs a, Plan plan, Workspace ws, int clusters) {
+// Joins the pieces of split groups.  A group is split when a cluster starts it
+// and does not finish it; its other pieces are the first ones of the next
+// clusters, up to the first that finishes one.  Every block finds the split
+// groups in the clusters' records (none: it leaves at once) and takes every
+// gridDim.x-th of their rows.
+constexpr int kJoinThreads = 128;
+static_assert(kMaxClusters <= kJoinThreads && kJoinThreads * 4 == DSI_D_LATENT, "a thread a record, four dims a thread");
+__global__ void __launch_bounds__(kJoinThreads)
+dense_mla_join(DenseArgs a, Plan plan, Workspace ws, int clusters, int rows) {
   __shared__ float weight[kMaxClusters];
   __shared__ float red[2][4];
-  __shared__ int end_s;
-  const int k = blockIdx.x, m = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ unsigned int starts_s[4], ends_s[4];
+  __shared__ int owner_s[kMaxClusters], group_s[kMaxClusters];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_wait();     // the pieces come from the kernel launched just before
   grid_dep_launch();
-  const int g = ws.rec[k].starts;
-  if (g < 0) return;
-  const int b = g / plan.per_seq, t0 = (g - b * plan.per_seq) * plan.tokens;
-  if (m >= min(plan.tokens, a.T - t0) * a.H) return;
-  if (tid == 0) end_s = clusters;
+  Record rec = {-1, -1, 0, 0};
+  if (tid < clusters) rec = ws.rec[tid];
+  const unsigned int starts = __ballot_sync(0xffffffffu, rec.starts >= 0);
+  const unsigned int ends = __ballot_sync(0xffffffffu, rec.finishes != 0);
+  if (lane == 0) { starts_s[warp] = starts; ends_s[warp] = ends; }
   __syncthreads();
-  const int j = k + 1 + tid;
-  if (j < clusters) {
-    const Record r = ws.rec[j];
-    if (r.continues == g && r.finishes) atomicMin(&end_s, j);
+  int at = __popc(starts & ((1u << lane) - 1u)), owners = 0;
+  for (int w = 0; w < 4; ++w) {
+    if (w < warp) at += __popc(starts_s[w]);
+    owners += __popc(starts_s[w]);
   }
-  __syncthreads();
-  const int pieces = min(end_s, clusters - 1) - k + 1;      // <= kMaxClusters
-  // piece 0: the last of cluster k; piece i: the first of cluster k + i
-  float2 ml = make_float2(-INFINITY, 0.f);
-  if (tid < pieces) ml = ws.ml[(2 * (k + tid) + (tid == 0 ? 1 : 0)) * kM + m];
-  float top = ml.x;
+  if (owners == 0) return;
+  if (rec.starts >= 0) { owner_s[at] = tid; group_s[at] = rec.starts; }
+  for (int i = blockIdx.x; i < owners * rows; i += gridDim.x) {
+    __syncthreads();   // the lists are complete; the row before is done with the weights
+    const int oi = i / rows, m = i - oi * rows, k = owner_s[oi], g = group_s[oi];
+    const int b = g / plan.per_seq, t0 = (g - b * plan.per_seq) * plan.tokens;
+    if (m >= min(plan.tokens, a.T - t0) * a.H) continue;
+    int end = clusters - 1;                      // the cluster that finishes the group
+    for (int w = 3; w >= 0; --w) {
+      const unsigned int later = w * 32 > k ? ends_s[w] : w * 32 + 31 <= k ? 0u : ends_s[w] & ~((2u << (k & 31)) - 1u);
+      if (later) end = w * 32 + __ffs(later) - 1;
+    }
+    const int pieces = end - k + 1;              // <= kMaxClusters
+    // piece 0: the last of cluster k; piece i: the first of cluster k + i
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (tid < pieces) ml = ws.ml[(2 * (k + tid) + (tid == 0 ? 1 : 0)) * kM + m];
+    float top = ml.x;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) red[0][warp] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-  const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-  weight[tid] = f;
-  float sum = f * ml.y;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) red[0][warp] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+    weight[tid] = f;
+    float sum = f * ml.y;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) red[1][warp] = sum;
-  __syncthreads();
-  sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) red[1][warp] = sum;
+    __syncthreads();
+    sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int i = 0; i < pieces; ++i) {
-    const int64_t slot = 2 * (k + i) + (i == 0 ? 1 : 0);
-    const float4 v = reinterpret_cast<const float4*>(ws.o + (slot * kM + m) * DSI_D_LATENT)[tid];
-    const float w = weight[i];
-    o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+    for (int j = 0; j < pieces; ++j) {
+      const int64_t slot = 2 * (k + j) + (j == 0 ? 1 : 0);
+      const float4 v = reinterpret_cast<const float4*>(ws.o + (slot * kM + m) * DSI_D_LATENT)[tid];
+      const float w = weight[j];
+      o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t row = ((int64_t)b * a.T + t0) * a.H + m;
+    __align__(8) bf16 o4[4] = {__float2bfloat16(o.x * inv), __float2bfloat16(o.y * inv),
+                               __float2bfloat16(o.z * inv), __float2bfloat16(o.w * inv)};
+    *reinterpret_cast<uint2*>(a.out + row * DSI_D_LATENT + tid * 4) = *reinterpret_cast<const uint2*>(o4);
+    if (a.lse && tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) / kLog2e;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t row = ((int64_t)b * a.T + t0) * a.H + m;
-  __align__(8) bf16 o4[4] = {__float2bfloat16(o.x * inv), __float2bfloat16(o.y * inv),
-                             __float2bfloat16(o.z * inv), __float2bfloat16(o.w * inv)};
-  *reinterpret_cast<uint2*>(a.out + row * DSI_D_LATENT + tid * 4) = *reinterpret_cast<const uint2*>(o4);
-  if (a.lse && tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) / kLog2e;
 }
 
 // Two-CTA clusters that fit on the current device at once (queried once per
@@ -1169,8 +1186,11 @@ cudaError_t launch_dense_mla(const DenseArgs& a, cudaStream_t st) {
   cudaError_t e = f8 ? launch<true>(map, rmap, qmap, a, plan, ws, box, clusters, st)
                      : launch<false>(map, rmap, qmap, a, plan, ws, box, clusters, st);
   if (e != cudaSuccess || !plan.split) return e;
-  e = launch_overlapped(dense_mla_join, dim3((unsigned)clusters, (unsigned)(plan.tokens * a.H)), dim3(128),
-                        0, st, a, plan, ws, clusters);
+  // enough blocks for one resident wave: a call without split groups pays little
+  const int64_t rows_at_most = (int64_t)clusters * plan.tokens * a.H;
+  const int64_t wave = 16 * clusters;
+  e = launch_overlapped(dense_mla_join, dim3((unsigned)(rows_at_most < wave ? rows_at_most : wave)),
+                        dim3(kJoinThreads), 0, st, a, plan, ws, clusters, plan.tokens * a.H);
   note_launch();
   return e;
 }
