@@ -473,7 +473,8 @@ size_t dsi_dense_mla_workspace_size(int32_t rows, int32_t n_heads);
  *                   rounding rules of dsi_mxfp8_quantize on z
  *   DSI_FP8_E4M3    E4M3 codes [out_rows, n_heads, d] and fp32 scales
  *                   [out_rows, n_heads, ceil(d / 128)], packed, one per tile of
- *                   128 dims: the rules of dsi_latent_fp8_append on z
+ *                   128 dims: scale = (largest |z| of the tile) / 448, codes
+ *                   E4M3 of z * (1 / scale) in fp32 (0 for an all-zero tile)
  * The quantised forms start from the fp32 z; a bf16 result that is quantised
  * by a second call is rounded twice and can differ in single codes.
  * Row i goes to out row dst_rows[i] (i when dst_rows is NULL).  A negative

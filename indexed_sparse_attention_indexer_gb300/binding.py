@@ -7,7 +7,6 @@ fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -208,11 +207,19 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _on(device: torch.device):
-    """The tensors' device made current for a call (kernels launch on the current device)."""
-    if device.type != "cuda" or device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _raw_stream(stream, device: torch.device) -> int:
+    """The cudaStream_t of ``stream``, or of the device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)   # no stream object is made
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _launch(fn, device: torch.device, stream, *args) -> int:
+    """A library call with the tensors' device current (kernels launch on the current device)."""
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _raw_stream(stream, device))
+    with torch.cuda.device(device):
+        return fn(*args, _raw_stream(stream, device))
 
 
 class Heads:
@@ -290,9 +297,10 @@ class Heads:
         s.out_rows = rows
         self.x, self.weight, self.bias, self.out = x, weight, bias, out
         self.out_scale, self.dst_rows, self.n, self.d, self.struct = out_scale, dst_rows, n, d, s
+        self.device, self._ref = x.device, ctypes.byref(s)
 
     def ref(self):
-        return ctypes.byref(self.struct)
+        return self._ref
 
 
 # ----------------------------------------------------------------------------
@@ -374,39 +382,44 @@ def dense_mla_workspace_size(rows: int, n_heads: int, checked: bool = False) -> 
 
 def _dense(fn: str, q, cache: Cache, args, rows: int, scale, out, lse, want_lse, workspace, stream,
            checked):
-    """Checks and buffers shared by the dense and window calls; the new buffers belong to the
-    stream that the kernels run on."""
+    """Checks and buffers shared by the dense and window calls; new buffers belong to the stream
+    that the kernels run on."""
     lib = load(checked)
-    _need(q.dtype == torch.bfloat16 and q.dim() == 3 and q.is_contiguous() and int(q.shape[2]) == D_QK,
-          f"q is a contiguous bf16 [rows, heads, {D_QK}] tensor")
-    _need(cache.latent is not None and cache.latent.device == q.device, "the cache has no latent rows on q's device")
-    n, H = int(q.shape[0]), int(q.shape[1])
-    _need(n == rows, f"q has {n} rows, the call {rows}")
-    if out is not None:
-        _need(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == (n, H, D_LATENT)
-              and out.device == q.device, f"out is a contiguous bf16 [rows, heads, {D_LATENT}] tensor")
-    if lse is not None:
-        _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (n, H)
-              and lse.device == q.device, "lse is a contiguous fp32 [rows, heads] tensor")
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous() or q.shape[2] != D_QK:
+        raise ValueError(f"q is a contiguous bf16 [rows, heads, {D_QK}] tensor")
+    device = q.device
+    if cache.latent is None or cache.latent.device != device:
+        raise ValueError("the cache has no latent rows on q's device")
+    n, H, _ = q.shape
+    if n != rows:
+        raise ValueError(f"q has {n} rows, the call {rows}")
+    if out is not None and (out.dtype != torch.bfloat16 or out.shape != (n, H, D_LATENT) or
+                            not out.is_contiguous() or out.device != device):
+        raise ValueError(f"out is a contiguous bf16 [rows, heads, {D_LATENT}] tensor")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, H) or
+                            not lse.is_contiguous() or lse.device != device):
+        raise ValueError("lse is a contiguous fp32 [rows, heads] tensor")
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError("workspace is a contiguous tensor on q's device")
     if n == 0 or H == 0:
         return (out if out is not None else q.new_empty((n, H, D_LATENT)),
                 lse if lse is not None or not want_lse else q.new_empty((n, H), dtype=torch.float32))
-    with _on(q.device):
-        if out is None or workspace is None or (lse is None and want_lse):
-            on = stream
-            if on is not None and not hasattr(on, "cuda_stream"):
-                on = torch.cuda.ExternalStream(int(on), device=q.device)
-            with torch.cuda.stream(on):
-                if workspace is None:
-                    workspace = alloc_workspace(lib.dsi_dense_mla_workspace_size(n, H), q.device)
-                if out is None:
-                    out = torch.empty((n, H, D_LATENT), dtype=torch.bfloat16, device=q.device)
-                if lse is None and want_lse:
-                    lse = torch.empty((n, H), dtype=torch.float32, device=q.device)
-        st = getattr(lib, fn)(q.data_ptr(), cache.ref(), *args, scale, out.data_ptr(),
-                              lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(lib, fn, st)
+    if out is None or workspace is None or (lse is None and want_lse):
+        on = stream
+        if on is not None and not hasattr(on, "cuda_stream"):
+            on = torch.cuda.ExternalStream(int(on), device=device)
+        with torch.cuda.device(device), torch.cuda.stream(on):
+            if workspace is None:
+                workspace = alloc_workspace(lib.dsi_dense_mla_workspace_size(n, H), device)
+            if out is None:
+                out = torch.empty((n, H, D_LATENT), dtype=torch.bfloat16, device=device)
+            if lse is None and want_lse:
+                lse = torch.empty((n, H), dtype=torch.float32, device=device)
+    st = _launch(getattr(lib, fn), device, stream, q.data_ptr(), cache.ref(), *args, scale,
+                 out.data_ptr(), lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size())
+    if st:
+        raise DsiError(fn, st, lib)
     return out, lse
 
 
@@ -457,23 +470,23 @@ def norm_rope(queries: Optional[Heads], keys: Optional[Heads], table, positions,
     lib = load(checked)
     side = queries if queries is not None else keys
     _need(side is not None, "queries, keys or both")
-    _need(queries is None or keys is None or
-          (queries.n, queries.d, queries.x.device) == (keys.n, keys.d, keys.x.device),
-          "queries and keys have the same rows, dims and device")
-    _need(table.dtype == torch.float32 and table.dim() == 2 and table.is_contiguous(),
-          "table is a contiguous fp32 [positions, rope_dim] tensor")
-    _need(positions.dtype == torch.int64 and positions.is_contiguous() and positions.numel() == side.n,
-          "positions is an int64 [n] tensor")
-    _need(table.device == side.x.device and positions.device == side.x.device,
-          "all tensors must be on one device")
-    if side.n:
-        with _on(side.x.device):
-            st = lib.dsi_norm_rope(queries.ref() if queries is not None else None,
-                                   keys.ref() if keys is not None else None, side.n, side.d, eps,
-                                   table.data_ptr(), table.shape[0], positions.data_ptr(),
-                                   int(rope_offset), table.shape[1], int(bool(interleaved)),
-                                   _stream(stream))
-        _check(lib, "dsi_norm_rope", st)
+    n, device = side.n, side.device
+    if queries is not None and keys is not None and (n != keys.n or side.d != keys.d or device != keys.device):
+        raise ValueError("queries and keys have the same rows, dims and device")
+    if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table is a contiguous fp32 [positions, rope_dim] tensor")
+    if positions.dtype != torch.int64 or positions.numel() != n or not positions.is_contiguous():
+        raise ValueError("positions is an int64 [n] tensor")
+    if table.device != device or positions.device != device:
+        raise ValueError("all tensors must be on one device")
+    if n:
+        rows, rope_dim = table.shape
+        st = _launch(lib.dsi_norm_rope, device, stream,
+                     queries._ref if queries is not None else None, keys._ref if keys is not None else None,
+                     n, side.d, eps, table.data_ptr(), rows, positions.data_ptr(), rope_offset, rope_dim,
+                     bool(interleaved))
+        if st:
+            raise DsiError("dsi_norm_rope", st, lib)
     return (queries.out if queries is not None else None), (keys.out if keys is not None else None)
 
 

@@ -1092,19 +1092,16 @@ dense_mla_join(DenseArgs a, Plan plan, Workspace ws, int clusters, int rows) {
   }
 }
 
-// Two-CTA clusters that fit on the current device at once (queried once per
-// device and form); half the SMs when the query fails (no device).
+// Two-CTA clusters that fit on the current device at once, queried once per
+// device and form, after the kernel has been given its shared memory there; 0
+// without a device.
 template <bool F8>
 int cluster_slots() {
   static std::atomic<int> cached[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) { cudaGetLastError(); return 76; }
-  int v = cached[dev].load(std::memory_order_relaxed);
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) { cudaGetLastError(); return 0; }
+  v = cached[dev].load(std::memory_order_relaxed);
   if (v) return v;
-  if (cudaFuncSetAttribute(dense_mla_tc<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<F8>::bytes) != cudaSuccess) {
-    cudaGetLastError();
-    return 76;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(kThreads);
@@ -1115,9 +1112,11 @@ int cluster_slots() {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&v, dense_mla_tc<F8>, &cfg) != cudaSuccess || v < 1) {
+  if (cudaFuncSetAttribute(dense_mla_tc<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Layout<F8>::bytes) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&v, dense_mla_tc<F8>, &cfg) != cudaSuccess || v < 1) {
     cudaGetLastError();
-    return 76;
+    return 0;
   }
   v = v < kMaxClusters ? v : kMaxClusters;
   cached[dev].store(v, std::memory_order_relaxed);
@@ -1127,13 +1126,12 @@ int cluster_slots() {
 constexpr size_t kSlotBytes = (size_t)kM * (DSI_D_LATENT * sizeof(float) + sizeof(float2));
 
 template <bool F8>
-cudaError_t launch(const CUtensorMap& map, const CUtensorMap& rmap, const CUtensorMap& qmap, const DenseArgs& a, const Plan& plan, const Workspace& ws,
-                   int box, int clusters, cudaStream_t st) {
-  // per device: the current one's attribute, whatever was set before
-  cudaError_t e = cudaFuncSetAttribute(dense_mla_tc<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<F8>::bytes);
-  if (e != cudaSuccess) return e;
-  e = launch_overlapped(dense_mla_tc<F8>, dim3(2u * (unsigned)clusters), dim3(kThreads), Layout<F8>::bytes, st,
-                        map, rmap, qmap, a, plan, ws, box);
+cudaError_t launch(const CUtensorMap& map, const CUtensorMap& rmap, const CUtensorMap& qmap,
+                   const DenseArgs& a, const Plan& plan, const Workspace& ws, int box, int clusters,
+                   cudaStream_t st) {
+  const cudaError_t e =
+      launch_overlapped(dense_mla_tc<F8>, dim3(2u * (unsigned)clusters), dim3(kThreads),
+                        Layout<F8>::bytes, st, map, rmap, qmap, a, plan, ws, box);
   note_launch();
   return e;
 }
@@ -1141,7 +1139,8 @@ cudaError_t launch(const CUtensorMap& map, const CUtensorMap& rmap, const CUtens
 }  // namespace
 
 size_t dense_mla_workspace() {
-  const int n = cluster_slots<false>() > cluster_slots<true>() ? cluster_slots<false>() : cluster_slots<true>();
+  int n = cluster_slots<false>() > cluster_slots<true>() ? cluster_slots<false>() : cluster_slots<true>();
+  if (n == 0) n = 76;                            // no device: what a GB300 takes
   return (size_t)n * (2 * kSlotBytes + sizeof(Record));
 }
 
@@ -1153,6 +1152,7 @@ cudaError_t launch_dense_mla(const DenseArgs& a, cudaStream_t st) {
   const int64_t groups = (int64_t)plan.per_seq * (a.rows / a.T);
   plan.groups = (int)groups;                     // <= rows
   const int slots = f8 ? cluster_slots<true>() : cluster_slots<false>();
+  if (slots == 0) return cudaErrorInvalidConfiguration;
   // at most a cluster a tile
   const int64_t span = a.window + a.n_sink < a.c.s_max ? a.window + a.n_sink + plan.tokens + 2 * kNp : a.c.s_max;
   const int64_t tiles = groups * ((span + kNp - 1) / kNp + 1);
