@@ -33,6 +33,8 @@
 //     (the accumulator is rescaled only when the max grows by more than 2^8),
 //     P in bf16 to shared memory, and the epilogue;
 //   value issuer (warp 2): O += P . V from the same stage.
+// Exchange and softmax warps of lane quarters without rows (few heads) leave at
+// once: what the tensor core computes there is never read.
 // Every wait is bounded; the cluster syncs after set-up and before exit.
 #include "dense_mla.h"
 
@@ -122,6 +124,7 @@ struct Plan {
   int per_seq;     // groups of a sequence
   int groups;
   int split;       // a workspace is there
+  int live;        // lane quarters (32 rows) that a full group has rows in
 };
 
 struct Group {
@@ -258,6 +261,18 @@ __device__ __forceinline__ uint64_t low_bits(int k) {
   return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1ull;
 }
 
+// 32 bytes, a whole sector: one store where the address allows, else two.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
@@ -329,23 +344,23 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 256);
+      mbar_init(&s_empty[i], 64 * plan.live);
       mbar_init(&p_empty[i], 1);
     }
-    mbar_init(p_full, 128);
-    mbar_init(q_ready, 128);
+    mbar_init(p_full, 32 * plan.live);
+    mbar_init(q_ready, 32 * plan.live);
     mbar_init(o_done, 1);
     for (int i = 0; i < 2 * kXRing; ++i) {
       mbar_init(&x_full[i], 1);
-      mbar_init(&x_empty[i], 4);
+      mbar_init(&x_empty[i], plan.live);
     }
     for (int i = 0; i < kRawStages; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&ref_set[i], 1);
-    mbar_init(sums_set, 4 * Y::sets);
-    mbar_init(o_free, 4 * Y::sets);
+    mbar_init(sums_set, plan.live * Y::sets);
+    mbar_init(o_free, plan.live * Y::sets);
     taken_s[0] = taken_s[1] = 0u;
     s_abort = 0;
     s_err = err;
@@ -416,8 +431,9 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     walk.left = share;
     walk.stride = 0;
   }
+  const uint32_t x_bytes = (uint32_t)plan.live * (kXBytes / 4);
   if (tid == 0)                                // the peer's first quarters
-    for (int i = 0; i < 2 * kXRing; ++i) mbar_arrive_expect_tx(&x_full[i], kXBytes);
+    for (int i = 0; i < 2 * kXRing; ++i) mbar_arrive_expect_tx(&x_full[i], x_bytes);
   tc_fence_before();
   cluster_sync();      // the peer's barriers exist (and are armed) before anyone uses them
   tc_fence_after();
@@ -441,7 +457,8 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         const int stage = slot % kStages;
         if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u))) break;
         if (lane == 0) {
-          if (warp == 0) {
+          // (bf16 rows: by warp 1, while warp 0 goes on to the tiles)
+          if (F8 || warp == 1) {
             uint8_t* st = smem + Y::c + stage * kStageBytes;
             mbar_arrive_expect_tx(&full[stage], 2 * kM * 128);
             issued |= 1u << stage;
@@ -558,7 +575,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       }
     }
     // never leave the CTA with a copy still landing in shared memory
-    if (warp == 0 && lane == 0 && s_abort) {
+    if (lane == 0 && s_abort) {
       volatile int no_abort = 0;    // the drain is bounded by time only
 #pragma unroll 1
       for (int s = 0; s < kStages; ++s) {
@@ -715,7 +732,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     int slot = 0, tg = 0;
     bool ok = true;
 #pragma unroll 1
-    while (ok && next_piece(a, plan, walk, x)) {
+    while (ok && (warp & 3) < plan.live && next_piece(a, plan, walk, x)) {
       // The query slice: the rope half by plain loads (begun first), the four 64-dim
       // blocks out of the two ring slots that the producers filled ahead.  The
       // logit MMAs of the piece before are done: this warp has seen all its tiles.
@@ -743,13 +760,13 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           tmem_st32(tmem + lane_base + TM_Q + (half * 2 + bx) * 32, w);
         }
         tmem_st_wait();
-        // the last of the four warps returns the slot (no barrier between them: a
+        // the last of the live warps returns the slot (no barrier between them: a
         // warp that has given up must not leave the others waiting); a warp can be a
         // slot ahead of another but not a piece, so each half has its own count
         __syncwarp();
         if (lane == 0) {
           __threadfence_block();
-          if ((atomicAdd(taken_s + half, 1u) & 3u) == 3u) mbar_arrive(&empty[stage]);
+          if ((atomicAdd(taken_s + half, 1u) + 1u) % (unsigned)plan.live == 0u) mbar_arrive(&empty[stage]);
         }
       }
       if (!ok) break;
@@ -803,12 +820,13 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     const uint32_t xempty_remote = map_to_rank(smem_u32(x_empty), peer);
     // a scale of 0 becomes the smallest normal one: logits of 0, and "masked" times it stays -inf
     const float sl2 = a.scale == 0.f ? 1.17549435e-38f : fabsf(a.scale) * kLog2e;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     Record rec = {-1, -1, 0, 0};
     Piece x;
     int tg = 0, pieces = 0;
     bool ok = true;
 #pragma unroll 1
-    while (ok && next_piece(a, plan, walk, x)) {
+    while (ok && quarter < plan.live && next_piece(a, plan, walk, x)) {
       const int tok = min(m / a.H, x.grp.nt - 1);
       const int n_row = tok == 0 ? x.grp.n_first
                                  : (int)visible_len(a.c, x.grp.row0 + tok, a.decode, a.q_offset);
@@ -843,7 +861,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           }
           __syncwarp();
           if (lane == 0) {                       // buffer credit; lane quarter 0 re-arms first
-            if (quarter == 0) mbar_arrive_expect_tx_relaxed(&x_full[buf], kXBytes);
+            if (quarter == 0) mbar_arrive_expect_tx_relaxed(&x_full[buf], x_bytes);
             mbar_arrive_remote_relaxed(xempty_remote + buf * 8);
           }
         }
@@ -964,41 +982,33 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       }
       const bool live = m < x.grp.nt * a.H;
       const int64_t orow = (int64_t)x.grp.row0 * a.H + m;
-      // nothing visible: 0; NaN stays NaN.  A direct output goes through the P
-      // tile (free: the piece's last P.V is done), each warp's 32 rows in its half
-      // of their 128 bytes, so that a store instruction writes eight rows of 64
-      // bytes instead of 32 rows of 16
+      // nothing visible: 0; NaN stays NaN
       const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
-      const int rows_here = min(32, x.grp.nt * a.H - quarter * 32);
+      uint8_t* const dst0 = reinterpret_cast<uint8_t*>(
+          entire ? (void*)(a.out + orow * DSI_D_LATENT + rho * 256)
+                 : (void*)(ws.o + ((int64_t)slot * kM + m) * DSI_D_LATENT + rho * 256));
 #pragma unroll 1
       for (int c0 = set * 128; c0 < set * 128 + 256 / Y::sets; c0 += 32) {
         float o[32];
-        __syncwarp();
+        __syncwarp();        // rows without an output skip the stores of the round before
         tmem_ld32(tmem + lane_base + TM_O + c0, o);
         tmem_ld_wait();
-        if (entire) {
+        if (!live) {
+        } else if (entire) {
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            __align__(16) bf16 o8[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o8[e] = __float2bfloat16(o[8 * i + e] * inv);
-            *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, set * 4 + i)) = *reinterpret_cast<const uint4*>(o8);
+          for (int i = 0; i < 16; ++i) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
+            w[i] = *reinterpret_cast<const uint32_t*>(&y);
           }
-          __syncwarp();
-          bf16* dst = a.out + ((int64_t)x.grp.row0 * a.H + quarter * 32) * DSI_D_LATENT + rho * 256 + c0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = i * 8 + (lane >> 2);
-            const uint4 y = *reinterpret_cast<const uint4*>(
-                pbuf + sw128_offset(quarter * 32 + rr, set * 4 + (lane & 3)));
-            if (rr < rows_here)
-              *reinterpret_cast<uint4*>(dst + (int64_t)rr * DSI_D_LATENT + (lane & 3) * 8) = y;
-          }
-        } else if (live) {
-          float* dst = ws.o + ((int64_t)slot * kM + m) * DSI_D_LATENT + rho * 256 + c0;
+          for (int i = 0; i < 2; ++i) st_global_32(dst0 + c0 * 2 + i * 32, w + 8 * i, wide);
+        } else {
+          uint32_t w[32];
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_global_32(dst0 + c0 * 4 + i * 32, w + 8 * i, true);
         }
       }
       if (live && rho == 0 && set == 0) {
@@ -1158,6 +1168,7 @@ cudaError_t launch_dense_mla(const DenseArgs& a, cudaStream_t st) {
   const int64_t tiles = groups * ((span + kNp - 1) / kNp + 1);
   const int clusters = (int)(tiles < slots ? tiles : slots);
   plan.split = a.ws != nullptr && clusters > 1;
+  plan.live = (plan.tokens * a.H + 31) / 32;
   Workspace ws = {nullptr, nullptr, nullptr};
   if (plan.split) {
     ws.o = static_cast<float*>(a.ws);
