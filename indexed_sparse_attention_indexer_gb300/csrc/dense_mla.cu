@@ -13,11 +13,12 @@
 //
 // A group's positions are cut into tiles of 64 aligned positions: those that
 // hold sinks, then those from the window's start to the end of the history.
-// The tiles of all groups, laid end to end, are dealt out in equal contiguous
-// runs to the clusters (one resident per SM pair): a run may end inside a
-// group, whose pieces are then joined by a second kernel from their running
-// maxima and sums.  Where dealing out whole groups costs at most
-// kWholeSlack tiles more, groups stay whole and nothing is joined.
+// The groups' tiles (and kGroupCost tiles' worth for each group's start and end),
+// laid end to end, are dealt out in equal contiguous runs to the clusters (one
+// resident per SM pair): a run may end inside a group, whose pieces are then
+// joined by a second kernel from their running maxima and sums.  Where dealing
+// out whole groups costs at most kWholeSlack tiles more, groups stay whole and
+// nothing is joined.
 //
 // Roles in a CTA (16 warps), each walking the same list of pieces; the tile
 // pipeline runs on across pieces:
@@ -66,7 +67,9 @@ constexpr int kSmWarp0 = 8;                    // softmax: warps 8-11 even tiles
 constexpr int kThreads = 16 * 32;
 constexpr int kMaxClusters = 128;
 constexpr int kWholeSlack = 8;
-constexpr int kAhead = 8;                      // tiles between L2 prefetch and copy
+constexpr int kGroupCost = 4;                  // what a piece costs beside its tiles, in tiles
+// tiles between L2 prefetch and copy (64 x 32768 x 128 heads: 2 661 us, 4 635, 8 645, 16 714)
+constexpr int kAhead = 4;
 // partial logits travel in quarters of a tile (16 positions): three in flight for
 // each softmax set hide the round trip of a buffer (credit, stores, landing)
 constexpr int kQuarter = 16;
@@ -160,33 +163,34 @@ __device__ __forceinline__ bool any_sees(const DenseArgs& a, const Group& g, int
   return p < g.n_last && (p >= g.lo || p < (int)a.n_sink);
 }
 
-// A cluster's pieces: whole groups g, g + stride, ..., or the groups of a run
-// of `left` tiles that starts at tile t of group g.
+// A cluster's pieces: whole groups g, g + stride, ..., or what lies in a run of
+// `left` units of the groups' costs laid end to end, from unit u of group g.  A
+// group costs kGroupCost units (its queries, its output), then one a tile; a run
+// that ends inside the former leaves the group to the next.
 struct Walk {
-  int g, t, left, stride;      // stride > 0: whole groups
+  int g, u, left, stride;      // stride > 0: whole groups
 };
 struct Piece {
   Group grp;
   int g, t0, t1;
-  bool last;                   // the cluster's last
 };
 __device__ __forceinline__ bool next_piece(const DenseArgs& a, const Plan& p, Walk& w, Piece& x) {
   if (w.g >= p.groups || w.left <= 0) return false;
   x.g = w.g;
   x.grp = group_of(a, p, w.g);
-  x.t0 = w.t;
   if (w.stride > 0) {
+    x.t0 = 0;
     x.t1 = x.grp.tiles;
     w.g += w.stride;
-    x.last = w.g >= p.groups;
-  } else {
-    x.t1 = min(x.grp.tiles, w.t + w.left);
-    w.left -= x.t1 - x.t0;
-    w.t = 0;
-    if (x.t1 == x.grp.tiles) ++w.g;
-    x.last = w.left <= 0 || w.g >= p.groups;
+    return true;
   }
-  return true;
+  const int end = min(x.grp.tiles + kGroupCost, w.u + w.left);
+  x.t0 = max(0, w.u - kGroupCost);
+  x.t1 = max(0, end - kGroupCost);
+  w.left -= end - w.u;
+  w.u = 0;
+  ++w.g;                       // (a run that ends inside the group has nothing left)
+  return x.t1 > x.t0;
 }
 
 // Cache row of position p of sequence b; -1 (reported) for a bad page id.
@@ -324,7 +328,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
   uint64_t* raw_full = x_empty + 2 * kXRing;   // [kRawStages] FP8: codes landed
   uint64_t* raw_empty = raw_full + kRawStages; // [kRawStages] FP8: codes converted
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Y::misc);
-  int* start_s = reinterpret_cast<int*>(smem + Y::misc + 8);                   // group, tile
+  int* start_s = reinterpret_cast<int*>(smem + Y::misc + 8);                   // group, unit
   int* widest_s = reinterpret_cast<int*>(smem + Y::misc + 16);
   unsigned long long* total_s = reinterpret_cast<unsigned long long*>(smem + Y::misc + 24);
   unsigned int* taken_s = reinterpret_cast<unsigned int*>(smem + Y::misc + 32);
@@ -384,7 +388,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     unsigned long long sum = 0;
     int widest = 0;
     for (int g = tid; g < plan.groups; g += kThreads) {
-      const int n = group_of(a, plan, g).tiles;
+      const int n = group_of(a, plan, g).tiles + kGroupCost;
       sum += (unsigned)n;
       widest = max(widest, n);
     }
@@ -406,7 +410,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
   Walk walk;
   if (!plan.split || total >= (1ull << 30) || whole <= even + kWholeSlack) {
     walk.g = k;
-    walk.t = 0;
+    walk.u = 0;
     walk.left = 1;
     walk.stride = clusters;
   } else {
@@ -415,7 +419,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     long long before = 0;
     for (int g0 = 0; g0 < plan.groups && start < (long long)total; g0 += kThreads) {
       const int g = g0 + tid;
-      const int n = g < plan.groups ? group_of(a, plan, g).tiles : 0;
+      const int n = g < plan.groups ? group_of(a, plan, g).tiles + kGroupCost : 0;
       int chunk;
       const int at = block_exclusive_scan(n, scan_s, chunk);
       if (n > 0 && start >= before + at && start < before + at + n) {
@@ -427,7 +431,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     }
     __syncthreads();
     walk.g = start_s[0];
-    walk.t = start_s[1];
+    walk.u = start_s[1];
     walk.left = share;
     walk.stride = 0;
   }
