@@ -29,8 +29,8 @@
 //   logit issuer (warp 3): S = Qslice . C^T into one of two TMEM tiles;
 //   exchange (warps 4-7): the group's query slice into TMEM (rope half: shared
 //     memory); this CTA's partial logits out of TMEM into the peer's buffer;
-//   softmax (warps 8-15, one row per thread, two sets of four warps on alternate
-//     tiles): own partial plus the peer's, mask, online softmax in log2 units with a lazily moved reference max
+//   softmax (warps 8-15, one row per thread, two sets of four warps, a half of each
+//     tile's positions a set): own partial plus the peer's, mask, online softmax in log2 units with a lazily moved reference max
 //     (the accumulator is rescaled only when the max grows by more than 2^8),
 //     P in bf16 to shared memory, and the epilogue;
 //   value issuer (warp 2): O += P . V from the same stage.
@@ -63,7 +63,7 @@ constexpr int kStageBytes = kNp * kRowBytes;   // 36 KB
 constexpr int kProducers = 2;                  // warps 0-1
 constexpr int kPvWarp = 2;
 constexpr int kQkWarp = 3;                     // then exchange: warps 4-7
-constexpr int kSmWarp0 = 8;                    // softmax: warps 8-11 even tiles, 12-15 odd ones
+constexpr int kSmWarp0 = 8;                    // softmax: warps 8-11 first halves, 12-15 second ones
 constexpr int kThreads = 16 * 32;
 constexpr int kMaxClusters = 128;
 constexpr int kWholeSlack = 8;
@@ -71,8 +71,9 @@ constexpr int kGroupCost = 4;                  // what a piece costs beside its 
 // tiles between L2 prefetch and copy (64 x 32768 x 128 heads: 2 661 us, 4 635, 8 645, 16 714)
 constexpr int kAhead = 4;
 // partial logits travel in quarters of a tile (16 positions): three in flight for
-// each softmax set hide the round trip of a buffer (credit, stores, landing)
+// each half of a tile hide the round trip of a buffer (credit, stores, landing)
 constexpr int kQuarter = 16;
+constexpr int kHalf = 32;                      // positions of a softmax step
 constexpr int kXRing = 3;
 constexpr int kXBytes = kM * kQuarter * 4;
 
@@ -90,12 +91,12 @@ struct Layout {                                // shared memory, bytes
   static constexpr int c = 0;
   static constexpr int raw = c + stages * kStageBytes;
   static constexpr int p = raw + (F8 ? kRawStages * kRawBytes : 0);   // P [128 x 64] bf16
-  static constexpr int x = p + kM * kNp * 2;   // [2][kXRing] the peer's partial logits
+  static constexpr int x = p + kM * kNp * 2;   // [2 halves][kXRing] the peer's partial logits
   static constexpr int qr = x + 2 * kXRing * kXBytes;                 // query rope half
   static constexpr int ref = qr + kM * kRopeHalf * 2;                 // reference maxima of the rows
   static constexpr int sums = ref + kM * 4;    // [2][2][128] (reference, sum) of both sets
   static constexpr int bar = sums + 4 * kM * 8;
-  static constexpr int bars = 3 * stages + 15 + 4 * kXRing + 2 * kRawStages;
+  static constexpr int bars = 3 * stages + 16 + 4 * kXRing + 2 * kRawStages;
   static constexpr int misc = bar + bars * 8;
   static constexpr int scan = misc + 64;       // 40 ints
   static constexpr int bytes = scan + 160 + 1024;
@@ -202,7 +203,8 @@ __device__ __forceinline__ int row_of(const CacheView& c, int b, int p, int* err
   return page * c.page_size + (p - pg * c.page_size);
 }
 
-// 16 E4M3 codes times their tile scale, rounded to bf16 (lo = codes 0..7).
+// 16 E4M3 codes times their tile scale, the fp32 product rounded to bf16 (lo =
+// codes 0..7).
 __device__ __forceinline__ void e4m3x16_scaled(const uint4& v, float sc, uint4& lo, uint4& hi) {
   float f[16];
   fp8x16_to_f32(v, f);
@@ -314,16 +316,14 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
   uint64_t* landed = empty + kStages;          // [kStages] an edge tile's copies landed
   uint64_t* s_full = landed + kStages;         // [2] logits in TMEM
   uint64_t* s_empty = s_full + 2;              // [2] logits read out (exchange and softmax)
-  // barriers that only one softmax set waits for at a tile come in pairs, one for
-  // even and one for odd tiles: a set that skips a phase could not tell it apart
-  uint64_t* p_empty = s_full + 4;              // [2] P.V done
-  uint64_t* p_full = s_full + 6;               // P written
-  uint64_t* q_ready = s_full + 7;              // query slice in place
-  uint64_t* o_done = s_full + 8;               // a piece's last P.V done
-  uint64_t* ref_set = s_full + 9;              // [4] a tile's reference maxima (per lane quarter)
-  uint64_t* sums_set = s_full + 13;            // both softmax sets' sums of a piece
-  uint64_t* o_free = s_full + 14;              // a piece's output read out
-  uint64_t* x_full = s_full + 15;              // [2][kXRing] the peer's partial logits landed
+  uint64_t* p_empty = s_full + 4;              // [2 halves] P.V done
+  uint64_t* p_full = s_full + 6;               // [2 halves] P written
+  uint64_t* q_ready = s_full + 8;              // query slice in place
+  uint64_t* o_done = s_full + 9;               // a piece's last P.V done
+  uint64_t* ref_set = s_full + 10;             // [4] a half tile's reference maxima (per lane quarter)
+  uint64_t* sums_set = s_full + 14;            // both softmax sets' sums of a piece
+  uint64_t* o_free = s_full + 15;              // a piece's output read out
+  uint64_t* x_full = s_full + 16;              // [2 halves][kXRing] the peer's partial logits landed
   uint64_t* x_empty = x_full + 2 * kXRing;     // [2][kXRing] the peer has read what we sent
   uint64_t* raw_full = x_empty + 2 * kXRing;   // [kRawStages] FP8: codes landed
   uint64_t* raw_empty = raw_full + kRawStages; // [kRawStages] FP8: codes converted
@@ -348,10 +348,10 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 64 * plan.live);
+      mbar_init(&s_empty[i], 32 * (1 + Y::sets) * plan.live);
       mbar_init(&p_empty[i], 1);
+      mbar_init(&p_full[i], 32 * plan.live);
     }
-    mbar_init(p_full, 32 * plan.live);
     mbar_init(q_ready, 32 * plan.live);
     mbar_init(o_done, 1);
     for (int i = 0; i < 2 * kXRing; ++i) {
@@ -626,13 +626,16 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         const int stage = slot % kStages, rs = tg % kRawStages, p = tile_pos(x.grp, t) + rr;
         const float2 sc_next = scales(row_next);
         row_next = lookup(t + 2);
-        const bool seen = any_sees(a, x.grp, p), partly = seen && !all_see(a, x.grp, p, 1);
+        const bool whole = all_see(a, x.grp, p - rr, kNp);       // the tile
+        const bool seen = whole || any_sees(a, x.grp, p), partly = seen && !whole && !all_see(a, x.grp, p, 1);
         const uint8_t* raw = smem + Y::raw + rs * kRawBytes;
         uint8_t* st = smem + Y::c + stage * kStageBytes;
         if (!(ok = wait32(&raw_full[rs], (uint32_t)(tg / kRawStages) & 1u))) break;
         if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u))) break;
         bool bad = false;
-#pragma unroll
+// (rolled: the roles share the instruction cache; nine copies took 3.3 us a tile,
+// the loop takes 1.8)
+#pragma unroll 1
         for (int u = 0; u < 9; ++u) {
           const bool rope = u == 8;              // (last: it takes the row's NaN)
           uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
@@ -642,11 +645,13 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
             e4m3x16_scaled(v, rope ? sc.y : sc.x, lo, hi);
           }
           // (edges: as for bf16 rows)
-          if (partly && !(bf16x8_finite(lo) && bf16x8_finite(hi))) {
-            bad = true;
-            lo = hi = make_uint4(0, 0, 0, 0);
+          if (__builtin_expect(!whole, 0)) {
+            if (partly && !(bf16x8_finite(lo) && bf16x8_finite(hi))) {
+              bad = true;
+              lo = hi = make_uint4(0, 0, 0, 0);
+            }
+            if (rope && bad) lo = hi = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
           }
-          if (rope && bad) lo = hi = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
           uint8_t* blk = rope ? st + kRopeOff : st + (hh * 2 + (u >> 2)) * kBlockBytes;
           const uint32_t ch = rope ? (uint32_t)hh * 2 : (uint32_t)(u & 3) * 2;
           *reinterpret_cast<uint4*>(blk + (rope ? sw64_offset(rr, ch) : sw128_offset(rr, ch))) = lo;
@@ -709,14 +714,18 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
 #pragma unroll 1
         for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
           const int stage = slot % kStages;
-          if (!(ok = wait1(p_full, (uint32_t)tg & 1u))) break;
-          tc_fence_after();
           const uint64_t vd = desc_sw128_mn(smem_u32(smem + Y::c + stage * kStageBytes), kBlockBytes);
 #pragma unroll
-          for (int i = 0; i < kNp / 16; ++i)
-            mma_bf16(tmem + TM_O, pd + (uint64_t)((i * 32) >> 4), vd + (uint64_t)((i * 2048) >> 4),
-                     IDESC_O, (t > x.t0 || i > 0) ? 1u : 0u);
-          mma_commit(&p_empty[tg & 1]);
+          for (int hf = 0; hf < 2; ++hf) {
+            if (!(ok = wait1(&p_full[hf], (uint32_t)tg & 1u))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 2 * hf; i < 2 * hf + 2; ++i)
+              mma_bf16(tmem + TM_O, pd + (uint64_t)((i * 32) >> 4), vd + (uint64_t)((i * 2048) >> 4),
+                       IDESC_O, (t > x.t0 || i > 0) ? 1u : 0u);
+            mma_commit(&p_empty[hf]);
+          }
+          if (!ok) break;
           mma_commit(&empty[stage]);
           if (t + 1 == x.t1) mma_commit(o_done);
         }
@@ -795,11 +804,10 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         tc_fence_before();
         mbar_arrive(&s_empty[sb]);
         // each quarter once the peer has read what was in its buffer
-        const int q0 = (tg >> 1) * 4;            // quarters sent to this set so far
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int buf = sb * kXRing + (q0 + i) % kXRing;
-          if (!(ok = wait32_cluster(&x_empty[buf], ((uint32_t)((q0 + i) / kXRing) & 1u) ^ 1u))) break;
+          const int n = tg * 2 + (i & 1), buf = (i >> 1) * kXRing + n % kXRing;   // n: of this half so far
+          if (!(ok = wait32_cluster(&x_empty[buf], ((uint32_t)(n / kXRing) & 1u) ^ 1u))) break;
 #pragma unroll
           for (int g4 = 0; g4 < kQuarter / 4; ++g4) {
             const int j = i * kQuarter + 4 * g4;
@@ -812,9 +820,9 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     }
   } else {
     // ======================= softmax + epilogue ==================================
-    // Two sets of four warps take alternate tiles: a tile is in its set's hands for
-    // two tile periods.  The reference maximum passes from set to set as soon as a
-    // tile's maximum is known; each set sums its own tiles' weights.
+    // Two sets of four warps take a half each of every tile (FP8 rows: one set both,
+    // in turn).  The reference maximum passes from half to half as soon as a half's
+    // maximum is known, and each half has its own P.V; each set sums its own weights.
     const int set = Y::sets == 2 ? (warp - kSmWarp0) >> 2 : 0;
     const int quarter = warp & 3, m = quarter * 32 + lane;   // row = TMEM lane
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -838,122 +846,128 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       float m_mine = -INFINITY, l_mine = 0.f;
 #pragma unroll 1
       for (int t = x.t0; t < x.t1; ++t, ++tg) {
-        if (Y::sets == 2 && (tg & 1) != set) continue;
         const int sb = tg & 1;
-        const int p0 = tile_pos(x.grp, t);
         if (!(ok = wait32(&s_full[sb], (uint32_t)(tg >> 1) & 1u))) break;
         tc_fence_after();
-        float v[kNp];
-        tmem_ld32(tmem + lane_base + TM_S + sb * kNp, v);
-        tmem_ld32(tmem + lane_base + TM_S + sb * kNp + 32, v + 32);
-        tmem_ld_wait();
-        tc_fence_before();
-        mbar_arrive(&s_empty[sb]);
-        // the peer's partial logits
-        const int q0 = (tg >> 1) * 4;            // quarters received for even or odd tiles so far
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int buf = sb * kXRing + (q0 + i) % kXRing;
-          if (!(ok = wait32_cluster(&x_full[buf], (uint32_t)((q0 + i) / kXRing) & 1u))) break;
-#pragma unroll
-          for (int g4 = 0; g4 < kQuarter / 4; ++g4) {
-            const int j = i * kQuarter + 4 * g4;
-            const float4 y = *reinterpret_cast<const float4*>(xrow + buf * kXBytes + g4 * (kM * 16));
-            const float2 s0 = unpack2(add2(pack2(v[j], v[j + 1]), pack2(y.x, y.y)));
-            const float2 s1 = unpack2(add2(pack2(v[j + 2], v[j + 3]), pack2(y.z, y.w)));
-            v[j] = s0.x; v[j + 1] = s0.y; v[j + 2] = s1.x; v[j + 3] = s1.y;
+#pragma unroll 1
+        for (int hf = set; hf < 2; hf += Y::sets) {
+          const int p0 = tile_pos(x.grp, t) + hf * kHalf;
+          float v[kHalf];
+          tmem_ld32(tmem + lane_base + TM_S + sb * kNp + hf * kHalf, v);
+          tmem_ld_wait();
+          if (Y::sets == 2 || hf == 1) {
+            tc_fence_before();
+            mbar_arrive(&s_empty[sb]);
           }
-          __syncwarp();
-          if (lane == 0) {                       // buffer credit; lane quarter 0 re-arms first
-            if (quarter == 0) mbar_arrive_expect_tx_relaxed(&x_full[buf], x_bytes);
-            mbar_arrive_remote_relaxed(xempty_remote + buf * 8);
+          // the peer's partial logits
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int n = tg * 2 + i, buf = hf * kXRing + n % kXRing;
+            if (!(ok = wait32_cluster(&x_full[buf], (uint32_t)(n / kXRing) & 1u))) break;
+#pragma unroll
+            for (int g4 = 0; g4 < kQuarter / 4; ++g4) {
+              const int j = i * kQuarter + 4 * g4;
+              const float4 y = *reinterpret_cast<const float4*>(xrow + buf * kXBytes + g4 * (kM * 16));
+              const float2 s0 = unpack2(add2(pack2(v[j], v[j + 1]), pack2(y.x, y.y)));
+              const float2 s1 = unpack2(add2(pack2(v[j + 2], v[j + 3]), pack2(y.z, y.w)));
+              v[j] = s0.x; v[j + 1] = s0.y; v[j + 2] = s1.x; v[j + 3] = s1.y;
+            }
+            __syncwarp();
+            if (lane == 0) {                     // buffer credit; lane quarter 0 re-arms first
+              if (quarter == 0) mbar_arrive_expect_tx_relaxed(&x_full[buf], x_bytes);
+              mbar_arrive_remote_relaxed(xempty_remote + buf * 8);
+            }
           }
+          if (!ok) break;
+          // masked positions: -inf
+          if (__builtin_expect(!all_see(a, x.grp, p0, kHalf), 0)) {
+            const uint32_t see = (uint32_t)(low_bits(n_row - p0) &
+                                            (~low_bits(lo_row - p0) | low_bits((int)a.n_sink - p0)));
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) v[j] = (see >> j) & 1u ? v[j] : -INFINITY;
+          }
+          float mx[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(v[j], v[j + 4]);
+#pragma unroll
+          for (int j = 8; j < kHalf; j += 8)     // (three-operand maxima)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], v[j + e]), v[j + 4 + e]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // (an infinite sum is a masked or an overflowed one: not scaled, 0 * inf is no logit)
+          const float tmax = top == -INFINITY ? -INFINITY : top * sl2;
+          // the reference after the half before (the other set's), moved when this
+          // half's maximum exceeds it by far; what is in the accumulator moves with it
+          if (Y::sets == 2 && (tg > 0 || hf > 0) &&
+              !(ok = wait32(&ref_set[quarter], (uint32_t)(hf ^ 1)))) break;
+          const float m_prev = t == x.t0 && hf == 0 ? -INFINITY : Y::sets == 2 ? ref_s[0] : m_mine;
+          float m_ref = m_prev, alpha = 1.f;
+          bool rescale = false;
+          if (m_prev == -INFINITY) {
+            m_ref = tmax;                        // nothing in the accumulator yet
+          } else if (tmax > m_prev + kRescaleLog2) {
+            alpha = ex2_approx(m_prev - tmax);
+            m_ref = tmax;
+            rescale = true;
+          }
+          if (Y::sets == 2) {
+            ref_s[0] = m_ref;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ref_set[quarter]);
+          }
+          // weights 2^(logit * sl2 - reference), rounded to bf16 for P.V (half a step, to
+          // nearest: the errors of a row's weights average out) and summed in fp32
+          // before the rounding, which keeps the lse exact to fp32
+          uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+          uint32_t pk[kHalf / 2];
+          const float nmr = (m_ref == -INFINITY) ? 0.f : -m_ref;
+          const uint64_t scale2 = pack2(sl2, sl2), nmr2 = pack2(nmr, nmr);
+#pragma unroll
+          for (int j = 0; j < kHalf / 2; ++j) {
+            const float2 x2 = unpack2(fma2(pack2(v[2 * j], v[2 * j + 1]), scale2, nmr2));
+            const float e0 = ex2_approx(x2.x), e1 = ex2_approx(x2.y);
+            sum2[j & 3] = add2(sum2[j & 3], pack2(e0, e1));
+            const __nv_bfloat162 p2 = __floats2bfloat162_rn(e0, e1);
+            pk[j] = *reinterpret_cast<const uint32_t*>(&p2);
+          }
+          const float2 tot = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
+          if (m_mine != m_ref) l_mine *= m_mine == -INFINITY ? 0.f : ex2_approx(m_mine - m_ref);
+          m_mine = m_ref;
+          l_mine += tot.x + tot.y;
+          // This half of the P tile is free once its last P.V is done; a piece's first P
+          // also waits until the output before is read out.
+          if (tg > 0 && !(ok = wait32(&p_empty[hf], (uint32_t)(tg - 1) & 1u))) break;
+          if (t == x.t0 && hf == 0 && pieces > 0 &&
+              !(ok = wait32(o_free, (uint32_t)(pieces - 1) & 1u))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, hf * 4 + u)) =
+                make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+          // TMEM loads and stores are warp-collective: rescale when any row of the
+          // warp needs it (the others multiply by 1)
+          if (__builtin_expect(__any_sync(0xffffffffu, rescale), 0)) {
+            // Nothing may be under way into the accumulator: the other half's P.V just
+            // before this one is done too.  (Its phase before that one is over, so the
+            // parity tells: that P.V was committed before this half's last one.)
+            if (!(ok = wait32(&p_empty[hf ^ 1], (uint32_t)(hf == 0 ? tg - 1 : tg) & 1u))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < 256; c0 += 16) {
+              float o[16];
+              tmem_ld16(tmem + lane_base + TM_O + c0, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= alpha;
+              tmem_st16(tmem + lane_base + TM_O + c0, o);
+            }
+            tmem_st_wait();
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          mbar_arrive(&p_full[hf]);
         }
         if (!ok) break;
-        // masked positions: -inf
-        if (__builtin_expect(!all_see(a, x.grp, p0, kNp), 0)) {
-          const uint64_t see = low_bits(n_row - p0) & (~low_bits(lo_row - p0) | low_bits((int)a.n_sink - p0));
-          const uint32_t half[2] = {(uint32_t)see, (uint32_t)(see >> 32)};
-#pragma unroll
-          for (int j = 0; j < kNp; ++j) v[j] = (half[j >> 5] >> (j & 31)) & 1u ? v[j] : -INFINITY;
-        }
-        float mx[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mx[j] = v[j];
-#pragma unroll
-        for (int j = 4; j < kNp; j += 8) {       // (three-operand maxima)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], v[j + e]), j + 4 + e < kNp ? v[j + 4 + e] : v[j + e]);
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        // (an infinite sum is a masked or an overflowed one: not scaled, 0 * inf is no logit)
-        const float tmax = top == -INFINITY ? -INFINITY : top * sl2;
-        // the reference after the tile before (set by the other set), moved when
-        // this tile's maximum exceeds it by far; what is in the accumulator moves
-        // with it
-        if (Y::sets == 2 && tg > 0 &&
-            !(ok = wait32(&ref_set[quarter], (uint32_t)(tg - 1) & 1u))) break;
-        const float m_prev = t == x.t0 ? -INFINITY : Y::sets == 2 ? ref_s[0] : m_mine;
-        float m_ref = m_prev, alpha = 1.f;
-        bool rescale = false;
-        if (m_prev == -INFINITY) {
-          m_ref = tmax;                        // nothing in the accumulator yet
-        } else if (tmax > m_prev + kRescaleLog2) {
-          alpha = ex2_approx(m_prev - tmax);
-          m_ref = tmax;
-          rescale = true;
-        }
-        if (Y::sets == 2) {
-          ref_s[0] = m_ref;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ref_set[quarter]);
-        }
-        // weights 2^(logit * sl2 - reference), rounded to bf16 for P.V (half a step, to
-        // nearest: the errors of a row's weights average out) and summed in fp32
-        // before the rounding, which keeps the lse exact to fp32
-        uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
-        uint32_t pk[kNp / 2];
-        const float nmr = (m_ref == -INFINITY) ? 0.f : -m_ref;
-        const uint64_t scale2 = pack2(sl2, sl2), nmr2 = pack2(nmr, nmr);
-#pragma unroll
-        for (int j = 0; j < kNp / 2; ++j) {
-          const float2 x2 = unpack2(fma2(pack2(v[2 * j], v[2 * j + 1]), scale2, nmr2));
-          const float e0 = ex2_approx(x2.x), e1 = ex2_approx(x2.y);
-          sum2[j & 3] = add2(sum2[j & 3], pack2(e0, e1));
-          const __nv_bfloat162 p2 = __floats2bfloat162_rn(e0, e1);
-          pk[j] = *reinterpret_cast<const uint32_t*>(&p2);
-        }
-        const float2 tot = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
-        if (m_mine != m_ref) l_mine *= m_mine == -INFINITY ? 0.f : ex2_approx(m_mine - m_ref);
-        m_mine = m_ref;
-        l_mine += tot.x + tot.y;
-        // the P tile is free, and P.V(t-1) has landed in the accumulator; a piece's
-        // first P also waits until both sets have read out the output before
-        if (tg > 0 && !(ok = wait32(&p_empty[sb ^ 1], (uint32_t)((tg - 1) >> 1) & 1u))) break;
-        if (t == x.t0 && pieces > 0 &&
-            !(ok = wait32(o_free, (uint32_t)(pieces - 1) & 1u))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, u)) =
-              make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
-        // TMEM loads and stores are warp-collective: rescale when any row of the
-        // warp needs it (the others multiply by 1)
-        if (__builtin_expect(__any_sync(0xffffffffu, rescale), 0)) {
-#pragma unroll 1
-          for (int c0 = 0; c0 < 256; c0 += 16) {
-            float o[16];
-            tmem_ld16(tmem + lane_base + TM_O + c0, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= alpha;
-            tmem_st16(tmem + lane_base + TM_O + c0, o);
-          }
-          tmem_st_wait();
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        mbar_arrive(p_full);
       }
       if (!ok) break;
       // ---- the piece's sum over both sets (a set without tiles has none) --------
