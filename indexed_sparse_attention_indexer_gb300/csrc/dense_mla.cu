@@ -20,7 +20,7 @@
 // out whole groups costs at most kWholeSlack tiles more, groups stay whole and
 // nothing is joined.
 //
-// Roles in a CTA (16 warps), each walking the same list of pieces; the tile
+// Roles in a CTA (16 warps; FP8 rows: 20), each walking the same list of pieces; the tile
 // pipeline runs on across pieces:
 //   producers (warps 0-1): a tile's rows into a 128-byte-swizzled stage (ring
 //     of 4) by TMA boxes; tiles at an edge (not wholly visible to every token
@@ -30,10 +30,13 @@
 //   exchange (warps 4-7): the group's query slice into TMEM (rope half: shared
 //     memory); this CTA's partial logits out of TMEM into the peer's buffer;
 //   softmax (warps 8-15, one row per thread, two sets of four warps, a half of each
-//     tile's positions a set): own partial plus the peer's, mask, online softmax in log2 units with a lazily moved reference max
-//     (the accumulator is rescaled only when the max grows by more than 2^8),
-//     P in bf16 to shared memory, and the epilogue;
-//   value issuer (warp 2): O += P . V from the same stage.
+//     tile's positions a set; FP8 rows: warps 8-11, both halves in turn): own partial
+//     plus the peer's, mask, online softmax in log2 units with a lazily moved
+//     reference max (the accumulator is rescaled only when the max grows by more
+//     than 2^8), P in bf16 to shared memory, and the epilogue;
+//   value issuer (warp 2): O += P . V from the same stage, a half tile at a time;
+//   conversion (FP8 rows, warps 12-19): codes times scales, rounded to bf16, out of
+//     the raw tiles into the stages; two groups of four warps take tiles in turn.
 // Exchange and softmax warps of lane quarters without rows (few heads) leave at
 // once: what the tensor core computes there is never read.
 // Every wait is bounded; the cluster syncs after set-up and before exit.
@@ -59,12 +62,11 @@ constexpr int kRopeHalf = 32;                  // rope dims of each CTA
 constexpr int kRopeOff = 4 * kBlockBytes;      // stage: four 64-dim blocks, then 64 rows of rope dims
 constexpr int kRowBytes = 4 * 128 + kRopeHalf * 2;
 constexpr int kStageBytes = kNp * kRowBytes;   // 36 KB
-// 16 warps (four per SM sub-partition): at most 128 registers a thread
+// 16 warps (four per SM sub-partition), at most 128 registers a thread; FP8 rows: 20, 96
 constexpr int kProducers = 2;                  // warps 0-1
 constexpr int kPvWarp = 2;
 constexpr int kQkWarp = 3;                     // then exchange: warps 4-7
 constexpr int kSmWarp0 = 8;                    // softmax: warps 8-11 first halves, 12-15 second ones
-constexpr int kThreads = 16 * 32;
 constexpr int kMaxClusters = 128;
 constexpr int kWholeSlack = 8;
 constexpr int kGroupCost = 4;                  // what a piece costs beside its tiles, in tiles
@@ -77,8 +79,9 @@ constexpr int kHalf = 32;                      // positions of a softmax step
 constexpr int kXRing = 3;
 constexpr int kXBytes = kM * kQuarter * 4;
 
-// FP8 rows: raw tiles of codes land beside the ring and are converted into it
-// by the warps that are the second softmax set of bf16 rows.
+// FP8 rows: raw tiles of codes land beside the ring and are converted into it.  One
+// group of four warps takes 1.8 us for a tile and was what bounded them; two groups
+// in turn: 107.6 -> 103.5 us for 777 tokens of 32 heads with a window of 511.
 constexpr int kRawStages = 2;
 constexpr int kRawRope = 2 * kNp * 128;        // two blocks of 128 dims, then 64 rows of 32 rope dims
 constexpr int kRawBytes = kNp * (256 + kRopeHalf);
@@ -86,6 +89,7 @@ constexpr int kRawBytes = kNp * (256 + kRopeHalf);
 template <bool F8>
 struct Layout {                                // shared memory, bytes
   static constexpr int stages = F8 ? 3 : 4;
+  static constexpr int threads = F8 ? 640 : 512;
   static constexpr int sets = F8 ? 1 : 2;      // softmax sets
   static constexpr int fill_warps = F8 ? 4 : 2;   // warps that hand a tile to the tensor core
   static constexpr int c = 0;
@@ -262,6 +266,20 @@ __device__ __forceinline__ bool wait32_cluster(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity) || wait_on(smem_u32(bar), parity));
 }
 
+// A wait in two parts, for roles whose time is latency: ask early, work on, and
+// wait only where the answer was no (a ready wait alone costs ~150 cycles).
+__device__ __forceinline__ bool ask_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool settle(bool asked, uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, asked || wait_on(smem_u32(bar), parity));
+}
+
 // Bits 0 .. k-1 of 64.
 __device__ __forceinline__ uint64_t low_bits(int k) {
   return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1ull;
@@ -302,7 +320,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 
 template <bool F8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<F8>::threads, 1)
 dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
              const __grid_constant__ CUtensorMap qmap, const __grid_constant__ DenseArgs a,
              const __grid_constant__ Plan plan, Workspace ws, int box) {
@@ -348,9 +366,9 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 32 * (1 + Y::sets) * plan.live);
+      mbar_init(&s_empty[i], (1 + Y::sets) * plan.live);
       mbar_init(&p_empty[i], 1);
-      mbar_init(&p_full[i], 32 * plan.live);
+      mbar_init(&p_full[i], plan.live);
     }
     mbar_init(q_ready, 32 * plan.live);
     mbar_init(o_done, 1);
@@ -387,7 +405,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
   {
     unsigned long long sum = 0;
     int widest = 0;
-    for (int g = tid; g < plan.groups; g += kThreads) {
+    for (int g = tid; g < plan.groups; g += Y::threads) {
       const int n = group_of(a, plan, g).tiles + kGroupCost;
       sum += (unsigned)n;
       widest = max(widest, n);
@@ -417,7 +435,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     const int share = (int)even;
     const long long start = (long long)share * k;
     long long before = 0;
-    for (int g0 = 0; g0 < plan.groups && start < (long long)total; g0 += kThreads) {
+    for (int g0 = 0; g0 < plan.groups && start < (long long)total; g0 += Y::threads) {
       const int g = g0 + tid;
       const int n = g < plan.groups ? group_of(a, plan, g).tiles + kGroupCost : 0;
       int chunk;
@@ -598,7 +616,8 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     // Two threads a row, nine pieces of 16 codes each: code * tile scale, rounded to
     // bf16, into the ring stage.  The page is looked up two tiles ahead and the scales
     // are loaded one ahead, within a piece.
-    const int c_thread = tid - (kSmWarp0 + 4) * 32, rr = c_thread & 63, hh = c_thread >> 6;
+    const int c_thread = (tid - (kSmWarp0 + 4) * 32) & 127, rr = c_thread & 63, hh = c_thread >> 6;
+    const int turn = (warp - kSmWarp0 - 4) >> 2; // the two groups of warps take the tiles in turn
     const int s0 = (int)rho * 2 + hh;            // tile of this thread's 128 latent dims
     Piece x = {};
     int slot = 0, tg = 0;
@@ -618,14 +637,19 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       for (int i = 0; i < 2 && ok; ++i, ++slot)
         ok = wait32(&empty[slot % kStages], ((uint32_t)(slot / kStages) & 1u) ^ 1u);
       if (!ok) break;
-      int row_next = lookup(x.t0);
+      const int first = x.t0 + ((tg ^ turn) & 1);
+      int row_next = lookup(first);
       float2 sc = scales(row_next);
-      row_next = lookup(x.t0 + 1);
+      row_next = lookup(first + 2);
 #pragma unroll 1
       for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
         const int stage = slot % kStages, rs = tg % kRawStages, p = tile_pos(x.grp, t) + rr;
+        if ((tg & 1) != turn) {                  // (the other group's: no phase goes unseen)
+          if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u))) break;
+          continue;
+        }
         const float2 sc_next = scales(row_next);
-        row_next = lookup(t + 2);
+        row_next = lookup(t + 4);
         const bool whole = all_see(a, x.grp, p - rr, kNp);       // the tile
         const bool seen = whole || any_sees(a, x.grp, p), partly = seen && !whole && !all_see(a, x.grp, p, 1);
         const uint8_t* raw = smem + Y::raw + rs * kRawBytes;
@@ -802,7 +826,8 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         tmem_ld32(tmem + lane_base + TM_S + sb * kNp + 32, v + 32);
         tmem_ld_wait();
         tc_fence_before();
-        mbar_arrive(&s_empty[sb]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[sb]);
         // each quarter once the peer has read what was in its buffer
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -852,33 +877,40 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
 #pragma unroll 1
         for (int hf = set; hf < 2; hf += Y::sets) {
           const int p0 = tile_pos(x.grp, t) + hf * kHalf;
+          // this CTA's partial logits and the peer's
           float v[kHalf];
           tmem_ld32(tmem + lane_base + TM_S + sb * kNp + hf * kHalf, v);
+          const int n0 = tg * 2, b0 = hf * kXRing + n0 % kXRing, b1 = hf * kXRing + (n0 + 1) % kXRing;
+          const uint32_t ph0 = (uint32_t)(n0 / kXRing) & 1u, ph1 = (uint32_t)((n0 + 1) / kXRing) & 1u;
+          const bool here0 = ask_cluster(&x_full[b0], ph0), here1 = ask_cluster(&x_full[b1], ph1);
+          if (!(ok = settle(here0 && here1, &x_full[b0], ph0) && settle(here1, &x_full[b1], ph1))) break;
+          float4 y[kHalf / 4];
+#pragma unroll
+          for (int g4 = 0; g4 < kHalf / 4; ++g4)
+            y[g4] = *reinterpret_cast<const float4*>(xrow + (g4 < kQuarter / 4 ? b0 : b1) * kXBytes +
+                                                     g4 % (kQuarter / 4) * (kM * 16));
           tmem_ld_wait();
           if (Y::sets == 2 || hf == 1) {
             tc_fence_before();
-            mbar_arrive(&s_empty[sb]);
-          }
-          // the peer's partial logits
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int n = tg * 2 + i, buf = hf * kXRing + n % kXRing;
-            if (!(ok = wait32_cluster(&x_full[buf], (uint32_t)(n / kXRing) & 1u))) break;
-#pragma unroll
-            for (int g4 = 0; g4 < kQuarter / 4; ++g4) {
-              const int j = i * kQuarter + 4 * g4;
-              const float4 y = *reinterpret_cast<const float4*>(xrow + buf * kXBytes + g4 * (kM * 16));
-              const float2 s0 = unpack2(add2(pack2(v[j], v[j + 1]), pack2(y.x, y.y)));
-              const float2 s1 = unpack2(add2(pack2(v[j + 2], v[j + 3]), pack2(y.z, y.w)));
-              v[j] = s0.x; v[j + 1] = s0.y; v[j + 2] = s1.x; v[j + 3] = s1.y;
-            }
             __syncwarp();
-            if (lane == 0) {                     // buffer credit; lane quarter 0 re-arms first
-              if (quarter == 0) mbar_arrive_expect_tx_relaxed(&x_full[buf], x_bytes);
-              mbar_arrive_remote_relaxed(xempty_remote + buf * 8);
-            }
+            if (lane == 0) mbar_arrive(&s_empty[sb]);
           }
-          if (!ok) break;
+#pragma unroll
+          for (int g4 = 0; g4 < kHalf / 4; ++g4) {
+            const int j = 4 * g4;
+            const float2 s0 = unpack2(add2(pack2(v[j], v[j + 1]), pack2(y[g4].x, y[g4].y)));
+            const float2 s1 = unpack2(add2(pack2(v[j + 2], v[j + 3]), pack2(y[g4].z, y[g4].w)));
+            v[j] = s0.x; v[j + 1] = s0.y; v[j + 2] = s1.x; v[j + 3] = s1.y;
+          }
+          __syncwarp();
+          if (lane == 0) {                       // what was read is free; lane quarter 0 re-arms first
+            if (quarter == 0) {
+              mbar_arrive_expect_tx_relaxed(&x_full[b0], x_bytes);
+              mbar_arrive_expect_tx_relaxed(&x_full[b1], x_bytes);
+            }
+            mbar_arrive_remote_relaxed(xempty_remote + b0 * 8);
+            mbar_arrive_remote_relaxed(xempty_remote + b1 * 8);
+          }
           // masked positions: -inf
           if (__builtin_expect(!all_see(a, x.grp, p0, kHalf), 0)) {
             const uint32_t see = (uint32_t)(low_bits(n_row - p0) &
@@ -886,6 +918,8 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) v[j] = (see >> j) & 1u ? v[j] : -INFINITY;
           }
+          const bool ref_here = Y::sets == 1 || (tg == 0 && hf == 0) ||
+                                mbar_test_wait(&ref_set[quarter], (uint32_t)(hf ^ 1));
           float mx[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) mx[j] = fmaxf(v[j], v[j + 4]);
@@ -898,8 +932,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           const float tmax = top == -INFINITY ? -INFINITY : top * sl2;
           // the reference after the half before (the other set's), moved when this
           // half's maximum exceeds it by far; what is in the accumulator moves with it
-          if (Y::sets == 2 && (tg > 0 || hf > 0) &&
-              !(ok = wait32(&ref_set[quarter], (uint32_t)(hf ^ 1)))) break;
+          if (Y::sets == 2 && !(ok = settle(ref_here, &ref_set[quarter], (uint32_t)(hf ^ 1)))) break;
           const float m_prev = t == x.t0 && hf == 0 ? -INFINITY : Y::sets == 2 ? ref_s[0] : m_mine;
           float m_ref = m_prev, alpha = 1.f;
           bool rescale = false;
@@ -915,6 +948,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
             __syncwarp();
             if (lane == 0) mbar_arrive(&ref_set[quarter]);
           }
+          const bool p_here = tg == 0 || mbar_test_wait(&p_empty[hf], (uint32_t)(tg - 1) & 1u);
           // weights 2^(logit * sl2 - reference), rounded to bf16 for P.V (half a step, to
           // nearest: the errors of a row's weights average out) and summed in fp32
           // before the rounding, which keeps the lse exact to fp32
@@ -936,7 +970,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           l_mine += tot.x + tot.y;
           // This half of the P tile is free once its last P.V is done; a piece's first P
           // also waits until the output before is read out.
-          if (tg > 0 && !(ok = wait32(&p_empty[hf], (uint32_t)(tg - 1) & 1u))) break;
+          if (!(ok = settle(p_here, &p_empty[hf], (uint32_t)(tg - 1) & 1u))) break;
           if (t == x.t0 && hf == 0 && pieces > 0 &&
               !(ok = wait32(o_free, (uint32_t)(pieces - 1) & 1u))) break;
           tc_fence_after();
@@ -965,7 +999,8 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           }
           fence_proxy_async_smem();
           tc_fence_before();
-          mbar_arrive(&p_full[hf]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[hf]);
         }
         if (!ok) break;
       }
@@ -1132,7 +1167,7 @@ int cluster_slots() {
   if (v) return v;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Layout<F8>::threads);
   cfg.dynamicSmemBytes = Layout<F8>::bytes;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
@@ -1158,7 +1193,7 @@ cudaError_t launch(const CUtensorMap& map, const CUtensorMap& rmap, const CUtens
                    const DenseArgs& a, const Plan& plan, const Workspace& ws, int box, int clusters,
                    cudaStream_t st) {
   const cudaError_t e =
-      launch_overlapped(dense_mla_tc<F8>, dim3(2u * (unsigned)clusters), dim3(kThreads),
+      launch_overlapped(dense_mla_tc<F8>, dim3(2u * (unsigned)clusters), dim3(Layout<F8>::threads),
                         Layout<F8>::bytes, st, map, rmap, qmap, a, plan, ws, box);
   note_launch();
   return e;
