@@ -85,7 +85,7 @@ dsi_status check_cache(const dsi_cache* c, int rows, int decode, int64_t q_offse
     if ((int64_t)rows != (int64_t)c->batch * tokens_per_seq || !c->seq_lens)
       return DSI_ERR_INVALID_ARG;
   } else {
-    if (c->batch != 1 || q_offset < 0 || q_offset + rows > c->s_max) return DSI_ERR_INVALID_ARG;
+    if (c->batch != 1 || q_offset < 0 || q_offset > c->s_max - rows) return DSI_ERR_INVALID_ARG;
   }
   return DSI_OK;
 }

@@ -199,3 +199,12 @@ def test_dense_binding_checks(L):
         binding.dense_mla_decode(q, binding.Cache(torch.zeros((2, 64, 64), dtype=torch.bfloat16), None), 0.04)
     with pytest.raises(ValueError):
         binding.window_mla_prefill(q.float(), cache, 0, 10, 1, 0.04)
+
+
+def test_prefill_offset_at_the_end_of_64_bits(L):
+    """q_offset + T past 2^63 is past s_max like any other."""
+    c = _cache(batch=1, k_idx=FAKE, d=128)
+    for off in ((1 << 63) - 1, (1 << 63) - 8):
+        assert L.dsi_window_mla_prefill(FAKE, ctypes.byref(c), 8, 16, off, 10, 1, 0.04, FAKE, None, None, 0, None) == E
+        assert L.dsi_index_score(FAKE, FAKE, ctypes.byref(c), 8, 64, 0, off, FAKE, 1024, None) == E
+        assert L.dsi_sparse_mla_prefill(FAKE, ctypes.byref(c), FAKE, 8, 16, 16, off, 0.04, FAKE, None, None, 0, None) == E
