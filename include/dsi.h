@@ -415,7 +415,7 @@ dsi_status dsi_latent_fp8_append(const void* x, int64_t n_rows, int64_t ld_x,
  * Errors: DSI_ERR_INVALID_ARG (null pointer, misaligned q, out or workspace,
  * T < 1, NaN scale, inconsistent cache), DSI_ERR_UNSUPPORTED (n_heads outside
  * 1..128, page_size not a multiple of 8, 2^31 cache rows or query heads
- * (batch * T * n_heads) or more),
+ * (batch * T * n_heads) or more, s_max above 2^31 - 1024),
  * DSI_ERR_WORKSPACE (workspace too small).
  */
 dsi_status dsi_dense_mla_decode(const void* q, const dsi_cache* cache, int32_t tokens_per_seq,
@@ -495,7 +495,8 @@ size_t dsi_dense_mla_workspace_size(int32_t rows, int32_t n_heads);
  * DSI_NORM_LAYER), DSI_ERR_UNSUPPORTED (d not a multiple of 8 or outside
  * 8..1024, norm_dim not a multiple of 8 or outside 8..d, rope_dim not a
  * multiple of 16, rope_offset not a multiple of 8, out_group not 32, 64 or
- * 128 or not dividing d, unknown norm or out_dtype).
+ * 128 or not dividing d, unknown norm or out_dtype, n_rows above 2^31 or
+ * n_rows * n_heads above 2^40).
  */
 typedef enum { DSI_NORM_NONE = 0, DSI_NORM_RMS = 1, DSI_NORM_LAYER = 2 } dsi_norm;
 

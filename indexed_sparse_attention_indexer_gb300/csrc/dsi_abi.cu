@@ -440,7 +440,8 @@ static dsi_status dense_common(const void* q, const dsi_cache* cache, int64_t ro
   const dsi_status s = check_cache(cache, (int)rows, decode, q_offset, false, true, decode ? T : 1);
   if (s != DSI_OK) return s;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSI_ERR_INVALID_ARG;
-  if (cache->s_max >= (1ll << 31) ||
+  // (positions are 32-bit and run up to a few tiles past the last one)
+  if (cache->s_max > (1ll << 31) - 1024 ||
       (cache->block_table ? cache->num_pages > ((1ll << 31) - 1) / cache->page_size
                           : cache->batch > 0 && cache->s_max > ((1ll << 31) - 1) / cache->batch))
     return DSI_ERR_UNSUPPORTED;
@@ -509,7 +510,8 @@ dsi_status dsi_norm_rope(const dsi_heads* queries, const dsi_heads* keys, int64_
   if (s != DSI_OK) return s;
   s = check_heads(keys, n_rows, d, &k);
   if (s != DSI_OK) return s;
-  if (n_rows > (1ll << 40)) return DSI_ERR_UNSUPPORTED;   // vector counts stay in 64 bits
+  if (n_rows > (1ll << 31) || n_rows * q.n_heads > (1ll << 40) || n_rows * k.n_heads > (1ll << 40))
+    return DSI_ERR_UNSUPPORTED;                            // blocks are counted in 32 bits
   if (n_rows == 0 || q.n_heads + (int64_t)k.n_heads == 0) return DSI_OK;
   RopeArgs a;
   a.table = rope_table;

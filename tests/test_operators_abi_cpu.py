@@ -208,3 +208,14 @@ def test_prefill_offset_at_the_end_of_64_bits(L):
         assert L.dsi_window_mla_prefill(FAKE, ctypes.byref(c), 8, 16, off, 10, 1, 0.04, FAKE, None, None, 0, None) == E
         assert L.dsi_index_score(FAKE, FAKE, ctypes.byref(c), 8, 64, 0, off, FAKE, 1024, None) == E
         assert L.dsi_sparse_mla_prefill(FAKE, ctypes.byref(c), FAKE, 8, 16, 16, off, 0.04, FAKE, None, None, 0, None) == E
+
+
+def test_largest_sizes_are_refused(L):
+    """Past what 32-bit positions and block counts hold."""
+    c = dict(block_table=FAKE, page_size=8, num_pages=100)
+    for pages, st in ((1 << 28, U), ((1 << 28) - 127, U)):
+        assert _dense(L, _cache(max_pages=pages, s_max=8 * pages, **c)) == st
+    h = dict(dst_rows=FAKE)
+    assert _rope(L, _heads(n_heads=1, **h), n=(1 << 31) + 1) == U
+    assert _rope(L, _heads(n_heads=1 << 20, **h), n=(1 << 20) + 1) == U
+    assert _rope(L, None, _heads(n_heads=(1 << 31) - 1, **h), n=1 << 31) == U
