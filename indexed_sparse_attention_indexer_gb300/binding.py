@@ -191,6 +191,35 @@ class Cache:
             s.num_pages = 0
         s.seq_lens = seq_lens.data_ptr() if seq_lens is not None else None
         self.struct = s
+        self._fault: Optional[str] = None
+
+    def latent_fault(self) -> str:
+        """What keeps the dense and window calls from reading this cache as its struct says, or ""
+        (looked for once: the struct's pointers are those of the tensors given at first)."""
+        if self._fault is None:
+            self._fault = self._find_latent_fault()
+        return self._fault
+
+    def _find_latent_fault(self) -> str:
+        lat, s = self.latent, self.struct
+        if lat is None or lat.dim() < 3 or lat.shape[-1] != D_QK:
+            return f"the latent cache is [batch, s_max, {D_QK}] or [pages, page_size, {D_QK}]"
+        if lat.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or not lat.is_contiguous():
+            return "the latent cache is contiguous, bf16 or E4M3"
+        rows = s.num_pages * s.page_size if self.block_table is not None else s.batch * s.s_max
+        if lat.numel() != rows * D_QK:
+            return "the latent cache has other rows than the index keys"
+        f8, sc = lat.dtype == torch.float8_e4m3fn, self.latent_scale
+        if f8 and (sc is None or sc.dtype != torch.float32 or not sc.is_contiguous() or sc.numel() != rows * 5):
+            return "E4M3 latent rows have contiguous fp32 scales [.., 5]"
+        for t, n, name in ((self.seq_lens, s.batch, "seq_lens"),
+                           (self.block_table, s.batch * s.max_pages, "block_table")):
+            if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n):
+                return f"{name} is a contiguous int32 tensor with an entry for every sequence"
+        for t in (sc if f8 else None, self.seq_lens, self.block_table):
+            if t is not None and t.device != lat.device:
+                return "the cache's tensors must be on one device"
+        return ""
 
     @classmethod
     def of(cls, ws) -> "Cache":
@@ -205,6 +234,13 @@ class Cache:
 def _need(ok: bool, what: str):
     if not ok:
         raise ValueError(what)
+
+
+def _i64(v) -> int:
+    """An integer argument that the library takes in 64 bits."""
+    v = int(v)
+    _need(-(1 << 63) <= v < 1 << 63, "an integer argument is past 64 bits")
+    return v
 
 
 def _raw_stream(stream, device: torch.device) -> int:
@@ -388,7 +424,10 @@ def _dense(fn: str, q, cache: Cache, args, rows: int, scale, out, lse, want_lse,
     if q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous() or q.shape[2] != D_QK:
         raise ValueError(f"q is a contiguous bf16 [rows, heads, {D_QK}] tensor")
     device = q.device
-    if cache.latent is None or cache.latent.device != device:
+    fault = cache.latent_fault()
+    if fault:
+        raise ValueError(fault)
+    if cache.latent.device != device:
         raise ValueError("the cache has no latent rows on q's device")
     n, H, _ = q.shape
     if n != rows:
@@ -438,7 +477,7 @@ def window_mla_decode(q, cache: Cache, window: int, n_sink: int, scale: float,
     """The newest tokens over their last ``window`` positions and the first ``n_sink``:
     ``dsi_window_mla_decode``."""
     T = int(tokens_per_seq)
-    return _dense("dsi_window_mla_decode", q, cache, (T, int(q.shape[1]), int(window), int(n_sink)),
+    return _dense("dsi_window_mla_decode", q, cache, (T, int(q.shape[1]), _i64(window), _i64(n_sink)),
                   cache.struct.batch * T, scale, out, lse, want_lse, workspace, stream, checked)
 
 
@@ -448,8 +487,8 @@ def window_mla_prefill(q, cache: Cache, q_offset: int, window: int, n_sink: int,
     """Tokens ``q_offset ...`` of one sequence, each over its last ``window`` positions and the
     first ``n_sink``: ``dsi_window_mla_prefill``."""
     T = int(q.shape[0])
-    return _dense("dsi_window_mla_prefill", q, cache, (T, int(q.shape[1]), int(q_offset), int(window),
-                                                       int(n_sink)),
+    return _dense("dsi_window_mla_prefill", q, cache, (T, int(q.shape[1]), _i64(q_offset), _i64(window),
+                                                       _i64(n_sink)),
                   T, scale, out, lse, want_lse, workspace, stream, checked)
 
 
@@ -481,6 +520,7 @@ def norm_rope(queries: Optional[Heads], keys: Optional[Heads], table, positions,
         raise ValueError("all tensors must be on one device")
     if n:
         rows, rope_dim = table.shape
+        _need(0 <= rope_offset <= side.d - rope_dim, "the rotated dims are dims of x")
         st = _launch(lib.dsi_norm_rope, device, stream,
                      queries._ref if queries is not None else None, keys._ref if keys is not None else None,
                      n, side.d, eps, table.data_ptr(), rows, positions.data_ptr(), rope_offset, rope_dim,

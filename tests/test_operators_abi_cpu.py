@@ -219,3 +219,38 @@ def test_largest_sizes_are_refused(L):
     assert _rope(L, _heads(n_heads=1, **h), n=(1 << 31) + 1) == U
     assert _rope(L, _heads(n_heads=1 << 20, **h), n=(1 << 20) + 1) == U
     assert _rope(L, None, _heads(n_heads=(1 << 31) - 1, **h), n=1 << 31) == U
+
+
+def test_dense_binding_checks_the_cache(L):
+    """What the cache's struct would misread is refused before any launch."""
+    bf, i32 = dict(dtype=torch.bfloat16), dict(dtype=torch.int32)
+    q, lat, lens = torch.zeros((2, 8, 576), **bf), torch.zeros((2, 64, 576), **bf), torch.zeros(2, **i32)
+    f8, sc = torch.zeros((2, 64, 576), dtype=torch.uint8).view(torch.float8_e4m3fn), torch.zeros((2, 64, 5))
+    table = torch.zeros((2, 1), **i32)
+    C = binding.Cache
+    for cache in (C(None, lat.half(), lens), C(None, lat.float(), lens), C(None, torch.zeros((2, 64, 512), **bf), lens),
+                  C(None, torch.zeros((2, 128, 576), **bf)[:, ::2], lens), C(None, lat, lens.long()), C(None, lat, lens[:1]),
+                  C(None, lat, torch.zeros(4, **i32)[::2]), C(None, f8, lens), C(None, f8, lens, latent_scale=sc[:1]),
+                  C(None, f8, lens, latent_scale=sc.double()), C(None, f8, lens, latent_scale=sc[..., :4]),
+                  C(None, lat, lens, block_table=table.long(), page_size=64),
+                  C(None, lat, lens, block_table=torch.zeros((2, 2), **i32)[:, ::2], page_size=64),
+                  C(None, lat, lens, block_table=table, page_size=128),
+                  C(torch.zeros((3, 64, 64), **bf), lat, torch.zeros(3, **i32), block_table=torch.zeros((3, 1), **i32), page_size=64),
+                  C(None, lat, torch.zeros(2, device="meta", **i32))):
+        with pytest.raises(ValueError):
+            binding.dense_mla_decode(q, cache, 0.04)
+    for good in (C(None, lat, lens), C(None, f8, lens, latent_scale=sc), C(None, lat, lens, block_table=table, page_size=64),
+                 C(torch.zeros((2, 64, 64), **bf), lat, lens)):
+        assert good.latent_fault() == ""
+    for kw in (dict(window=1 << 63, n_sink=0), dict(window=5, n_sink=1 << 64), dict(window=-(1 << 63) - 1, n_sink=0)):
+        with pytest.raises(ValueError):
+            binding.window_mla_decode(q, C(None, lat, lens), scale=0.04, **kw)
+    with pytest.raises(ValueError):
+        binding.window_mla_prefill(q, C(None, lat[:1], None), 1 << 64, 5, 0, 0.04)
+
+
+def test_norm_rope_binding_range(L):
+    x, table, pos = torch.zeros((3, 2, 128), dtype=torch.bfloat16), torch.zeros((9, 64)), torch.zeros(3, dtype=torch.int64)
+    for off in (1 << 32, -(1 << 32), 72, -8):
+        with pytest.raises(ValueError):
+            binding.norm_rope(binding.Heads(x), None, table, pos, rope_offset=off)
