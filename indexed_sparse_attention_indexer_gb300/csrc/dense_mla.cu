@@ -1017,8 +1017,9 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         if (!(ok = wait32(sums_set, (uint32_t)pieces & 1u))) break;
         const float2 other = make_float2(sums[(set ^ 1) * kM].x, sums[(set ^ 1) * kM].y);
         m_ref = fmaxf(m_mine, other.x);
-        l_sum = m_mine == -INFINITY ? 0.f : l_mine * exp2f(m_mine - m_ref);
-        if (other.x != -INFINITY) l_sum += other.y * exp2f(other.x - m_ref);
+        // (a sum without a maximum is 0, or NaN: every logit was)
+        l_sum = l_mine * (m_mine == -INFINITY ? 1.f : exp2f(m_mine - m_ref));
+        l_sum += other.y * (other.x == -INFINITY ? 1.f : exp2f(other.x - m_ref));
       }
       if (!(ok = wait32(o_done, (uint32_t)pieces & 1u))) break;
       ++pieces;

@@ -406,3 +406,38 @@ def test_long_offsets():
     L = (q[0].double().abs() @ c.abs().T * SCALE).amax(-1)[:, None]
     assert bool(((out[0].double() - ref).abs() <= 2.0 ** -8 * (A + 2 * ref.abs()) + 2.0 ** -11 * L * A).all())
     assert binding.device_status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens", [[70, 300], [9000, 70]], ids=["whole", "split"])
+def test_non_finite_queries(lens, fp8):
+    """A head whose query holds NaN gets NaN outputs and a NaN lse, the others what they get without."""
+    case = Case(lens, 1, 32, 64, fp8, seed=15, garbage=False)
+    cache = case.device()
+    good, good_lse = (t.clone() for t in binding.dense_mla_decode(case.d_q, cache, SCALE))
+    case.d_q[0, 5, 7] = math.nan
+    case.d_q[1, 31, 570] = math.nan
+    out, lse = binding.dense_mla_decode(case.d_q, cache, SCALE)
+    torch.cuda.synchronize()
+    bad = torch.zeros((2, 32), dtype=torch.bool, device=DEV)
+    bad[0, 5] = bad[1, 31] = True
+    assert bool(torch.isnan(out[bad]).all()) and bool(torch.isnan(lse[bad]).all())
+    assert torch.equal(out[~bad], good[~bad]) and torch.equal(lse[~bad], good_lse[~bad])
+
+
+@pytest.mark.parametrize("where", ["latent", "rope", "scale"])
+def test_non_finite_fp8_rows(where):
+    """A row that only the later tokens of a step see, with a NaN code or an infinite scale."""
+    case = Case([200, 200], 4, 16, 16, True, seed=16, garbage=False)
+    views = decode_views(case)
+    at = int(case.phys(0, torch.tensor([198])))
+    case.latent.view(torch.uint8).view(-1, 576)[at, :] = 0x31             # (no zero codes: inf * 0 is NaN)
+    if where == "scale":
+        case.scales.view(-1, 5)[at, 1] = math.inf
+    else:
+        case.latent.view(torch.uint8).view(-1, 576)[at, 300 if where == "latent" else 560] = 0xFF
+    cache = case.device()
+    out, lse = binding.dense_mla_decode(case.d_q, cache, SCALE, tokens_per_seq=4)
+    torch.cuda.synchronize()
+    check(case, out, lse, [v for v in views if v[0] not in (2, 3)])
+    assert bool(torch.isnan(out[2:4]).any(-1).all())
