@@ -91,7 +91,7 @@ struct Layout {                                // shared memory, bytes
   static constexpr int stages = F8 ? 3 : 4;
   static constexpr int threads = F8 ? 640 : 512;
   static constexpr int sets = F8 ? 1 : 2;      // softmax sets
-  static constexpr int fill_warps = F8 ? 4 : 2;   // warps that hand a tile to the tensor core
+  static constexpr int fill_warps = F8 ? 9 : 2;   // warps that pass a slot of the ring on
   static constexpr int c = 0;
   static constexpr int raw = c + stages * kStageBytes;
   static constexpr int p = raw + (F8 ? kRawStages * kRawBytes : 0);   // P [128 x 64] bf16
@@ -471,16 +471,20 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     uint32_t issued = 0, issued_edge = 0;      // stages with a copy in flight; into an edge tile
     const int64_t cache_rows = a.c.block_table ? a.c.num_pages * a.c.page_size : a.c.batch * a.c.s_max;
     bool ok = true;
-    // (FP8 rows: warp 0 alone, the tiles' copies go to the raw stages)
+    // Every warp that waits for the ring's slots waits for each of them and arrives on
+    // each of their full barriers, whoever fills it: a phase that it has not seen cannot
+    // pass.  (A warp that left slots out could not tell by a parity which release it saw.)
+    // FP8 rows: the ring is filled by the converting warps and, with queries, warp 1;
+    // warp 0's copies go to the raw stages.
 #pragma unroll 1
-    while (ok && (!F8 || warp == 0) && next_piece(a, plan, walk, x)) {
+    while (ok && next_piece(a, plan, walk, x)) {
 #pragma unroll 1
-      for (int i = 0; i < 2; ++i, ++slot) {
+      for (int i = 0; i < 2 && (!F8 || warp == 1); ++i, ++slot) {
         const int stage = slot % kStages;
         if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u))) break;
         if (lane == 0) {
-          // (bf16 rows: by warp 1, while warp 0 goes on to the tiles)
-          if (F8 || warp == 1) {
+          // (by warp 1, while warp 0 goes on to the tiles)
+          if (warp == 1) {
             uint8_t* st = smem + Y::c + stage * kStageBytes;
             mbar_arrive_expect_tx(&full[stage], 2 * kM * 128);
             issued |= 1u << stage;
@@ -488,8 +492,6 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
             for (int bx = 0; bx < 2; ++bx)
               tma_load_2d(st + bx * kM * 128, &qmap, (int)rho * 256 + (2 * i + bx) * 64,
                           x.grp.row0 * a.H, &full[stage]);
-            if (F8)
-              for (int w = 1; w < Y::fill_warps; ++w) mbar_arrive(&full[stage]);
           } else {
             mbar_arrive(&full[stage]);
           }
@@ -499,8 +501,9 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       int asked = x.t0;
 #pragma unroll 1
       for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
-        const int stage = F8 ? tg % kRawStages : slot % kStages;
-        const uint32_t ph = (uint32_t)(F8 ? tg / kRawStages : slot / kStages) & 1u;
+        const bool raw = F8 && warp == 0;
+        const int stage = raw ? tg % kRawStages : slot % kStages;
+        const uint32_t ph = (uint32_t)(raw ? tg / kRawStages : slot / kStages) & 1u;
         const int p0 = tile_pos(x.grp, t);
         uint8_t* st = smem + (F8 ? Y::raw + stage * kRawBytes : Y::c + stage * kStageBytes);
         const bool whole = F8 || all_see(a, x.grp, p0, kNp);
@@ -557,7 +560,8 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           }
           __syncwarp();
         } else {
-          // bf16 rows, warp 1: passes a whole tile on and cleans one at an edge first
+          // warp 1 passes a whole tile on and cleans one at an edge first (FP8 rows: passes
+          // on the slot, which holds no copy of its own any more)
           if (!whole) {
             // rows that no token sees become zeros (weight 0 times what they hold must
             // be 0); a row that only some tokens see and that holds NaN or an infinity
@@ -593,6 +597,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           } else if (!(ok = wait32(&empty[stage], ph ^ 1))) {
             break;
           }
+          if (F8) issued &= ~(1u << stage);
           if (lane == 0) mbar_arrive(&full[stage]);
         }
       }
@@ -608,7 +613,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         if ((issued_edge >> s) & 1u) mbar_wait(&landed[s], ((edge_ph >> s) & 1u) ^ 1u, &no_abort, err, 100000000ull);
         else mbar_wait(&full[s], (uint32_t)(last / kStages) & 1u, &no_abort, err, 100000000ull);
       }
-      if (F8)
+      if (F8 && warp == 0)
         for (int i = max(0, tg - kRawStages); i < tg; ++i)
           mbar_wait(&raw_full[i % kRawStages], (uint32_t)(i / kRawStages) & 1u, &no_abort, err, 100000000ull);
     }
@@ -634,9 +639,11 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     };
 #pragma unroll 1
     while (ok && next_piece(a, plan, walk, x)) {
-      // (the query slots are waited for too: a skipped phase could not be told apart)
-      for (int i = 0; i < 2 && ok; ++i, ++slot)
+      // (the query slots, like the other group's tiles below, are waited for and passed on)
+      for (int i = 0; i < 2 && ok; ++i, ++slot) {
         ok = wait32(&empty[slot % kStages], ((uint32_t)(slot / kStages) & 1u) ^ 1u);
+        if (ok && lane == 0) mbar_arrive(&full[slot % kStages]);
+      }
       if (!ok) break;
       const int first = x.t0 + ((tg ^ turn) & 1);
       int row_next = lookup(first);
@@ -645,8 +652,9 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
 #pragma unroll 1
       for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
         const int stage = slot % kStages, rs = tg % kRawStages, p = tile_pos(x.grp, t) + rr;
-        if ((tg & 1) != turn) {                  // (the other group's: no phase goes unseen)
+        if ((tg & 1) != turn) {
           if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u))) break;
+          if (lane == 0) mbar_arrive(&full[stage]);
           continue;
         }
         const float2 sc_next = scales(row_next);

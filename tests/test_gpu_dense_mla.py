@@ -441,3 +441,33 @@ def test_non_finite_fp8_rows(where):
     torch.cuda.synchronize()
     check(case, out, lse, [v for v in views if v[0] not in (2, 3)])
     assert bool(torch.isnan(out[2:4]).any(-1).all())
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("name", ["one_tile", "two_tiles", "window_two_tiles", "window_three_tiles", "mixed"])
+def test_many_short_groups(name, fp8):
+    """Many groups of one to three tiles for every pair of SMs: query slices and tiles take turns
+    in the ring, and every one of its slots has to be seen by all who wait for it."""
+    T, H, page, window, sink, lens = {
+        "one_tile": (1, 128, 0, None, 0, [1 + 7 * i % 64 for i in range(700)]),
+        "two_tiles": (1, 128, 16, None, 0, [65 + 11 * i % 64 for i in range(700)]),
+        "window_two_tiles": (850, 64, 16, 40, 0, [1000]),
+        "window_three_tiles": (850, 64, 16, 59, 4, [2855]),
+        "mixed": (1, 128, 64, None, 0, [(1, 70, 130, 0, 64, 200, 65)[i % 7] for i in range(700)]),
+    }[name]
+    case = Case(lens, T, H, page, fp8, seed=17)
+    if T == 1:
+        views = decode_views(case)
+    else:
+        views = [(t, 0, spots(lens[0] - T + t + 1, window, sink)) for t in range(T)]
+    cache = case.device([(b, pos) for _, b, pos in views])
+    runs = []
+    for _ in range(20):
+        if T == 1:
+            runs.append(binding.dense_mla_decode(case.d_q, cache, SCALE))
+        else:
+            runs.append(binding.window_mla_prefill(case.d_q, cache, lens[0] - T, window, sink, SCALE))
+    torch.cuda.synchronize()
+    check(case, *runs[0], views[::13] + views[-5:])
+    for out, lse in runs[1:]:
+        assert torch.equal(out, runs[0][0]) and torch.equal(lse, runs[0][1])
