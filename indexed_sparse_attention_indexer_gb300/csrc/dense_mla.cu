@@ -20,7 +20,7 @@
 // out whole groups costs at most kWholeSlack tiles more, groups stay whole and
 // nothing is joined.
 //
-// Roles in a CTA (16 warps; FP8 rows: 20), each walking the same list of pieces; the tile
+// Roles in a CTA (16 warps; FP8 rows: 24), each walking the same list of pieces; the tile
 // pipeline runs on across pieces:
 //   producers (warps 0-1): a tile's rows into a 128-byte-swizzled stage (ring
 //     of 4) by TMA boxes; tiles at an edge (not wholly visible to every token
@@ -30,13 +30,12 @@
 //   exchange (warps 4-7): the group's query slice into TMEM (rope half: shared
 //     memory); this CTA's partial logits out of TMEM into the peer's buffer;
 //   softmax (warps 8-15, one row per thread, two sets of four warps, a half of each
-//     tile's positions a set; FP8 rows: warps 8-11, both halves in turn): own partial
-//     plus the peer's, mask, online softmax in log2 units with a lazily moved
+//     tile's positions a set): own partial plus the peer's, mask, online softmax in log2 units with a lazily moved
 //     reference max (the accumulator is rescaled only when the max grows by more
 //     than 2^8), P in bf16 to shared memory, and the epilogue;
 //   value issuer (warp 2): O += P . V from the same stage, a half tile at a time;
-//   conversion (FP8 rows, warps 12-19): codes times scales, rounded to bf16, out of
-//     the raw tiles into the stages; two groups of four warps take tiles in turn.
+//   conversion (FP8 rows, warps 16-23): codes times scales, rounded to bf16, out of
+//     the raw tiles into the stages.
 // Exchange and softmax warps of lane quarters without rows (few heads) leave at
 // once: what the tensor core computes there is never read.
 // Every wait is bounded; the cluster syncs after set-up and before exit.
@@ -62,10 +61,11 @@ constexpr int kRopeHalf = 32;                  // rope dims of each CTA
 constexpr int kRopeOff = 4 * kBlockBytes;      // stage: four 64-dim blocks, then 64 rows of rope dims
 constexpr int kRowBytes = 4 * 128 + kRopeHalf * 2;
 constexpr int kStageBytes = kNp * kRowBytes;   // 36 KB
-// 16 warps (four per SM sub-partition), at most 128 registers a thread; FP8 rows: 20, 96
+// 16 warps (four per SM sub-partition), at most 128 registers a thread; FP8 rows: 24, 80
 constexpr int kProducers = 2;                  // warps 0-1
 constexpr int kPvWarp = 2;
 constexpr int kQkWarp = 3;                     // then exchange: warps 4-7
+constexpr int kConvWarp0 = 16;                 // FP8 rows: conversion, warps 16-23
 constexpr int kSmWarp0 = 8;                    // softmax: warps 8-11 first halves, 12-15 second ones
 constexpr int kMaxClusters = 128;
 constexpr int kWholeSlack = 8;
@@ -79,9 +79,11 @@ constexpr int kHalf = 32;                      // positions of a softmax step
 constexpr int kXRing = 3;
 constexpr int kXBytes = kM * kQuarter * 4;
 
-// FP8 rows: raw tiles of codes land beside the ring and are converted into it.  One
-// group of four warps takes 1.8 us for a tile and was what bounded them; two groups
-// in turn: 107.6 -> 103.5 us for 777 tokens of 32 heads with a window of 511.
+// FP8 rows: raw tiles of codes land beside the ring and are converted into it by eight
+// warps (with four: 308 us instead of 289 for 64 x 8192 x 128 heads).  A stage is held
+// from the start of its conversion to the end of its P.V, 14,000 cycles over the three
+// stages that there is room for (conversion 3500, logits 2400, exchange 3300, softmax and
+// P.V 3400): that bounds them, not the bytes.
 constexpr int kRawStages = 2;
 constexpr int kRawRope = 2 * kNp * 128;        // two blocks of 128 dims, then 64 rows of 32 rope dims
 constexpr int kRawBytes = kNp * (256 + kRopeHalf);
@@ -89,8 +91,7 @@ constexpr int kRawBytes = kNp * (256 + kRopeHalf);
 template <bool F8>
 struct Layout {                                // shared memory, bytes
   static constexpr int stages = F8 ? 3 : 4;
-  static constexpr int threads = F8 ? 640 : 512;
-  static constexpr int sets = F8 ? 1 : 2;      // softmax sets
+  static constexpr int threads = F8 ? 768 : 512;
   static constexpr int fill_warps = F8 ? 9 : 2;   // warps that pass a slot of the ring on
   static constexpr int c = 0;
   static constexpr int raw = c + stages * kStageBytes;
@@ -207,6 +208,33 @@ __device__ __forceinline__ int row_of(const CacheView& c, int b, int p, int* err
   return page * c.page_size + (p - pg * c.page_size);
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // 16 E4M3 codes times their tile scale, the fp32 product rounded to bf16 (lo =
 // codes 0..7).
 __device__ __forceinline__ void e4m3x16_scaled(const uint4& v, float sc, uint4& lo, uint4& hi) {
@@ -215,7 +243,8 @@ __device__ __forceinline__ void e4m3x16_scaled(const uint4& v, float sc, uint4& 
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i] * sc, f[2 * i + 1] * sc);
+    const float2 p = unpack2(mul2(pack2(f[2 * i], f[2 * i + 1]), pack2(sc, sc)));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
   lo = make_uint4(w[0], w[1], w[2], w[3]);
@@ -297,28 +326,6 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w, bool wi
   }
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 template <bool F8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<F8>::threads, 1)
 dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
@@ -366,7 +373,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], (1 + Y::sets) * plan.live);
+      mbar_init(&s_empty[i], 3 * plan.live);
       mbar_init(&p_empty[i], 1);
       mbar_init(&p_full[i], plan.live);
     }
@@ -378,11 +385,11 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     }
     for (int i = 0; i < kRawStages; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 4);
+      mbar_init(&raw_empty[i], 8);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&ref_set[i], 1);
-    mbar_init(sums_set, plan.live * Y::sets);
-    mbar_init(o_free, plan.live * Y::sets);
+    mbar_init(sums_set, plan.live * 2);
+    mbar_init(o_free, plan.live * 2);
     taken_s[0] = taken_s[1] = 0u;
     s_abort = 0;
     s_err = err;
@@ -617,13 +624,12 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         for (int i = max(0, tg - kRawStages); i < tg; ++i)
           mbar_wait(&raw_full[i % kRawStages], (uint32_t)(i / kRawStages) & 1u, &no_abort, err, 100000000ull);
     }
-  } else if (F8 && warp >= kSmWarp0 + 4) {
+  } else if (F8 && warp >= kConvWarp0) {
     // ======================= FP8: conversion ======================================
-    // Two threads a row, nine pieces of 16 codes each: code * tile scale, rounded to
-    // bf16, into the ring stage.  The page is looked up two tiles ahead and the scales
+    // Two threads for each half of a row: four pieces of 16 codes and half of the rope
+    // piece for each: code * tile scale, rounded to bf16, into the ring stage.  The page is looked up two tiles ahead and the scales
     // are loaded one ahead, within a piece.
-    const int c_thread = (tid - (kSmWarp0 + 4) * 32) & 127, rr = c_thread & 63, hh = c_thread >> 6;
-    const int turn = (warp - kSmWarp0 - 4) >> 2; // the two groups of warps take the tiles in turn
+    const int c_thread = tid - kConvWarp0 * 32, rr = c_thread & 63, hh = c_thread >> 7, part = (c_thread >> 6) & 1;
     const int s0 = (int)rho * 2 + hh;            // tile of this thread's 128 latent dims
     Piece x = {};
     int slot = 0, tg = 0;
@@ -639,26 +645,20 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     };
 #pragma unroll 1
     while (ok && next_piece(a, plan, walk, x)) {
-      // (the query slots, like the other group's tiles below, are waited for and passed on)
+      // (the query slots are waited for and passed on)
       for (int i = 0; i < 2 && ok; ++i, ++slot) {
         ok = wait32(&empty[slot % kStages], ((uint32_t)(slot / kStages) & 1u) ^ 1u);
         if (ok && lane == 0) mbar_arrive(&full[slot % kStages]);
       }
       if (!ok) break;
-      const int first = x.t0 + ((tg ^ turn) & 1);
-      int row_next = lookup(first);
+      int row_next = lookup(x.t0);
       float2 sc = scales(row_next);
-      row_next = lookup(first + 2);
+      row_next = lookup(x.t0 + 1);
 #pragma unroll 1
       for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
         const int stage = slot % kStages, rs = tg % kRawStages, p = tile_pos(x.grp, t) + rr;
-        if ((tg & 1) != turn) {
-          if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u))) break;
-          if (lane == 0) mbar_arrive(&full[stage]);
-          continue;
-        }
         const float2 sc_next = scales(row_next);
-        row_next = lookup(t + 4);
+        row_next = lookup(t + 2);
         const bool whole = all_see(a, x.grp, p - rr, kNp);       // the tile
         const bool seen = whole || any_sees(a, x.grp, p), partly = seen && !whole && !all_see(a, x.grp, p, 1);
         const uint8_t* raw = smem + Y::raw + rs * kRawBytes;
@@ -666,11 +666,10 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         if (!(ok = wait32(&raw_full[rs], (uint32_t)(tg / kRawStages) & 1u))) break;
         if (!(ok = wait32(&empty[stage], ((uint32_t)(slot / kStages) & 1u) ^ 1u))) break;
         bool bad = false;
-// (rolled: the roles share the instruction cache; nine copies took 3.3 us a tile,
-// the loop takes 1.8)
 #pragma unroll 1
-        for (int u = 0; u < 9; ++u) {
-          const bool rope = u == 8;              // (last: it takes the row's NaN)
+        for (int i = 0; i < 5; ++i) {
+          const bool rope = i == 4;              // (last: it takes the pieces' NaN)
+          const int u = part * 4 + i;
           uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
           if (seen) {
             const uint4 v = *reinterpret_cast<const uint4*>(
@@ -685,10 +684,12 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
             }
             if (rope && bad) lo = hi = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
           }
-          uint8_t* blk = rope ? st + kRopeOff : st + (hh * 2 + (u >> 2)) * kBlockBytes;
-          const uint32_t ch = rope ? (uint32_t)hh * 2 : (uint32_t)(u & 3) * 2;
-          *reinterpret_cast<uint4*>(blk + (rope ? sw64_offset(rr, ch) : sw128_offset(rr, ch))) = lo;
-          *reinterpret_cast<uint4*>(blk + (rope ? sw64_offset(rr, ch + 1) : sw128_offset(rr, ch + 1))) = hi;
+          uint8_t* blk = st + (hh * 2 + part) * kBlockBytes;
+          if (rope)
+            *reinterpret_cast<uint4*>(st + kRopeOff + sw64_offset(rr, hh * 2 + part)) = part ? hi : lo;
+          else
+            *reinterpret_cast<uint4*>(blk + sw128_offset(rr, 2 * i)) = lo,
+            *reinterpret_cast<uint4*>(blk + sw128_offset(rr, 2 * i + 1)) = hi;
         }
         sc = sc_next;
         fence_proxy_async_smem();   // the tensor core reads the stage through the async proxy
@@ -854,10 +855,9 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     }
   } else {
     // ======================= softmax + epilogue ==================================
-    // Two sets of four warps take a half each of every tile (FP8 rows: one set both,
-    // in turn).  The reference maximum passes from half to half as soon as a half's
+    // Two sets of four warps take a half each of every tile.  The reference maximum passes from half to half as soon as a half's
     // maximum is known, and each half has its own P.V; each set sums its own weights.
-    const int set = Y::sets == 2 ? (warp - kSmWarp0) >> 2 : 0;
+    const int set = (warp - kSmWarp0) >> 2, hf = set;        // the half of a tile
     const int quarter = warp & 3, m = quarter * 32 + lane;   // row = TMEM lane
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     uint8_t* const pbuf = smem + Y::p;
@@ -883,152 +883,140 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         const int sb = tg & 1;
         if (!(ok = wait32(&s_full[sb], (uint32_t)(tg >> 1) & 1u))) break;
         tc_fence_after();
-#pragma unroll 1
-        for (int hf = set; hf < 2; hf += Y::sets) {
-          const int p0 = tile_pos(x.grp, t) + hf * kHalf;
-          // this CTA's partial logits and the peer's
-          float v[kHalf];
-          tmem_ld32(tmem + lane_base + TM_S + sb * kNp + hf * kHalf, v);
-          const int n0 = tg * 2, b0 = hf * kXRing + n0 % kXRing, b1 = hf * kXRing + (n0 + 1) % kXRing;
-          const uint32_t ph0 = (uint32_t)(n0 / kXRing) & 1u, ph1 = (uint32_t)((n0 + 1) / kXRing) & 1u;
-          const bool here0 = ask_cluster(&x_full[b0], ph0), here1 = ask_cluster(&x_full[b1], ph1);
-          if (!(ok = settle(here0 && here1, &x_full[b0], ph0) && settle(here1, &x_full[b1], ph1))) break;
-          float4 y[kHalf / 4];
+        const int p0 = tile_pos(x.grp, t) + hf * kHalf;
+        // this CTA's partial logits and the peer's
+        float v[kHalf];
+        tmem_ld32(tmem + lane_base + TM_S + sb * kNp + hf * kHalf, v);
+        const int n0 = tg * 2, b0 = hf * kXRing + n0 % kXRing, b1 = hf * kXRing + (n0 + 1) % kXRing;
+        const uint32_t ph0 = (uint32_t)(n0 / kXRing) & 1u, ph1 = (uint32_t)((n0 + 1) / kXRing) & 1u;
+        const bool here0 = ask_cluster(&x_full[b0], ph0), here1 = ask_cluster(&x_full[b1], ph1);
+        if (!(ok = settle(here0 && here1, &x_full[b0], ph0) && settle(here1, &x_full[b1], ph1))) break;
+        float4 y[kHalf / 4];
 #pragma unroll
-          for (int g4 = 0; g4 < kHalf / 4; ++g4)
-            y[g4] = *reinterpret_cast<const float4*>(xrow + (g4 < kQuarter / 4 ? b0 : b1) * kXBytes +
-                                                     g4 % (kQuarter / 4) * (kM * 16));
-          tmem_ld_wait();
-          if (Y::sets == 2 || hf == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[sb]);
-          }
+        for (int g4 = 0; g4 < kHalf / 4; ++g4)
+          y[g4] = *reinterpret_cast<const float4*>(xrow + (g4 < kQuarter / 4 ? b0 : b1) * kXBytes +
+                                                   g4 % (kQuarter / 4) * (kM * 16));
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[sb]);
 #pragma unroll
-          for (int g4 = 0; g4 < kHalf / 4; ++g4) {
-            const int j = 4 * g4;
-            const float2 s0 = unpack2(add2(pack2(v[j], v[j + 1]), pack2(y[g4].x, y[g4].y)));
-            const float2 s1 = unpack2(add2(pack2(v[j + 2], v[j + 3]), pack2(y[g4].z, y[g4].w)));
-            v[j] = s0.x; v[j + 1] = s0.y; v[j + 2] = s1.x; v[j + 3] = s1.y;
-          }
-          __syncwarp();
-          if (lane == 0) {                       // what was read is free; lane quarter 0 re-arms first
-            if (quarter == 0) {
-              mbar_arrive_expect_tx_relaxed(&x_full[b0], x_bytes);
-              mbar_arrive_expect_tx_relaxed(&x_full[b1], x_bytes);
-            }
-            mbar_arrive_remote_relaxed(xempty_remote + b0 * 8);
-            mbar_arrive_remote_relaxed(xempty_remote + b1 * 8);
-          }
-          // masked positions: -inf
-          if (__builtin_expect(!all_see(a, x.grp, p0, kHalf), 0)) {
-            const uint32_t see = (uint32_t)(low_bits(n_row - p0) &
-                                            (~low_bits(lo_row - p0) | low_bits((int)a.n_sink - p0)));
-#pragma unroll
-            for (int j = 0; j < kHalf; ++j) v[j] = (see >> j) & 1u ? v[j] : -INFINITY;
-          }
-          const bool ref_here = Y::sets == 1 || (tg == 0 && hf == 0) ||
-                                mbar_test_wait(&ref_set[quarter], (uint32_t)(hf ^ 1));
-          float mx[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(v[j], v[j + 4]);
-#pragma unroll
-          for (int j = 8; j < kHalf; j += 8)     // (three-operand maxima)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], v[j + e]), v[j + 4 + e]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          // (an infinite sum is a masked or an overflowed one: not scaled, 0 * inf is no logit)
-          const float tmax = top == -INFINITY ? -INFINITY : top * sl2;
-          // the reference after the half before (the other set's), moved when this
-          // half's maximum exceeds it by far; what is in the accumulator moves with it
-          if (Y::sets == 2 && !(ok = settle(ref_here, &ref_set[quarter], (uint32_t)(hf ^ 1)))) break;
-          const float m_prev = t == x.t0 && hf == 0 ? -INFINITY : Y::sets == 2 ? ref_s[0] : m_mine;
-          float m_ref = m_prev, alpha = 1.f;
-          bool rescale = false;
-          if (m_prev == -INFINITY) {
-            m_ref = tmax;                        // nothing in the accumulator yet
-          } else if (tmax > m_prev + kRescaleLog2) {
-            alpha = ex2_approx(m_prev - tmax);
-            m_ref = tmax;
-            rescale = true;
-          }
-          if (Y::sets == 2) {
-            ref_s[0] = m_ref;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ref_set[quarter]);
-          }
-          const bool p_here = tg == 0 || mbar_test_wait(&p_empty[hf], (uint32_t)(tg - 1) & 1u);
-          // weights 2^(logit * sl2 - reference), rounded to bf16 for P.V (half a step, to
-          // nearest: the errors of a row's weights average out) and summed in fp32
-          // before the rounding, which keeps the lse exact to fp32
-          uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
-          uint32_t pk[kHalf / 2];
-          const float nmr = (m_ref == -INFINITY) ? 0.f : -m_ref;
-          const uint64_t scale2 = pack2(sl2, sl2), nmr2 = pack2(nmr, nmr);
-#pragma unroll
-          for (int j = 0; j < kHalf / 2; ++j) {
-            const float2 x2 = unpack2(fma2(pack2(v[2 * j], v[2 * j + 1]), scale2, nmr2));
-            const float e0 = ex2_approx(x2.x), e1 = ex2_approx(x2.y);
-            sum2[j & 3] = add2(sum2[j & 3], pack2(e0, e1));
-            const __nv_bfloat162 p2 = __floats2bfloat162_rn(e0, e1);
-            pk[j] = *reinterpret_cast<const uint32_t*>(&p2);
-          }
-          const float2 tot = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
-          if (m_mine != m_ref) l_mine *= m_mine == -INFINITY ? 0.f : ex2_approx(m_mine - m_ref);
-          m_mine = m_ref;
-          l_mine += tot.x + tot.y;
-          // This half of the P tile is free once its last P.V is done; a piece's first P
-          // also waits until the output before is read out.
-          if (!(ok = settle(p_here, &p_empty[hf], (uint32_t)(tg - 1) & 1u))) break;
-          if (t == x.t0 && hf == 0 && pieces > 0 &&
-              !(ok = wait32(o_free, (uint32_t)(pieces - 1) & 1u))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, hf * 4 + u)) =
-                make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
-          // TMEM loads and stores are warp-collective: rescale when any row of the
-          // warp needs it (the others multiply by 1)
-          if (__builtin_expect(__any_sync(0xffffffffu, rescale), 0)) {
-            // Nothing may be under way into the accumulator: the other half's P.V just
-            // before this one is done too.  (Its phase before that one is over, so the
-            // parity tells: that P.V was committed before this half's last one.)
-            if (!(ok = wait32(&p_empty[hf ^ 1], (uint32_t)(hf == 0 ? tg - 1 : tg) & 1u))) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c0 = 0; c0 < 256; c0 += 16) {
-              float o[16];
-              tmem_ld16(tmem + lane_base + TM_O + c0, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= alpha;
-              tmem_st16(tmem + lane_base + TM_O + c0, o);
-            }
-            tmem_st_wait();
-          }
-          fence_proxy_async_smem();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[hf]);
+        for (int g4 = 0; g4 < kHalf / 4; ++g4) {
+          const int j = 4 * g4;
+          const float2 s0 = unpack2(add2(pack2(v[j], v[j + 1]), pack2(y[g4].x, y[g4].y)));
+          const float2 s1 = unpack2(add2(pack2(v[j + 2], v[j + 3]), pack2(y[g4].z, y[g4].w)));
+          v[j] = s0.x; v[j + 1] = s0.y; v[j + 2] = s1.x; v[j + 3] = s1.y;
         }
-        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) {                       // what was read is free; lane quarter 0 re-arms first
+          if (quarter == 0) {
+            mbar_arrive_expect_tx_relaxed(&x_full[b0], x_bytes);
+            mbar_arrive_expect_tx_relaxed(&x_full[b1], x_bytes);
+          }
+          mbar_arrive_remote_relaxed(xempty_remote + b0 * 8);
+          mbar_arrive_remote_relaxed(xempty_remote + b1 * 8);
+        }
+        // masked positions: -inf
+        if (__builtin_expect(!all_see(a, x.grp, p0, kHalf), 0)) {
+          const uint32_t see = (uint32_t)(low_bits(n_row - p0) &
+                                          (~low_bits(lo_row - p0) | low_bits((int)a.n_sink - p0)));
+#pragma unroll
+          for (int j = 0; j < kHalf; ++j) v[j] = (see >> j) & 1u ? v[j] : -INFINITY;
+        }
+        const bool ref_here = (tg == 0 && hf == 0) || mbar_test_wait(&ref_set[quarter], (uint32_t)(hf ^ 1));
+        float mx[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(v[j], v[j + 4]);
+#pragma unroll
+        for (int j = 8; j < kHalf; j += 8)     // (three-operand maxima)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], v[j + e]), v[j + 4 + e]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // (an infinite sum is a masked or an overflowed one: not scaled, 0 * inf is no logit)
+        const float tmax = top == -INFINITY ? -INFINITY : top * sl2;
+        // the reference after the half before (the other set's), moved when this
+        // half's maximum exceeds it by far; what is in the accumulator moves with it
+        if (!(ok = settle(ref_here, &ref_set[quarter], (uint32_t)(hf ^ 1)))) break;
+        const float m_prev = t == x.t0 && hf == 0 ? -INFINITY : ref_s[0];
+        float m_ref = m_prev, alpha = 1.f;
+        bool rescale = false;
+        if (m_prev == -INFINITY) {
+          m_ref = tmax;                        // nothing in the accumulator yet
+        } else if (tmax > m_prev + kRescaleLog2) {
+          alpha = ex2_approx(m_prev - tmax);
+          m_ref = tmax;
+          rescale = true;
+        }
+        ref_s[0] = m_ref;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ref_set[quarter]);
+        const bool p_here = tg == 0 || mbar_test_wait(&p_empty[hf], (uint32_t)(tg - 1) & 1u);
+        // weights 2^(logit * sl2 - reference), rounded to bf16 for P.V (half a step, to
+        // nearest: the errors of a row's weights average out) and summed in fp32
+        // before the rounding, which keeps the lse exact to fp32
+        uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t pk[kHalf / 2];
+        const float nmr = (m_ref == -INFINITY) ? 0.f : -m_ref;
+        const uint64_t scale2 = pack2(sl2, sl2), nmr2 = pack2(nmr, nmr);
+#pragma unroll
+        for (int j = 0; j < kHalf / 2; ++j) {
+          const float2 x2 = unpack2(fma2(pack2(v[2 * j], v[2 * j + 1]), scale2, nmr2));
+          const float e0 = ex2_approx(x2.x), e1 = ex2_approx(x2.y);
+          sum2[j & 3] = add2(sum2[j & 3], pack2(e0, e1));
+          const __nv_bfloat162 p2 = __floats2bfloat162_rn(e0, e1);
+          pk[j] = *reinterpret_cast<const uint32_t*>(&p2);
+        }
+        const float2 tot = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
+        if (m_mine != m_ref) l_mine *= m_mine == -INFINITY ? 0.f : ex2_approx(m_mine - m_ref);
+        m_mine = m_ref;
+        l_mine += tot.x + tot.y;
+        // This half of the P tile is free once its last P.V is done; a piece's first P
+        // also waits until the output before is read out.
+        if (!(ok = settle(p_here, &p_empty[hf], (uint32_t)(tg - 1) & 1u))) break;
+        if (t == x.t0 && hf == 0 && pieces > 0 &&
+            !(ok = wait32(o_free, (uint32_t)(pieces - 1) & 1u))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, hf * 4 + u)) =
+              make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+        // TMEM loads and stores are warp-collective: rescale when any row of the
+        // warp needs it (the others multiply by 1)
+        if (__builtin_expect(__any_sync(0xffffffffu, rescale), 0)) {
+          // Nothing may be under way into the accumulator: the other half's P.V just
+          // before this one is done too.  (Its phase before that one is over, so the
+          // parity tells: that P.V was committed before this half's last one.)
+          if (!(ok = wait32(&p_empty[hf ^ 1], (uint32_t)(hf == 0 ? tg - 1 : tg) & 1u))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < 256; c0 += 16) {
+            float o[16];
+            tmem_ld16(tmem + lane_base + TM_O + c0, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tmem_st16(tmem + lane_base + TM_O + c0, o);
+          }
+          tmem_st_wait();
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[hf]);
       }
       if (!ok) break;
       // ---- the piece's sum over both sets (a set without tiles has none) --------
-      float m_ref = m_mine, l_sum = l_mine;
-      if (Y::sets == 2) {
-        volatile float2* const sums = reinterpret_cast<float2*>(smem + Y::sums) + (pieces & 1) * 2 * kM + m;
-        sums[set * kM].x = m_mine;
-        sums[set * kM].y = l_mine;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sums_set);
-        if (!(ok = wait32(sums_set, (uint32_t)pieces & 1u))) break;
-        const float2 other = make_float2(sums[(set ^ 1) * kM].x, sums[(set ^ 1) * kM].y);
-        m_ref = fmaxf(m_mine, other.x);
-        // (a sum without a maximum is 0, or NaN: every logit was)
-        l_sum = l_mine * (m_mine == -INFINITY ? 1.f : exp2f(m_mine - m_ref));
-        l_sum += other.y * (other.x == -INFINITY ? 1.f : exp2f(other.x - m_ref));
-      }
+      volatile float2* const sums = reinterpret_cast<float2*>(smem + Y::sums) + (pieces & 1) * 2 * kM + m;
+      sums[set * kM].x = m_mine;
+      sums[set * kM].y = l_mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sums_set);
+      if (!(ok = wait32(sums_set, (uint32_t)pieces & 1u))) break;
+      const float2 other = make_float2(sums[(set ^ 1) * kM].x, sums[(set ^ 1) * kM].y);
+      const float m_ref = fmaxf(m_mine, other.x);
+      // (a sum without a maximum is 0, or NaN: every logit was)
+      float l_sum = l_mine * (m_mine == -INFINITY ? 1.f : exp2f(m_mine - m_ref));
+      l_sum += other.y * (other.x == -INFINITY ? 1.f : exp2f(other.x - m_ref));
       if (!(ok = wait32(o_done, (uint32_t)pieces & 1u))) break;
       ++pieces;
       tc_fence_after();
@@ -1051,7 +1039,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           entire ? (void*)(a.out + orow * DSI_D_LATENT + rho * 256)
                  : (void*)(ws.o + ((int64_t)slot * kM + m) * DSI_D_LATENT + rho * 256));
 #pragma unroll 1
-      for (int c0 = set * 128; c0 < set * 128 + 256 / Y::sets; c0 += 32) {
+      for (int c0 = set * 128; c0 < set * 128 + 128; c0 += 32) {
         float o[32];
         __syncwarp();        // rows without an output skip the stores of the round before
         tmem_ld32(tmem + lane_base + TM_O + c0, o);
