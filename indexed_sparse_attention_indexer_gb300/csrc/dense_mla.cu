@@ -80,10 +80,10 @@ constexpr int kXRing = 3;
 constexpr int kXBytes = kM * kQuarter * 4;
 
 // FP8 rows: raw tiles of codes land beside the ring and are converted into it by eight
-// warps (with four: 308 us instead of 289 for 64 x 8192 x 128 heads).  A stage is held
-// from the start of its conversion to the end of its P.V, 14,000 cycles over the three
-// stages that there is room for (conversion 3500, logits 2400, exchange 3300, softmax and
-// P.V 3400): that bounds them, not the bytes.
+// warps (with four 308 us against 289 for 64 x 8192 x 128 heads, now 262).  A stage is
+// held from the start of its conversion to the end of its P.V, 14,000 cycles over the
+// three stages that there is room for (conversion 3500, logits 2400, exchange 3300,
+// softmax and P.V 3400): that bounds them, not the bytes.
 constexpr int kRawStages = 2;
 constexpr int kRawRope = 2 * kNp * 128;        // two blocks of 128 dims, then 64 rows of 32 rope dims
 constexpr int kRawBytes = kNp * (256 + kRopeHalf);
@@ -831,24 +831,26 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         const int sb = tg & 1;
         if (!(ok = wait32(&s_full[sb], (uint32_t)(tg >> 1) & 1u))) break;
         tc_fence_after();
-        float v[kNp];
-        tmem_ld32(tmem + lane_base + TM_S + sb * kNp, v);
-        tmem_ld32(tmem + lane_base + TM_S + sb * kNp + 32, v + 32);
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty[sb]);
-        // each quarter once the peer has read what was in its buffer
-#pragma unroll
+        // (a short loop and few registers at a time, here and in the softmax: the roles
+        // share an instruction cache and, FP8 rows, 80 registers; with 64 logits at
+        // once 4 % more time, FP8 8 %)
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
+          float v[kQuarter];
+          tmem_ld16(tmem + lane_base + TM_S + sb * kNp + i * kQuarter, v);
+          // once the peer has read what was in its buffer
           const int n = tg * 2 + (i & 1), buf = (i >> 1) * kXRing + n % kXRing;   // n: of this half so far
           if (!(ok = wait32_cluster(&x_empty[buf], ((uint32_t)(n / kXRing) & 1u) ^ 1u))) break;
-#pragma unroll
-          for (int g4 = 0; g4 < kQuarter / 4; ++g4) {
-            const int j = i * kQuarter + 4 * g4;
-            st_async_v4(x_remote + buf * kXBytes + g4 * (kM * 16),
-                        make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]), xfull_remote + buf * 8);
+          tmem_ld_wait();
+          if (i == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[sb]);
           }
+#pragma unroll
+          for (int j = 0; j < kQuarter; j += 4)
+            st_async_v4(x_remote + buf * kXBytes + j * (kM * 4),
+                        make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]), xfull_remote + buf * 8);
         }
         if (!ok) break;
       }
@@ -891,21 +893,24 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         const uint32_t ph0 = (uint32_t)(n0 / kXRing) & 1u, ph1 = (uint32_t)((n0 + 1) / kXRing) & 1u;
         const bool here0 = ask_cluster(&x_full[b0], ph0), here1 = ask_cluster(&x_full[b1], ph1);
         if (!(ok = settle(here0 && here1, &x_full[b0], ph0) && settle(here1, &x_full[b1], ph1))) break;
-        float4 y[kHalf / 4];
-#pragma unroll
-        for (int g4 = 0; g4 < kHalf / 4; ++g4)
-          y[g4] = *reinterpret_cast<const float4*>(xrow + (g4 < kQuarter / 4 ? b0 : b1) * kXBytes +
-                                                   g4 % (kQuarter / 4) * (kM * 16));
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[sb]);
 #pragma unroll
-        for (int g4 = 0; g4 < kHalf / 4; ++g4) {
-          const int j = 4 * g4;
-          const float2 s0 = unpack2(add2(pack2(v[j], v[j + 1]), pack2(y[g4].x, y[g4].y)));
-          const float2 s1 = unpack2(add2(pack2(v[j + 2], v[j + 3]), pack2(y[g4].z, y[g4].w)));
-          v[j] = s0.x; v[j + 1] = s0.y; v[j + 2] = s1.x; v[j + 3] = s1.y;
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* xb = xrow + (i ? b1 : b0) * kXBytes;
+          float4 y[kQuarter / 4];
+          asm volatile("" ::: "memory");         // (the loads stay in their batch)
+#pragma unroll
+          for (int g4 = 0; g4 < kQuarter / 4; ++g4) y[g4] = *reinterpret_cast<const float4*>(xb + g4 * (kM * 16));
+#pragma unroll
+          for (int g4 = 0; g4 < kQuarter / 4; ++g4) {
+            const int j = i * kQuarter + 4 * g4;
+            const float2 s0 = unpack2(add2(pack2(v[j], v[j + 1]), pack2(y[g4].x, y[g4].y)));
+            const float2 s1 = unpack2(add2(pack2(v[j + 2], v[j + 3]), pack2(y[g4].z, y[g4].w)));
+            v[j] = s0.x; v[j + 1] = s0.y; v[j + 2] = s1.x; v[j + 3] = s1.y;
+          }
         }
         __syncwarp();
         if (lane == 0) {                       // what was read is free; lane quarter 0 re-arms first
@@ -950,36 +955,36 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         ref_s[0] = m_ref;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ref_set[quarter]);
-        const bool p_here = tg == 0 || mbar_test_wait(&p_empty[hf], (uint32_t)(tg - 1) & 1u);
+        // This half of the P tile is free once its last P.V is done; a piece's first P
+        // also waits until the output before is read out.
+        if (!(ok = (tg == 0 || wait32(&p_empty[hf], (uint32_t)(tg - 1) & 1u)))) break;
+        if (t == x.t0 && hf == 0 && pieces > 0 &&
+            !(ok = wait32(o_free, (uint32_t)(pieces - 1) & 1u))) break;
+        tc_fence_after();
         // weights 2^(logit * sl2 - reference), rounded to bf16 for P.V (half a step, to
         // nearest: the errors of a row's weights average out) and summed in fp32
         // before the rounding, which keeps the lse exact to fp32
         uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
-        uint32_t pk[kHalf / 2];
         const float nmr = (m_ref == -INFINITY) ? 0.f : -m_ref;
         const uint64_t scale2 = pack2(sl2, sl2), nmr2 = pack2(nmr, nmr);
 #pragma unroll
-        for (int j = 0; j < kHalf / 2; ++j) {
-          const float2 x2 = unpack2(fma2(pack2(v[2 * j], v[2 * j + 1]), scale2, nmr2));
-          const float e0 = ex2_approx(x2.x), e1 = ex2_approx(x2.y);
-          sum2[j & 3] = add2(sum2[j & 3], pack2(e0, e1));
-          const __nv_bfloat162 p2 = __floats2bfloat162_rn(e0, e1);
-          pk[j] = *reinterpret_cast<const uint32_t*>(&p2);
+        for (int u = 0; u < 4; ++u) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = 4 * u + i;
+            const float2 x2 = unpack2(fma2(pack2(v[2 * j], v[2 * j + 1]), scale2, nmr2));
+            const float e0 = ex2_approx(x2.x), e1 = ex2_approx(x2.y);
+            sum2[j & 3] = add2(sum2[j & 3], pack2(e0, e1));
+            const __nv_bfloat162 p2 = __floats2bfloat162_rn(e0, e1);
+            pk[i] = *reinterpret_cast<const uint32_t*>(&p2);
+          }
+          *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, hf * 4 + u)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
         const float2 tot = unpack2(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
         if (m_mine != m_ref) l_mine *= m_mine == -INFINITY ? 0.f : ex2_approx(m_mine - m_ref);
         m_mine = m_ref;
         l_mine += tot.x + tot.y;
-        // This half of the P tile is free once its last P.V is done; a piece's first P
-        // also waits until the output before is read out.
-        if (!(ok = settle(p_here, &p_empty[hf], (uint32_t)(tg - 1) & 1u))) break;
-        if (t == x.t0 && hf == 0 && pieces > 0 &&
-            !(ok = wait32(o_free, (uint32_t)(pieces - 1) & 1u))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          *reinterpret_cast<uint4*>(pbuf + sw128_offset(m, hf * 4 + u)) =
-              make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
         // TMEM loads and stores are warp-collective: rescale when any row of the
         // warp needs it (the others multiply by 1)
         if (__builtin_expect(__any_sync(0xffffffffu, rescale), 0)) {
