@@ -30,15 +30,26 @@
 //   exchange (warps 4-7): the group's query slice into TMEM (rope half: shared
 //     memory); this CTA's partial logits out of TMEM into the peer's buffer;
 //   softmax (warps 8-15, one row per thread, two sets of four warps, a half of each
-//     tile's positions a set): own partial plus the peer's, mask, online softmax in log2 units with a lazily moved
-//     reference max (the accumulator is rescaled only when the max grows by more
-//     than 2^8), P in bf16 to shared memory, and the epilogue;
+//     tile's positions a set): own partial plus the peer's, mask, online softmax in
+//     log2 units with a lazily moved reference max (the accumulator is rescaled only
+//     when the max grows by more than 2^8), P in bf16 to shared memory, and the epilogue;
 //   value issuer (warp 2): O += P . V from the same stage, a half tile at a time;
 //   conversion (FP8 rows, warps 16-23): codes times scales, rounded to bf16, out of
 //     the raw tiles into the stages.
 // Exchange and softmax warps of lane quarters without rows (few heads) leave at
 // once: what the tensor core computes there is never read.
 // Every wait is bounded; the cluster syncs after set-up and before exit.
+//
+// What bounds it.  64 sequences of 32768 positions, 128 heads, bf16 rows: 623 us, 3.9
+// TB/s (58 % of the measured copy rate) and 937 TFLOP/s (49 % of the library GEMM's).  A
+// tile takes a cluster about 2700 cycles.  Its bytes take 1700, its MMAs 1340 (64 columns
+// take 46 cycles, not 32; P.V is at its rate), the exchange 1600 (distributed shared
+// memory carries 20 bytes a cycle and SM each way): each is idle for a third to a half of
+// the time, because a stage is held for ~10,000 cycles, from its copy to the end of its
+// P.V, and there is room for four.  4096 tokens of 128 heads over windows of 1024: 1362
+// us, 761 TFLOP/s: the same, and some 4 us a token for queries in and output out.
+// Three softmax sets (640 threads) took 650 us, 64 positions of a tile in each of two
+// sets in turn 812.
 #include "dense_mla.h"
 
 #include <string.h>
@@ -206,6 +217,54 @@ __device__ __forceinline__ int row_of(const CacheView& c, int b, int p, int* err
   const int page = __ldg(c.block_table + (int64_t)b * c.max_pages + pg);
   if (page < 0 || page >= c.num_pages) { report(err, kErrBounds); return -1; }
   return page * c.page_size + (p - pg * c.page_size);
+}
+
+// Asks for `bytes` contiguous bytes (16-byte aligned, a multiple of 16) to be
+// brought into L2.
+__device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Shared-memory descriptor of a K-major operand with rows of 64 bytes and 64-byte
+// swizzle (atoms of 512 bytes).
+__device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(16u >> 4) << 16;                  // leading byte offset (unused here)
+  d |= (uint64_t)(512u >> 4) << 32;                 // stride byte offset: next 8-row atom
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)4 << 61;                           // 64-byte swizzle
+  return d;
+}
+
+// 16-byte chunk u of row r of such a tile (byte offset).
+__host__ __device__ __forceinline__ uint32_t sw64_offset(uint32_t r, uint32_t u) {
+  return r * 64u + ((u ^ ((r >> 1) & 3u)) << 4);
 }
 
 // Two fp32 operations in one instruction.

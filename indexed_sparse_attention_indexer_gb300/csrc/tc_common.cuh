@@ -240,11 +240,6 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
-// Asks for `bytes` contiguous bytes (16-byte aligned, a multiple of 16) to be
-// brought into L2.
-__device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(src), "r"(bytes) : "memory");
-}
 // Plain bulk copy of `bytes` contiguous bytes (both addresses 16-byte
 // aligned, size a multiple of 16), counted on `bar` when they land.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
@@ -299,29 +294,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
       : "r"(taddr));
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15}, [%16];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
-  uint32_t r[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16};\n" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
 }
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
@@ -445,17 +417,6 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
   return d;
 }
 
-// Same for rows of 64 bytes with 64-byte swizzle (atoms of 512 bytes).
-__device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(16u >> 4) << 16;                  // leading byte offset (unused here)
-  d |= (uint64_t)(512u >> 4) << 32;                 // stride byte offset: next 8-row atom
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)4 << 61;                           // 64-byte swizzle
-  return d;
-}
-
 // Instruction descriptor: fp32 accumulate, A/B K-major, M x N tile.
 // ab_format: 1 = bf16 (kind::f16), 0 = e4m3 (kind::f8f6f4).
 __host__ __device__ constexpr uint32_t idesc_f32(uint32_t ab_format, uint32_t M, uint32_t N) {
@@ -475,11 +436,6 @@ __host__ __device__ constexpr uint32_t idesc_f32_bmn(uint32_t ab_format, uint32_
 // 16-byte chunk u of row r of a 128-byte-swizzled tile (byte offset).
 __host__ __device__ __forceinline__ uint32_t sw128_offset(uint32_t r, uint32_t u) {
   return r * 128u + ((u ^ (r & 7u)) << 4);
-}
-
-// Same of a tile with rows of 64 bytes and 64-byte swizzle.
-__host__ __device__ __forceinline__ uint32_t sw64_offset(uint32_t r, uint32_t u) {
-  return r * 64u + ((u ^ ((r >> 1) & 3u)) << 4);
 }
 
 }  // namespace tc
