@@ -318,6 +318,22 @@ __device__ __forceinline__ bool bf16x8_finite(const uint4& v) {
   return ok;
 }
 
+// The rows of a stage whose bits are set become zeros, by a warp: a store of the warp
+// covers four rows of a block, or eight rows of rope dims.  (One lane a row took 2500 to
+// 9500 cycles for a tile at an edge.)
+__device__ __forceinline__ void clear_rows(uint8_t* st, uint64_t rows, int lane) {
+  const uint64_t four = rows >> (lane >> 3), eight = rows >> (lane >> 2);
+  uint8_t* at = st + lane * 16;
+#pragma unroll 1
+  for (int blk = 0; blk < 4; ++blk, at += kBlockBytes)
+#pragma unroll
+    for (int i = 0; i < kNp / 4; ++i)
+      if ((four >> (4 * i)) & 1u) *reinterpret_cast<uint4*>(at + i * 512) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < kNp / 8; ++i)
+    if ((eight >> (8 * i)) & 1u) *reinterpret_cast<uint4*>(at + i * 512) = make_uint4(0, 0, 0, 0);
+}
+
 // Bounded waits whose slow path is out of line and takes few arguments: the
 // roles' loops together have to stay small enough for the instruction cache.
 __shared__ volatile int s_abort;               // a role has given up: the others follow
@@ -633,29 +649,24 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
             // be 0); a row that only some tokens see and that holds NaN or an infinity
             // becomes zeros as a value and NaN in its rope dims: its logits are NaN, for
             // those that see it
+            uint64_t none = 0, some = 0;         // rows that no token sees; that only some see
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int p = p0 + h * 32 + lane;
+              const bool seen = any_sees(a, x.grp, p);
+              none |= (uint64_t)__ballot_sync(0xffffffffu, !seen) << (32 * h);
+              some |= (uint64_t)__ballot_sync(0xffffffffu, seen && !all_see(a, x.grp, p, 1)) << (32 * h);
+            }
             if (!(ok = wait32(&landed[stage], (edge_ph >> stage) & 1u))) break;
             edge_ph ^= 1u << stage;
-#pragma unroll 1
-            for (int rr = lane; rr < kNp; rr += 32) {        // a lane clears whole rows
-              const bool none = !any_sees(a, x.grp, p0 + rr);
-              bool bad = false;
-              if (!none && !all_see(a, x.grp, p0 + rr, 1)) {
-                // (four loads under way: with one, four tokens' windows took 28.6 us, not 25.9)
-#pragma unroll 4
-                for (int u = 0; u < 36; ++u)
-                  bad |= !bf16x8_finite(*reinterpret_cast<const uint4*>(
-                      u < 32 ? st + (u >> 3) * kBlockBytes + sw128_offset(rr, u & 7)
-                             : st + kRopeOff + sw64_offset(rr, u & 3)));
-              }
-              if (none || bad) {
-#pragma unroll 4
-                for (int u = 0; u < 32; ++u)
-                  *reinterpret_cast<uint4*>(st + (u >> 3) * kBlockBytes + sw128_offset(rr, u & 7)) =
-                      make_uint4(0, 0, 0, 0);
-                const uint32_t y = bad ? 0x7FFF7FFFu : 0u;
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                  *reinterpret_cast<uint4*>(st + kRopeOff + sw64_offset(rr, u)) = make_uint4(y, y, y, y);
+            clear_rows(st, none, lane);
+            for (; some != 0ull; some &= some - 1ull) {      // (the warp looks at a row together)
+              const int rr = __ffsll((long long)some) - 1;
+              uint4* const c = reinterpret_cast<uint4*>(st + (lane >> 3) * kBlockBytes + sw128_offset(rr, lane & 7));
+              uint4* const e = reinterpret_cast<uint4*>(st + kRopeOff + sw64_offset(rr, lane & 3));
+              if (__any_sync(0xffffffffu, !bf16x8_finite(*c) || !bf16x8_finite(*e))) {
+                *c = make_uint4(0, 0, 0, 0);
+                if (lane < 4) *e = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
               }
             }
             fence_proxy_async_smem();   // the tensor core reads the stage through the async proxy
@@ -1284,7 +1295,7 @@ cudaError_t launch_dense_mla(const DenseArgs& a, cudaStream_t st) {
   const int clusters = (int)(tiles < slots ? tiles : slots);
   // Groups that cannot be long enough for a split to pay, whatever the lengths are, stay
   // whole: no sums of tiles, no second kernel (24 x 4 tokens with windows of 129: 25.7 us
-  // with them, 23.2 without).
+  // with them, 23.2 without; 17.4 now).
   const int64_t all = (a.c.s_max + kNp - 1) / kNp;
   const int64_t seen = (a.window + plan.tokens - 1 + kNp - 1) / kNp + 1 + (a.n_sink + kNp - 1) / kNp;
   const int64_t most = (all < seen ? all : seen) + kGroupCost;
