@@ -20,12 +20,13 @@
 // out whole groups costs at most kWholeSlack tiles more, groups stay whole and
 // nothing is joined.
 //
-// Roles in a CTA (16 warps; FP8 rows: 24), each walking the same list of pieces; the tile
-// pipeline runs on across pieces:
-//   producers (warps 0-1): a tile's rows into a 128-byte-swizzled stage (ring
-//     of 4) by TMA boxes; tiles at an edge (not wholly visible to every token
-//     of the group) and FP8 rows with plain loads, rows that nobody sees as
-//     zeros, so that what they hold never meets the tensor core;
+// Roles in a CTA (16 warps; FP8 rows: 24), each walking the same list of pieces; the
+// tile pipeline runs on across pieces:
+//   producers (warps 0-1): a tile's rows into a 128-byte-swizzled stage (ring of 4)
+//     by TMA boxes (warp 0; FP8 rows: into raw tiles), a group's queries (warp 1);
+//     in tiles at an edge (not wholly visible to every token of the group) warp 1
+//     turns rows that nobody sees into zeros, so that what they hold never meets the
+//     tensor core (FP8 rows: the converting warps do);
 //   logit issuer (warp 3): S = Qslice . C^T into one of two TMEM tiles;
 //   exchange (warps 4-7): the group's query slice into TMEM (rope half: shared
 //     memory); this CTA's partial logits out of TMEM into the peer's buffer;
@@ -40,14 +41,14 @@
 // once: what the tensor core computes there is never read.
 // Every wait is bounded; the cluster syncs after set-up and before exit.
 //
-// What bounds it.  64 sequences of 32768 positions, 128 heads, bf16 rows: 623 us, 3.9
-// TB/s (58 % of the measured copy rate) and 937 TFLOP/s (49 % of the library GEMM's).  A
+// What bounds it.  64 sequences of 32768 positions, 128 heads, bf16 rows: 609 us, 4.0
+// TB/s (59 % of the measured copy rate) and 959 TFLOP/s (50 % of the library GEMM's).  A
 // tile takes a cluster about 2700 cycles.  Its bytes take 1700, its MMAs 1340 (64 columns
 // take 46 cycles, not 32; P.V is at its rate), the exchange 1600 (distributed shared
 // memory carries 20 bytes a cycle and SM each way): each is idle for a third to a half of
 // the time, because a stage is held for ~10,000 cycles, from its copy to the end of its
-// P.V, and there is room for four.  4096 tokens of 128 heads over windows of 1024: 1362
-// us, 761 TFLOP/s: the same, and some 4 us a token for queries in and output out.
+// P.V, and there is room for four.  4096 tokens of 128 heads over windows of 1024: 1345
+// us, 770 TFLOP/s: the same, and the softmax warps' 2.5 us for each group's output.
 // Three softmax sets (640 threads) took 650 us, 64 positions of a tile in each of two
 // sets in turn 812.
 #include "dense_mla.h"
@@ -79,8 +80,10 @@ constexpr int kQkWarp = 3;                     // then exchange: warps 4-7
 constexpr int kConvWarp0 = 16;                 // FP8 rows: conversion, warps 16-23
 constexpr int kSmWarp0 = 8;                    // softmax: warps 8-11 first halves, 12-15 second ones
 constexpr int kMaxClusters = 128;
+// in tiles (777 tokens of 32 heads over windows of 511: 81 us whole, 94 split at a slack of 5)
 constexpr int kWholeSlack = 8;
-constexpr int kGroupCost = 4;                  // what a piece costs beside its tiles, in tiles
+// what a piece costs beside its tiles, in tiles (17 x 3000 x 128 heads: 4 39.1 us, 2 39.9)
+constexpr int kGroupCost = 4;
 // tiles between L2 prefetch and copy (64 x 32768 x 128 heads: 2 661 us, 4 635, 8 645, 16 714)
 constexpr int kAhead = 4;
 // partial logits travel in quarters of a tile (16 positions): three in flight for
