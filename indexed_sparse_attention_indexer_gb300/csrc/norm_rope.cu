@@ -68,7 +68,7 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
 
 // What a unit's eight pairs are turned by, weights included:
 //   z_a = t_a a - t_b b + ea,  z_b = t_a c + t_b d + eb   (t: the normed vector
-// before weight and bias; dims outside the rotation have cosine 1 and sine 0).
+// before weight and bias; dims outside the rotation: t_a a + ea and t_b d + eb alone).
 // (b is kept negated.)  Half-split: pair p is dim p of the unit's first and of its second chunk;
 // interleaved: dims 2 (p % 4) and 2 (p % 4) + 1 of chunk p / 4.
 template <bool LAYER>
@@ -180,26 +180,30 @@ __device__ __forceinline__ void side(const dsi_heads& s, const RopeArgs& a, int6
       }
     }
   };
+  const bool turns = sub < hc;                  // the lane's only unit is rotated
   auto turn_of = [&](Turn<LAYER>& t) {          // of the lane's only unit
     float c[8], sn[8], w[2][8], b[2][8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) { w[h][e] = 1.f; b[h][e] = 0.f; }
+      for (int e = 0; e < 8; ++e) { w[h][e] = 1.f; b[h][e] = -0.f; }   // (-0 added keeps every value)
       if (normed(0, h) && s.weight) load8(s.weight + off[0][h], w[h]);
       if (LAYER && normed(0, h) && s.bias) load8(s.bias + off[0][h], b[h]);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) { c[e] = 1.f; sn[e] = 0.f; }
-    if (sub < hc) angles(sub, c, sn);
+    if (turns) angles(sub, c, sn);
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       const float wa = w[chunk_a<IL>(p)][dim_a<IL>(p)], wb = w[chunk_b<IL>(p)][dim_b<IL>(p)];
-      t.a[p] = wa * c[p]; t.b[p] = -(wb * sn[p]); t.c[p] = wa * sn[p]; t.d[p] = wb * c[p];
+      t.a[p] = wa * c[p];
+      t.d[p] = wb * c[p];
+      t.b[p] = turns ? -(wb * sn[p]) : -0.f;
+      t.c[p] = turns ? wa * sn[p] : -0.f;
       if (LAYER) {
         const float ba = b[chunk_a<IL>(p)][dim_a<IL>(p)], bb = b[chunk_b<IL>(p)][dim_b<IL>(p)];
-        t.ea[p] = ba * c[p] - bb * sn[p];
-        t.eb[p] = ba * sn[p] + bb * c[p];
+        t.ea[p] = turns ? ba * c[p] - bb * sn[p] : ba;
+        t.eb[p] = turns ? ba * sn[p] + bb * c[p] : bb;
       }
     }
   };
@@ -284,9 +288,10 @@ __device__ __forceinline__ void side(const dsi_heads& s, const RopeArgs& a, int6
       for (int p = 0; p < 8; ++p) {
         float& za = y[0][chunk_a<IL>(p)][dim_a<IL>(p)];
         float& zb = y[0][chunk_b<IL>(p)][dim_b<IL>(p)];
-        const float ta = za, tb = zb;
-        za = fmaf(ta, kept.a[p], LAYER ? fmaf(tb, kept.b[p], kept.ea[p]) : tb * kept.b[p]);
-        zb = fmaf(tb, kept.d[p], LAYER ? fmaf(ta, kept.c[p], kept.eb[p]) : ta * kept.c[p]);
+        // (a dim outside the rotation never meets its neighbour, which may be infinite)
+        const float ta = za, tb = zb, oa = turns ? ta : 0.f, ob = turns ? tb : 0.f;
+        za = fmaf(ta, kept.a[p], LAYER ? fmaf(ob, kept.b[p], kept.ea[p]) : ob * kept.b[p]);
+        zb = fmaf(tb, kept.d[p], LAYER ? fmaf(oa, kept.c[p], kept.eb[p]) : oa * kept.c[p]);
       }
     } else {
 #pragma unroll
