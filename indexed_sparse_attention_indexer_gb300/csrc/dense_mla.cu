@@ -985,15 +985,6 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
             v[j] = s0.x; v[j + 1] = s0.y; v[j + 2] = s1.x; v[j + 3] = s1.y;
           }
         }
-        __syncwarp();
-        if (lane == 0) {                       // what was read is free; lane quarter 0 re-arms first
-          if (quarter == 0) {
-            mbar_arrive_expect_tx_relaxed(&x_full[b0], x_bytes);
-            mbar_arrive_expect_tx_relaxed(&x_full[b1], x_bytes);
-          }
-          mbar_arrive_remote_relaxed(xempty_remote + b0 * 8);
-          mbar_arrive_remote_relaxed(xempty_remote + b1 * 8);
-        }
         // masked positions: -inf
         if (__builtin_expect(!all_see(a, x.grp, p0, kHalf), 0)) {
           const uint32_t see = (uint32_t)(low_bits(n_row - p0) &
@@ -1010,6 +1001,21 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], v[j + e]), v[j + 4 + e]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // What was read is free; lane quarter 0 re-arms first.  The credits are relaxed arrivals: one that
+        // releases at cluster scope takes ~1000 cycles (64 x 32768 x 128 heads 580 -> 943 us, one fence
+        // for both 797, by a warp of its own 757).  What they protect are this warp's loads, whose values
+        // the peer's next stores can no longer change once they have arrived in registers, and an
+        // arrival is not issued before they have: it waits for a vote on a maximum over all of them
+        // (which is never the signalling NaN that the vote asks for: no arithmetic gives one).
+        const bool arrived = !__any_sync(0xffffffffu, __float_as_uint(top) == 0x7F800001u);
+        if (lane == 0 && arrived) {
+          if (quarter == 0) {
+            mbar_arrive_expect_tx_relaxed(&x_full[b0], x_bytes);
+            mbar_arrive_expect_tx_relaxed(&x_full[b1], x_bytes);
+          }
+          mbar_arrive_remote_relaxed(xempty_remote + b0 * 8);
+          mbar_arrive_remote_relaxed(xempty_remote + b1 * 8);
+        }
         // (an infinite sum is a masked or an overflowed one: not scaled, 0 * inf is no logit)
         const float tmax = top == -INFINITY ? -INFINITY : top * sl2;
         // the reference after the half before (the other set's), moved when this
