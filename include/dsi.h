@@ -397,7 +397,9 @@ dsi_status dsi_latent_fp8_append(const void* x, int64_t n_rows, int64_t ld_x,
  *   l_s = scale * q[r, h, :] . c_s   (576 dims)
  *   out[r, h, :] = sum_s softmax(l)_s * c_s[0:512];  lse[r, h] = ln sum_s exp(l_s)
  * With an FP8 latent cache c_s is code * tile scale, the fp32 product rounded
- * to bf16 (what the tensor cores multiply).
+ * to bf16 (what the tensor cores multiply).  Logits, maxima and sums are fp32;
+ * a weight is rounded to bf16 before it multiplies the values, and summed for
+ * the denominator and lse before that rounding.
  *   q    bf16 [batch*T, n_heads, 576], n_heads 1..128
  *   out  bf16 [batch*T, n_heads, 512]
  *   lse  fp32 [batch*T, n_heads] or NULL
@@ -407,7 +409,10 @@ dsi_status dsi_latent_fp8_append(const void* x, int64_t n_rows, int64_t ld_x,
  *        over the device and joined (without it a sequence stays on one pair
  *        of SMs).  Calls that may run at once need a workspace each.
  * Cache rows outside the visible range of a sequence are never used: they may
- * hold anything, as may block_table entries of pages past the history.  The
+ * hold anything, as may block_table entries of pages past the history.  A
+ * visible row with a NaN or an infinity reaches the tokens that see it and no
+ * others: by the formula's arithmetic, or with NaN throughout where another
+ * token of the same step or prompt does not see it.  The
  * page ids of visible positions are checked on the device: one outside the
  * pool reads as rows of zeros and sets the device status to DSI_ERR_BOUNDS.
  * Results do not depend on the split beyond rounding, and are the same from

@@ -262,10 +262,10 @@ class Heads:
     """Queries or keys of ``norm_rope``: the tensors plus the ``dsi_heads`` struct that points
     at them (it can be kept and used again while the tensors live).
 
-    ``x [n, heads, d]`` bf16 (any row and head strides); ``norm`` None, "rms" or "layer" over
+    ``x [n, heads, d]`` bf16 (any row and head strides that are multiples of 8 and at least d); ``norm`` None, "rms" or "layer" over
     the first ``norm_dim`` dims (all of them unless given) with fp32 ``weight`` / ``bias``.
-    ``out`` is a bf16 tensor ``[rows, heads, d]`` (``x`` itself for in place; a new one unless
-    given) or an E4M3 one, packed, with ``out_scale``: uint8 ``[rows, heads, d / group]`` makes it
+    ``out`` is a bf16 tensor ``[rows, heads, d]`` (``x`` itself for in place; a new one, made on
+    the current stream, unless given) or an E4M3 one, packed, with ``out_scale``: uint8 ``[rows, heads, d / group]`` makes it
     MXFP8, fp32 ``[rows, heads, ceil(d / 128)]`` FP8 with tile scales.  The ``heads`` dim may be
     left out of ``out`` and ``out_scale`` when there is one head, and page pools
     ``[pages, page_size, ...]`` may stand for their rows.  ``dst_rows`` (int64 ``[n]``): the out
@@ -522,7 +522,7 @@ def norm_rope(queries: Optional[Heads], keys: Optional[Heads], table, positions,
         rows, rope_dim = table.shape
         _need(0 <= rope_offset <= side.d - rope_dim, "the rotated dims are dims of x")
         st = _launch(lib.dsi_norm_rope, device, stream,
-                     queries._ref if queries is not None else None, keys._ref if keys is not None else None,
+                     queries.ref() if queries is not None else None, keys.ref() if keys is not None else None,
                      n, side.d, eps, table.data_ptr(), rows, positions.data_ptr(), rope_offset, rope_dim,
                      bool(interleaved))
         if st:

@@ -41,19 +41,19 @@
 // once: what the tensor core computes there is never read.
 // Every wait is bounded; the cluster syncs after set-up and before exit.
 //
-// What bounds it.  64 sequences of 32768 positions, 128 heads, bf16 rows: 609 us, 4.0
-// TB/s (59 % of the measured copy rate) and 959 TFLOP/s (50 % of the library GEMM's).  A
-// tile takes a cluster about 2700 cycles.  Its bytes take 1700, its MMAs 1340 (64 columns
+// What bounds it.  64 sequences of 32768 positions, 128 heads, bf16 rows: 580 us at 2070
+// MHz, 4.2 TB/s (62 % of the measured copy rate) and 1007 TFLOP/s (53 % of the library
+// GEMM's); 605 to 622 us where the power cap holds the clock near 1950 MHz.  A tile takes
+// a cluster about 2750 cycles (the time's cycles over its 431 tiles).  Its bytes take
+// 1700, its MMAs 1340 (64 columns
 // take 46 cycles, not 32; P.V is at its rate), the exchange 1600 (distributed shared
 // memory carries 20 bytes a cycle and SM each way): each is idle for a third to a half of
 // the time, because a stage is held for ~10,000 cycles, from its copy to the end of its
-// P.V, and there is room for four.  4096 tokens of 128 heads over windows of 1024: 1345
-// us, 770 TFLOP/s: the same, and the softmax warps' 2.5 us for each group's output.
+// P.V, and there is room for four.  4096 tokens of 128 heads over windows of 1024: 1349
+// us, 768 TFLOP/s: the same, and the softmax warps' 2.5 us for each group's output.
 // Three softmax sets (640 threads) took 650 us, 64 positions of a tile in each of two
 // sets in turn 812.
 #include "dense_mla.h"
-
-#include <string.h>
 
 #include <atomic>
 
@@ -80,9 +80,14 @@ constexpr int kQkWarp = 3;                     // then exchange: warps 4-7
 constexpr int kConvWarp0 = 16;                 // FP8 rows: conversion, warps 16-23
 constexpr int kSmWarp0 = 8;                    // softmax: warps 8-11 first halves, 12-15 second ones
 constexpr int kMaxClusters = 128;
-// in tiles (777 tokens of 32 heads over windows of 511: 81 us whole, 94 split at a slack of 5)
+// In tiles.  us at 4 / 8 / 16 / 32: 777 tokens of 32 heads over windows of 511 79.5 / 67.3 /
+// 67.3 / 67.3 (FP8 rows 107.6 / 95.8 / 95.9 / 95.9), 100 x 512 x 128 heads 44.5 / 39.8 / 39.8 /
+// 37.0, 48 x 2 tokens x 700 x 64 heads 45.1 / 27.6 / 25.3 / 25.3, 1000 tokens of 64 heads over
+// windows of 200 103.3 / 103.5 / 90.1 / 90.1, 90 x 2000 x 128 heads 90.5 / 90.2 / 90.1 / 99.2.
 constexpr int kWholeSlack = 8;
-// what a piece costs beside its tiles, in tiles (17 x 3000 x 128 heads: 4 39.1 us, 2 39.9)
+// What a piece costs beside its tiles, in tiles.  us at 2 / 4 / 6 / 8: 17 x 3000 x 128 heads 41.6 /
+// 39.8 / 39.5 / 40.4, 90 x 2000 92.2 / 90.2 / 90.1 / 86.6, 100 x 512 39.8 / 39.8 / 49.1 / 46.4, 120
+// of up to 1500 41.1 / 40.7 / 41.3 / 43.6.
 constexpr int kGroupCost = 4;
 // tiles between L2 prefetch and copy (64 x 32768 x 128 heads: 2 661 us, 4 635, 8 645, 16 714)
 constexpr int kAhead = 4;
@@ -94,10 +99,11 @@ constexpr int kXRing = 3;
 constexpr int kXBytes = kM * kQuarter * 4;
 
 // FP8 rows: raw tiles of codes land beside the ring and are converted into it by eight
-// warps (with four 308 us against 289 for 64 x 8192 x 128 heads, now 262).  A stage is
+// warps (with four 308 us against 289 for 64 x 8192 x 128 heads, now 265).  A stage is
 // held from the start of its conversion to the end of its P.V, 14,000 cycles over the
 // three stages that there is room for (conversion 3500, logits 2400, exchange 3300,
-// softmax and P.V 3400): that bounds them, not the bytes.
+// softmax and P.V 3400): that bounds them, not the bytes, of which bf16 rows have twice
+// as many and take 175 us.
 constexpr int kRawStages = 2;
 constexpr int kRawRope = 2 * kNp * 128;        // two blocks of 128 dims, then 64 rows of 32 rope dims
 constexpr int kRawBytes = kNp * (256 + kRopeHalf);

@@ -14,9 +14,11 @@
 //
 // What bounds it.  Issue slots: ~200 instructions a unit of 16 dims (conversions,
 // statistics, rotation, codes), 53-58 % of them used at the two resident blocks that
-// 115-128 registers a thread leave.  8192 tokens of 64 + 1 heads of 128: 55.2 us, 5.0
-// TB/s, 74 % of the measured copy rate.  65537 latent rows to FP8: 62.6 us, 2.1 TB/s (31
-// %).  One token with 65 heads: 6.7 us, a launch.
+// 115-128 registers a thread leave.  8192 tokens of 64 + 1 heads of 128: 55.5 us, 5.0
+// TB/s, 73 % of the measured copy rate.  65537 latent rows to FP8: 62.6 us, 2.1 TB/s (31
+// %); there a quarter of the lanes' units lie past the vector (36 units on 16 lanes of three),
+// and every chunk of 8 dims computes its scale and reciprocal anew.  One token with 65 heads:
+// 6.8 us, a launch.
 #include "kernels.h"
 #include "norm_rope.h"
 #include "tc_common.cuh"
