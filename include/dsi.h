@@ -497,7 +497,7 @@ size_t dsi_dense_mla_workspace_size(int32_t rows, int32_t n_heads);
  * x, out, weight, bias and rope_table 16-byte aligned; pitches multiples of 8.
  * Errors: DSI_ERR_INVALID_ARG (null pointer, negative size, misalignment,
  * a pitch below the vector's width, eps < 0 or NaN, bias without
- * DSI_NORM_LAYER), DSI_ERR_UNSUPPORTED (d not a multiple of 8 or outside
+ * DSI_NORM_LAYER, x as out with other pitches, dst_rows or quantised), DSI_ERR_UNSUPPORTED (d not a multiple of 8 or outside
  * 8..1024, norm_dim not a multiple of 8 or outside 8..d, rope_dim not a
  * multiple of 16, rope_offset not a multiple of 8, out_group not 32, 64 or
  * 128 or not dividing d, unknown norm or out_dtype, n_rows above 2^31 or

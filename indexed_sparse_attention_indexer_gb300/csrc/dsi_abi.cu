@@ -200,6 +200,13 @@ dsi_status check_heads(const dsi_heads* h, int64_t n_rows, int d, dsi_heads* out
   return aligned(h->out_scale, 4) ? DSI_OK : DSI_ERR_INVALID_ARG;
 }
 
+// x as out: every vector has to be written where it was read.
+bool in_place_ok(const dsi_heads& h, int64_t n_rows) {
+  if (h.n_heads == 0 || h.x != h.out) return true;
+  return h.out_dtype == DSI_BF16 && !h.dst_rows && (n_rows == 1 || h.ld_row == h.ld_out_row) &&
+         (h.n_heads == 1 || h.ld_head == h.ld_out_head);
+}
+
 }  // namespace
 
 void dsi::note_launch(int n) { g_launches.fetch_add((unsigned long long)n, std::memory_order_relaxed); }
@@ -513,6 +520,7 @@ dsi_status dsi_norm_rope(const dsi_heads* queries, const dsi_heads* keys, int64_
   if (n_rows > (1ll << 31) || n_rows * q.n_heads > (1ll << 40) || n_rows * k.n_heads > (1ll << 40))
     return DSI_ERR_UNSUPPORTED;                            // blocks are counted in 32 bits
   if (n_rows == 0 || q.n_heads + (int64_t)k.n_heads == 0) return DSI_OK;
+  if (!in_place_ok(q, n_rows) || !in_place_ok(k, n_rows)) return DSI_ERR_INVALID_ARG;
   RopeArgs a;
   a.table = rope_table;
   a.positions = positions;
