@@ -403,7 +403,7 @@ dsi_status dsi_latent_fp8_append(const void* x, int64_t n_rows, int64_t ld_x,
  *   q    bf16 [batch*T, n_heads, 576], n_heads 1..128
  *   out  bf16 [batch*T, n_heads, 512]
  *   lse  fp32 [batch*T, n_heads] or NULL
- *   A row that sees nothing gives out = 0 and lse = -inf.
+ *   A row that sees nothing, or whose every logit is -inf, gives out = 0 and lse = -inf.
  *   workspace / workspace_bytes: NULL and 0, or 256-byte aligned with at least
  *        dsi_dense_mla_workspace_size() bytes: then long histories are split
  *        over the device and joined (without it a sequence stays on one pair

@@ -77,6 +77,60 @@ def test_a_partly_visible_row_that_is_not_finite(bad):
         assert bool(torch.isnan(out[2:4]).all()) and bool(torch.isnan(lse[2:4]).all())
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("sink", [0, 130])
+def test_a_row_that_leaves_the_window(sink, fp8):
+    """Not finite and seen by the first tokens of a step only, at the window's lower edge: theirs alone."""
+    n, T, H, window = 900, 4, 16, 333
+    lo = n - T + 1 - window                          # the first token's first position
+    for dim in (7, 400, 570):
+        case = Case([n, 50], T, H, 64, fp8, seed=21, garbage=False)
+        clean, clean_lse = binding.window_mla_decode(case.q.to(DEV), case.device(), window, sink, SCALE,
+                                                     tokens_per_seq=T)
+        at = int(case.phys(0, torch.tensor([lo + 1])))                 # tokens 0 and 1
+        if fp8:
+            case.latent.view(torch.uint8).view(-1, 576)[at, dim] = 0x7F
+        else:
+            case.latent.view(-1, 576)[at, dim] = math.inf
+        out, lse = binding.window_mla_decode(case.q.to(DEV), case.device(), window, sink, SCALE, tokens_per_seq=T)
+        torch.cuda.synchronize()
+        assert torch.equal(out[2:], clean[2:]) and torch.equal(lse[2:], clean_lse[2:])
+        assert bool(torch.isnan(out[:2]).all()) and bool(torch.isnan(lse[:2]).all())
+        assert binding.device_status() == 0
+
+
+@pytest.mark.parametrize("lens", [[70, 300], [9000, 70]], ids=["whole", "split"])
+def test_logits_that_are_all_minus_infinity(lens):
+    """A head whose query makes every logit -inf weighs nothing: zeros, and an lse of -inf."""
+    case = Case(lens, 1, 32, 64, seed=23, garbage=False)
+    case.latent[..., 10] = case.latent[..., 10].abs() + 0.5
+    cache = case.device()
+    clean, clean_lse = (t.clone() for t in binding.dense_mla_decode(case.d_q, cache, SCALE))
+    case.d_q[0, 5, 10] = case.d_q[1, 31, 10] = -math.inf
+    out, lse = binding.dense_mla_decode(case.d_q, cache, SCALE)
+    torch.cuda.synchronize()
+    hit = torch.zeros((2, 32), dtype=torch.bool, device=DEV)
+    hit[0, 5] = hit[1, 31] = True
+    assert bool((out[hit] == 0).all()) and bool((lse[hit] == -math.inf).all())
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
+def test_the_checked_library():
+    """The build with bounds checks gives the same bits."""
+    case = Case([2000, 5, 0], 2, 48, 16, True, seed=22, garbage=False)
+    cache = case.device()
+    for call in (lambda c: binding.dense_mla_decode(case.d_q, cache, SCALE, tokens_per_seq=2, checked=c),
+                 lambda c: binding.window_mla_decode(case.d_q, cache, 70, 3, SCALE, tokens_per_seq=2, checked=c)):
+        a, b = call(False), call(True)
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    table, pos = binding.rope_table(3000, 64, device=DEV), torch.arange(6, device=DEV)
+    a, b = (binding.norm_rope(binding.Heads(case.d_q, "rms"), None, table, pos, rope_offset=512, checked=c)[0]
+            for c in (False, True))
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and binding.device_status() == 0 and binding.device_status(checked=True) == 0
+
+
 def test_a_first_call_that_is_captured():
     """A process whose first calls of the library are captured into a graph."""
     import os
