@@ -530,6 +530,92 @@ dsi_status dsi_norm_rope(const dsi_heads* queries, const dsi_heads* keys, int64_
                          int32_t interleaved, void* stream);
 
 /*
+ * dsi_linear_prefill / dsi_linear_decode — linear attention with a decay for
+ * each head: the layers between the attention layers of hybrid models ("Day 0
+ * Inference Acceleration for New LLM Architectures: Hybrid Attention
+ * Adaptation and Optimization Practices": the linear branch keeps a state of
+ * fixed size in place of a cache).
+ *
+ * For head h, with g = log_decay[h], and the tokens i = 0, 1, .. of a sequence:
+ *   S_i = exp(g) S_(i-1) + k_i v_i^T      (S: dk x dv, fp32)
+ *   out_i = scale * S_i^T q_i
+ * S_(-1) is the state that the sequence starts from, or zeros.  Head h reads key
+ * and value head h / (n_heads / n_kv_heads).
+ *
+ * Prefill: prompts of any length laid end to end; sequence b has the tokens
+ * seq_starts[b] .. seq_starts[b + 1] - 1.  Rows before seq_starts[0] and behind
+ * seq_starts[batch] are neither read nor written.  The chunked form: 128 tokens meet
+ * each other and the state by matrix products.  Decode: tokens_per_seq (T) tokens of
+ * every sequence, rows T to a sequence, in order.
+ *
+ * States live in slots.  Sequence b starts from slot in_slots[b] (negative: from
+ * zeros) and leaves its state in slot out_slots[b] (negative: nowhere); in_slots
+ * NULL: slot b, out_slots NULL: the in slots.  An out slot other than the in slot
+ * makes a copy that goes on by itself: any number of sequences may start from one
+ * slot that none of them writes.  A slot that one sequence writes may not be the in
+ * or out slot of another one in the same call (their results would be undefined).  A
+ * sequence without tokens passes its state on.  state NULL: every sequence
+ * starts from zeros and its state is not kept.
+ *
+ * Numbers.  The state is fp32 throughout, its decay applied as S + expm1(g) S, so
+ * that a decay near one keeps its distance from one.  Decode computes in fp32 with one
+ * rounding to bf16 at the end.  Prefill multiplies on the tensor cores: the weights
+ * exp(g (i - j)) q_i . k_j and the state that a chunk's queries meet are rounded to
+ * bf16 (off by at most 2^-8 of a value), the decayed values that enter the state are
+ * split in two bf16 parts (2^-16).
+ * A token whose q is not finite gives an out of that kind by itself; a k or
+ * v that is not reaches the outputs of that head from its token on and its state, as NaN or by
+ * the formula's arithmetic, and nothing else.  log_decay is at most 0 in use; -inf (no
+ * memory) is allowed, values above 0 grow as the formula says until they overflow.
+ *
+ *   q, k   bf16 [n_tokens, n_heads, dk], [n_tokens, n_kv_heads, dk]
+ *   v, out bf16 [n_tokens, n_kv_heads, dv], [n_tokens, n_heads, dv]
+ *          each with pitches of its own (multiples of 8 elements), 16-byte aligned,
+ *          dims contiguous; out overlaps nothing else
+ *   state  fp32 [n_slots, n_heads, dk, dv], packed, 16-byte aligned
+ *   dk, dv multiples of 8 in 8 .. 128
+ * A slot >= n_slots, or a start that is negative, above n_tokens or below the one
+ * before it, sets the device status to DSI_ERR_BOUNDS: the slot counts as
+ * negative, the start as 0 or n_tokens, and a sequence that would end before it
+ * starts has no tokens.
+ *   workspace / workspace_bytes (prefill): NULL and 0, or 256-byte aligned with
+ *          dsi_linear_workspace_size() bytes: then calls of few heads and sequences
+ *          are split along the sequences.  Calls that may run at once need one each.
+ * Results are the same from one call to the next.
+ * Errors: DSI_ERR_INVALID_ARG (null pointer, negative size, misalignment, a pitch
+ * below the vector's width, n_heads not a multiple of n_kv_heads, slots without a
+ * state, fewer slots than sequences without in_slots, NaN scale, T < 1, out at q, k or v),
+ * DSI_ERR_UNSUPPORTED (dk or dv, n_tokens or batch * n_heads * 4 of 2^31 or more),
+ * DSI_ERR_WORKSPACE (workspace too small).
+ */
+typedef struct dsi_linear {
+  const void*    q;
+  const void*    k;
+  const void*    v;
+  void*          out;
+  int64_t        ld_q_row, ld_q_head;      /* elements from one token / head to the next */
+  int64_t        ld_k_row, ld_k_head;
+  int64_t        ld_v_row, ld_v_head;
+  int64_t        ld_out_row, ld_out_head;
+  int32_t        n_heads, n_kv_heads, dk, dv;
+  const float*   log_decay;                /* fp32 [n_heads] */
+  float          scale;
+  float*         state;
+  int64_t        n_slots;
+  const int32_t* in_slots;                 /* [batch] or NULL */
+  const int32_t* out_slots;                /* [batch] or NULL */
+} dsi_linear;
+
+dsi_status dsi_linear_prefill(const dsi_linear* a, int64_t n_tokens, const int32_t* seq_starts,
+                              int32_t batch, void* workspace, size_t workspace_bytes, void* stream);
+dsi_status dsi_linear_decode(const dsi_linear* a, int32_t batch, int32_t tokens_per_seq, void* stream);
+
+/* Bytes of workspace with which dsi_linear_prefill splits its work over the
+ * current device (256 where it never does, or when a size is not positive). */
+size_t dsi_linear_workspace_size(int64_t n_tokens, int32_t batch, int32_t n_heads, int32_t dk,
+                                 int32_t dv);
+
+/*
  * dsi_selftest_wait_timeout — exercises the failure-detection path.  The
  * pages have no counterpart: every wait inside the library's kernels is
  * bounded, and a wait that runs out sets the device status word to

@@ -44,6 +44,17 @@ class DsiHeads(ctypes.Structure):
                 ("dst_rows", c_void_p), ("out_rows", c_int64), ("out_group", c_int32)]
 
 
+class DsiLinear(ctypes.Structure):
+    """Mirror of ``struct dsi_linear``."""
+    _fields_ = [("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("out", c_void_p),
+                ("ld_q_row", c_int64), ("ld_q_head", c_int64), ("ld_k_row", c_int64),
+                ("ld_k_head", c_int64), ("ld_v_row", c_int64), ("ld_v_head", c_int64),
+                ("ld_out_row", c_int64), ("ld_out_head", c_int64), ("n_heads", c_int32),
+                ("n_kv_heads", c_int32), ("dk", c_int32), ("dv", c_int32), ("log_decay", c_void_p),
+                ("scale", c_float), ("state", c_void_p), ("n_slots", c_int64), ("in_slots", c_void_p),
+                ("out_slots", c_void_p)]
+
+
 # name -> (restype, argtypes); the exported surface of include/dsi.h
 SIGNATURES = {
     "dsi_index_score": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(DsiCache), c_int32, c_int32,
@@ -87,6 +98,10 @@ SIGNATURES = {
     "dsi_norm_rope": (c_int32, [ctypes.POINTER(DsiHeads), ctypes.POINTER(DsiHeads), c_int64,
                                 c_int32, c_float, c_void_p, c_int64, c_void_p, c_int32, c_int32,
                                 c_int32, c_void_p]),
+    "dsi_linear_prefill": (c_int32, [ctypes.POINTER(DsiLinear), c_int64, c_void_p, c_int32, c_void_p,
+                                     c_size_t, c_void_p]),
+    "dsi_linear_decode": (c_int32, [ctypes.POINTER(DsiLinear), c_int32, c_int32, c_void_p]),
+    "dsi_linear_workspace_size": (c_size_t, [c_int64, c_int32, c_int32, c_int32, c_int32]),
     "dsi_workspace_size": (c_size_t, [c_int32, c_int32, c_int32, c_int32, c_int64, c_int32]),
     "dsi_layer_workspace_size": (c_size_t, [ctypes.POINTER(DsiCache), c_int32, c_int32, c_int32,
                                             c_int32, c_int64, c_int32]),
@@ -528,6 +543,110 @@ def norm_rope(queries: Optional[Heads], keys: Optional[Heads], table, positions,
         if st:
             raise DsiError("dsi_norm_rope", st, lib)
     return (queries.out if queries is not None else None), (keys.out if keys is not None else None)
+
+
+def linear_workspace_size(n_tokens: int, batch: int, n_heads: int, dk: int, dv: int,
+                          checked: bool = False) -> int:
+    """Bytes of workspace with which ``linear_prefill`` splits its work over the device."""
+    return int(load(checked).dsi_linear_workspace_size(int(n_tokens), int(batch), int(n_heads), int(dk),
+                                                       int(dv)))
+
+
+def _on(stream, device: torch.device):
+    """Context in which new tensors belong to the stream that the kernels run on."""
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _linear(q, k, v, log_decay, scale, state, in_slots, out_slots, out, batch: int, stream):
+    """The checked ``dsi_linear`` struct of the linear attention calls, and out."""
+    device = q.device
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _need(t.dim() == 3 and t.dtype == torch.bfloat16, f"{name} is a bf16 [tokens, heads, dims] tensor")
+    (n, H, dk), (nk, Hk, dkk), (nv, Hv, dv) = q.shape, k.shape, v.shape
+    _need(nk == n and nv == n and Hv == Hk and dkk == dk, "q, k and v have the same tokens, k the dims of q, "
+          "v the heads of k")
+    _need(log_decay.dtype == torch.float32 and log_decay.is_contiguous() and log_decay.numel() == H,
+          "log_decay is a contiguous fp32 [heads] tensor")
+    _need(out is None or (out.dtype == torch.bfloat16 and out.shape == (n, H, dv)),
+          "out is a bf16 [tokens, heads, dv] tensor")
+    for t in (q, k, v, out):
+        _need(t is None or t.stride(2) == 1 or t.numel() == 0, "the dims of a head must be contiguous")
+    if state is not None:
+        _need(state.dtype == torch.float32 and state.dim() == 4 and state.is_contiguous() and
+              state.shape[1:] == (H, dk, dv), "state is a contiguous fp32 [slots, heads, dk, dv] tensor")
+    for t, name in ((in_slots, "in_slots"), (out_slots, "out_slots")):
+        _need(t is None or (state is not None and t.dtype == torch.int32 and t.is_contiguous() and
+                            t.numel() == batch), f"{name} is a contiguous int32 [batch] tensor beside a state")
+    for t in (k, v, log_decay, out, state, in_slots, out_slots):
+        _need(t is None or t.device == device, "all tensors must be on one device")
+    if out is None and (n == 0 or H == 0 or dv == 0):
+        out = q.new_empty((n, H, dv))
+    elif out is None:
+        with torch.cuda.device(device), _on(stream, device):
+            out = torch.empty((n, H, dv), dtype=torch.bfloat16, device=device)
+    s = DsiLinear()
+    s.q, s.k, s.v, s.out = (t.data_ptr() or None for t in (q, k, v, out))
+    # a dim of size one has no pitch that matters
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+        d = t.shape[2]
+        setattr(s, f"ld_{name}_row", t.stride(0) if n > 1 else d)
+        setattr(s, f"ld_{name}_head", t.stride(1) if t.shape[1] > 1 else d)
+    s.n_heads, s.n_kv_heads, s.dk, s.dv = H, Hk, dk, dv
+    s.log_decay, s.scale = log_decay.data_ptr() or None, scale
+    if state is not None:
+        s.state, s.n_slots = state.data_ptr() or None, state.shape[0]
+        s.in_slots = in_slots.data_ptr() or None if in_slots is not None else None
+        s.out_slots = out_slots.data_ptr() or None if out_slots is not None else None
+    return s, out
+
+
+def linear_prefill(q, k, v, log_decay, scale: float, seq_starts, state=None, in_slots=None, out_slots=None,
+                   out=None, workspace=None, stream=None, checked: bool = False):
+    """Linear attention with a decay for each head over prompts laid end to end: ``dsi_linear_prefill``.
+
+    ``q [n, heads, dk]``, ``k [n, kv_heads, dk]``, ``v [n, kv_heads, dv]`` bf16 (any row and head strides
+    that are multiples of 8), ``log_decay`` fp32 ``[heads]``, ``seq_starts`` int32 ``[batch + 1]``.
+    ``state`` fp32 ``[slots, heads, dk, dv]``: sequence b starts from slot ``in_slots[b]`` (b unless given;
+    negative: zeros) and leaves its state in ``out_slots[b]`` (the in slot unless given; negative:
+    nowhere).  Returns out ``[n, heads, dv]`` bf16."""
+    lib = load(checked)
+    _need(seq_starts.dim() == 1 and seq_starts.dtype == torch.int32 and seq_starts.is_contiguous() and
+          seq_starts.numel() >= 1 and seq_starts.device == q.device,
+          "seq_starts is a contiguous int32 [batch + 1] tensor on q's device")
+    batch = seq_starts.numel() - 1
+    s, out = _linear(q, k, v, log_decay, scale, state, in_slots, out_slots, out, batch, stream)
+    device = q.device
+    if workspace is not None:
+        _need(workspace.device == device and workspace.is_contiguous(), "workspace is a contiguous tensor on q's device")
+    elif batch and s.n_heads:
+        with torch.cuda.device(device), _on(stream, device):
+            workspace = alloc_workspace(
+                lib.dsi_linear_workspace_size(q.shape[0], batch, s.n_heads, s.dk, s.dv), device)
+    if batch:
+        st = _launch(lib.dsi_linear_prefill, device, stream, ctypes.byref(s), q.shape[0], seq_starts.data_ptr(),
+                     batch, workspace.data_ptr() if workspace is not None else None,
+                     workspace.numel() * workspace.element_size() if workspace is not None else 0)
+        if st:
+            raise DsiError("dsi_linear_prefill", st, lib)
+    return out
+
+
+def linear_decode(q, k, v, log_decay, scale: float, state=None, tokens_per_seq: int = 1, in_slots=None,
+                  out_slots=None, out=None, stream=None, checked: bool = False):
+    """The same for ``tokens_per_seq`` new tokens of every sequence, rows in the sequences' order:
+    ``dsi_linear_decode``."""
+    lib = load(checked)
+    T = int(tokens_per_seq)
+    _need(T >= 1 and q.dim() == 3 and q.shape[0] % T == 0, "q has tokens_per_seq rows for every sequence")
+    batch = q.shape[0] // T
+    s, out = _linear(q, k, v, log_decay, scale, state, in_slots, out_slots, out, batch, stream)
+    if batch:
+        st = _launch(lib.dsi_linear_decode, q.device, stream, ctypes.byref(s), batch, T)
+        if st:
+            raise DsiError("dsi_linear_decode", st, lib)
+    return out
 
 
 def topk(scores, K: int, row_len=None, q_offset: int = 0, idx=None, count=None, stream=None,

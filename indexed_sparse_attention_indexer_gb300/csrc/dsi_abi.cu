@@ -8,6 +8,7 @@
 #include "dense_mla.h"
 #include "kernels.h"
 #include "latent_fp8.h"
+#include "linear_attn.h"
 #include "norm_rope.h"
 
 using namespace dsi;
@@ -205,6 +206,40 @@ bool in_place_ok(const dsi_heads& h, int64_t n_rows) {
   if (h.n_heads == 0 || h.x != h.out) return true;
   return h.out_dtype == DSI_BF16 && !h.dst_rows && (n_rows == 1 || h.ld_row == h.ld_out_row) &&
          (h.n_heads == 1 || h.ld_head == h.ld_out_head);
+}
+
+// The linear attention calls: rows of q, k, v and out, heads, states.
+dsi_status check_linear(const dsi_linear* a, int64_t n_tokens, int batch, LinearArgs* p) {
+  if (!a || n_tokens < 0 || batch < 0 || a->n_heads < 1 || a->n_kv_heads < 1 || !a->log_decay ||
+      !(a->scale == a->scale) || a->n_slots < 0)
+    return DSI_ERR_INVALID_ARG;
+  if (a->dk < 8 || a->dk > 128 || a->dk % 8 != 0 || a->dv < 8 || a->dv > 128 || a->dv % 8 != 0)
+    return DSI_ERR_UNSUPPORTED;
+  if (a->n_heads % a->n_kv_heads != 0) return DSI_ERR_INVALID_ARG;
+  // (blocks and tokens are counted in 32 bits)
+  if (n_tokens >= (1ll << 31) || (int64_t)batch * a->n_heads >= (1ll << 29)) return DSI_ERR_UNSUPPORTED;
+  if (n_tokens > 0) {
+    if (!a->q || !a->k || !a->v || !a->out || a->out == a->q || a->out == a->k || a->out == a->v)
+      return DSI_ERR_INVALID_ARG;
+    if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->out, 16))
+      return DSI_ERR_INVALID_ARG;
+    const int64_t pitch[4][3] = {{a->ld_q_row, a->ld_q_head, a->dk}, {a->ld_k_row, a->ld_k_head, a->dk},
+                                 {a->ld_v_row, a->ld_v_head, a->dv}, {a->ld_out_row, a->ld_out_head, a->dv}};
+    for (const auto& x : pitch)
+      if (x[0] < x[2] || x[1] < x[2] || x[0] % 8 != 0 || x[1] % 8 != 0) return DSI_ERR_INVALID_ARG;
+  }
+  if (!aligned(a->log_decay, 4) || !aligned(a->state, 16) || !aligned(a->in_slots, 4) || !aligned(a->out_slots, 4))
+    return DSI_ERR_INVALID_ARG;
+  if (!a->state && (a->in_slots || a->out_slots)) return DSI_ERR_INVALID_ARG;
+  if (a->state && !a->in_slots && a->n_slots < batch) return DSI_ERR_INVALID_ARG;
+  p->a = *a;
+  p->starts = nullptr;
+  p->n_tokens = n_tokens;
+  p->batch = batch;
+  p->T = 0;
+  p->group = a->n_heads / a->n_kv_heads;
+  p->err = status_ptr();
+  return DSI_OK;
 }
 
 }  // namespace
@@ -532,6 +567,38 @@ dsi_status dsi_norm_rope(const dsi_heads* queries, const dsi_heads* keys, int64_
   a.rope_dim = rope_dim;
   a.interleaved = interleaved;
   return from_cuda(launch_norm_rope(q, k, a, status_ptr(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t dsi_linear_workspace_size(int64_t n_tokens, int32_t batch, int32_t n_heads, int32_t dk,
+                                 int32_t dv) {
+  if (n_tokens <= 0 || batch <= 0 || n_heads <= 0 || dk <= 0 || dv <= 0) return 256;
+  return linear_prefill_workspace(n_tokens, batch, n_heads, dk, dv);
+}
+
+dsi_status dsi_linear_prefill(const dsi_linear* a, int64_t n_tokens, const int32_t* seq_starts,
+                              int32_t batch, void* workspace, size_t workspace_bytes, void* stream) {
+  LinearArgs p;
+  const dsi_status s = check_linear(a, n_tokens, batch, &p);
+  if (s != DSI_OK) return s;
+  if (!seq_starts || !aligned(seq_starts, 4)) return DSI_ERR_INVALID_ARG;
+  if (workspace) {
+    if (!aligned(workspace, 256)) return DSI_ERR_INVALID_ARG;
+    if (workspace_bytes < dsi_linear_workspace_size(n_tokens, batch, a->n_heads, a->dk, a->dv))
+      return DSI_ERR_WORKSPACE;
+  }
+  if (batch == 0) return DSI_OK;
+  p.starts = seq_starts;
+  return from_cuda(launch_linear_prefill(p, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dsi_status dsi_linear_decode(const dsi_linear* a, int32_t batch, int32_t tokens_per_seq, void* stream) {
+  if (tokens_per_seq < 1) return DSI_ERR_INVALID_ARG;
+  LinearArgs p;
+  const dsi_status s = check_linear(a, (int64_t)(batch > 0 ? batch : 0) * tokens_per_seq, batch, &p);
+  if (s != DSI_OK) return s;
+  if (batch == 0) return DSI_OK;
+  p.T = tokens_per_seq;
+  return from_cuda(launch_linear_recurrent(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 dsi_status dsi_selftest_wait_timeout(uint64_t limit_ns, void* stream) {
