@@ -455,6 +455,38 @@ dsi_status dsi_window_mla_prefill(const void* q, const dsi_cache* cache, int32_t
 size_t dsi_dense_mla_workspace_size(int32_t rows, int32_t n_heads);
 
 /*
+ * dsi_prefix_mla_decode — dsi_dense_mla_decode for a batch whose sequences go on
+ * from one common prefix, which is read and multiplied once for all: 128
+ * (query row, head) pairs of any sequences meet its rows together, where
+ * dsi_dense_mla_decode has only the pairs of one sequence.
+ *
+ * Candidate t of sequence b (rows T to a sequence) sees all positions of the
+ * prefix and positions 0 .. n_b - T + t of the sequence's own rows, n_b =
+ * cache.seq_lens[b] (none where that is negative: a sequence of length 0 sees the
+ * prefix alone).  For head h over both:
+ *   l_s = scale * q[r, h, :] . c_s;  out = sum_s softmax(l)_s * c_s[0:512];
+ *   lse = ln sum_s exp(l_s)
+ *   prefix  a cache of one sequence (batch == 1): its latent rows, contiguous or paged,
+ *           seq_lens[0] of them (on the device, like the others)
+ *   cache   the sequences' own rows.  Both have latent_dtype in common; they may be pages
+ *           of one pool, of one or of different sizes, or separate tensors
+ *   workspace  256-byte aligned, at least dsi_prefix_mla_workspace_size() bytes: the prefix's
+ *           and the sequences' parts are joined from there.  Calls that may run at once
+ *           need one each.
+ * Numbers, rows outside the visible range, rows that are not finite, page ids and errors as for
+ * dsi_dense_mla_decode; DSI_ERR_INVALID_ARG also for a prefix of other than
+ * one sequence, DSI_ERR_UNSUPPORTED for different latent dtypes,
+ * DSI_ERR_WORKSPACE for a missing workspace.
+ */
+dsi_status dsi_prefix_mla_decode(const void* q, const dsi_cache* prefix, const dsi_cache* cache,
+                                 int32_t tokens_per_seq, int32_t n_heads, float scale, void* out,
+                                 float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of dsi_prefix_mla_decode on the current device (256 when
+ * rows or n_heads is not positive). */
+size_t dsi_prefix_mla_workspace_size(int32_t rows, int32_t n_heads);
+
+/*
  * dsi_norm_rope — head norms and position rotation of new tokens' queries and
  * keys in one pass, the keys written straight into their cache rows (the
  * pages have no counterpart: they start at normed, rotated queries and keys).

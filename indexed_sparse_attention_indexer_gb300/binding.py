@@ -94,6 +94,9 @@ SIGNATURES = {
     "dsi_window_mla_prefill": (c_int32, [c_void_p, ctypes.POINTER(DsiCache), c_int32, c_int32,
                                          c_int64, c_int64, c_int64, c_float, c_void_p, c_void_p,
                                          c_void_p, c_size_t, c_void_p]),
+    "dsi_prefix_mla_decode": (c_int32, [c_void_p, ctypes.POINTER(DsiCache), ctypes.POINTER(DsiCache), c_int32,
+                                        c_int32, c_float, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "dsi_prefix_mla_workspace_size": (c_size_t, [c_int32, c_int32]),
     "dsi_dense_mla_workspace_size": (c_size_t, [c_int32, c_int32]),
     "dsi_norm_rope": (c_int32, [ctypes.POINTER(DsiHeads), ctypes.POINTER(DsiHeads), c_int64,
                                 c_int32, c_float, c_void_p, c_int64, c_void_p, c_int32, c_int32,
@@ -432,18 +435,19 @@ def dense_mla_workspace_size(rows: int, n_heads: int, checked: bool = False) -> 
 
 
 def _dense(fn: str, q, cache: Cache, args, rows: int, scale, out, lse, want_lse, workspace, stream,
-           checked):
-    """Checks and buffers shared by the dense and window calls; new buffers belong to the stream
-    that the kernels run on."""
+           checked, prefix: Optional[Cache] = None):
+    """Checks and buffers shared by the dense, window and prefix calls; new buffers belong to the
+    stream that the kernels run on."""
     lib = load(checked)
     if q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous() or q.shape[2] != D_QK:
         raise ValueError(f"q is a contiguous bf16 [rows, heads, {D_QK}] tensor")
     device = q.device
-    fault = cache.latent_fault()
-    if fault:
-        raise ValueError(fault)
-    if cache.latent.device != device:
-        raise ValueError("the cache has no latent rows on q's device")
+    for c in (cache,) if prefix is None else (cache, prefix):
+        fault = c.latent_fault()
+        if fault:
+            raise ValueError(fault)
+        if c.latent.device != device:
+            raise ValueError("the cache has no latent rows on q's device")
     n, H, _ = q.shape
     if n != rows:
         raise ValueError(f"q has {n} rows, the call {rows}")
@@ -464,12 +468,14 @@ def _dense(fn: str, q, cache: Cache, args, rows: int, scale, out, lse, want_lse,
             on = torch.cuda.ExternalStream(int(on), device=device)
         with torch.cuda.device(device), torch.cuda.stream(on):
             if workspace is None:
-                workspace = alloc_workspace(lib.dsi_dense_mla_workspace_size(n, H), device)
+                size = lib.dsi_dense_mla_workspace_size if prefix is None else lib.dsi_prefix_mla_workspace_size
+                workspace = alloc_workspace(size(n, H), device)
             if out is None:
                 out = torch.empty((n, H, D_LATENT), dtype=torch.bfloat16, device=device)
             if lse is None and want_lse:
                 lse = torch.empty((n, H), dtype=torch.float32, device=device)
-    st = _launch(getattr(lib, fn), device, stream, q.data_ptr(), cache.ref(), *args, scale,
+    caches = (cache.ref(),) if prefix is None else (prefix.ref(), cache.ref())
+    st = _launch(getattr(lib, fn), device, stream, q.data_ptr(), *caches, *args, scale,
                  out.data_ptr(), lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
                  workspace.numel() * workspace.element_size())
     if st:
@@ -505,6 +511,21 @@ def window_mla_prefill(q, cache: Cache, q_offset: int, window: int, n_sink: int,
     return _dense("dsi_window_mla_prefill", q, cache, (T, int(q.shape[1]), _i64(q_offset), _i64(window),
                                                        _i64(n_sink)),
                   T, scale, out, lse, want_lse, workspace, stream, checked)
+
+
+def prefix_mla_workspace_size(rows: int, n_heads: int, checked: bool = False) -> int:
+    """Bytes of workspace of ``prefix_mla_decode``."""
+    return int(load(checked).dsi_prefix_mla_workspace_size(rows, n_heads))
+
+
+def prefix_mla_decode(q, prefix: Cache, cache: Cache, scale: float, tokens_per_seq: int = 1, out=None,
+                      lse=None, want_lse=True, workspace=None, stream=None, checked: bool = False):
+    """Attention of the newest tokens over a prefix that the whole batch shares (a cache of one
+    sequence, read once for all) and over the sequences' own rows: ``dsi_prefix_mla_decode``.
+    ``q`` bf16 ``[batch * tokens_per_seq, heads, 576]``; returns (out, lse)."""
+    T = int(tokens_per_seq)
+    return _dense("dsi_prefix_mla_decode", q, cache, (T, int(q.shape[1])), cache.struct.batch * T, scale,
+                  out, lse, want_lse, workspace, stream, checked, prefix)
 
 
 def rope_table(n_positions: int, rope_dim: int, theta: float = 10000.0, device="cuda"):

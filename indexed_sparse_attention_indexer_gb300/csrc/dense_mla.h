@@ -25,4 +25,9 @@ struct DenseArgs {
 size_t dense_mla_workspace();
 cudaError_t launch_dense_mla(const DenseArgs& a, cudaStream_t st);
 
+// The same over a prefix that all rows see, and over a.c, every sequence's own rows.
+size_t prefix_mla_workspace(int rows, int H);
+cudaError_t launch_prefix_mla(const DenseArgs& a, const CacheView& prefix, const float* prefix_scale,
+                              cudaStream_t st);
+
 }  // namespace dsi

@@ -471,6 +471,13 @@ size_t dsi_dense_mla_workspace_size(int32_t rows, int32_t n_heads) {
   return dense_mla_workspace();
 }
 
+// What positions in 32 bits leave room for (they run up to a few tiles past the last one).
+static bool positions_fit(const dsi_cache* c) {
+  return c->s_max <= (1ll << 31) - 1024 &&
+         (c->block_table ? c->num_pages <= ((1ll << 31) - 1) / c->page_size
+                         : c->batch <= 0 || c->s_max <= ((1ll << 31) - 1) / c->batch);
+}
+
 // The dense and window calls: rows of a decode batch or of a prefill.
 static dsi_status dense_common(const void* q, const dsi_cache* cache, int64_t rows, int T, int H,
                                int decode, int64_t q_offset, int64_t window, int64_t n_sink,
@@ -482,11 +489,7 @@ static dsi_status dense_common(const void* q, const dsi_cache* cache, int64_t ro
   const dsi_status s = check_cache(cache, (int)rows, decode, q_offset, false, true, decode ? T : 1);
   if (s != DSI_OK) return s;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSI_ERR_INVALID_ARG;
-  // (positions are 32-bit and run up to a few tiles past the last one)
-  if (cache->s_max > (1ll << 31) - 1024 ||
-      (cache->block_table ? cache->num_pages > ((1ll << 31) - 1) / cache->page_size
-                          : cache->batch > 0 && cache->s_max > ((1ll << 31) - 1) / cache->batch))
-    return DSI_ERR_UNSUPPORTED;
+  if (!positions_fit(cache)) return DSI_ERR_UNSUPPORTED;
   if (ws) {
     if (!aligned(ws, 256)) return DSI_ERR_INVALID_ARG;
     if (ws_bytes < dense_mla_workspace()) return DSI_ERR_WORKSPACE;
@@ -511,6 +514,52 @@ static dsi_status dense_common(const void* q, const dsi_cache* cache, int64_t ro
   a.ws = ws;
   a.err = status_ptr();
   return from_cuda(launch_dense_mla(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t dsi_prefix_mla_workspace_size(int32_t rows, int32_t n_heads) {
+  if (rows <= 0 || n_heads <= 0) return 256;
+  return prefix_mla_workspace(rows, n_heads);
+}
+
+dsi_status dsi_prefix_mla_decode(const void* q, const dsi_cache* prefix, const dsi_cache* cache,
+                                 int32_t tokens_per_seq, int32_t n_heads, float scale, void* out,
+                                 float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !out || !prefix || !cache || tokens_per_seq < 1 || cache->batch < 0 || !(scale == scale))
+    return DSI_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)cache->batch * tokens_per_seq;
+  if (n_heads < 1 || n_heads > 128 || rows > 0x7fffffff / n_heads) return DSI_ERR_UNSUPPORTED;
+  if (prefix->batch != 1) return DSI_ERR_INVALID_ARG;
+  dsi_status s = check_cache(prefix, 1, 1, 0, false, true);
+  if (s != DSI_OK) return s;
+  s = check_cache(cache, (int)rows, 1, 0, false, true, tokens_per_seq);
+  if (s != DSI_OK) return s;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSI_ERR_INVALID_ARG;
+  if (prefix->latent_dtype != cache->latent_dtype || !positions_fit(prefix) || !positions_fit(cache))
+    return DSI_ERR_UNSUPPORTED;
+  if (rows == 0) return DSI_OK;
+  if (!workspace) return DSI_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return DSI_ERR_INVALID_ARG;
+  if (workspace_bytes < prefix_mla_workspace((int)rows, n_heads)) return DSI_ERR_WORKSPACE;
+  DenseArgs a;
+  a.q = reinterpret_cast<const bf16*>(q);
+  a.c = view_of(cache);
+  a.c.tokens_per_seq = tokens_per_seq;
+  a.latent_scale = cache->latent_dtype == DSI_FP8_E4M3 ? cache->latent_scale : nullptr;
+  a.rows = (int)rows;
+  a.T = tokens_per_seq;
+  a.H = n_heads;
+  a.decode = 1;
+  a.q_offset = 0;
+  a.window = (1ll << 31) - 1;
+  a.n_sink = 0;
+  a.scale = scale;
+  a.out = reinterpret_cast<bf16*>(out);
+  a.lse = lse;
+  a.ws = workspace;
+  a.err = status_ptr();
+  return from_cuda(launch_prefix_mla(a, view_of(prefix),
+                                     prefix->latent_dtype == DSI_FP8_E4M3 ? prefix->latent_scale : nullptr,
+                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 
 dsi_status dsi_dense_mla_decode(const void* q, const dsi_cache* cache, int32_t tokens_per_seq,
