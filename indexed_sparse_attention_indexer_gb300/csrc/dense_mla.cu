@@ -146,6 +146,22 @@ struct Workspace {
   float* o;        // [2 * clusters][128][512] unnormalised outputs
   float2* ml;      // [2 * clusters][128] reference max, sum of weights
   Record* rec;     // [clusters]
+  // shared prefix: groups in one piece, [prefix, own][rows * H], and every group's clusters
+  float* whole_o;
+  float2* whole_ml;
+  int2* spans;     // [groups] first and last
+};
+
+// A prefix that all rows see, in the form of the kernel that has one.  Its groups are
+// consecutive rows of any sequences and come before those of the sequences' own rows.
+template <bool PFX>
+struct Prefix {};
+template <>
+struct Prefix<true> {
+  CUtensorMap lmap, rmap;
+  CacheView c;
+  const float* scale;
+  int tokens, groups, box;
 };
 
 struct Plan {
@@ -157,13 +173,28 @@ struct Plan {
 };
 
 struct Group {
+  bool shared;                 // of the prefix
   int b, row0, nt;             // sequence, first query row, tokens
   int n_first, n_last;         // visible lengths of the first and last token
   int lo, main0, sink_tiles, tiles;
 };
 
-__device__ __forceinline__ Group group_of(const DenseArgs& a, const Plan& p, int g) {
+template <bool PFX>
+__device__ __forceinline__ Group group_of(const DenseArgs& a, const Plan& p, const Prefix<PFX>& sh, int g) {
   Group r;
+  r.shared = false;
+  if constexpr (PFX) {
+    if (g < sh.groups) {
+      r.shared = true;
+      r.b = r.lo = r.main0 = r.sink_tiles = 0;
+      r.row0 = g * sh.tokens;
+      r.nt = min(sh.tokens, a.rows - r.row0);
+      r.n_first = r.n_last = (int)visible_len(sh.c, 0, 1, 0);
+      r.tiles = max(1, (r.n_last + kNp - 1) / kNp);
+      return r;
+    }
+    g -= sh.groups;
+  }
   r.b = p.per_seq == 1 ? g : g / p.per_seq;
   const int t0 = (g - r.b * p.per_seq) * p.tokens;
   r.nt = min(p.tokens, a.T - t0);
@@ -200,10 +231,12 @@ struct Piece {
   Group grp;
   int g, t0, t1;
 };
-__device__ __forceinline__ bool next_piece(const DenseArgs& a, const Plan& p, Walk& w, Piece& x) {
+template <bool PFX>
+__device__ __forceinline__ bool next_piece(const DenseArgs& a, const Plan& p, const Prefix<PFX>& sh, Walk& w,
+                                           Piece& x) {
   if (w.g >= p.groups || w.left <= 0) return false;
   x.g = w.g;
-  x.grp = group_of(a, p, w.g);
+  x.grp = group_of(a, p, sh, w.g);
   if (w.stride > 0) {
     x.t0 = 0;
     x.t1 = x.grp.tiles;
@@ -217,6 +250,13 @@ __device__ __forceinline__ bool next_piece(const DenseArgs& a, const Plan& p, Wa
   w.u = 0;
   ++w.g;                       // (a run that ends inside the group has nothing left)
   return x.t1 > x.t0;
+}
+
+// The rows that a group attends to.
+template <bool PFX>
+__device__ __forceinline__ const CacheView& rows_of(const DenseArgs& a, const Prefix<PFX>& sh, const Group& g) {
+  if constexpr (PFX) return g.shared ? sh.c : a.c;
+  return a.c;
 }
 
 // Cache row of position p of sequence b; -1 (reported) for a bad page id.
@@ -410,11 +450,11 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w, bool wi
   }
 }
 
-template <bool F8>
+template <bool F8, bool PFX>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<F8>::threads, 1)
 dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
              const __grid_constant__ CUtensorMap qmap, const __grid_constant__ DenseArgs a,
-             const __grid_constant__ Plan plan, Workspace ws, int box) {
+             const __grid_constant__ Plan plan, Workspace ws, int box, const __grid_constant__ Prefix<PFX> sh) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -488,6 +528,10 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     prefetch_tmap(&lmap);
     prefetch_tmap(&rmap);
     prefetch_tmap(&qmap);
+    if constexpr (PFX) {
+      prefetch_tmap(&sh.lmap);
+      prefetch_tmap(&sh.rmap);
+    }
   }
   grid_dep_wait();     // lengths, queries and cache rows may come from the kernel before
   __syncthreads();
@@ -497,7 +541,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     unsigned long long sum = 0;
     int widest = 0;
     for (int g = tid; g < plan.groups; g += Y::threads) {
-      const int n = group_of(a, plan, g).tiles + kGroupCost;
+      const int n = group_of(a, plan, sh, g).tiles + kGroupCost;
       sum += (unsigned)n;
       widest = max(widest, n);
     }
@@ -528,7 +572,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     long long before = 0;
     for (int g0 = 0; g0 < plan.groups && start < (long long)total; g0 += Y::threads) {
       const int g = g0 + tid;
-      const int n = g < plan.groups ? group_of(a, plan, g).tiles + kGroupCost : 0;
+      const int n = g < plan.groups ? group_of(a, plan, sh, g).tiles + kGroupCost : 0;
       int chunk;
       const int at = block_exclusive_scan(n, scan_s, chunk);
       if (n > 0 && start >= before + at && start < before + at + n) {
@@ -560,7 +604,6 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     int slot = 0, tg = 0;                      // ring slots; tiles
     uint32_t edge_ph = 0;                      // parities of landed[]
     uint32_t issued = 0, issued_edge = 0;      // stages with a copy in flight; into an edge tile
-    const int64_t cache_rows = a.c.block_table ? a.c.num_pages * a.c.page_size : a.c.batch * a.c.s_max;
     bool ok = true;
     // Every warp that waits for the ring's slots waits for each of them and arrives on
     // each of their full barriers, whoever fills it: a phase that it has not seen cannot
@@ -568,7 +611,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     // FP8 rows: the ring is filled by the converting warps and, with queries, warp 1;
     // warp 0's copies go to the raw stages.
 #pragma unroll 1
-    while (ok && next_piece(a, plan, walk, x)) {
+    while (ok && next_piece(a, plan, sh, walk, x)) {
 #pragma unroll 1
       for (int i = 0; i < 2 && (!F8 || warp == 1); ++i, ++slot) {
         const int stage = slot % kStages;
@@ -589,6 +632,16 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         }
       }
       if (!ok) break;
+      const CacheView& c = rows_of(a, sh, x.grp);
+      const int64_t cache_rows = c.block_table ? c.num_pages * c.page_size : c.batch * c.s_max;
+      const CUtensorMap *rows_map = &lmap, *rope_map = &rmap;
+      int rows_box = box;
+      if constexpr (PFX)
+        if (x.grp.shared) {
+          rows_map = &sh.lmap;
+          rope_map = &sh.rmap;
+          rows_box = sh.box;
+        }
       int asked = x.t0;
 #pragma unroll 1
       for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
@@ -599,17 +652,17 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         uint8_t* st = smem + (F8 ? Y::raw + stage * kRawBytes : Y::c + stage * kStageBytes);
         const bool whole = F8 || all_see(a, x.grp, p0, kNp);
         if (warp == 0) {
-          // the tile by TMA, boxes of `box` rows (a page or a part of one) by 128 bytes of
+          // the tile by TMA, boxes of `rows_box` rows (a page or a part of one) by 128 bytes of
           // dims; boxes that no token sees are left out
           uint64_t* bar = F8 ? &raw_full[stage] : whole ? &full[stage] : &landed[stage];
           if (!(ok = wait32(F8 ? &raw_empty[stage] : &empty[stage], ph ^ 1))) break;
           constexpr int kBlks = F8 ? 3 : 5;      // blocks of 128 bytes a row, the last the rope half
-          const int boxes = kNp / box;
-          const int pb = p0 + lane * box;        // lane's box, if it has one
-          const bool seen = lane < boxes && pb < x.grp.n_last && (pb + box > x.grp.lo || pb < (int)a.n_sink);
+          const int boxes = kNp / rows_box;
+          const int pb = p0 + lane * rows_box;        // lane's rows_box, if it has one
+          const bool seen = lane < boxes && pb < x.grp.n_last && (pb + rows_box > x.grp.lo || pb < (int)a.n_sink);
           const int n = __popc(__ballot_sync(0xffffffffu, seen));
           if (lane == 0) {
-            mbar_arrive_expect_tx(bar, (uint32_t)(n * box * (F8 ? kRawBytes / kNp : kRowBytes)));
+            mbar_arrive_expect_tx(bar, (uint32_t)(n * rows_box * (F8 ? kRawBytes / kNp : kRowBytes)));
             if (!whole) mbar_arrive(&full[stage]);
             if (!F8) {
               issued |= 1u << stage;
@@ -620,17 +673,17 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           __syncwarp();
 #pragma unroll 1
           for (int i = lane; i < boxes * kBlks; i += 32) {
-            const int bx = i / kBlks, blk = i - bx * kBlks, p = p0 + bx * box;
-            if (!(p < x.grp.n_last && (p + box > x.grp.lo || p < (int)a.n_sink))) continue;
-            const int row = row_of(a.c, x.grp.b, p, err);
-            // a bad page id: the box past the tensor's last row, which reads as zeros
-            const int y = row < 0 ? (int)a.c.num_pages * a.c.page_size : row;
+            const int bx = i / kBlks, blk = i - bx * kBlks, p = p0 + bx * rows_box;
+            if (!(p < x.grp.n_last && (p + rows_box > x.grp.lo || p < (int)a.n_sink))) continue;
+            const int row = row_of(c, x.grp.b, p, err);
+            // a bad page id: the rows_box past the tensor's last row, which reads as zeros
+            const int y = row < 0 ? (int)c.num_pages * c.page_size : row;
             if (blk < kBlks - 1)
-              tma_load_2d(st + blk * kBlockBytes + bx * box * 128, &lmap,
+              tma_load_2d(st + blk * kBlockBytes + bx * rows_box * 128, rows_map,
                           (int)rho * 256 + blk * (256 / (kBlks - 1)), y, bar);
             else
-              tma_load_2d(st + (F8 ? kRawRope + bx * box * kRopeHalf : kRopeOff + bx * box * kRopeHalf * 2),
-                          &rmap, DSI_D_LATENT + (int)rho * kRopeHalf, y, bar);
+              tma_load_2d(st + (F8 ? kRawRope + bx * rows_box * kRopeHalf : kRopeOff + bx * rows_box * kRopeHalf * 2),
+                          rope_map, DSI_D_LATENT + (int)rho * kRopeHalf, y, bar);
           }
           // decode: the caches come from HBM; tiles are asked for into L2 kAhead tiles
           // before their copies (two a step until that far ahead, each CTA every other
@@ -638,14 +691,14 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           if (a.decode) {
             asked = max(asked, t + 2);
             for (int n2 = 0; n2 < 2 && asked < min(x.t1, t + kAhead); ++n2, ++asked) {
-              const int p = tile_pos(x.grp, asked) + lane * box;
+              const int p = tile_pos(x.grp, asked) + lane * rows_box;
               if ((asked & 1) == (int)rho && lane < boxes && p < x.grp.n_last &&
-                  (p + box > x.grp.lo || p < (int)a.n_sink)) {
-                const int row = row_of(a.c, x.grp.b, p, err);
+                  (p + rows_box > x.grp.lo || p < (int)a.n_sink)) {
+                const int row = row_of(c, x.grp.b, p, err);
                 constexpr int kPitch = F8 ? DSI_D_QK : 2 * DSI_D_QK;
-                if (row >= 0 && (int64_t)row + box <= cache_rows)
-                  bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(a.c.latent) + (int64_t)row * kPitch,
-                                   (uint32_t)(box * kPitch));
+                if (row >= 0 && (int64_t)row + rows_box <= cache_rows)
+                  bulk_prefetch_l2(reinterpret_cast<const uint8_t*>(c.latent) + (int64_t)row * kPitch,
+                                   (uint32_t)(rows_box * kPitch));
               }
             }
           }
@@ -715,15 +768,16 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     bool ok = true;
     auto lookup = [&](int t) {                    // cache row of this thread's row of tile t
       const int p = t < x.t1 ? tile_pos(x.grp, t) + rr : -1;
-      return p >= 0 && any_sees(a, x.grp, p) ? row_of(a.c, x.grp.b, p, err) : -1;
+      return p >= 0 && any_sees(a, x.grp, p) ? row_of(rows_of(a, sh, x.grp), x.grp.b, p, err) : -1;
     };
     auto scales = [&](int row) {                  // of the latent dims and of the rope dims
+      const float* from = a.latent_scale;
+      if constexpr (PFX) from = x.grp.shared ? sh.scale : from;
       return row < 0 ? make_float2(0.f, 0.f)
-                     : make_float2(__ldg(a.latent_scale + (int64_t)row * 5 + s0),
-                                   __ldg(a.latent_scale + (int64_t)row * 5 + 4));
+                     : make_float2(__ldg(from + (int64_t)row * 5 + s0), __ldg(from + (int64_t)row * 5 + 4));
     };
 #pragma unroll 1
-    while (ok && next_piece(a, plan, walk, x)) {
+    while (ok && next_piece(a, plan, sh, walk, x)) {
       // (the query slots are waited for and passed on)
       for (int i = 0; i < 2 && ok; ++i, ++slot) {
         ok = wait32(&empty[slot % kStages], ((uint32_t)(slot / kStages) & 1u) ^ 1u);
@@ -787,7 +841,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       bool ok = true;
       const uint64_t qr = desc_sw64(smem_u32(smem + Y::qr));
 #pragma unroll 1
-      while (ok && next_piece(a, plan, walk, x)) {
+      while (ok && next_piece(a, plan, sh, walk, x)) {
         if (!(ok = wait1(q_ready, (uint32_t)pieces & 1u))) break;
         ++pieces;
         slot += 2;                               // the query slice
@@ -822,7 +876,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       bool ok = true;
       const uint64_t pd = desc_sw128(smem_u32(smem + Y::p));
 #pragma unroll 1
-      while (ok && next_piece(a, plan, walk, x)) {
+      while (ok && next_piece(a, plan, sh, walk, x)) {
         slot += 2;                               // the query slice
 #pragma unroll 1
         for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
@@ -858,7 +912,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     int slot = 0, tg = 0;
     bool ok = true;
 #pragma unroll 1
-    while (ok && (warp & 3) < plan.live && next_piece(a, plan, walk, x)) {
+    while (ok && (warp & 3) < plan.live && next_piece(a, plan, sh, walk, x)) {
       // The query slice: the rope half by plain loads (begun first), the four 64-dim
       // blocks out of the two ring slots that the producers filled ahead.  The
       // logit MMAs of the piece before are done: this warp has seen all its tiles.
@@ -953,9 +1007,9 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     int tg = 0, pieces = 0;
     bool ok = true;
 #pragma unroll 1
-    while (ok && quarter < plan.live && next_piece(a, plan, walk, x)) {
+    while (ok && quarter < plan.live && next_piece(a, plan, sh, walk, x)) {
       const int tok = min(m / a.H, x.grp.nt - 1);
-      const int n_row = tok == 0 ? x.grp.n_first
+      const int n_row = tok == 0 || x.grp.shared ? x.grp.n_first
                                  : (int)visible_len(a.c, x.grp.row0 + tok, a.decode, a.q_offset);
       const int lo_row = n_row - (int)a.window;
       float m_mine = -INFINITY, l_mine = 0.f;
@@ -1113,7 +1167,12 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       // ---- the piece's output: this CTA's 256 dims, 128 of them by each set ------
       const bool entire = x.t0 == 0 && x.t1 == x.grp.tiles;
       const int slot = 2 * k + (x.t0 == 0 ? 1 : 0);
-      if (!entire) {
+      if constexpr (PFX) {
+        if (rho == 0 && set == 0 && m == 0) {
+          if (x.t0 == 0) ws.spans[x.g].x = k;
+          if (x.t1 == x.grp.tiles) ws.spans[x.g].y = k;
+        }
+      } else if (!entire) {
         if (x.t0 == 0) {
           rec.starts = x.g;
         } else {
@@ -1125,9 +1184,11 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
       const int64_t orow = (int64_t)x.grp.row0 * a.H + m;
       // nothing visible: 0; NaN stays NaN
       const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+      // (with a prefix a row's output is always joined: from the rows' places for groups in one piece)
+      const int64_t part = PFX && entire ? orow + (x.grp.shared ? 0 : (int64_t)a.rows * a.H) : (int64_t)slot * kM + m;
       uint8_t* const dst0 = reinterpret_cast<uint8_t*>(
-          entire ? (void*)(a.out + orow * DSI_D_LATENT + rho * 256)
-                 : (void*)(ws.o + ((int64_t)slot * kM + m) * DSI_D_LATENT + rho * 256));
+          !PFX && entire ? (void*)(a.out + orow * DSI_D_LATENT + rho * 256)
+                         : (void*)((PFX && entire ? ws.whole_o : ws.o) + part * DSI_D_LATENT + rho * 256));
 #pragma unroll 1
       for (int c0 = set * 128; c0 < set * 128 + 128; c0 += 32) {
         float o[32];
@@ -1135,7 +1196,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         tmem_ld32(tmem + lane_base + TM_O + c0, o);
         tmem_ld_wait();
         if (!live) {
-        } else if (entire) {
+        } else if (!PFX && entire) {
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -1153,14 +1214,14 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
         }
       }
       if (live && rho == 0 && set == 0) {
-        if (!entire) ws.ml[slot * kM + m] = make_float2(m_ref, l_sum);
+        if (PFX || !entire) (PFX && entire ? ws.whole_ml : ws.ml)[part] = make_float2(m_ref, l_sum);
         else if (a.lse) a.lse[orow] = l_sum == 0.f ? -INFINITY : (m_ref + log2f(l_sum)) / kLog2e;
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free);
     }
-    if (plan.split && rho == 0 && set == 0 && m == 0) ws.rec[k] = rec;
+    if (!PFX && plan.split && rho == 0 && set == 0 && m == 0) ws.rec[k] = rec;
   }
   tc_fence_before();
   __syncthreads();
@@ -1243,10 +1304,57 @@ dense_mla_join(DenseArgs a, Plan plan, Workspace ws, int clusters, int rows) {
   }
 }
 
+// Joins a row's parts over the prefix and over its sequence's own rows, each of one piece or
+// more: a warp takes 128 dims of a head.  Bound by the parts' 2 KB each, which mostly are in L2.
+__global__ void __launch_bounds__(kJoinThreads)
+prefix_mla_join(DenseArgs a, Plan plan, Workspace ws, int prefix_tokens, int prefix_groups) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int vectors = a.rows * a.H;
+  grid_dep_wait();     // the parts come from the kernel launched just before
+  grid_dep_launch();
+  for (int at = blockIdx.x; at < vectors; at += gridDim.x) {
+    const int row = at / a.H, h = at - row * a.H, b = row / a.T, t = row - b * a.T;
+    const int gp = row / prefix_tokens, go = prefix_groups + b * plan.per_seq + t / plan.tokens;
+    const int mp = (row - gp * prefix_tokens) * a.H + h, mo = t % plan.tokens * a.H + h;
+    const int2 sp = ws.spans[gp], so = ws.spans[go];
+    const int np = sp.y - sp.x + 1, n = np + so.y - so.x + 1;
+    // piece j: where it is (an index of the pieces' slots, or of the rows' places, below 0)
+    auto place = [&](int j) {
+      const bool own = j >= np;
+      const int2 s = own ? so : sp;
+      if (own) j -= np;
+      if (s.x == s.y) return -1 - (own ? (int64_t)vectors + at : (int64_t)at);
+      return (int64_t)(2 * (s.x + j) + (j == 0 ? 1 : 0)) * kM + (own ? mo : mp);
+    };
+    auto stats = [&](int64_t p) { return p < 0 ? ws.whole_ml[-1 - p] : ws.ml[p]; };
+    float top = -INFINITY;
+    for (int j = lane; j < n; j += 32) top = fmaxf(top, stats(place(j)).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const int64_t p = place(j);
+      const float2 ml = stats(p);
+      const float4 v = reinterpret_cast<const float4*>(p < 0 ? ws.whole_o + (-1 - p) * DSI_D_LATENT
+                                                             : ws.o + p * DSI_D_LATENT)[tid];
+      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+      sum += w * ml.y;
+      o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    __align__(8) bf16 o4[4] = {__float2bfloat16(o.x * inv), __float2bfloat16(o.y * inv),
+                               __float2bfloat16(o.z * inv), __float2bfloat16(o.w * inv)};
+    *reinterpret_cast<uint2*>(a.out + (int64_t)at * DSI_D_LATENT + tid * 4) = *reinterpret_cast<const uint2*>(o4);
+    if (a.lse && tid == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) / kLog2e;
+  }
+}
+
 // Two-CTA clusters that fit on the current device at once, queried once per
 // device and form, after the kernel has been given its shared memory there; 0
 // without a device.
-template <bool F8>
+template <bool F8, bool PFX>
 int cluster_slots() {
   static std::atomic<int> cached[64];
   int dev = 0, v = 0;
@@ -1263,9 +1371,9 @@ int cluster_slots() {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(dense_mla_tc<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(dense_mla_tc<F8, PFX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Layout<F8>::bytes) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&v, dense_mla_tc<F8>, &cfg) != cudaSuccess || v < 1) {
+      cudaOccupancyMaxActiveClusters(&v, dense_mla_tc<F8, PFX>, &cfg) != cudaSuccess || v < 1) {
     cudaGetLastError();
     return 0;
   }
@@ -1276,21 +1384,38 @@ int cluster_slots() {
 
 constexpr size_t kSlotBytes = (size_t)kM * (DSI_D_LATENT * sizeof(float) + sizeof(float2));
 
-template <bool F8>
+template <bool F8, bool PFX>
 cudaError_t launch(const CUtensorMap& map, const CUtensorMap& rmap, const CUtensorMap& qmap,
-                   const DenseArgs& a, const Plan& plan, const Workspace& ws, int box, int clusters,
-                   cudaStream_t st) {
+                   const DenseArgs& a, const Plan& plan, const Workspace& ws, int box, const Prefix<PFX>& sh,
+                   int clusters, cudaStream_t st) {
   const cudaError_t e =
-      launch_overlapped(dense_mla_tc<F8>, dim3(2u * (unsigned)clusters), dim3(Layout<F8>::threads),
-                        Layout<F8>::bytes, st, map, rmap, qmap, a, plan, ws, box);
+      launch_overlapped(dense_mla_tc<F8, PFX>, dim3(2u * (unsigned)clusters), dim3(Layout<F8>::threads),
+                        Layout<F8>::bytes, st, map, rmap, qmap, a, plan, ws, box, sh);
   note_launch();
   return e;
+}
+
+// Maps of a cache's rows, in boxes of the largest part of 64 rows that its pages are made of.
+bool map_rows(const CacheView& c, bool f8, CUtensorMap* map, CUtensorMap* rmap, int* box) {
+  *box = kNp;
+  if (c.block_table)
+    while (c.page_size % *box != 0) *box /= 2;   // page sizes are multiples of 8
+  const uint64_t rows = c.block_table ? (uint64_t)c.num_pages * c.page_size : (uint64_t)c.batch * c.s_max;
+  return f8 ? tma_map_2d(map, c.latent, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, DSI_D_QK, 128, (uint32_t)*box) &&
+                  tma_map_2d(rmap, c.latent, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, DSI_D_QK, kRopeHalf,
+                             (uint32_t)*box, CU_TENSOR_MAP_SWIZZLE_NONE)
+            : tma_map_2d(map, c.latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, DSI_D_QK, 64, (uint32_t)*box) &&
+                  tma_map_2d(rmap, c.latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, DSI_D_QK, kRopeHalf,
+                             (uint32_t)*box, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+bool map_queries(const DenseArgs& a, CUtensorMap* qmap) {
+  return tma_map_2d(qmap, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)a.rows * a.H, DSI_D_QK, 64, kM);
 }
 
 }  // namespace
 
 size_t dense_mla_workspace() {
-  int n = cluster_slots<false>() > cluster_slots<true>() ? cluster_slots<false>() : cluster_slots<true>();
+  int n = cluster_slots<false, false>() > cluster_slots<true, false>() ? cluster_slots<false, false>() : cluster_slots<true, false>();
   if (n == 0) n = 76;                            // no device: what a GB300 takes
   return (size_t)n * (2 * kSlotBytes + sizeof(Record));
 }
@@ -1302,7 +1427,7 @@ cudaError_t launch_dense_mla(const DenseArgs& a, cudaStream_t st) {
   plan.per_seq = (a.T + plan.tokens - 1) / plan.tokens;
   const int64_t groups = (int64_t)plan.per_seq * (a.rows / a.T);
   plan.groups = (int)groups;                     // <= rows
-  const int slots = f8 ? cluster_slots<true>() : cluster_slots<false>();
+  const int slots = f8 ? cluster_slots<true, false>() : cluster_slots<false, false>();
   if (slots == 0) return cudaErrorInvalidConfiguration;
   // at most a cluster a tile
   const int64_t span = a.window + a.n_sink < a.c.s_max ? a.window + a.n_sink + plan.tokens + 2 * kNp : a.c.s_max;
@@ -1318,39 +1443,75 @@ cudaError_t launch_dense_mla(const DenseArgs& a, cudaStream_t st) {
   plan.split = a.ws != nullptr && clusters > 1 &&
                (groups + clusters - 1) / clusters * most > least + kWholeSlack;
   plan.live = (plan.tokens * a.H + 31) / 32;
-  Workspace ws = {nullptr, nullptr, nullptr};
+  Workspace ws = {};
   if (plan.split) {
     ws.o = static_cast<float*>(a.ws);
     ws.ml = reinterpret_cast<float2*>(ws.o + (size_t)2 * clusters * kM * DSI_D_LATENT);
     ws.rec = reinterpret_cast<Record*>(ws.ml + (size_t)2 * clusters * kM);
   }
-  // TMA boxes: the largest part of 64 rows that pages are made of
-  int box = kNp;
-  if (a.c.block_table)
-    while (a.c.page_size % box != 0) box /= 2;   // page sizes are multiples of 8
-  CUtensorMap map, rmap;
-  const uint64_t rows = a.c.block_table ? (uint64_t)a.c.num_pages * a.c.page_size
-                                        : (uint64_t)a.c.batch * a.c.s_max;
-  const bool mapped =
-      f8 ? tma_map_2d(&map, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, DSI_D_QK, 128, (uint32_t)box) &&
-               tma_map_2d(&rmap, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, DSI_D_QK, kRopeHalf,
-                          (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_NONE)
-         : tma_map_2d(&map, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, DSI_D_QK, 64,
-                      (uint32_t)box) &&
-               tma_map_2d(&rmap, a.c.latent, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, DSI_D_QK,
-                          kRopeHalf, (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_64B);
-  if (!mapped) return cudaErrorInvalidValue;
-  CUtensorMap qmap;
-  if (!tma_map_2d(&qmap, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)a.rows * a.H, DSI_D_QK, 64, kM))
-    return cudaErrorInvalidValue;
-  cudaError_t e = f8 ? launch<true>(map, rmap, qmap, a, plan, ws, box, clusters, st)
-                     : launch<false>(map, rmap, qmap, a, plan, ws, box, clusters, st);
+  int box;
+  CUtensorMap map, rmap, qmap;
+  if (!map_rows(a.c, f8, &map, &rmap, &box) || !map_queries(a, &qmap)) return cudaErrorInvalidValue;
+  cudaError_t e = f8 ? launch<true, false>(map, rmap, qmap, a, plan, ws, box, {}, clusters, st)
+                     : launch<false, false>(map, rmap, qmap, a, plan, ws, box, {}, clusters, st);
   if (e != cudaSuccess || !plan.split) return e;
   // enough blocks for one resident wave: a call without split groups pays little
   const int64_t rows_at_most = (int64_t)clusters * plan.tokens * a.H;
   const int64_t wave = 16 * clusters;
   e = launch_overlapped(dense_mla_join, dim3((unsigned)(rows_at_most < wave ? rows_at_most : wave)),
                         dim3(kJoinThreads), 0, st, a, plan, ws, clusters, plan.tokens * a.H);
+  note_launch();
+  return e;
+}
+
+size_t prefix_mla_workspace(int rows, int H) {
+  int n = cluster_slots<false, true>() > cluster_slots<true, true>() ? cluster_slots<false, true>()
+                                                                     : cluster_slots<true, true>();
+  if (n == 0) n = 76;                            // no device: what a GB300 takes
+  const size_t vectors = (size_t)rows * H;
+  return (size_t)n * 2 * kSlotBytes + 2 * vectors * (DSI_D_LATENT * sizeof(float) + sizeof(float2)) +
+         2 * (size_t)rows * sizeof(int2);
+}
+
+cudaError_t launch_prefix_mla(const DenseArgs& a, const CacheView& prefix, const float* prefix_scale,
+                              cudaStream_t st) {
+  const bool f8 = a.latent_scale != nullptr;
+  Prefix<true> sh;
+  sh.c = prefix;
+  sh.scale = prefix_scale;
+  sh.tokens = kM / a.H < a.rows ? kM / a.H : a.rows;
+  sh.groups = (a.rows + sh.tokens - 1) / sh.tokens;
+  Plan plan;
+  plan.tokens = kM / a.H < a.T ? kM / a.H : a.T;
+  plan.per_seq = (a.T + plan.tokens - 1) / plan.tokens;
+  const int64_t groups = sh.groups + (int64_t)plan.per_seq * (a.rows / a.T);
+  plan.groups = (int)groups;                     // <= 2 * rows
+  plan.live = (sh.tokens * a.H + 31) / 32;
+  const int slots = f8 ? cluster_slots<true, true>() : cluster_slots<false, true>();
+  if (slots == 0) return cudaErrorInvalidConfiguration;
+  // at most a cluster a tile
+  const int64_t tiles = sh.groups * ((prefix.s_max + kNp - 1) / kNp) +
+                        (groups - sh.groups) * ((a.c.s_max + kNp - 1) / kNp);
+  const int clusters = (int)(tiles < slots ? tiles : slots);
+  plan.split = clusters > 1;
+  const size_t vectors = (size_t)a.rows * a.H;
+  Workspace ws = {};
+  ws.o = static_cast<float*>(a.ws);
+  ws.whole_o = ws.o + (size_t)2 * clusters * kM * DSI_D_LATENT;
+  ws.ml = reinterpret_cast<float2*>(ws.whole_o + 2 * vectors * DSI_D_LATENT);
+  ws.whole_ml = ws.ml + (size_t)2 * clusters * kM;
+  ws.spans = reinterpret_cast<int2*>(ws.whole_ml + 2 * vectors);
+  int box;
+  CUtensorMap map, rmap, qmap;
+  if (!map_rows(a.c, f8, &map, &rmap, &box) || !map_rows(prefix, f8, &sh.lmap, &sh.rmap, &sh.box) ||
+      !map_queries(a, &qmap))
+    return cudaErrorInvalidValue;
+  cudaError_t e = f8 ? launch<true, true>(map, rmap, qmap, a, plan, ws, box, sh, clusters, st)
+                     : launch<false, true>(map, rmap, qmap, a, plan, ws, box, sh, clusters, st);
+  if (e != cudaSuccess) return e;
+  const int64_t wave = 32 * clusters;
+  e = launch_overlapped(prefix_mla_join, dim3((unsigned)((int64_t)vectors < wave ? (int64_t)vectors : wave)),
+                        dim3(kJoinThreads), 0, st, a, plan, ws, sh.tokens, sh.groups);
   note_launch();
   return e;
 }

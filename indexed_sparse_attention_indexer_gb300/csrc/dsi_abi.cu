@@ -550,7 +550,7 @@ dsi_status dsi_prefix_mla_decode(const void* q, const dsi_cache* prefix, const d
   a.H = n_heads;
   a.decode = 1;
   a.q_offset = 0;
-  a.window = (1ll << 31) - 1;
+  a.window = prefix->s_max > cache->s_max ? prefix->s_max : cache->s_max;   // everything
   a.n_sink = 0;
   a.scale = scale;
   a.out = reinterpret_cast<bf16*>(out);
