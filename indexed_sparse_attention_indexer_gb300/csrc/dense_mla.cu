@@ -59,6 +59,7 @@
 
 #include "kernels.h"
 #include "tc_common.cuh"
+#include "tc_waits.cuh"
 #include "tma_host.h"
 
 namespace dsi {
@@ -383,38 +384,7 @@ __device__ __forceinline__ void clear_rows(uint8_t* st, uint64_t rows, int lane)
     if ((eight >> (8 * i)) & 1u) *reinterpret_cast<uint4*>(at + i * 512) = make_uint4(0, 0, 0, 0);
 }
 
-// Bounded waits whose slow path is out of line and takes few arguments: the
-// roles' loops together have to stay small enough for the instruction cache.
-__shared__ volatile int s_abort;               // a role has given up: the others follow
-__shared__ int* s_err;                         // device status word
-
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = global_ns();
-  for (uint32_t i = 1;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    if (ok) return true;
-    if ((i & 255u) == 0) {
-      if (s_abort) return false;
-      if (global_ns() - t0 > kWaitLimitNs) {
-        s_abort = 1;
-        report(s_err, kErrTimeout);
-        return false;
-      }
-    }
-  }
-}
-__device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity) {
-  return mbar_try_wait(bar, parity) || wait_on(smem_u32(bar), parity);
-}
-// Whole warps: all lanes proceed or none.
-__device__ __forceinline__ bool wait32(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait1(bar, parity));
-}
-// ... for phases that the other CTA's arrivals and stores complete
+// wait32 for phases that the other CTA's arrivals and stores complete
 __device__ __forceinline__ bool wait32_cluster(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity) || wait_on(smem_u32(bar), parity));
 }
@@ -688,7 +658,9 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           // decode: the caches come from HBM; tiles are asked for into L2 kAhead tiles
           // before their copies (two a step until that far ahead, each CTA every other
           // tile, whole rows), so that a copy holds its stage only as long as L2 takes
-          if (a.decode) {
+          // (a prefix's rows are other clusters' too and mostly there: with them 64 x 32768 x 128 heads
+          // 701 us, without 608; 16 heads 118 and 105; a prefix of 151 MB 448 and 452)
+          if (a.decode && !x.grp.shared) {
             asked = max(asked, t + 2);
             for (int n2 = 0; n2 < 2 && asked < min(x.t1, t + kAhead); ++n2, ++asked) {
               const int p = tile_pos(x.grp, asked) + lane * rows_box;
