@@ -133,7 +133,4 @@ cudaError_t launch_linear_recurrent(const LinearArgs& p, cudaStream_t st) {
   return p.a.dv > 32 ? launch<16>(p, st) : launch<8>(p, st);
 }
 
-size_t linear_prefill_workspace(int64_t, int, int, int, int) { return 256; }
-cudaError_t launch_linear_prefill(const LinearArgs& p, void*, cudaStream_t st) { return launch_linear_recurrent(p, st); }
-
 }  // namespace dsi
