@@ -6,15 +6,22 @@
 //
 // A CTA takes 64 of the dv columns of one head: they do not meet the other columns but
 // in q . k, which is computed again.  Per chunk four products, all 128 rows high:
-//   P  = Q K^T                [tokens x tokens]   decayed, masked, to bf16 in place (TMEM)
-//   OI = P V                  [tokens x 64]
-//   OX = Q S                  [tokens x 64]       S rounded to bf16
-//   ST += K^T V'              [dk x 64]           V' = decayed V in two bf16 parts: the state
-//                                                 stays exact to 2^-16 of what enters it
-// and ST, the state, stays in fp32 in TMEM from a sequence's first chunk to its last.
+//   P  = Q K^T     [tokens x tokens]   decayed, masked, to bf16 in place (TMEM)
+//   OI = P V       [tokens x 64]
+//   OX = Q S       [tokens x 64]       S rounded to bf16
+//   D  = K^T V'    [dk x 64]           V' = decayed V in two bf16 parts, exact to 2^-16;
+//                                      K^T is turned into TMEM (as an MN-major operand in shared
+//                                      memory a product of 16 tokens takes 130 cycles, not 46)
+// and the state, S <- S + expm1(g r) S + D, stays in the registers of its warps, in fp32, from a
+// sequence's first chunk to its last.  (Summed in TMEM by the products themselves its error
+// was 3e-6 of its norm: the tensor core cuts its sums off.)
 //
-// Roles (20 warps), each walking the same list of (sequence, head, columns):
-//   0 copies (TMA), 1 MMAs, 4-7 P, 8-11 V', 12-15 the state, 16-19 outputs.
+// Roles (28 warps), each walking the same list of (sequence, head, columns):
+//   0 copies (TMA), 1 products K^T V', 2 Q K^T, 3 Q S and P V, 4-7 P, 8-15 V' and K^T,
+//   16-23 the state, 24-27 outputs.
+// (A lane that issues products in a branch of its own takes 110 cycles for each, of 16 dims or
+// tokens; an elected lane of a converged warp less, and three warps issue side by side: a
+// chunk took 5100 cycles with one issuer.)
 // A chunk's rows behind the sequence's end (other sequences') are cleared or never
 // stored.  A v that is not finite is taken out of V before P V (its weight
 // of 0 for earlier tokens would give NaN) and the column's later outputs become
@@ -32,32 +39,35 @@ namespace {
 constexpr int kC = 128;                        // tokens of a chunk
 constexpr int kCols = 64;                      // columns of the state that a CTA takes
 constexpr int kTile = kC * 128;                // 64 dims of a chunk, 16 KB
-constexpr int kStages = 2;
-constexpr int kStageBytes = 5 * kTile;         // Q (two tiles), K (two), V
-constexpr int kThreads = 640;
+constexpr int kQk = 2;                         // chunks of Q and of K in shared memory
+constexpr int kV = 3;                          // of V
+constexpr int kSplit = 2;                      // bf16 parts of V'
+constexpr int kThreads = 896;
 
-constexpr int oVh = kStages * kStageBytes;     // V', high and low parts
-constexpr int oVl = oVh + kTile;
-constexpr int oS = oVl + kTile;                // the state in bf16: [dk][64]
-constexpr int oPow = oS + kTile;               // P's warps: powers of lam, [4][128]
-constexpr int oRev = oPow + 4 * 128 * 4;       // ... lam^31 .. lam^0, [4][32]
-constexpr int kMarks = 3;                      // (V' is up to two chunks before the outputs)
-constexpr int oBad = oRev + 4 * 32 * 4;        // [kMarks][4] a warp's rows of V hold something not finite
-constexpr int oFirst = oBad + kMarks * 4 * 4;  // [kMarks][4][64] the first such row of a column
-constexpr int oBar = oFirst + kMarks * 4 * 64;
-constexpr int kBars = 3 * kStages + 2 + 2 + 2 + 5;
+constexpr int oQ = 0;                          // [kQk][2] tiles
+constexpr int oK = oQ + kQk * 2 * kTile;       // [kQk][2]
+constexpr int oV = oK + kQk * 2 * kTile;       // [kV]
+constexpr int oVp = oV + kV * kTile;           // V', its parts
+constexpr int oS = oVp + kSplit * kTile;       // the state in bf16: [dk][64]
+constexpr int kMarks = 5;                      // (the place of V t + 5 is free once P V of t + 2 is done, whose
+                                               // P's tile was free once the outputs of t were read)
+constexpr int oBad = oS + kTile;               // [kMarks][8] a warp's part of V holds something not finite
+constexpr int oFirst = oBad + kMarks * 8 * 4;  // [kMarks][8][32] the first such row of a column
+constexpr int oBar = oFirst + kMarks * 8 * 32;
+constexpr int kBars = 4 * kQk + 3 * kV + 4 * 2 + 5;
 constexpr int oSlot = oBar + kBars * 8;
-constexpr int kSmem = oSlot + 16 + 1024;
-static_assert(kSmem <= 227 * 1024 && oBar % 8 == 0, "shared memory");
+constexpr int kSmem = oSlot + 8;
+// (static variables take a kilobyte of their own, aligned like the rest)
+static_assert(kSmem <= 226 * 1024 && oBad % 16 == 0 && oBar % 8 == 0, "shared memory");
 
-constexpr uint32_t TM_P = 0;                   // two tiles of 128 columns
-constexpr uint32_t TM_OI = 256;
-constexpr uint32_t TM_ST = 320;
-constexpr uint32_t TM_OX = 384;                // two tiles of 64 columns
+constexpr uint32_t TM_P = 0;                   // two tiles of 128 columns: q . k, then P in the first half
+constexpr uint32_t TM_OI = 64;                 // ... and OI in the second
+constexpr uint32_t TM_OX = 256;                // two tiles of 64 columns
+constexpr uint32_t TM_D = 384;
+constexpr uint32_t TM_KT = 448;                // K^T in bf16: [dk][128 tokens]
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t IDESC_P = idesc_f32(1, kC, kC);
 constexpr uint32_t IDESC_O = idesc_f32_bmn(1, kC, kCols);
-constexpr uint32_t IDESC_ST = IDESC_O | (1u << 15);   // A, too, is MN-major (K^T)
 
 struct Plan {
   int parts;                                   // 64-column parts of dv
@@ -92,6 +102,19 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 __device__ __forceinline__ void tmem_st16w(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
@@ -105,47 +128,106 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&y);
 }
-__device__ __forceinline__ bool bf16x2_finite(uint32_t w) {
-  return (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u;
+
+// Four 8 x 8 blocks of 16-bit values, transposed: thread i gets values 2 (i % 4) and + 1 of
+// column i / 4 of each block, whose rows' addresses lanes 8 b .. 8 b + 7 give for block b.
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t saddr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
+}
+// 16 lanes x 32 columns: registers 2 c and 2 c + 1 hold column 4 c + i % 4 of lanes i / 4 and i / 4 + 8.
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
+// The MMA and its commit, issued by one lane of a converged warp.
+__device__ __forceinline__ void e_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void e_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void e_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
+// Two fp32 products in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n"
+      " mov.b64 {%0, %1}, z;\n}\n"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+// KB: blocks of 64 dims that dk takes.
+template <int KB>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
              const __grid_constant__ CUtensorMap vmap, const __grid_constant__ LinearArgs p,
              const __grid_constant__ Plan plan) {
+  __shared__ __align__(16) float pow_table[4][32];   // P's warps: lam^0 .. lam^31
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* qk_full = reinterpret_cast<uint64_t*>(smem + oBar);   // [kStages] Q and K landed
-  uint64_t* v_full = qk_full + kStages;        // [kStages] V landed
-  uint64_t* empty = v_full + kStages;          // [kStages] a chunk's MMAs done
-  uint64_t* s_full = empty + kStages;          // [2] q . k in TMEM
+  uint8_t* const smem = smem_raw;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + oBar);   // [kQk] Q landed
+  uint64_t* k_full = q_full + kQk;             // [kQk] K landed
+  uint64_t* q_empty = k_full + kQk;            // [kQk] Q done with
+  uint64_t* k_empty = q_empty + kQk;           // [kQk] K done with: turned, and q . k done
+  uint64_t* v_full = k_empty + kQk;            // [kV]
+  uint64_t* v_empty = v_full + kV;             // [kV]
+  uint64_t* v_clean = v_empty + kV;            // [kV] V without what is not finite or not the sequence's
+  uint64_t* s_full = v_clean + kV;             // [2] q . k in TMEM
   uint64_t* p_full = s_full + 2;               // [2] P in TMEM
-  uint64_t* p_empty = p_full + 2;              // [2] P V done
-  uint64_t* v_ready = p_empty + 2;             // V cleaned, V' written
-  uint64_t* st_ready = v_ready + 1;            // state decayed, its bf16 form written
-  uint64_t* st_done = v_ready + 2;             // K^T V' (and Q S) done
-  uint64_t* o_full = v_ready + 3;              // OI and OX done
-  uint64_t* o_empty = v_ready + 4;             // ... read out
+  uint64_t* o_full = p_full + 2;               // [2] OI and OX done
+  uint64_t* o_empty = o_full + 2;              // [2] ... read out: P's tile and OX's are free
+  uint64_t* v_ready = o_empty + 2;             // V' and K^T written
+  uint64_t* st_ready = v_ready + 1;            // the state's bf16 form written
+  uint64_t* st_taken = v_ready + 2;            // Q S done
+  uint64_t* d_full = v_ready + 3;              // K^T V' done
+  uint64_t* d_empty = v_ready + 4;             // ... added to the state
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + oSlot);
   const dsi_linear& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&qk_full[s], 1);
-      mbar_init(&v_full[s], 1);
-      mbar_init(&empty[s], 1);
+    for (int i = 0; i < kQk; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&k_full[i], 1);
+      mbar_init(&q_empty[i], 2);
+      mbar_init(&k_empty[i], 1 + 8);
+    }
+    for (int i = 0; i < kV; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_clean[i], 8);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
-      mbar_init(&p_empty[i], 1);
+      mbar_init(&o_full[i], 2);
+      mbar_init(&o_empty[i], 4);
     }
-    mbar_init(v_ready, 4);
-    mbar_init(st_ready, 4);
-    mbar_init(st_done, 1);
-    mbar_init(o_full, 1);
-    mbar_init(o_empty, 4);
+    mbar_init(v_ready, 8);
+    mbar_init(st_ready, 8);
+    mbar_init(st_taken, 1);
+    mbar_init(d_full, 1);
+    mbar_init(d_empty, 8);
     s_abort = 0;
     s_err = p.err;
     fence_barrier_init();
@@ -172,109 +254,116 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
   if (warp == 0) {
     // ======================= copies ==============================================
     if (lane == 0) {
-      const bool wide = a.dk > 64;             // (else the second tiles are not read, but for
-                                               // rows of ST that nobody reads)
 #pragma unroll 1
       while (ok && next_item(p, plan, walk, it)) {
         const int hk = it.h / p.group;
 #pragma unroll 1
         for (int c = 0; c < it.chunks; ++c, ++t) {
-          const int s = t % kStages;
-          if (!(ok = wait1(&empty[s], ((uint32_t)(t / kStages) & 1u) ^ 1u))) break;
-          uint8_t* st = smem + s * kStageBytes;
-          const int at = (int)it.first + c * kC;
-          mbar_arrive_expect_tx(&qk_full[s], (wide ? 4 : 2) * kTile);
-          tma_load_3d(st, &qmap, 0, it.h, at, &qk_full[s]);
-          tma_load_3d(st + 2 * kTile, &kmap, 0, hk, at, &qk_full[s]);
-          if (wide) {
-            tma_load_3d(st + kTile, &qmap, 64, it.h, at, &qk_full[s]);
-            tma_load_3d(st + 3 * kTile, &kmap, 64, hk, at, &qk_full[s]);
-          }
-          mbar_arrive_expect_tx(&v_full[s], kTile);
-          tma_load_3d(st + 4 * kTile, &vmap, it.part * kCols, hk, at, &v_full[s]);
+          const int s = t % kQk, sv = t % kV, at = (int)it.first + c * kC;
+          const uint32_t ph = ((uint32_t)(t / kQk) & 1u) ^ 1u;
+          if (!(ok = wait1(&k_empty[s], ph))) break;
+          mbar_arrive_expect_tx(&k_full[s], KB * kTile);
+#pragma unroll
+          for (int x = 0; x < KB; ++x)
+            tma_load_3d(smem + oK + (s * 2 + x) * kTile, &kmap, x * 64, hk, at, &k_full[s]);
+          if (!(ok = wait1(&v_empty[sv], ((uint32_t)(t / kV) & 1u) ^ 1u))) break;
+          mbar_arrive_expect_tx(&v_full[sv], kTile);
+          tma_load_3d(smem + oV + sv * kTile, &vmap, it.part * kCols, hk, at, &v_full[sv]);
+          if (!(ok = wait1(&q_empty[s], ph))) break;
+          mbar_arrive_expect_tx(&q_full[s], KB * kTile);
+#pragma unroll
+          for (int x = 0; x < KB; ++x)
+            tma_load_3d(smem + oQ + (s * 2 + x) * kTile, &qmap, x * 64, it.h, at, &q_full[s]);
         }
       }
-      // never leave the CTA with a copy still landing in shared memory
+      // never leave the CTA with a copy still landing in shared memory (of chunk t some may be
+      // under way: a wait that nothing ends is bounded)
       if (s_abort) {
         volatile int no_abort = 0;
-        for (int i = max(0, t - kStages); i < t; ++i) {
-          mbar_wait(&qk_full[i % kStages], (uint32_t)(i / kStages) & 1u, &no_abort, p.err, 100000000ull);
-          mbar_wait(&v_full[i % kStages], (uint32_t)(i / kStages) & 1u, &no_abort, p.err, 100000000ull);
+        for (int i = max(0, t + 1 - kV); i <= t; ++i) {
+          mbar_wait(&q_full[i % kQk], (uint32_t)(i / kQk) & 1u, &no_abort, p.err, 1000000ull);
+          mbar_wait(&k_full[i % kQk], (uint32_t)(i / kQk) & 1u, &no_abort, p.err, 1000000ull);
+          mbar_wait(&v_full[i % kV], (uint32_t)(i / kV) & 1u, &no_abort, p.err, 1000000ull);
         }
       }
     }
   } else if (warp == 1) {
-    // ======================= MMAs ================================================
-    if (lane == 0) {
-      const int steps = (a.dk + 15) / 16;
-      const uint64_t d_vh = desc_sw128_mn(smem_u32(smem + oVh), kTile), d_vl = desc_sw128_mn(smem_u32(smem + oVl), kTile);
+    // ======================= D = K^T V' ==========================================
+    {
+      const uint64_t d_vp = desc_sw128_mn(smem_u32(smem + oVp), kTile);
+#pragma unroll 1
+      while (ok && next_item(p, plan, walk, it)) {
+#pragma unroll 1
+        for (int c = 0; c < it.chunks; ++c, ++t) {
+          const uint32_t ph = (uint32_t)t & 1u;
+          if (!(ok = wait32(v_ready, ph) && wait32(d_empty, ph ^ 1u))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int x = 0; x < kSplit * (kC / 16); ++x)
+            e_mma_ta(tmem + TM_D, tmem + TM_KT + (x & 7) * 8,
+                            d_vp + (uint64_t)(((x >> 3) * kTile + (x & 7) * 2048) >> 4), IDESC_O, x > 0 ? 1u : 0u);
+          e_commit(d_full);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ======================= Q K^T ===============================================
+    {
+#pragma unroll 1
+      while (ok && next_item(p, plan, walk, it)) {
+#pragma unroll 1
+        for (int c = 0; c < it.chunks; ++c, ++t) {
+          const int s = t % kQk;
+          const uint32_t ph = (uint32_t)(t / kQk) & 1u;
+          if (!(ok = wait32(&k_full[s], ph) && wait32(&q_full[s], ph) &&
+                     wait32(&o_empty[t & 1], ((uint32_t)(t >> 1) & 1u) ^ 1u)))
+            break;
+          tc_fence_after();
+          const uint64_t q = desc_sw128(smem_u32(smem + oQ + s * 2 * kTile)), k = desc_sw128(smem_u32(smem + oK + s * 2 * kTile));
+#pragma unroll
+          for (int x = 0; x < 4 * KB; ++x) {
+            const uint64_t off = (uint64_t)(((x >> 2) * kTile + (x & 3) * 32) >> 4);
+            e_mma(tmem + TM_P + (t & 1) * kC, q + off, k + off, IDESC_P, x > 0 ? 1u : 0u);
+          }
+          e_commit(&s_full[t & 1]);
+          e_commit(&k_empty[s]);
+          e_commit(&q_empty[s]);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ======================= Q S, P V ============================================
+    {
       const uint64_t d_s = desc_sw128_mn(smem_u32(smem + oS), kTile);
-      auto qk = [&](int i) {                   // chunk i's q . k
-        const int s = i % kStages;
-        if (!wait1(&qk_full[s], (uint32_t)(i / kStages) & 1u)) return false;
-        if (!wait1(&p_empty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u)) return false;
-        tc_fence_after();
-        const uint32_t base = smem_u32(smem + s * kStageBytes);
-        const uint64_t q = desc_sw128(base), k = desc_sw128(base + 2 * kTile);
 #pragma unroll 1
-        for (int x = 0; x < steps; ++x) {
-          const uint64_t off = (uint64_t)(((x >> 2) * kTile + (x & 3) * 32) >> 4);
-          mma_bf16(tmem + TM_P + (i & 1) * kC, q + off, k + off, IDESC_P, x > 0 ? 1u : 0u);
-        }
-        mma_commit(&s_full[i & 1]);
-        return true;
-      };
-      // one chunk ahead: whether there is one
-      int c = -1;
-      it.chunks = 0;
-      auto advance = [&]() {
-        if (++c < it.chunks) return true;
-        c = 0;
-        do {
-          if (!next_item(p, plan, walk, it)) return false;
-        } while (it.chunks == 0);
-        return true;
-      };
-      bool more = advance();
-      if (more) ok = qk(0);
+      while (ok && next_item(p, plan, walk, it)) {
 #pragma unroll 1
-      while (ok && more) {
-        more = advance();
-        const int s = t % kStages;
-        const uint32_t base = smem_u32(smem + s * kStageBytes);
-        if (!(ok = wait1(st_ready, (uint32_t)t & 1u))) break;
-        tc_fence_after();
-        const uint64_t q = desc_sw128(base);
-#pragma unroll 1
-        for (int x = 0; x < steps; ++x)
-          mma_bf16(tmem + TM_OX + (t & 1) * kCols, q + (uint64_t)(((x >> 2) * kTile + (x & 3) * 32) >> 4),
-                   d_s + (uint64_t)((x * 2048) >> 4), IDESC_O, x > 0 ? 1u : 0u);
-        if (!(ok = wait1(v_ready, (uint32_t)t & 1u))) break;
-        tc_fence_after();
-        const uint64_t k = desc_sw128_mn(base + 2 * kTile, kTile);
+        for (int c = 0; c < it.chunks; ++c, ++t) {
+          const int s = t % kQk;
+          const uint32_t ph = (uint32_t)t & 1u;
+          if (!(ok = wait32(st_ready, ph) && wait32(&q_full[s], (uint32_t)(t / kQk) & 1u) &&
+                     wait32(&o_empty[t & 1], ((uint32_t)(t >> 1) & 1u) ^ 1u))) break;
+          tc_fence_after();
+          const uint64_t q = desc_sw128(smem_u32(smem + oQ + s * 2 * kTile));
 #pragma unroll
-        for (int x = 0; x < 2 * (kC / 16); ++x)
-          mma_bf16(tmem + TM_ST, k + (uint64_t)(((x & 7) * 2048) >> 4),
-                   (x < 8 ? d_vh : d_vl) + (uint64_t)(((x & 7) * 2048) >> 4), IDESC_ST, 1u);
-        mma_commit(st_done);
-        // the next chunk's q . k before this one's P V, if it is there already
-        bool ahead = false;
-        if (more && mbar_test_wait(&qk_full[(t + 1) % kStages], (uint32_t)((t + 1) / kStages) & 1u)) {
-          if (!(ok = qk(t + 1))) break;
-          ahead = true;
-        }
-        if (!(ok = wait1(&p_full[t & 1], (uint32_t)(t >> 1) & 1u) && wait1(o_empty, ((uint32_t)t & 1u) ^ 1u))) break;
-        tc_fence_after();
-        const uint64_t v = desc_sw128_mn(base + 4 * kTile, kTile);
+          for (int x = 0; x < 4 * KB; ++x)
+            e_mma(tmem + TM_OX + (t & 1) * kCols, q + (uint64_t)(((x >> 2) * kTile + (x & 3) * 32) >> 4), d_s + (uint64_t)((x * 2048) >> 4),
+                     IDESC_O, x > 0 ? 1u : 0u);
+          e_commit(st_taken);
+          e_commit(&q_empty[s]);
+          e_commit(&o_full[t & 1]);
+          if (!(ok = wait32(&v_clean[t % kV], (uint32_t)(t / kV) & 1u) && wait32(&p_full[t & 1], (uint32_t)(t >> 1) & 1u))) break;
+          tc_fence_after();
+          const uint64_t v = desc_sw128_mn(smem_u32(smem + oV + (t % kV) * kTile), kTile);
 #pragma unroll
-        for (int x = 0; x < kC / 16; ++x)
-          mma_bf16_tmem_a(tmem + TM_OI, tmem + TM_P + (t & 1) * kC + x * 8, v + (uint64_t)((x * 2048) >> 4), IDESC_O,
-                          x > 0 ? 1u : 0u);
-        mma_commit(o_full);
-        mma_commit(&p_empty[t & 1]);
-        mma_commit(&empty[s]);
-        ++t;
-        if (more && !ahead && !(ok = qk(t))) break;
+          for (int x = 0; x < kC / 16; ++x)
+            e_mma_ta(tmem + TM_OI + (t & 1) * kC, tmem + TM_P + (t & 1) * kC + x * 8, v + (uint64_t)((x * 2048) >> 4), IDESC_O,
+                            x > 0 ? 1u : 0u);
+          e_commit(&o_full[t & 1]);
+          e_commit(&v_empty[t % kV]);
+        }
       }
     }
     __syncwarp();
@@ -284,8 +373,8 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     // lam^(i-j) as lam^(i-j31) lam^(j31-j) (j31 the block's last token: both
     // exponents are positive), the warp's own block by table; the rest is 0.
     const int w = warp & 3;
-    float* pow_s = reinterpret_cast<float*>(smem + oPow) + w * 128;
-    float* rev_s = reinterpret_cast<float*>(smem + oRev) + w * 32;
+    float* const pow_s = pow_table[w];
+    float far_of[3] = {0.f, 0.f, 0.f};         // lam^(i-j31) of the blocks before the warp's own
     int h = -1;
 #pragma unroll 1
     while (ok && next_item(p, plan, walk, it)) {
@@ -293,9 +382,9 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         h = it.h;
         const float g = __ldg(a.log_decay + h);
         __syncwarp();
+        pow_s[lane] = power(g, lane);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pow_s[i * 32 + lane] = power(g, i * 32 + lane);
-        rev_s[lane] = power(g, 31 - lane);
+        for (int i = 0; i < 3; ++i) far_of[i] = power(g, max(0, row - i * 32 - 31));
         __syncwarp();
       }
 #pragma unroll 1
@@ -311,12 +400,14 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
             tmem_ld32(t_p + blk * 32, v);
             tmem_ld_wait();
             if (blk < w) {
-              const float far = pow_s[row - blk * 32 - 31];
+              const float far = blk == 0 ? far_of[0] : blk == 1 ? far_of[1] : far_of[2];
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(rev_s + j);
-                out[j / 2] = pack_bf16(v[j] * (far * f.x), v[j + 1] * (far * f.y));
-                out[j / 2 + 1] = pack_bf16(v[j + 2] * (far * f.z), v[j + 3] * (far * f.w));
+                const float4 f = *reinterpret_cast<const float4*>(pow_s + 28 - j);
+                const float2 y0 = mul2(make_float2(v[j], v[j + 1]), mul2(make_float2(far, far), make_float2(f.w, f.z)));
+                const float2 y1 = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(far, far), make_float2(f.y, f.x)));
+                out[j / 2] = pack_bf16(y0.x, y0.y);
+                out[j / 2 + 1] = pack_bf16(y1.x, y1.y);
               }
             } else {
 #pragma unroll
@@ -337,146 +428,166 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         if (lane == 0) mbar_arrive(&p_full[t & 1]);
       }
     }
-  } else if (warp >= 8 && warp < 12) {
-    // ======================= V' ==================================================
-    const int w = warp & 3;
+  } else if (warp >= 8 && warp < 16) {
+    // ======================= V' and K^T ==========================================
+    // V': thread = half a row of V, its parts held in registers until the products with the
+    // V' before are done.  K^T: a warp turns 32 dims of 64 tokens, 8 x 8 at a time.
+    const int w = warp - 8, u0 = (w >> 2) * 4, quarter = w & 3;
+    const uint32_t k_lane = (uint32_t)((w >> 2) * 64 + ((lane >> 4) & 1) * 8 + (lane & 7));   // token whose address this lane gives
+    const uint32_t k_u = (uint32_t)((quarter & 1) * 4 + ((lane >> 3) & 1));                  // ... and 8 dims
 #pragma unroll 1
     while (ok && next_item(p, plan, walk, it)) {
       const float g = __ldg(a.log_decay + it.h);
 #pragma unroll 1
       for (int c = 0; c < it.chunks; ++c, ++t) {
-        const int s = t % kStages, r = min(kC, it.n - c * kC);
-        uint8_t* st = smem + s * kStageBytes;
+        const int s = t % kQk, sv = t % kV, r = min(kC, it.n - c * kC);
+        uint8_t* st = smem + oV + sv * kTile;
         const float f = row < r ? power(g, r - 1 - row) : 0.f;
-        if (!(ok = wait32(&v_full[s], (uint32_t)(t / kStages) & 1u))) break;
-        if (t > 0 && !(ok = wait32(st_done, (uint32_t)(t - 1) & 1u))) break;
-        bool bad = false;
-#pragma unroll 1
-        for (int u = 0; u < 8; ++u) {
-          const uint32_t off = sw128_offset((uint32_t)row, (uint32_t)u);
-          const uint4 v4 = *reinterpret_cast<const uint4*>(st + 4 * kTile + off);
+        if (!(ok = wait32(&v_full[sv], (uint32_t)(t / kV) & 1u))) break;
+        uint32_t part[kSplit][16], big = 0u;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint4 v4 = *reinterpret_cast<const uint4*>(st + sw128_offset((uint32_t)row, (uint32_t)(u0 + u)));
           const uint32_t x[4] = {v4.x, v4.y, v4.z, v4.w};
-          uint32_t hi[4], lo[4];
-          bool fine = true;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            fine = fine && bf16x2_finite(x[e]);
-            const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[e]));
-            const float y0 = y.x * f, y1 = y.y * f;
-            hi[e] = pack_bf16(y0, y1);
-            const float2 z = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi[e]));
-            lo[e] = pack_bf16(y0 - z.x, y1 - z.y);
-          }
-          if (row >= r) {
+            big = __vmaxu2(big, x[e] & 0x7FFF7FFFu);
+            const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[e]));
+            float2 y = mul2(v, make_float2(f, f));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) hi[e] = lo[e] = 0u;
-            *reinterpret_cast<uint4*>(st + 4 * kTile + off) = make_uint4(0, 0, 0, 0);
-          } else {
-            bad = bad || !fine;
+            for (int i = 0; i < kSplit; ++i) {
+              part[i][4 * u + e] = pack_bf16(y.x, y.y);
+              const float2 z = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&part[i][4 * u + e]));
+              y = make_float2(y.x - z.x, y.y - z.y);
+            }
           }
-          *reinterpret_cast<uint4*>(smem + oVh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(smem + oVl + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-        if (row >= r) {                        // K's, too: what they hold must not meet V' of 0
+        const bool bad = row < r && ((big & 0xFFFFu) >= 0x7F80u || big >= 0x7F800000u);
+        if (row >= r) {                        // behind the sequence: what K and V hold must not meet weights of 0
 #pragma unroll
-          for (int u = 0; u < 16; ++u)
-            *reinterpret_cast<uint4*>(st + 2 * kTile + (u >> 3) * kTile + sw128_offset((uint32_t)row, (uint32_t)(u & 7))) =
-                make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < kSplit; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) part[i][e] = 0u;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t off = sw128_offset((uint32_t)row, (uint32_t)(u0 + u));
+            *reinterpret_cast<uint4*>(st + off) = make_uint4(0, 0, 0, 0);
+          }
         }
         const bool any = __any_sync(0xffffffffu, bad);
-        if (lane == 0) reinterpret_cast<volatile int*>(smem + oBad)[t % kMarks * 4 + w] = any;
+        if (lane == 0) reinterpret_cast<volatile int*>(smem + oBad)[t % kMarks * 8 + w] = any;
         if (__builtin_expect(any, 0)) {
-          uint8_t* first = smem + oFirst + (t % kMarks * 4 + w) * kCols;
+          uint8_t* first = smem + oFirst + (t % kMarks * 8 + w) * 32;
 #pragma unroll 1
-          for (int x = 0; x < kCols; ++x) {
-            uint16_t* e = reinterpret_cast<uint16_t*>(st + 4 * kTile + sw128_offset((uint32_t)row, (uint32_t)(x >> 3))) + (x & 7);
+          for (int x = 0; x < 32; ++x) {
+            uint16_t* e = reinterpret_cast<uint16_t*>(st + sw128_offset((uint32_t)row, (uint32_t)(u0 + (x >> 3)))) + (x & 7);
             const bool out = row < r && (*e & 0x7F80u) == 0x7F80u;
             const uint32_t who = __ballot_sync(0xffffffffu, out);
             if (out) *e = 0;
-            if (lane == 0) first[x] = who ? (uint8_t)(w * 32 + __ffs(who) - 1) : (uint8_t)kC;
+            if (lane == 0) first[x] = who ? (uint8_t)((w & 3) * 32 + __ffs(who) - 1) : (uint8_t)kC;
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(v_ready);
+        if (lane == 0) mbar_arrive(&v_clean[sv]);
+        if (t > 0 && !(ok = wait32(d_full, (uint32_t)(t - 1) & 1u))) break;
+#pragma unroll
+        for (int i = 0; i < kSplit; ++i)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(smem + oVp + i * kTile + sw128_offset((uint32_t)row, (uint32_t)(u0 + u))) =
+                make_uint4(part[i][4 * u], part[i][4 * u + 1], part[i][4 * u + 2], part[i][4 * u + 3]);
+        fence_proxy_async_smem();
+        if (!(ok = wait32(&k_full[s], (uint32_t)(t / kQk) & 1u))) break;
+        tc_fence_after();
+        if (quarter < 2 * KB) {
+          const uint32_t kt = smem_u32(smem + oK + (s * 2 + (quarter >> 1)) * kTile);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {        // 16 dims
+            uint32_t x[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)        // 16 tokens
+              ldmatrix4_trans(kt + sw128_offset(k_lane + i * 16, k_u + m * 2), x + 4 * i);
+            if (r < kC) {                      // behind the sequence: zeros
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int j = (w >> 2) * 64 + (i >> 1) * 8 + (lane & 3) * 2;
+                x[i] &= (j < r ? 0xFFFFu : 0u) | (j + 1 < r ? 0xFFFF0000u : 0u);
+              }
+            }
+            tmem_st_16x128b_x8(tmem + ((uint32_t)(quarter * 32 + m * 16) << 16) + TM_KT + (w >> 2) * 32, x);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&k_empty[s]);
+          mbar_arrive(v_ready);
+        }
       }
     }
-  } else if (warp >= 12 && warp < 16) {
+  } else if (warp >= 16 && warp < 24) {
     // ======================= the state ===========================================
-    // Thread = row of the state; rows that the head does not have are left alone.
-    const bool rows = (warp & 3) * 32 < a.dk, live = row < a.dk;
+    // Thread = 32 columns of a row of the state; rows from dk on are zeros, and none behind the
+    // last block of 64.
+    const bool rows = (warp & 3) < 2 * KB, live = row < a.dk;
+    const int half = (warp - 16) >> 2;
 #pragma unroll 1
     while (ok && next_item(p, plan, walk, it)) {
       const float g = __ldg(a.log_decay + it.h);
       const int64_t src = in_slot(p, it.b), dst = out_slot(p, it.b);
-      const int cols = min(kCols, a.dv - it.part * kCols);          // a multiple of 8
-      const int64_t head = ((int64_t)it.h * a.dk + row) * a.dv + it.part * kCols;
+      const int cols = live ? min(32, a.dv - it.part * kCols - half * 32) : 0;   // a multiple of 8, or none
+      const int64_t head = ((int64_t)it.h * a.dk + row) * a.dv + it.part * kCols + half * 32;
       const int64_t slot = (int64_t)a.n_heads * a.dk * a.dv;
-      if (it.chunks == 0) {
-        if (dst >= 0 && dst != src && live)
-          for (int x = 0; x < cols; x += 4)
-            *reinterpret_cast<float4*>(a.state + dst * slot + head + x) =
-                src >= 0 ? *reinterpret_cast<const float4*>(a.state + src * slot + head + x) : make_float4(0.f, 0.f, 0.f, 0.f);
-        continue;
+      float s[32];
+#pragma unroll
+      for (int x = 0; x < 32; x += 4) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (src >= 0 && x < cols) y = *reinterpret_cast<const float4*>(a.state + src * slot + head + x);
+        s[x] = y.x; s[x + 1] = y.y; s[x + 2] = y.z; s[x + 3] = y.w;
       }
 #pragma unroll 1
       for (int c = 0; c < it.chunks; ++c, ++t) {
         const float d1 = expm1f(g * (float)min(kC, it.n - c * kC));
-        if (c > 0 && !(ok = wait32(st_done, (uint32_t)(t - 1) & 1u))) break;
-        tc_fence_after();
+        if (t > 0 && !(ok = wait32(st_taken, (uint32_t)(t - 1) & 1u))) break;
         if (rows) {
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            float s[32];
-            if (c == 0) {
 #pragma unroll
-              for (int x = 0; x < 32; x += 4) {
-                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (src >= 0 && live && half * 32 + x < cols)
-                  y = *reinterpret_cast<const float4*>(a.state + src * slot + head + half * 32 + x);
-                s[x] = y.x; s[x + 1] = y.y; s[x + 2] = y.z; s[x + 3] = y.w;
-              }
-              __syncwarp();
-            } else {
-              tmem_ld32(tmem + lane_base + TM_ST + half * 32, s);
-              tmem_ld_wait();
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              *reinterpret_cast<uint4*>(smem + oS + sw128_offset((uint32_t)row, (uint32_t)(half * 4 + u))) =
-                  make_uint4(pack_bf16(s[8 * u], s[8 * u + 1]), pack_bf16(s[8 * u + 2], s[8 * u + 3]),
-                             pack_bf16(s[8 * u + 4], s[8 * u + 5]), pack_bf16(s[8 * u + 6], s[8 * u + 7]));
-            uint32_t y[32];
-#pragma unroll
-            for (int x = 0; x < 32; ++x) y[x] = __float_as_uint(fmaf(s[x], d1, s[x]));
-            tmem_st32(tmem + lane_base + TM_ST + half * 32, y);
-          }
-          tmem_st_wait();
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(smem + oS + sw128_offset((uint32_t)row, (uint32_t)(half * 4 + u))) =
+                make_uint4(pack_bf16(s[8 * u], s[8 * u + 1]), pack_bf16(s[8 * u + 2], s[8 * u + 3]),
+                           pack_bf16(s[8 * u + 4], s[8 * u + 5]), pack_bf16(s[8 * u + 6], s[8 * u + 7]));
         }
         fence_proxy_async_smem();
-        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(st_ready);
-      }
-      if (!ok) break;
-      if (!(ok = wait32(st_done, (uint32_t)(t - 1) & 1u))) break;
-      tc_fence_after();
-      if (rows && dst >= 0) {
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          float s[32];
-          tmem_ld32(tmem + lane_base + TM_ST + half * 32, s);
-          tmem_ld_wait();
 #pragma unroll
-          for (int x = 0; x < 32; x += 4)
-            if (live && half * 32 + x < cols)
-              *reinterpret_cast<float4*>(a.state + dst * slot + head + half * 32 + x) =
-                  make_float4(s[x], s[x + 1], s[x + 2], s[x + 3]);
-          __syncwarp();
+        for (int x = 0; x < 32; ++x) s[x] = fmaf(s[x], d1, s[x]);
+        if (!(ok = wait32(d_full, (uint32_t)t & 1u))) break;
+        tc_fence_after();
+        if (rows) {
+#pragma unroll
+          for (int x = 0; x < 32; x += 16) {
+            float d[16];
+            tmem_ld16(tmem + lane_base + TM_D + half * 32 + x, d);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[x + i] += d[i];
+          }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d_empty);
       }
+      if (ok && dst >= 0 && (dst != src || it.chunks > 0)) {
+#pragma unroll
+        for (int x = 0; x < 32; x += 4)
+          if (x < cols)
+            *reinterpret_cast<float4*>(a.state + dst * slot + head + x) = make_float4(s[x], s[x + 1], s[x + 2], s[x + 3]);
+      }
+      __syncwarp();
     }
-  } else if (warp >= 16) {
+  } else if (warp >= 24) {
     // ======================= outputs =============================================
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.ld_out_row % 16 == 0 && a.ld_out_head % 16 == 0;
 #pragma unroll 1
@@ -485,54 +596,49 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       const int cols = min(kCols, a.dv - it.part * kCols);
 #pragma unroll 1
       for (int c = 0; c < it.chunks; ++c, ++t) {
-        if (!(ok = wait32(o_full, (uint32_t)t & 1u))) break;
+        if (!(ok = wait32(&o_full[t & 1], (uint32_t)(t >> 1) & 1u))) break;
         tc_fence_after();
-        const int4 bad = *reinterpret_cast<const int4*>(smem + oBad + t % kMarks * 16);
         const bool live = row < it.n - c * kC;
         bf16* to = reinterpret_cast<bf16*>(a.out) + (it.first + c * kC + row) * a.ld_out_row +
                    (int64_t)it.h * a.ld_out_head + it.part * kCols;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          float x[32], y[32];
-          tmem_ld32(tmem + lane_base + TM_OI + half * 32, x);
-          tmem_ld32(tmem + lane_base + TM_OX + (t & 1) * kCols + half * 32, y);
+        for (int q = 0; q < 4; ++q) {          // 16 columns at a time
+          float x[16], y[16];
+          tmem_ld16(tmem + lane_base + TM_OI + (t & 1) * kC + q * 16, x);
+          tmem_ld16(tmem + lane_base + TM_OX + (t & 1) * kCols + q * 16, y);
+          const int4 bad = *reinterpret_cast<const int4*>(smem + oBad + t % kMarks * 32 + (q >> 1) * 16);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = fmaf(y[i], since, x[i] * a.scale);
+          for (int i = 0; i < 16; ++i) x[i] = fmaf(y[i], since, x[i] * a.scale);
           if (__builtin_expect(bad.x | bad.y | bad.z | bad.w, 0)) {
-            const uint8_t* first = smem + oFirst + t % kMarks * 4 * kCols + half * 32;
+            const uint8_t* first = smem + oFirst + (t % kMarks * 8 + (q >> 1) * 4) * 32 + (q & 1) * 16;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 16; ++i) {
               int from = kC;
               if (bad.x) from = min(from, (int)first[i]);
-              if (bad.y) from = min(from, (int)first[kCols + i]);
-              if (bad.z) from = min(from, (int)first[2 * kCols + i]);
-              if (bad.w) from = min(from, (int)first[3 * kCols + i]);
+              if (bad.y) from = min(from, (int)first[32 + i]);
+              if (bad.z) from = min(from, (int)first[64 + i]);
+              if (bad.w) from = min(from, (int)first[96 + i]);
               if (row >= from) x[i] = __int_as_float(0x7fc00000);
             }
           }
-          if (half == 1) {
+          if (q == 3) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(o_empty);
+            if (lane == 0) mbar_arrive(&o_empty[t & 1]);
           }
-          uint32_t o[16];
+          uint32_t o[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+          for (int i = 0; i < 8; ++i) o[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+          const int left = cols - q * 16;
           if (live) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              bf16* at = to + half * 32 + i * 16;
-              const int left = cols - half * 32 - i * 16;
-              if (wide && left >= 16) {
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(at), "r"(o[8 * i]),
-                             "r"(o[8 * i + 1]), "r"(o[8 * i + 2]), "r"(o[8 * i + 3]), "r"(o[8 * i + 4]),
-                             "r"(o[8 * i + 5]), "r"(o[8 * i + 6]), "r"(o[8 * i + 7])
-                             : "memory");
-              } else {
-                if (left >= 8) reinterpret_cast<uint4*>(at)[0] = make_uint4(o[8 * i], o[8 * i + 1], o[8 * i + 2], o[8 * i + 3]);
-                if (left >= 16) reinterpret_cast<uint4*>(at)[1] = make_uint4(o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]);
-              }
+            if (wide && left >= 16) {
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(to + q * 16), "r"(o[0]),
+                           "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                           : "memory");
+            } else {
+              if (left >= 8) reinterpret_cast<uint4*>(to + q * 16)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+              if (left >= 16) reinterpret_cast<uint4*>(to + q * 16)[1] = make_uint4(o[4], o[5], o[6], o[7]);
             }
           }
           __syncwarp();
@@ -566,7 +672,8 @@ cudaError_t launch_linear_prefill(const LinearArgs& p, void*, cudaStream_t st) {
   int dev = 0, sms = 152;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_chunk, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const auto kernel = p.a.dk > 64 ? linear_chunk<2> : linear_chunk<1>;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   if (p.n_tokens == 0) return launch_linear_recurrent(p, st);   // (nothing but states to pass on)
   Plan plan;
@@ -577,7 +684,7 @@ cudaError_t launch_linear_prefill(const LinearArgs& p, void*, cudaStream_t st) {
       !map_heads(&kmap, p.a.k, p.n_tokens, p.a.n_kv_heads, p.a.dk, p.a.ld_k_row, p.a.ld_k_head) ||
       !map_heads(&vmap, p.a.v, p.n_tokens, p.a.n_kv_heads, p.a.dv, p.a.ld_v_row, p.a.ld_v_head))
     return cudaErrorInvalidValue;
-  e = launch_overlapped(linear_chunk, dim3((unsigned)(plan.items < sms ? plan.items : sms)), dim3(kThreads), kSmem, st,
+  e = launch_overlapped(kernel, dim3((unsigned)(plan.items < sms ? plan.items : sms)), dim3(kThreads), kSmem, st,
                         qmap, kmap, vmap, p, plan);
   note_launch();
   return e;
