@@ -17,7 +17,7 @@
 // was 3e-6 of its norm: the tensor core cuts its sums off.)
 //
 // Roles (28 warps), each walking the same list of (sequence, head, columns):
-//   0 copies (TMA), 1 products K^T V', 2 Q K^T, 3 Q S and P V, 4-7 P, 8-15 V' and K^T,
+//   0 products Q S and P V, 1 K^T V', 2 Q K^T, 3 copies (TMA), 4-7 P, 8-15 V' and K^T,
 //   16-23 the state, 24-27 outputs.
 // (A lane that issues products in a branch of its own takes 110 cycles for each, of 16 dims or
 // tokens; an elected lane of a converged warp less, and three warps issue side by side: a
@@ -79,7 +79,8 @@ struct Item {
   int chunks;
   int64_t first;                               // its first token
 };
-__device__ __forceinline__ bool next_item(const LinearArgs& p, const Plan& plan, int& walk, Item& it) {
+// (not inline: the roles' code together has to stay small for the instruction cache)
+__device__ __noinline__ bool next_item(const LinearArgs& p, const Plan& plan, int& walk, Item& it) {
   if (walk >= plan.items) return false;
   it.part = walk % plan.parts;
   const int bh = walk / plan.parts;
@@ -167,7 +168,21 @@ __device__ __forceinline__ void e_commit(uint64_t* bar) {
       : "memory");
 }
 
-// Two fp32 products in one instruction.
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 w, x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 z, x, y;\n"
+      " mov.b64 {%0, %1}, z;\n}\n"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 r;
   asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n"
@@ -182,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
              const __grid_constant__ CUtensorMap vmap, const __grid_constant__ LinearArgs p,
              const __grid_constant__ Plan plan) {
-  __shared__ __align__(16) float pow_table[4][32];   // P's warps: lam^0 .. lam^31
+  __shared__ __align__(16) float pow_table[4][60];   // P's warps: 28 of anything, scale lam^0 .. scale lam^31
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + oBar);   // [kQk] Q landed
@@ -251,7 +266,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
   int t = 0;                                   // chunks so far
   bool ok = true;
 
-  if (warp == 0) {
+  if (warp == 3) {
     // ======================= copies ==============================================
     if (lane == 0) {
 #pragma unroll 1
@@ -333,7 +348,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       }
     }
     __syncwarp();
-  } else if (warp == 3) {
+  } else if (warp == 0) {
     // ======================= Q S, P V ============================================
     {
       const uint64_t d_s = desc_sw128_mn(smem_u32(smem + oS), kTile);
@@ -373,7 +388,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     // lam^(i-j) as lam^(i-j31) lam^(j31-j) (j31 the block's last token: both
     // exponents are positive), the warp's own block by table; the rest is 0.
     const int w = warp & 3;
-    float* const pow_s = pow_table[w];
+    float* const pow_s = pow_table[w] + 28;
     float far_of[3] = {0.f, 0.f, 0.f};         // lam^(i-j31) of the blocks before the warp's own
     int h = -1;
 #pragma unroll 1
@@ -382,7 +397,8 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         h = it.h;
         const float g = __ldg(a.log_decay + h);
         __syncwarp();
-        pow_s[lane] = power(g, lane);
+        pow_s[lane] = a.scale * power(g, lane);
+        if (lane < 28) pow_s[lane - 28] = 0.f;
 #pragma unroll
         for (int i = 0; i < 3; ++i) far_of[i] = power(g, max(0, row - i * 32 - 31));
         __syncwarp();
@@ -412,8 +428,11 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
             } else {
 #pragma unroll
               for (int j = 0; j < 32; j += 2) {
-                const float f0 = pow_s[max(0, lane - j)], f1 = pow_s[max(0, lane - j - 1)];
-                out[j / 2] = pack_bf16(j <= lane ? v[j] * f0 : 0.f, j + 1 <= lane ? v[j + 1] * f1 : 0.f);
+                // (what is read in front of the table is masked)
+                const float2 f = make_float2(pow_s[j < 28 ? lane - j : max(0, lane - j)],
+                                             pow_s[j + 1 < 28 ? lane - j - 1 : max(0, lane - j - 1)]);
+                const float2 y = mul2(make_float2(v[j], v[j + 1]), f);
+                out[j / 2] = pack_bf16(j <= lane ? y.x : 0.f, j + 1 <= lane ? y.y : 0.f);
               }
             }
           } else {
@@ -444,25 +463,26 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         uint8_t* st = smem + oV + sv * kTile;
         const float f = row < r ? power(g, r - 1 - row) : 0.f;
         if (!(ok = wait32(&v_full[sv], (uint32_t)(t / kV) & 1u))) break;
-        uint32_t part[kSplit][16], big = 0u;
+        uint32_t part[kSplit][16];
+        float2 all = make_float2(0.f, 0.f);    // not finite if one of the values is not
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const uint4 v4 = *reinterpret_cast<const uint4*>(st + sw128_offset((uint32_t)row, (uint32_t)(u0 + u)));
           const uint32_t x[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            big = __vmaxu2(big, x[e] & 0x7FFF7FFFu);
             const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[e]));
+            all = add2(all, v);
             float2 y = mul2(v, make_float2(f, f));
 #pragma unroll
             for (int i = 0; i < kSplit; ++i) {
               part[i][4 * u + e] = pack_bf16(y.x, y.y);
               const float2 z = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&part[i][4 * u + e]));
-              y = make_float2(y.x - z.x, y.y - z.y);
+              if (i + 1 < kSplit) y = fma2(z, make_float2(-1.f, -1.f), y);
             }
           }
         }
-        const bool bad = row < r && ((big & 0xFFFFu) >= 0x7F80u || big >= 0x7F800000u);
+        const bool bad = row < r && !(fabsf(all.x) + fabsf(all.y) < INFINITY);   // (or their sum)
         if (row >= r) {                        // behind the sequence: what K and V hold must not meet weights of 0
 #pragma unroll
           for (int i = 0; i < kSplit; ++i)
@@ -502,7 +522,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         tc_fence_after();
         if (quarter < 2 * KB) {
           const uint32_t kt = smem_u32(smem + oK + (s * 2 + (quarter >> 1)) * kTile);
-#pragma unroll
+#pragma unroll 1
           for (int m = 0; m < 2; ++m) {        // 16 dims
             uint32_t x[16];
 #pragma unroll
@@ -562,7 +582,10 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         __syncwarp();
         if (lane == 0) mbar_arrive(st_ready);
 #pragma unroll
-        for (int x = 0; x < 32; ++x) s[x] = fmaf(s[x], d1, s[x]);
+        for (int x = 0; x < 32; x += 2) {
+          const float2 y = make_float2(s[x], s[x + 1]), z = fma2(y, make_float2(d1, d1), y);
+          s[x] = z.x; s[x + 1] = z.y;
+        }
         if (!(ok = wait32(d_full, (uint32_t)t & 1u))) break;
         tc_fence_after();
         if (rows) {
@@ -572,7 +595,10 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
             tmem_ld16(tmem + lane_base + TM_D + half * 32 + x, d);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[x + i] += d[i];
+            for (int i = 0; i < 16; i += 2) {
+              const float2 z = add2(make_float2(s[x + i], s[x + i + 1]), make_float2(d[i], d[i + 1]));
+              s[x + i] = z.x; s[x + i + 1] = z.y;
+            }
           }
         }
         tc_fence_before();
@@ -606,30 +632,13 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
           float x[16], y[16];
           tmem_ld16(tmem + lane_base + TM_OI + (t & 1) * kC + q * 16, x);
           tmem_ld16(tmem + lane_base + TM_OX + (t & 1) * kCols + q * 16, y);
-          const int4 bad = *reinterpret_cast<const int4*>(smem + oBad + t % kMarks * 32 + (q >> 1) * 16);
           tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = fmaf(y[i], since, x[i] * a.scale);
-          if (__builtin_expect(bad.x | bad.y | bad.z | bad.w, 0)) {
-            const uint8_t* first = smem + oFirst + (t % kMarks * 8 + (q >> 1) * 4) * 32 + (q & 1) * 16;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              int from = kC;
-              if (bad.x) from = min(from, (int)first[i]);
-              if (bad.y) from = min(from, (int)first[32 + i]);
-              if (bad.z) from = min(from, (int)first[64 + i]);
-              if (bad.w) from = min(from, (int)first[96 + i]);
-              if (row >= from) x[i] = __int_as_float(0x7fc00000);
-            }
-          }
-          if (q == 3) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&o_empty[t & 1]);
-          }
           uint32_t o[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+          for (int i = 0; i < 8; ++i) {
+            const float2 z = fma2(make_float2(y[2 * i], y[2 * i + 1]), make_float2(since, since), make_float2(x[2 * i], x[2 * i + 1]));
+            o[i] = pack_bf16(z.x, z.y);
+          }
           const int left = cols - q * 16;
           if (live) {
             if (wide && left >= 16) {
@@ -643,6 +652,23 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
           }
           __syncwarp();
         }
+        const uint4 bad0 = *reinterpret_cast<const uint4*>(smem + oBad + t % kMarks * 32);
+        const uint4 bad1 = *reinterpret_cast<const uint4*>(smem + oBad + t % kMarks * 32 + 16);
+        if (__builtin_expect(bad0.x | bad0.y | bad0.z | bad0.w | bad1.x | bad1.y | bad1.z | bad1.w, 0u)) {
+          const uint8_t* first = smem + oFirst + t % kMarks * 8 * 32;
+#pragma unroll 1
+          for (int x = 0; x < (live ? cols : 0); ++x) {
+            const int part = (x >> 5) * 4;     // the warps that had this column
+            int from = kC;
+#pragma unroll 1
+            for (int i = part; i < part + 4; ++i)
+              if (reinterpret_cast<const int*>(smem + oBad)[t % kMarks * 8 + i]) from = min(from, (int)first[i * 32 + (x & 31)]);
+            if (row >= from) to[x] = __float2bfloat16(__int_as_float(0x7fc00000));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_empty[t & 1]);
       }
     }
   }
