@@ -56,7 +56,8 @@ constexpr int oFirst = oBad + kMarks * 8 * 4;  // [kMarks][8][32] the first such
 constexpr int oBar = oFirst + kMarks * 8 * 32;
 constexpr int kBars = 4 * kQk + 3 * kV + 4 * 2 + 5;
 constexpr int oSlot = oBar + kBars * 8;
-constexpr int kSmem = oSlot + 8;
+constexpr int oTable = oSlot + 8;              // next_item's
+constexpr int kSmem = oTable + 264;
 // (static variables take a kilobyte of their own, aligned like the rest)
 static_assert(kSmem <= 226 * 1024 && oBad % 16 == 0 && oBar % 8 == 0, "shared memory");
 
@@ -71,25 +72,60 @@ constexpr uint32_t IDESC_O = idesc_f32_bmn(1, kC, kCols);
 
 struct Plan {
   int parts;                                   // 64-column parts of dv
-  int items;                                   // (sequence, head, part)
+  int items;                                   // (sequence, head, part); with a split an upper bound
+  int split;                                   // chunks of a segment, or 0: sequences stay whole
+  float* seg;                                  // split: [segments][heads][dk][dv] states
 };
 
+// Long sequences of few heads are cut into segments of plan.split chunks.  A first pass
+// (LOCAL) leaves what each but a sequence's last one adds to a state of zeros, linear_carry turns
+// that into the state that each segment finds, and then all of them run side by side.
 struct Item {
   int b, h, part, n;                           // n: the sequence's tokens
-  int chunks;
-  int64_t first;                               // its first token
+  int c0, c1;                                  // chunks of the sequence
+  int seg;                                     // segment's place in plan.seg, or -1
+  bool last;                                   // of the sequence
+  int64_t first;                               // the sequence's first token
 };
+constexpr int kMaxSplit = 64;                  // sequences of a call that is split
+constexpr int kMaxOrder = 256;                 // ... whose sequences are taken in order of length
+
+// The CTA's next piece of work; `round` counts them.  Rounds go back and forth over the CTAs,
+// whole sequences from the longest to the shortest (table: their order), so that every CTA has about the same
+// to do.  Split: table[b] is the first segment of sequence b.
 // (not inline: the roles' code together has to stay small for the instruction cache)
-__device__ __noinline__ bool next_item(const LinearArgs& p, const Plan& plan, int& walk, Item& it) {
-  if (walk >= plan.items) return false;
-  it.part = walk % plan.parts;
-  const int bh = walk / plan.parts;
-  it.b = bh / p.a.n_heads;
-  it.h = bh - it.b * p.a.n_heads;
-  tokens_of(p, it.b, it.first, it.n);
-  it.chunks = (it.n + kC - 1) / kC;
-  walk += gridDim.x;
-  return true;
+template <bool LOCAL>
+__device__ __noinline__ bool next_item(const LinearArgs& p, const Plan& plan, const uint8_t* table_s, int& round, Item& it) {
+  for (;;) {
+    const int G = gridDim.x, at = (round & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x;
+    const int64_t i64 = (int64_t)round * G + at;
+    if (i64 >= plan.items) return false;
+    const int i = (int)i64, g = i / (plan.parts * p.a.n_heads), hp = i - g * plan.parts * p.a.n_heads;
+    ++round;
+    it.h = hp / plan.parts;
+    it.part = hp - it.h * plan.parts;
+    if (plan.split) {
+      const int* first = reinterpret_cast<const int*>(table_s);
+      if (g >= first[p.batch]) return false;
+      it.b = 0;
+      while (first[it.b + 1] <= g) ++it.b;
+      tokens_of(p, it.b, it.first, it.n);
+      const int s = g - first[it.b], chunks = (it.n + kC - 1) / kC;
+      it.c0 = s * plan.split;
+      it.c1 = min(chunks, it.c0 + plan.split);
+      it.last = g + 1 == first[it.b + 1];
+      it.seg = first[it.b + 1] - first[it.b] > 1 ? g : -1;
+      if (LOCAL && it.last) continue;
+      return true;
+    }
+    it.b = p.batch <= kMaxOrder ? table_s[g] : g;
+    tokens_of(p, it.b, it.first, it.n);
+    it.c0 = 0;
+    it.c1 = (it.n + kC - 1) / kC;
+    it.seg = -1;
+    it.last = true;
+    return true;
+  }
 }
 
 // lam^n: 1 for n = 0, whatever lam is.
@@ -191,8 +227,8 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return r;
 }
 
-// KB: blocks of 64 dims that dk takes.
-template <int KB>
+// KB: blocks of 64 dims that dk takes.  LOCAL: the first pass over segments.
+template <int KB, bool LOCAL>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
              const __grid_constant__ CUtensorMap vmap, const __grid_constant__ LinearArgs p,
@@ -225,11 +261,11 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       mbar_init(&q_full[i], 1);
       mbar_init(&k_full[i], 1);
       mbar_init(&q_empty[i], 2);
-      mbar_init(&k_empty[i], 1 + 8);
+      mbar_init(&k_empty[i], LOCAL ? 8 : 1 + 8);
     }
     for (int i = 0; i < kV; ++i) {
       mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_empty[i], LOCAL ? 8 : 1);
       mbar_init(&v_clean[i], 8);
     }
     for (int i = 0; i < 2; ++i) {
@@ -257,12 +293,39 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (plan.split) {                            // the sequences' first segments
+    int n = 0, total;
+    if (tid < p.batch) {
+      int64_t first;
+      tokens_of(p, tid, first, n);
+      n = max(1, ((n + kC - 1) / kC + plan.split - 1) / plan.split);
+    }
+    const int before = block_exclusive_scan(n, reinterpret_cast<int*>(smem), total);
+    if (tid <= p.batch) reinterpret_cast<int*>(smem + oTable)[tid] = before;
+    __syncthreads();
+  } else if (p.batch <= kMaxOrder) {           // the sequences, longest first
+    int* len = reinterpret_cast<int*>(smem);
+    int64_t first;
+    int n = 0;
+    if (tid < p.batch) tokens_of(p, tid, first, n);
+    if (tid < p.batch) len[tid] = n;
+    __syncthreads();
+    if (tid < p.batch) {
+      int rank = 0;
+      for (int b = 0; b < p.batch; ++b) rank += len[b] > n || (len[b] == n && b < tid);
+      smem[oTable + rank] = (uint8_t)tid;
+    }
+    __syncthreads();
+  }
+  fence_proxy_async_smem();                    // copies land where the lengths were
+  __syncthreads();
   grid_dep_launch();
   const uint32_t tmem = *tmem_slot;
   const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
   const int row = (warp & 3) * 32 + lane;      // of a chunk, or of the state
-  int walk = blockIdx.x;
+  int round = 0;
   Item it;
+  const uint8_t* const table = smem + oTable;
   int t = 0;                                   // chunks so far
   bool ok = true;
 
@@ -270,10 +333,10 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     // ======================= copies ==============================================
     if (lane == 0) {
 #pragma unroll 1
-      while (ok && next_item(p, plan, walk, it)) {
+      while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
         const int hk = it.h / p.group;
 #pragma unroll 1
-        for (int c = 0; c < it.chunks; ++c, ++t) {
+        for (int c = it.c0; c < it.c1; ++c, ++t) {
           const int s = t % kQk, sv = t % kV, at = (int)it.first + c * kC;
           const uint32_t ph = ((uint32_t)(t / kQk) & 1u) ^ 1u;
           if (!(ok = wait1(&k_empty[s], ph))) break;
@@ -284,11 +347,13 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
           if (!(ok = wait1(&v_empty[sv], ((uint32_t)(t / kV) & 1u) ^ 1u))) break;
           mbar_arrive_expect_tx(&v_full[sv], kTile);
           tma_load_3d(smem + oV + sv * kTile, &vmap, it.part * kCols, hk, at, &v_full[sv]);
-          if (!(ok = wait1(&q_empty[s], ph))) break;
-          mbar_arrive_expect_tx(&q_full[s], KB * kTile);
+          if constexpr (!LOCAL) {
+            if (!(ok = wait1(&q_empty[s], ph))) break;
+            mbar_arrive_expect_tx(&q_full[s], KB * kTile);
 #pragma unroll
-          for (int x = 0; x < KB; ++x)
-            tma_load_3d(smem + oQ + (s * 2 + x) * kTile, &qmap, x * 64, it.h, at, &q_full[s]);
+            for (int x = 0; x < KB; ++x)
+              tma_load_3d(smem + oQ + (s * 2 + x) * kTile, &qmap, x * 64, it.h, at, &q_full[s]);
+          }
         }
       }
       // never leave the CTA with a copy still landing in shared memory (of chunk t some may be
@@ -296,7 +361,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       if (s_abort) {
         volatile int no_abort = 0;
         for (int i = max(0, t + 1 - kV); i <= t; ++i) {
-          mbar_wait(&q_full[i % kQk], (uint32_t)(i / kQk) & 1u, &no_abort, p.err, 1000000ull);
+          if (!LOCAL) mbar_wait(&q_full[i % kQk], (uint32_t)(i / kQk) & 1u, &no_abort, p.err, 1000000ull);
           mbar_wait(&k_full[i % kQk], (uint32_t)(i / kQk) & 1u, &no_abort, p.err, 1000000ull);
           mbar_wait(&v_full[i % kV], (uint32_t)(i / kV) & 1u, &no_abort, p.err, 1000000ull);
         }
@@ -307,9 +372,9 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     {
       const uint64_t d_vp = desc_sw128_mn(smem_u32(smem + oVp), kTile);
 #pragma unroll 1
-      while (ok && next_item(p, plan, walk, it)) {
+      while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
 #pragma unroll 1
-        for (int c = 0; c < it.chunks; ++c, ++t) {
+        for (int c = it.c0; c < it.c1; ++c, ++t) {
           const uint32_t ph = (uint32_t)t & 1u;
           if (!(ok = wait32(v_ready, ph) && wait32(d_empty, ph ^ 1u))) break;
           tc_fence_after();
@@ -322,13 +387,13 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       }
     }
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (!LOCAL && warp == 2) {
     // ======================= Q K^T ===============================================
     {
 #pragma unroll 1
-      while (ok && next_item(p, plan, walk, it)) {
+      while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
 #pragma unroll 1
-        for (int c = 0; c < it.chunks; ++c, ++t) {
+        for (int c = it.c0; c < it.c1; ++c, ++t) {
           const int s = t % kQk;
           const uint32_t ph = (uint32_t)(t / kQk) & 1u;
           if (!(ok = wait32(&k_full[s], ph) && wait32(&q_full[s], ph) &&
@@ -348,14 +413,14 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       }
     }
     __syncwarp();
-  } else if (warp == 0) {
+  } else if (!LOCAL && warp == 0) {
     // ======================= Q S, P V ============================================
     {
       const uint64_t d_s = desc_sw128_mn(smem_u32(smem + oS), kTile);
 #pragma unroll 1
-      while (ok && next_item(p, plan, walk, it)) {
+      while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
 #pragma unroll 1
-        for (int c = 0; c < it.chunks; ++c, ++t) {
+        for (int c = it.c0; c < it.c1; ++c, ++t) {
           const int s = t % kQk;
           const uint32_t ph = (uint32_t)t & 1u;
           if (!(ok = wait32(st_ready, ph) && wait32(&q_full[s], (uint32_t)(t / kQk) & 1u) &&
@@ -382,7 +447,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       }
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 8) {
+  } else if (!LOCAL && warp >= 4 && warp < 8) {
     // ======================= P ===================================================
     // Thread = token i, blocks of 32 tokens j: whole ones before the warp's own rows take
     // lam^(i-j) as lam^(i-j31) lam^(j31-j) (j31 the block's last token: both
@@ -392,7 +457,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     float far_of[3] = {0.f, 0.f, 0.f};         // lam^(i-j31) of the blocks before the warp's own
     int h = -1;
 #pragma unroll 1
-    while (ok && next_item(p, plan, walk, it)) {
+    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
       if (it.h != h) {
         h = it.h;
         const float g = __ldg(a.log_decay + h);
@@ -404,7 +469,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         __syncwarp();
       }
 #pragma unroll 1
-      for (int c = 0; c < it.chunks; ++c, ++t) {
+      for (int c = it.c0; c < it.c1; ++c, ++t) {
         if (!(ok = wait32(&s_full[t & 1], (uint32_t)(t >> 1) & 1u))) break;
         tc_fence_after();
         const uint32_t t_p = tmem + lane_base + TM_P + (t & 1) * kC;
@@ -455,10 +520,10 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     const uint32_t k_lane = (uint32_t)((w >> 2) * 64 + ((lane >> 4) & 1) * 8 + (lane & 7));   // token whose address this lane gives
     const uint32_t k_u = (uint32_t)((quarter & 1) * 4 + ((lane >> 3) & 1));                  // ... and 8 dims
 #pragma unroll 1
-    while (ok && next_item(p, plan, walk, it)) {
+    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
       const float g = __ldg(a.log_decay + it.h);
 #pragma unroll 1
-      for (int c = 0; c < it.chunks; ++c, ++t) {
+      for (int c = it.c0; c < it.c1; ++c, ++t) {
         const int s = t % kQk, sv = t % kV, r = min(kC, it.n - c * kC);
         uint8_t* st = smem + oV + sv * kTile;
         const float f = row < r ? power(g, r - 1 - row) : 0.f;
@@ -509,7 +574,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&v_clean[sv]);
+        if (lane == 0) mbar_arrive(LOCAL ? &v_empty[sv] : &v_clean[sv]);   // (nobody else reads it, or P V does)
         if (t > 0 && !(ok = wait32(d_full, (uint32_t)(t - 1) & 1u))) break;
 #pragma unroll
         for (int i = 0; i < kSplit; ++i)
@@ -554,33 +619,41 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     const bool rows = (warp & 3) < 2 * KB, live = row < a.dk;
     const int half = (warp - 16) >> 2;
 #pragma unroll 1
-    while (ok && next_item(p, plan, walk, it)) {
+    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
       const float g = __ldg(a.log_decay + it.h);
       const int64_t src = in_slot(p, it.b), dst = out_slot(p, it.b);
       const int cols = live ? min(32, a.dv - it.part * kCols - half * 32) : 0;   // a multiple of 8, or none
       const int64_t head = ((int64_t)it.h * a.dk + row) * a.dv + it.part * kCols + half * 32;
       const int64_t slot = (int64_t)a.n_heads * a.dk * a.dv;
       float s[32];
+      const float* from = it.seg >= 0 ? plan.seg + it.seg * slot + head : src >= 0 ? a.state + src * slot + head : nullptr;
+      float* to = it.last && dst >= 0 && (dst != src || it.n > 0) ? a.state + dst * slot + head : nullptr;
+      if (LOCAL) {
+        from = nullptr;
+        to = plan.seg + it.seg * slot + head;
+      }
 #pragma unroll
       for (int x = 0; x < 32; x += 4) {
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (src >= 0 && x < cols) y = *reinterpret_cast<const float4*>(a.state + src * slot + head + x);
+        if (from && x < cols) y = *reinterpret_cast<const float4*>(from + x);
         s[x] = y.x; s[x + 1] = y.y; s[x + 2] = y.z; s[x + 3] = y.w;
       }
 #pragma unroll 1
-      for (int c = 0; c < it.chunks; ++c, ++t) {
+      for (int c = it.c0; c < it.c1; ++c, ++t) {
         const float d1 = expm1f(g * (float)min(kC, it.n - c * kC));
-        if (t > 0 && !(ok = wait32(st_taken, (uint32_t)(t - 1) & 1u))) break;
-        if (rows) {
+        if constexpr (!LOCAL) {
+          if (t > 0 && !(ok = wait32(st_taken, (uint32_t)(t - 1) & 1u))) break;
+          if (rows) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<uint4*>(smem + oS + sw128_offset((uint32_t)row, (uint32_t)(half * 4 + u))) =
-                make_uint4(pack_bf16(s[8 * u], s[8 * u + 1]), pack_bf16(s[8 * u + 2], s[8 * u + 3]),
-                           pack_bf16(s[8 * u + 4], s[8 * u + 5]), pack_bf16(s[8 * u + 6], s[8 * u + 7]));
+            for (int u = 0; u < 4; ++u)
+              *reinterpret_cast<uint4*>(smem + oS + sw128_offset((uint32_t)row, (uint32_t)(half * 4 + u))) =
+                  make_uint4(pack_bf16(s[8 * u], s[8 * u + 1]), pack_bf16(s[8 * u + 2], s[8 * u + 3]),
+                             pack_bf16(s[8 * u + 4], s[8 * u + 5]), pack_bf16(s[8 * u + 6], s[8 * u + 7]));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(st_ready);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(st_ready);
 #pragma unroll
         for (int x = 0; x < 32; x += 2) {
           const float2 y = make_float2(s[x], s[x + 1]), z = fma2(y, make_float2(d1, d1), y);
@@ -605,23 +678,22 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         __syncwarp();
         if (lane == 0) mbar_arrive(d_empty);
       }
-      if (ok && dst >= 0 && (dst != src || it.chunks > 0)) {
+      if (ok && to) {
 #pragma unroll
         for (int x = 0; x < 32; x += 4)
-          if (x < cols)
-            *reinterpret_cast<float4*>(a.state + dst * slot + head + x) = make_float4(s[x], s[x + 1], s[x + 2], s[x + 3]);
+          if (x < cols) *reinterpret_cast<float4*>(to + x) = make_float4(s[x], s[x + 1], s[x + 2], s[x + 3]);
       }
       __syncwarp();
     }
-  } else if (warp >= 24) {
+  } else if (!LOCAL && warp >= 24) {
     // ======================= outputs =============================================
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.ld_out_row % 16 == 0 && a.ld_out_head % 16 == 0;
 #pragma unroll 1
-    while (ok && next_item(p, plan, walk, it)) {
+    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
       const float since = a.scale * power(__ldg(a.log_decay + it.h), row + 1);
       const int cols = min(kCols, a.dv - it.part * kCols);
 #pragma unroll 1
-      for (int c = 0; c < it.chunks; ++c, ++t) {
+      for (int c = it.c0; c < it.c1; ++c, ++t) {
         if (!(ok = wait32(&o_full[t & 1], (uint32_t)(t >> 1) & 1u))) break;
         tc_fence_after();
         const bool live = row < it.n - c * kC;
@@ -678,6 +750,52 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
   if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
 }
 
+// Split: what the segments of a sequence add, one after another, becomes what each of them finds.  A
+// thread takes four columns of a row; eight segments' loads are under way together.
+constexpr int kCarryThreads = 256;
+__global__ void __launch_bounds__(kCarryThreads)
+linear_carry(const __grid_constant__ LinearArgs p, const __grid_constant__ Plan plan) {
+  __shared__ int first_s;
+  const int per = p.a.dk * p.a.dv / 4, heads = p.a.n_heads;     // float4s of a head's state
+  const int blocks = (heads * per + kCarryThreads - 1) / kCarryThreads;
+  const int b = blockIdx.x / blocks, e = (blockIdx.x - b * blocks) * kCarryThreads + threadIdx.x;
+  grid_dep_wait();
+  grid_dep_launch();
+  if (threadIdx.x == 0) first_s = 0;
+  __syncthreads();
+  int64_t tok;
+  int n;
+  for (int i = threadIdx.x; i < b; i += kCarryThreads) {        // segments of the sequences before
+    tokens_of(p, i, tok, n);
+    atomicAdd(&first_s, max(1, ((n + kC - 1) / kC + plan.split - 1) / plan.split));
+  }
+  __syncthreads();
+  tokens_of(p, b, tok, n);
+  // (starts that go back could ask for more segments than there is room for)
+  const int segs = min(max(1, ((n + kC - 1) / kC + plan.split - 1) / plan.split),
+                       plan.items / (heads * plan.parts) - first_s);
+  if (segs <= 1 || e >= heads * per) return;
+  const int64_t slot = (int64_t)heads * per, src = in_slot(p, b);
+  float4* at = reinterpret_cast<float4*>(plan.seg) + first_s * slot + e;
+  const float d1 = expm1f(__ldg(p.a.log_decay + e / per) * (float)(plan.split * kC));
+  float4 s = src >= 0 ? reinterpret_cast<const float4*>(p.a.state)[src * slot + e] : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < segs; i0 += 8) {
+    float4 add[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      add[i] = i0 + i + 1 < segs ? at[(i0 + i) * slot] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i0 + i >= segs) break;
+      at[(i0 + i) * slot] = s;
+      s.x = fmaf(s.x, d1, s.x) + add[i].x;
+      s.y = fmaf(s.y, d1, s.y) + add[i].y;
+      s.z = fmaf(s.z, d1, s.z) + add[i].z;
+      s.w = fmaf(s.w, d1, s.w) + add[i].w;
+    }
+  }
+}
+
 // Map of [tokens, heads, dims] with any pitches, boxes of 128 tokens by 64 dims.
 bool map_heads(CUtensorMap* m, const void* base, int64_t tokens, int heads, int dims, int64_t ld_row, int64_t ld_head) {
   auto enc = tma_encode_fn();
@@ -692,28 +810,76 @@ bool map_heads(CUtensorMap* m, const void* base, int64_t tokens, int heads, int 
 
 }  // namespace
 
-size_t linear_prefill_workspace(int64_t, int, int, int, int) { return 256; }
+namespace {
 
-cudaError_t launch_linear_prefill(const LinearArgs& p, void*, cudaStream_t st) {
-  int dev = 0, sms = 152;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const auto kernel = p.a.dk > 64 ? linear_chunk<2> : linear_chunk<1>;
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+    cudaGetLastError();
+    return 152;                                // no device: a GB300's
+  }
+  return sms;
+}
+
+// Chunks of a segment, or 0 where sequences stay whole.  Times in chunks of one CTA: whole
+// sequences take their length; a split takes its share of all chunks 1.6 times (the first
+// pass reads K and V again) and three launches, about kSplitCost.
+constexpr int kSplitCost = 8;
+int segment_chunks(int64_t n_tokens, int batch, int H, int dv, int sms) {
+  const int64_t chunks = (n_tokens + kC - 1) / kC, columns = (int64_t)H * ((dv + kCols - 1) / kCols);
+  if (batch > kMaxSplit || batch * columns >= sms) return 0;
+  const int64_t share = ((chunks + batch - 1) * columns + sms - 1) / sms;
+  if (10 * (chunks / batch) <= 16 * share + 10 * kSplitCost) return 0;
+  return (int)(share < 2 ? 2 : share);
+}
+// At most so many segments (a sequence has one more than it has whole ones).
+int64_t segments(int64_t n_tokens, int batch, int split) {
+  return ((n_tokens + kC - 1) / kC + batch) / split + batch;
+}
+
+template <int KB, bool LOCAL>
+cudaError_t launch(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, const LinearArgs& p,
+                   const Plan& plan, int sms, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(linear_chunk<KB, LOCAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
+  e = launch_overlapped(linear_chunk<KB, LOCAL>, dim3((unsigned)(plan.items < sms ? plan.items : sms)), dim3(kThreads),
+                        kSmem, st, qmap, kmap, vmap, p, plan);
+  note_launch();
+  return e;
+}
+
+}  // namespace
+
+size_t linear_prefill_workspace(int64_t n_tokens, int batch, int H, int dk, int dv) {
+  const int split = segment_chunks(n_tokens, batch, H, dv, sm_count());
+  return split ? (size_t)segments(n_tokens, batch, split) * H * dk * dv * sizeof(float) : 256;
+}
+
+cudaError_t launch_linear_prefill(const LinearArgs& p, void* ws, cudaStream_t st) {
   if (p.n_tokens == 0) return launch_linear_recurrent(p, st);   // (nothing but states to pass on)
+  const int sms = sm_count();
   Plan plan;
   plan.parts = (p.a.dv + kCols - 1) / kCols;
-  plan.items = p.batch * p.a.n_heads * plan.parts;
+  plan.split = ws ? segment_chunks(p.n_tokens, p.batch, p.a.n_heads, p.a.dv, sms) : 0;
+  plan.items = (int)((plan.split ? segments(p.n_tokens, p.batch, plan.split) : p.batch) * p.a.n_heads * plan.parts);
+  plan.seg = static_cast<float*>(ws);
   CUtensorMap qmap, kmap, vmap;
   if (!map_heads(&qmap, p.a.q, p.n_tokens, p.a.n_heads, p.a.dk, p.a.ld_q_row, p.a.ld_q_head) ||
       !map_heads(&kmap, p.a.k, p.n_tokens, p.a.n_kv_heads, p.a.dk, p.a.ld_k_row, p.a.ld_k_head) ||
       !map_heads(&vmap, p.a.v, p.n_tokens, p.a.n_kv_heads, p.a.dv, p.a.ld_v_row, p.a.ld_v_head))
     return cudaErrorInvalidValue;
-  e = launch_overlapped(kernel, dim3((unsigned)(plan.items < sms ? plan.items : sms)), dim3(kThreads), kSmem, st,
-                        qmap, kmap, vmap, p, plan);
-  note_launch();
-  return e;
+  const bool wide = p.a.dk > 64;
+  cudaError_t e;
+  if (plan.split) {
+    e = wide ? launch<2, true>(qmap, kmap, vmap, p, plan, sms, st) : launch<1, true>(qmap, kmap, vmap, p, plan, sms, st);
+    if (e != cudaSuccess) return e;
+    const int blocks = (p.a.n_heads * p.a.dk * p.a.dv / 4 + kCarryThreads - 1) / kCarryThreads;
+    e = launch_overlapped(linear_carry, dim3((unsigned)(p.batch * blocks)), dim3(kCarryThreads), 0, st, p, plan);
+    note_launch();
+    if (e != cudaSuccess) return e;
+  }
+  return wide ? launch<2, false>(qmap, kmap, vmap, p, plan, sms, st) : launch<1, false>(qmap, kmap, vmap, p, plan, sms, st);
 }
 
 }  // namespace dsi

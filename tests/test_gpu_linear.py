@@ -13,6 +13,7 @@ exp(g (i + 1)) |S_0|^T |q_i|) (the same sums of magnitudes) and N_S the state's 
     2^-8 (|out| + scale (sum over the token's 128 |w_ij| |v_j| + exp(..) |S|^T |q_i|)) + (2^-14 + (n + dk) 2^-22) M_i;
     state (2^-14 + n 2^-22) N_S.
 """
+import ctypes
 import math
 
 import pytest
@@ -168,6 +169,73 @@ PREFILLS = [
 def test_prefill(kw):
     c = Case(**kw)
     c.check(*c.prefill())
+
+
+# long sequences of few heads, which a workspace lets the call cut into segments
+LONG = [
+    dict(lens=[9000], H=1), dict(lens=[4000], H=2, kind="none", dk=64, dv=64), dict(lens=[4097], H=2, kind="near"),
+    dict(lens=[7000, 0, 8000, 1, 129], H=2), dict(lens=[5000, 2500], H=2, fork=True), dict(lens=[3500], H=2, state=False),
+    dict(lens=[4000], H=4, kind="strong", dk=96, dv=40), dict(lens=[256 * 12], H=1, dk=128, dv=128), dict(lens=[3333], H=3, Hk=1),
+]
+
+
+@pytest.mark.parametrize("kw", LONG, ids=str)
+def test_long_prefill(kw):
+    """Cut into segments and whole (without a workspace), each against the formula."""
+    c = Case(**kw)
+    heads = (c.H, c.dk, c.dv)
+    assert binding.linear_workspace_size(c.n, c.B, *heads) > 256
+    a = c.prefill()
+    c.check(*a)
+    again = c.prefill()
+    assert torch.equal(a[0], again[0])
+    out = torch.full((c.n, c.H, c.dv), 7.0, dtype=torch.bfloat16, device=DEV)
+    state = c.state.to(DEV) if c.state is not None else None
+    s, _ = binding._linear(c.dq, c.dk_, c.dv_, c.log_decay.to(DEV), c.scale, state,
+                           None if state is None else c.in_slots.to(DEV), None if state is None else c.out_slots.to(DEV),
+                           out, c.B, None)
+    keep = [c.log_decay.to(DEV)] + ([] if state is None else [c.in_slots.to(DEV), c.out_slots.to(DEV)])
+    s.log_decay = keep[0].data_ptr()
+    if state is not None:
+        s.in_slots, s.out_slots = keep[1].data_ptr(), keep[2].data_ptr()
+    st = binding.load().dsi_linear_prefill(ctypes.byref(s), c.n, c.starts.data_ptr(), c.B, None, 0, binding._stream(None))
+    assert st == 0
+    torch.cuda.synchronize()
+    c.check(out, state)
+
+
+@pytest.mark.parametrize("where", ["q", "k", "v"])
+def test_long_values_that_are_not_finite(where):
+    """As below, over the segments of a cut sequence."""
+    c = Case([4000, 300], H=2, lead=0, tail=0, seed=12)
+    clean = c.prefill()[0]
+    x = {"q": c.dq, "k": c.dk_, "v": c.dv_}[where]
+    x[1500, 1, 5] = math.nan
+    out, state = c.prefill()
+    assert binding.device_status() == 0
+    hit = torch.zeros(out.shape, dtype=torch.bool, device=DEV)
+    hit[1500:1501 if where == "q" else 4000, 1] = True
+    assert torch.equal(out[~hit], clean[~hit])
+    ok = out.isfinite()
+    if where == "v":
+        assert not bool(ok[1500:4000, 1, 5].any())
+    else:
+        assert not bool(ok[hit.any(-1)].all(-1).any())
+    assert bool(state[int(c.out_slots[0])][0].isfinite().all()) and bool(state[int(c.out_slots[1])].isfinite().all())
+    assert bool(state[int(c.out_slots[0])][1].isfinite().all()) == (where == "q")
+
+
+def test_long_starts_that_go_back():
+    """More tokens in sequences than there are rows: reported, and nothing beyond the workspace."""
+    c = Case([3000, 1000], H=1, lead=0, tail=0, seed=13)
+    want = c.prefill()[0]
+    size = binding.linear_workspace_size(c.n, 8, 1, 128, 128)
+    ws = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+    starts = torch.tensor([0, 3000, 0, 4000, 0, 4000, 0, 4000, 0], dtype=torch.int32, device=DEV)
+    out = torch.zeros_like(want)
+    binding.linear_prefill(c.dq, c.dk_, c.dv_, c.log_decay.to(DEV), c.scale, starts, out=out, workspace=ws[:size])
+    assert binding.device_status() == binding.DSI_ERR_BOUNDS
+    assert bool((ws[size:] == 0x5A).all())
 
 
 @pytest.mark.parametrize("kw", [
