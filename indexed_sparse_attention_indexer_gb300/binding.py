@@ -581,46 +581,66 @@ def _on(stream, device: torch.device):
 
 
 def _linear(q, k, v, log_decay, scale, state, in_slots, out_slots, out, batch: int, stream):
-    """The checked ``dsi_linear`` struct of the linear attention calls, and out."""
-    device = q.device
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _need(t.dim() == 3 and t.dtype == torch.bfloat16, f"{name} is a bf16 [tokens, heads, dims] tensor")
-    (n, H, dk), (nk, Hk, dkk), (nv, Hv, dv) = q.shape, k.shape, v.shape
-    _need(nk == n and nv == n and Hv == Hk and dkk == dk, "q, k and v have the same tokens, k the dims of q, "
-          "v the heads of k")
-    _need(log_decay.dtype == torch.float32 and log_decay.is_contiguous() and log_decay.numel() == H,
-          "log_decay is a contiguous fp32 [heads] tensor")
-    _need(out is None or (out.dtype == torch.bfloat16 and out.shape == (n, H, dv)),
-          "out is a bf16 [tokens, heads, dv] tensor")
-    for t in (q, k, v, out):
-        _need(t is None or t.stride(2) == 1 or t.numel() == 0, "the dims of a head must be contiguous")
+    """The checked ``dsi_linear`` struct of the linear attention calls, and out (a new one belongs to
+    the stream that the kernels run on)."""
+    bf16, fp32, device = torch.bfloat16, torch.float32, q.get_device()
+    qs, ks, vs = q.shape, k.shape, v.shape
+    for t, shape, name in ((q, qs, "q"), (k, ks, "k"), (v, vs, "v")):
+        if len(shape) != 3 or t.dtype is not bf16:
+            raise ValueError(f"{name} is a bf16 [tokens, heads, dims] tensor")
+    n, H, dk = qs
+    Hk, dv = ks[1], vs[2]
+    if ks != (n, Hk, dk) or vs != (n, Hk, dv):
+        raise ValueError("q, k and v have the same tokens, k the dims of q, v the heads of k")
+    if log_decay.dtype is not fp32 or log_decay.shape != (H,) or not log_decay.is_contiguous():
+        raise ValueError("log_decay is a contiguous fp32 [heads] tensor")
+    if out is None:
+        where = None
+    elif out.dtype is not bf16 or out.shape != (n, H, dv):
+        raise ValueError("out is a bf16 [tokens, heads, dv] tensor")
+    else:
+        where = out.get_device()
+    same = k.get_device() == device and v.get_device() == device and log_decay.get_device() == device
+    at_state = slots = at_in = at_out = None
     if state is not None:
-        _need(state.dtype == torch.float32 and state.dim() == 4 and state.is_contiguous() and
-              state.shape[1:] == (H, dk, dv), "state is a contiguous fp32 [slots, heads, dk, dv] tensor")
-    for t, name in ((in_slots, "in_slots"), (out_slots, "out_slots")):
-        _need(t is None or (state is not None and t.dtype == torch.int32 and t.is_contiguous() and
-                            t.numel() == batch), f"{name} is a contiguous int32 [batch] tensor beside a state")
-    for t in (k, v, log_decay, out, state, in_slots, out_slots):
-        _need(t is None or t.device == device, "all tensors must be on one device")
-    if out is None and (n == 0 or H == 0 or dv == 0):
-        out = q.new_empty((n, H, dv))
-    elif out is None:
-        with torch.cuda.device(device), _on(stream, device):
-            out = torch.empty((n, H, dv), dtype=torch.bfloat16, device=device)
-    s = DsiLinear()
-    s.q, s.k, s.v, s.out = (t.data_ptr() or None for t in (q, k, v, out))
+        if state.dtype is not fp32 or state.shape[1:] != (H, dk, dv) or not state.is_contiguous():
+            raise ValueError("state is a contiguous fp32 [slots, heads, dk, dv] tensor")
+        at_state, slots = state.data_ptr(), state.shape[0]
+        same = same and state.get_device() == device
+    for t, name in ((in_slots, "in_slots"), (out_slots if out_slots is not in_slots else None, "out_slots")):
+        if t is not None:
+            if state is None or t.dtype is not torch.int32 or t.shape != (batch,) or not t.is_contiguous():
+                raise ValueError(f"{name} is a contiguous int32 [batch] tensor beside a state")
+            same = same and t.get_device() == device
+    if in_slots is not None:
+        at_in = in_slots.data_ptr()
+    if out_slots is not None:
+        at_out = out_slots.data_ptr()
+    if not same or (where is not None and where != device):
+        raise ValueError("all tensors must be on one device")
+    q_row, q_head, q_dim = q.stride()
+    k_row, k_head, k_dim = k.stride()
+    v_row, v_head, v_dim = v.stride()
+    if out is None:
+        if n == 0 or H == 0 or dv == 0:
+            out = q.new_empty((n, H, dv))
+        else:
+            with torch.cuda.device(q.device), _on(stream, q.device):
+                out = torch.empty((n, H, dv), dtype=bf16, device=q.device)
+    o_row, o_head, o_dim = out.stride()
+    if n and not q_dim == k_dim == v_dim == o_dim == 1:
+        raise ValueError("the dims of a head must be contiguous")
     # a dim of size one has no pitch that matters
-    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-        d = t.shape[2]
-        setattr(s, f"ld_{name}_row", t.stride(0) if n > 1 else d)
-        setattr(s, f"ld_{name}_head", t.stride(1) if t.shape[1] > 1 else d)
-    s.n_heads, s.n_kv_heads, s.dk, s.dv = H, Hk, dk, dv
-    s.log_decay, s.scale = log_decay.data_ptr() or None, scale
-    if state is not None:
-        s.state, s.n_slots = state.data_ptr() or None, state.shape[0]
-        s.in_slots = in_slots.data_ptr() or None if in_slots is not None else None
-        s.out_slots = out_slots.data_ptr() or None if out_slots is not None else None
-    return s, out
+    if n <= 1:
+        q_row = k_row = dk
+        v_row = o_row = dv
+    if H <= 1:
+        q_head, o_head = dk, dv
+    if Hk <= 1:
+        k_head, v_head = dk, dv
+    return DsiLinear(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), q_row, q_head, k_row, k_head, v_row,
+                     v_head, o_row, o_head, H, Hk, dk, dv, log_decay.data_ptr(), scale, at_state, slots or 0, at_in,
+                     at_out), out
 
 
 def linear_prefill(q, k, v, log_decay, scale: float, seq_starts, state=None, in_slots=None, out_slots=None,

@@ -129,7 +129,7 @@ __device__ __noinline__ bool next_item(const LinearArgs& p, const Plan& plan, co
 }
 
 // lam^n: 1 for n = 0, whatever lam is.
-__device__ __forceinline__ float power(float g, int n) { return n == 0 ? 1.f : expf(g * (float)n); }
+__device__ __noinline__ float power(float g, int n) { return n == 0 ? 1.f : expf(g * (float)n); }
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
              const __grid_constant__ CUtensorMap vmap, const __grid_constant__ LinearArgs p,
              const __grid_constant__ Plan plan) {
-  __shared__ __align__(16) float pow_table[4][60];   // P's warps: 28 of anything, scale lam^0 .. scale lam^31
+  __shared__ __align__(16) float pow_table[5][32];   // P's warps, from 1 on: scale lam^0 .. scale lam^31
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + oBar);   // [kQk] Q landed
@@ -378,7 +378,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
           const uint32_t ph = (uint32_t)t & 1u;
           if (!(ok = wait32(v_ready, ph) && wait32(d_empty, ph ^ 1u))) break;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 4
           for (int x = 0; x < kSplit * (kC / 16); ++x)
             e_mma_ta(tmem + TM_D, tmem + TM_KT + (x & 7) * 8,
                             d_vp + (uint64_t)(((x >> 3) * kTile + (x & 7) * 2048) >> 4), IDESC_O, x > 0 ? 1u : 0u);
@@ -401,7 +401,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
             break;
           tc_fence_after();
           const uint64_t q = desc_sw128(smem_u32(smem + oQ + s * 2 * kTile)), k = desc_sw128(smem_u32(smem + oK + s * 2 * kTile));
-#pragma unroll
+#pragma unroll 4
           for (int x = 0; x < 4 * KB; ++x) {
             const uint64_t off = (uint64_t)(((x >> 2) * kTile + (x & 3) * 32) >> 4);
             e_mma(tmem + TM_P + (t & 1) * kC, q + off, k + off, IDESC_P, x > 0 ? 1u : 0u);
@@ -427,7 +427,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
                      wait32(&o_empty[t & 1], ((uint32_t)(t >> 1) & 1u) ^ 1u))) break;
           tc_fence_after();
           const uint64_t q = desc_sw128(smem_u32(smem + oQ + s * 2 * kTile));
-#pragma unroll
+#pragma unroll 4
           for (int x = 0; x < 4 * KB; ++x)
             e_mma(tmem + TM_OX + (t & 1) * kCols, q + (uint64_t)(((x >> 2) * kTile + (x & 3) * 32) >> 4), d_s + (uint64_t)((x * 2048) >> 4),
                      IDESC_O, x > 0 ? 1u : 0u);
@@ -437,7 +437,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
           if (!(ok = wait32(&v_clean[t % kV], (uint32_t)(t / kV) & 1u) && wait32(&p_full[t & 1], (uint32_t)(t >> 1) & 1u))) break;
           tc_fence_after();
           const uint64_t v = desc_sw128_mn(smem_u32(smem + oV + (t % kV) * kTile), kTile);
-#pragma unroll
+#pragma unroll 4
           for (int x = 0; x < kC / 16; ++x)
             e_mma_ta(tmem + TM_OI + (t & 1) * kC, tmem + TM_P + (t & 1) * kC + x * 8, v + (uint64_t)((x * 2048) >> 4), IDESC_O,
                             x > 0 ? 1u : 0u);
@@ -453,7 +453,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     // lam^(i-j) as lam^(i-j31) lam^(j31-j) (j31 the block's last token: both
     // exponents are positive), the warp's own block by table; the rest is 0.
     const int w = warp & 3;
-    float* const pow_s = pow_table[w] + 28;
+    float* const pow_s = pow_table[w + 1];
     float far_of[3] = {0.f, 0.f, 0.f};         // lam^(i-j31) of the blocks before the warp's own
     int h = -1;
 #pragma unroll 1
@@ -463,7 +463,6 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         const float g = __ldg(a.log_decay + h);
         __syncwarp();
         pow_s[lane] = a.scale * power(g, lane);
-        if (lane < 28) pow_s[lane - 28] = 0.f;
 #pragma unroll
         for (int i = 0; i < 3; ++i) far_of[i] = power(g, max(0, row - i * 32 - 31));
         __syncwarp();
@@ -474,37 +473,37 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         tc_fence_after();
         const uint32_t t_p = tmem + lane_base + TM_P + (t & 1) * kC;
 #pragma unroll 1
-        for (int blk = 0; blk < 4; ++blk) {
-          uint32_t out[16];
-          if (blk <= w) {
-            float v[32];
-            tmem_ld32(t_p + blk * 32, v);
+        for (int b = 0; b < 8; ++b) {          // 16 tokens
+          uint32_t out[8];
+          if (b <= 2 * w + 1) {
+            float v[16];
+            tmem_ld16(t_p + b * 16, v);
+            const float* f_s = pow_s - (b & 1) * 16;
+            float far = b < 2 ? far_of[0] : b < 4 ? far_of[1] : far_of[2];
             tmem_ld_wait();
-            if (blk < w) {
-              const float far = blk == 0 ? far_of[0] : blk == 1 ? far_of[1] : far_of[2];
+            if (b < 2 * w) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(pow_s + 28 - j);
+              for (int j = 0; j < 16; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(f_s + 28 - j);
                 const float2 y0 = mul2(make_float2(v[j], v[j + 1]), mul2(make_float2(far, far), make_float2(f.w, f.z)));
                 const float2 y1 = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(far, far), make_float2(f.y, f.x)));
                 out[j / 2] = pack_bf16(y0.x, y0.y);
                 out[j / 2 + 1] = pack_bf16(y1.x, y1.y);
               }
             } else {
+              const int own = lane - (b & 1) * 16;   // (what is read in front of the table is masked)
 #pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                // (what is read in front of the table is masked)
-                const float2 f = make_float2(pow_s[j < 28 ? lane - j : max(0, lane - j)],
-                                             pow_s[j + 1 < 28 ? lane - j - 1 : max(0, lane - j - 1)]);
+              for (int j = 0; j < 16; j += 2) {
+                const float2 f = make_float2(f_s[lane - j], f_s[lane - j - 1]);
                 const float2 y = mul2(make_float2(v[j], v[j + 1]), f);
-                out[j / 2] = pack_bf16(j <= lane ? y.x : 0.f, j + 1 <= lane ? y.y : 0.f);
+                out[j / 2] = pack_bf16(j <= own ? y.x : 0.f, j + 1 <= own ? y.y : 0.f);
               }
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) out[j] = 0u;
+            for (int j = 0; j < 8; ++j) out[j] = 0u;
           }
-          tmem_st16w(t_p + blk * 16, out);     // (over logits that this thread has read)
+          tmem_st_words<8>(t_p + b * 8, out);  // (over logits that this thread has read)
         }
         tmem_st_wait();
         tc_fence_before();
@@ -522,11 +521,12 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
 #pragma unroll 1
     while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
       const float g = __ldg(a.log_decay + it.h);
+      float f = 0.f;
 #pragma unroll 1
       for (int c = it.c0; c < it.c1; ++c, ++t) {
         const int s = t % kQk, sv = t % kV, r = min(kC, it.n - c * kC);
         uint8_t* st = smem + oV + sv * kTile;
-        const float f = row < r ? power(g, r - 1 - row) : 0.f;
+        if (c == it.c0 || r < kC) f = row < r ? power(g, r - 1 - row) : 0.f;
         if (!(ok = wait32(&v_full[sv], (uint32_t)(t / kV) & 1u))) break;
         uint32_t part[kSplit][16];
         float2 all = make_float2(0.f, 0.f);    // not finite if one of the values is not
@@ -625,7 +625,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       const int cols = live ? min(32, a.dv - it.part * kCols - half * 32) : 0;   // a multiple of 8, or none
       const int64_t head = ((int64_t)it.h * a.dk + row) * a.dv + it.part * kCols + half * 32;
       const int64_t slot = (int64_t)a.n_heads * a.dk * a.dv;
-      float s[32];
+      float s[32], d1 = 0.f;
       const float* from = it.seg >= 0 ? plan.seg + it.seg * slot + head : src >= 0 ? a.state + src * slot + head : nullptr;
       float* to = it.last && dst >= 0 && (dst != src || it.n > 0) ? a.state + dst * slot + head : nullptr;
       if (LOCAL) {
@@ -640,7 +640,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       }
 #pragma unroll 1
       for (int c = it.c0; c < it.c1; ++c, ++t) {
-        const float d1 = expm1f(g * (float)min(kC, it.n - c * kC));
+        if (c == it.c0 || it.n - c * kC < kC) d1 = expm1f(g * (float)min(kC, it.n - c * kC));
         if constexpr (!LOCAL) {
           if (t > 0 && !(ok = wait32(st_taken, (uint32_t)(t - 1) & 1u))) break;
           if (rows) {
