@@ -52,6 +52,17 @@ __device__ __forceinline__ void tokens_of(const LinearArgs& p, int b, int64_t& f
   n = s1 > s0 ? s1 - s0 : 0;
 }
 
+// SMs of the current device.
+inline int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+    cudaGetLastError();
+    return 152;                                // no device: a GB300's
+  }
+  return sms;
+}
+
 cudaError_t launch_linear_recurrent(const LinearArgs& p, cudaStream_t st);
 size_t linear_prefill_workspace(int64_t n_tokens, int batch, int H, int dk, int dv);
 cudaError_t launch_linear_prefill(const LinearArgs& p, void* ws, cudaStream_t st);

@@ -812,16 +812,6 @@ bool map_heads(CUtensorMap* m, const void* base, int64_t tokens, int heads, int 
 
 namespace {
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
-    cudaGetLastError();
-    return 152;                                // no device: a GB300's
-  }
-  return sms;
-}
-
 // Chunks of a segment, or 0 where sequences stay whole.  Times in chunks of one CTA: whole
 // sequences take their length; a split takes its share of all chunks 1.6 times (the first
 // pass reads K and V again) and three launches, about kSplitCost.

@@ -6,6 +6,10 @@
 // 8th group of rows a thread) from the load of the state to its store.  q and k of up to
 // four tokens wait in shared memory; every thread sums its rows' share of q^T S,
 // and the shares meet in shared memory once for those tokens.
+//
+// Bound by the state's bytes, each way once: 64 x 64 heads of 128 x 128, 537 MB, 88.8 us, 6.1 TB/s (91 %
+// of the measured copy rate); in registers of 64-column halves 106 us, with four CTAs an SM (64
+// registers a thread, some spilled) 126.  24 sequences x 4 tokens x 32 heads of 64 x 64, 26 MB: 7.4 us.
 #include "kernels.h"
 #include "linear_attn.h"
 
@@ -15,14 +19,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = 4;                       // tokens between two meetings of the CTA
-constexpr int kMaxDim = 128;
 
-template <int COLS>
+// DIMS: 64 or 128, what dk is at most.
+template <int COLS, int DIMS>
 __global__ void __launch_bounds__(kThreads)
 linear_recurrent(const __grid_constant__ LinearArgs p, int parts) {
   constexpr int kRows = 32 / COLS;               // rows of a warp at a time
-  constexpr int kSteps = kMaxDim / (kRows * kWarps);
-  __shared__ __align__(16) float q_s[kTokens][kMaxDim], k_s[kTokens][kMaxDim];
+  constexpr int kSteps = DIMS / (kRows * kWarps);
+  __shared__ __align__(16) float q_s[kTokens][DIMS], k_s[kTokens][DIMS];
   __shared__ float4 sum_s[kTokens][kWarps][32];
   const dsi_linear& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -51,9 +55,9 @@ linear_recurrent(const __grid_constant__ LinearArgs p, int parts) {
   for (int t0 = 0; t0 < n; t0 += kTokens) {
     const int nt = min(kTokens, n - t0);
     if (t0 > 0) __syncthreads();                 // the tokens before are done with
-    for (int i = tid; i < nt * 2 * (kMaxDim / 8); i += kThreads) {
-      const int u = i % (kMaxDim / 8), t = (i / (kMaxDim / 8)) >> 1;
-      const bool key = (i / (kMaxDim / 8)) & 1;
+    for (int i = tid; i < nt * 2 * (DIMS / 8); i += kThreads) {
+      const int u = i % (DIMS / 8), t = (i / (DIMS / 8)) >> 1;
+      const bool key = (i / (DIMS / 8)) & 1;
       const bf16* x = key ? reinterpret_cast<const bf16*>(a.k) + (first + t0 + t) * a.ld_k_row + hk * a.ld_k_head
                           : reinterpret_cast<const bf16*>(a.q) + (first + t0 + t) * a.ld_q_row + h * a.ld_q_head;
       float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -117,20 +121,28 @@ linear_recurrent(const __grid_constant__ LinearArgs p, int parts) {
   }
 }
 
-template <int COLS>
-cudaError_t launch(const LinearArgs& p, cudaStream_t st) {
+template <int COLS, int DIMS>
+cudaError_t launch_for(const LinearArgs& p, cudaStream_t st) {
   const int parts = (p.a.dv + 4 * COLS - 1) / (4 * COLS);
-  const cudaError_t e = launch_overlapped(linear_recurrent<COLS>, dim3((unsigned)(p.batch * p.a.n_heads * parts)),
+  const cudaError_t e = launch_overlapped(linear_recurrent<COLS, DIMS>, dim3((unsigned)(p.batch * p.a.n_heads * parts)),
                                           dim3(kThreads), 0, st, p, parts);
   note_launch();
   return e;
 }
 
+template <int COLS>
+cudaError_t launch(const LinearArgs& p, cudaStream_t st) {
+  return p.a.dk > 64 ? launch_for<COLS, 128>(p, st) : launch_for<COLS, 64>(p, st);
+}
+
 }  // namespace
 
 cudaError_t launch_linear_recurrent(const LinearArgs& p, cudaStream_t st) {
-  if (p.a.dv > 64) return launch<32>(p, st);
-  return p.a.dv > 32 ? launch<16>(p, st) : launch<8>(p, st);
+  // A wide head is one CTA, or four where they fill the device at most three times.  us for 16 / 64 /
+  // 100 / 128 / 256 heads of 128 x 128: one 3.70 / 3.81 / 3.91 / 3.90 / 5.55, two 2.98 / 3.18 / 3.90 / 3.87 / 6.55,
+  // four 2.47 / 2.98 / 3.70 / 4.21 / 6.67.
+  if (p.a.dv > 64 && (int64_t)p.batch * p.a.n_heads * 4 > 3 * sm_count()) return launch<32>(p, st);
+  return p.a.dv > 32 && p.a.dv <= 64 ? launch<16>(p, st) : launch<8>(p, st);
 }
 
 }  // namespace dsi
