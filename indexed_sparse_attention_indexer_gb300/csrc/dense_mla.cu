@@ -807,42 +807,42 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     }
   } else if (warp == kQkWarp) {
     // ======================= logit issuer =======================================
-    if (lane == 0) {
+    {
       Piece x;
       int slot = 0, tg = 0, pieces = 0;
       bool ok = true;
       const uint64_t qr = desc_sw64(smem_u32(smem + Y::qr));
 #pragma unroll 1
       while (ok && next_piece(a, plan, sh, walk, x)) {
-        if (!(ok = wait1(q_ready, (uint32_t)pieces & 1u))) break;
+        if (!(ok = wait32(q_ready, (uint32_t)pieces & 1u))) break;
         ++pieces;
         slot += 2;                               // the query slice
 #pragma unroll 1
         for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
           const int stage = slot % kStages, sb = tg & 1;
-          if (!(ok = wait1(&full[stage], (uint32_t)(slot / kStages) & 1u))) break;
-          if (!(ok = wait1(&s_empty[sb], ((uint32_t)(tg >> 1) & 1u) ^ 1u))) break;
+          if (!(ok = wait32(&full[stage], (uint32_t)(slot / kStages) & 1u))) break;
+          if (!(ok = wait32(&s_empty[sb], ((uint32_t)(tg >> 1) & 1u) ^ 1u))) break;
           tc_fence_after();
           const uint32_t t_s = tmem + TM_S + sb * kNp;
           const uint32_t base = smem_u32(smem + Y::c + stage * kStageBytes);
           const uint64_t d0 = desc_sw128(base);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            mma_bf16_tmem_a(t_s, tmem + TM_Q + i * 8,
+            e_mma_ta(t_s, tmem + TM_Q + i * 8,
                             d0 + (uint64_t)(((i >> 2) * kBlockBytes + (i & 3) * 32) >> 4), IDESC_S,
                             i > 0 ? 1u : 0u);
           const uint64_t dr = desc_sw64(base + kRopeOff);
 #pragma unroll
           for (int i = 0; i < kRopeHalf / 16; ++i)
-            mma_bf16(t_s, qr + (uint64_t)((i * 32) >> 4), dr + (uint64_t)((i * 32) >> 4), IDESC_S, 1u);
-          mma_commit(&s_full[sb]);
+            e_mma(t_s, qr + (uint64_t)((i * 32) >> 4), dr + (uint64_t)((i * 32) >> 4), IDESC_S, 1u);
+          e_commit(&s_full[sb]);
         }
       }
     }
     __syncwarp();
   } else if (warp == kPvWarp) {
     // ======================= value issuer =======================================
-    if (lane == 0) {
+    {
       Piece x;
       int slot = 0, tg = 0;
       bool ok = true;
@@ -856,17 +856,17 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           const uint64_t vd = desc_sw128_mn(smem_u32(smem + Y::c + stage * kStageBytes), kBlockBytes);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            if (!(ok = wait1(&p_full[hf], (uint32_t)tg & 1u))) break;
+            if (!(ok = wait32(&p_full[hf], (uint32_t)tg & 1u))) break;
             tc_fence_after();
 #pragma unroll
             for (int i = 2 * hf; i < 2 * hf + 2; ++i)
-              mma_bf16(tmem + TM_O, pd + (uint64_t)((i * 32) >> 4), vd + (uint64_t)((i * 2048) >> 4),
+              e_mma(tmem + TM_O, pd + (uint64_t)((i * 32) >> 4), vd + (uint64_t)((i * 2048) >> 4),
                        IDESC_O, (t > x.t0 || i > 0) ? 1u : 0u);
-            mma_commit(&p_empty[hf]);
+            e_commit(&p_empty[hf]);
           }
           if (!ok) break;
-          mma_commit(&empty[stage]);
-          if (t + 1 == x.t1) mma_commit(o_done);
+          e_commit(&empty[stage]);
+          if (t + 1 == x.t1) e_commit(o_done);
         }
       }
     }
