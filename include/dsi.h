@@ -475,8 +475,8 @@ size_t dsi_dense_mla_workspace_size(int32_t rows, int32_t n_heads);
  *           need one each.
  * Numbers, rows outside the visible range, rows that are not finite, page ids and errors as for
  * dsi_dense_mla_decode; DSI_ERR_INVALID_ARG also for a prefix of other than
- * one sequence, DSI_ERR_UNSUPPORTED for different latent dtypes,
- * DSI_ERR_WORKSPACE for a missing workspace.
+ * one sequence, DSI_ERR_UNSUPPORTED for different latent dtypes and
+ * for 2^30 query heads (batch * T * n_heads) or more, DSI_ERR_WORKSPACE for a missing workspace.
  */
 dsi_status dsi_prefix_mla_decode(const void* q, const dsi_cache* prefix, const dsi_cache* cache,
                                  int32_t tokens_per_seq, int32_t n_heads, float scale, void* out,

@@ -527,7 +527,8 @@ dsi_status dsi_prefix_mla_decode(const void* q, const dsi_cache* prefix, const d
   if (!q || !out || !prefix || !cache || tokens_per_seq < 1 || cache->batch < 0 || !(scale == scale))
     return DSI_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)cache->batch * tokens_per_seq;
-  if (n_heads < 1 || n_heads > 128 || rows > 0x7fffffff / n_heads) return DSI_ERR_UNSUPPORTED;
+  // (groups of both kinds are counted in 32 bits)
+  if (n_heads < 1 || n_heads > 128 || rows > 0x3fffffff / n_heads) return DSI_ERR_UNSUPPORTED;
   if (prefix->batch != 1) return DSI_ERR_INVALID_ARG;
   dsi_status s = check_cache(prefix, 1, 1, 0, false, true);
   if (s != DSI_OK) return s;

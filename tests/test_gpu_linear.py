@@ -162,6 +162,7 @@ PREFILLS = [
     dict(lens=[200, 31], H=2, dk=64, dv=64), dict(lens=[300], H=2, dk=96, dv=80), dict(lens=[257], H=2, dk=8, dv=8),
     dict(lens=[140], H=3, dk=72, dv=128), dict(lens=[140], H=3, dk=128, dv=24), dict(lens=[390], H=4, Hk=1, dk=40, dv=104),
     dict(lens=[150, 150], H=5, heads_first=True), dict(lens=[130] * 40, H=8), dict(lens=[1500], H=1),
+    dict(lens=[7 * i % 41 for i in range(300)], H=2, dk=64, dv=64), dict(lens=[i % 3 * 100 for i in range(256)], H=1, dk=32, dv=16),
 ]
 
 
@@ -175,7 +176,7 @@ def test_prefill(kw):
 LONG = [
     dict(lens=[9000], H=1), dict(lens=[4000], H=2, kind="none", dk=64, dv=64), dict(lens=[4097], H=2, kind="near"),
     dict(lens=[7000, 0, 8000, 1, 129], H=2), dict(lens=[5000, 2500], H=2, fork=True), dict(lens=[3500], H=2, state=False),
-    dict(lens=[4000], H=4, kind="strong", dk=96, dv=40), dict(lens=[256 * 12], H=1, dk=128, dv=128), dict(lens=[3333], H=3, Hk=1),
+    dict(lens=[4000], H=4, kind="strong", dk=96, dv=40), dict(lens=[128 * 25], H=1), dict(lens=[3333], H=3, Hk=1),
 ]
 
 
@@ -383,3 +384,48 @@ def test_streams_and_captures():
         torch.cuda.synchronize()
         assert torch.equal(o2, out) and torch.equal(s2.view(torch.int32), state.view(torch.int32))
         assert torch.equal(y2, y) and torch.equal(p2.view(torch.int32), pool.view(torch.int32))
+
+
+@pytest.mark.parametrize("lens,H", [([300, 5], 3), ([4000], 1)])
+def test_checked_library(lens, H):
+    """The bounds-checked build gives the same bits."""
+    c = Case(lens, H=H, lead=0, tail=0, seed=21)
+    out, state = c.prefill()
+    again = c.state.to(DEV)
+    out2 = binding.linear_prefill(c.dq, c.dk_, c.dv_, c.log_decay.to(DEV), c.scale, c.starts, again, c.in_slots.to(DEV),
+                                  c.out_slots.to(DEV), checked=True)
+    assert torch.equal(out, out2) and torch.equal(state.view(torch.int32), again.view(torch.int32))
+    args = (c.dq[:4], c.dk_[:4], c.dv_[:4], c.log_decay.to(DEV), c.scale)
+    a, b = (torch.ones((2, H, 128, 128), device=DEV) for _ in range(2))
+    assert torch.equal(binding.linear_decode(*args, a, 2), binding.linear_decode(*args, b, 2, checked=True))
+    assert torch.equal(a, b) and binding.device_status() == 0 and binding.device_status(checked=True) == 0
+
+
+def test_offsets_past_32_bits():
+    """Rows and slots that lie past 2^32 bytes: the same bits as close together."""
+    n, wide = 33100, 65536                        # 4.3 GB of token rows
+    g = torch.Generator(device=DEV).manual_seed(4)
+    near = torch.randn((n, 3, 64), generator=g, device=DEV).to(torch.bfloat16)
+    far = torch.empty((n, wide), dtype=torch.bfloat16, device=DEV)
+    far[:, :192] = near.view(n, 192)
+    far = far[:, :192].view(n, 3, 64)
+    dec = torch.tensor([-0.01], device=DEV)
+    starts = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    outs, states = [], []
+    for x in (near, far):
+        state = torch.zeros((1, 1, 64, 64), device=DEV)
+        out = torch.empty((n, wide), dtype=torch.bfloat16, device=DEV)[:, :64].view(n, 1, 64) if x is far else None
+        outs.append(binding.linear_prefill(x[:, :1], x[:, 1:2], x[:, 2:], dec, 0.125, starts, state, out=out))
+        states.append(state)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(states[0], states[1])
+    del far, outs
+    slots = 70000                                 # 4.6 GB of states
+    pool = torch.zeros((slots, 1, 128, 128), device=DEV)
+    pool[-2:] = torch.randn((2, 1, 128, 128), generator=g, device=DEV)
+    small = pool[-2:].clone()
+    q, k, v = (torch.randn((2, 1, 128), generator=g, device=DEV).to(torch.bfloat16) for _ in range(3))
+    at = torch.tensor([slots - 1, slots - 2], dtype=torch.int32, device=DEV)
+    a = binding.linear_decode(q, k, v, dec, 0.1, pool, in_slots=at)
+    b = binding.linear_decode(q, k, v, dec, 0.1, small, in_slots=at - (slots - 2))
+    assert torch.equal(a, b) and torch.equal(pool[-2:], small) and not bool(pool[:-2].any())
+    assert binding.device_status() == 0

@@ -312,3 +312,11 @@ def test_every_tile_counts(fp8, H):
     for b, n in enumerate(lens):
         assert bool(((lse[b].double() - math.log(P + n)).abs() <= 2.0 ** -20 * (1 + math.log(P + n))).all())
     case.check(out, lse)
+
+
+def test_checked_library():
+    case = Shared(900, [70, 300, 0, 5], 1, 16, 64, seed=31).device()
+    out, lse = case.run()
+    again = case.run(checked=True)
+    torch.cuda.synchronize()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and binding.device_status(checked=True) == 0

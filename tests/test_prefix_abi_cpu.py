@@ -54,6 +54,7 @@ def test_refusals(L):
         assert call(prefix=_cache(1, **kw)) == U and call(cache=_cache(**kw)) == U, kw
     assert call(cache=_cache(-1)) == E and call(cache=_cache(1 << 30), T=4) == U
     assert call(cache=_cache(1 << 21, s_max=1 << 10)) == U                # 2^31 cache rows
+    assert call(cache=_cache(1 << 30, s_max=1), H=1) == U == call(cache=_cache(1 << 23, s_max=1), H=128)   # 2^30 outputs
     assert call(cache=_cache(0), ws=None, size=0) == OK
 
 
