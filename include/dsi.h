@@ -471,8 +471,8 @@ size_t dsi_dense_mla_workspace_size(int32_t rows, int32_t n_heads);
  *   cache   the sequences' own rows.  Both have latent_dtype in common; they may be pages
  *           of one pool, of one or of different sizes, or separate tensors
  *   workspace  256-byte aligned, at least dsi_prefix_mla_workspace_size() bytes: the prefix's
- *           and the sequences' parts are joined from there.  Calls that may run at once
- *           need one each.
+ *           and the sequences' parts are joined from there, and a long FP8 prefix of up to
+ *           65536 positions is converted into it.  Calls that may run at once need one each.
  * Numbers, rows outside the visible range, rows that are not finite, page ids and errors as for
  * dsi_dense_mla_decode; DSI_ERR_INVALID_ARG also for a prefix of other than
  * one sequence, DSI_ERR_UNSUPPORTED for different latent dtypes and

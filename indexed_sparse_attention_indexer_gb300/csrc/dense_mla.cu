@@ -1276,10 +1276,34 @@ dense_mla_join(DenseArgs a, Plan plan, Workspace ws, int clusters, int rows) {
   }
 }
 
+// An FP8 prefix that several groups read, as the bf16 rows that they multiply: `to` [positions, 576].  A warp a
+// row, bound by its 596 bytes read and 1152 written.
+constexpr int kExpandRows = 65536;             // positions that the workspace has room for
+__global__ void __launch_bounds__(256)
+prefix_expand(CacheView c, const float* scale, bf16* to, int* err) {
+  const int lane = threadIdx.x & 31;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int n = (int)visible_len(c, 0, 1, 0);
+  for (int p = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5); p < n; p += (int)((gridDim.x * blockDim.x) >> 5)) {
+    const int row = row_of(c, 0, p, err);
+#pragma unroll
+    for (int u = lane; u < DSI_D_QK / 16; u += 32) {
+      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+      if (row >= 0)
+        e4m3x16_scaled(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(c.latent) + (int64_t)row * DSI_D_QK) + u),
+                       __ldg(scale + (int64_t)row * 5 + (u >> 3)), lo, hi);
+      uint4* at = reinterpret_cast<uint4*>(to + (int64_t)p * DSI_D_QK + u * 16);
+      at[0] = lo;
+      at[1] = hi;
+    }
+  }
+}
+
 // Joins a row's parts over the prefix and over its sequence's own rows, each of one piece or
 // more: a warp takes 128 dims of a head.  Bound by the parts' 2 KB each, which mostly are in L2.
 __global__ void __launch_bounds__(kJoinThreads)
-prefix_mla_join(DenseArgs a, Plan plan, Workspace ws, int prefix_tokens, int prefix_groups) {
+prefix_mla_join(DenseArgs a, Plan plan, Workspace ws, int prefix_tokens, int prefix_groups, int own_slot0) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int vectors = a.rows * a.H;
   grid_dep_wait();     // the parts come from the kernel launched just before
@@ -1296,7 +1320,7 @@ prefix_mla_join(DenseArgs a, Plan plan, Workspace ws, int prefix_tokens, int pre
       const int2 s = own ? so : sp;
       if (own) j -= np;
       if (s.x == s.y) return -1 - (own ? (int64_t)vectors + at : (int64_t)at);
-      return (int64_t)(2 * (s.x + j) + (j == 0 ? 1 : 0)) * kM + (own ? mo : mp);
+      return (int64_t)((own ? own_slot0 : 0) + 2 * (s.x + j) + (j == 0 ? 1 : 0)) * kM + (own ? mo : mp);
     };
     auto stats = [&](int64_t p) { return p < 0 ? ws.whole_ml[-1 - p] : ws.ml[p]; };
     float top = -INFINITY;
@@ -1436,13 +1460,15 @@ cudaError_t launch_dense_mla(const DenseArgs& a, cudaStream_t st) {
   return e;
 }
 
+// Workspace: 2 * clusters slots for either of two launches, the rows' places, the spans, and
+// kExpandRows bf16 rows.
 size_t prefix_mla_workspace(int rows, int H) {
   int n = cluster_slots<false, true>() > cluster_slots<true, true>() ? cluster_slots<false, true>()
                                                                      : cluster_slots<true, true>();
   if (n == 0) n = 76;                            // no device: what a GB300 takes
   const size_t vectors = (size_t)rows * H;
-  return (size_t)n * 2 * kSlotBytes + 2 * vectors * (DSI_D_LATENT * sizeof(float) + sizeof(float2)) +
-         2 * (size_t)rows * sizeof(int2);
+  return (size_t)kExpandRows * DSI_D_QK * sizeof(bf16) + (size_t)n * 4 * kSlotBytes +
+         2 * vectors * (DSI_D_LATENT * sizeof(float) + sizeof(float2)) + 2 * (size_t)rows * sizeof(int2);
 }
 
 cudaError_t launch_prefix_mla(const DenseArgs& a, const CacheView& prefix, const float* prefix_scale,
@@ -1456,34 +1482,71 @@ cudaError_t launch_prefix_mla(const DenseArgs& a, const CacheView& prefix, const
   Plan plan;
   plan.tokens = kM / a.H < a.T ? kM / a.H : a.T;
   plan.per_seq = (a.T + plan.tokens - 1) / plan.tokens;
-  const int64_t groups = sh.groups + (int64_t)plan.per_seq * (a.rows / a.T);
-  plan.groups = (int)groups;                     // <= 2 * rows
-  plan.live = (sh.tokens * a.H + 31) / 32;
-  const int slots = f8 ? cluster_slots<true, true>() : cluster_slots<false, true>();
+  const int own_groups = plan.per_seq * (a.rows / a.T);
+  int slots = cluster_slots<false, true>();
+  if (f8) slots = slots < cluster_slots<true, true>() ? slots : cluster_slots<true, true>();
   if (slots == 0) return cudaErrorInvalidConfiguration;
-  // at most a cluster a tile
-  const int64_t tiles = sh.groups * ((prefix.s_max + kNp - 1) / kNp) +
-                        (groups - sh.groups) * ((a.c.s_max + kNp - 1) / kNp);
-  const int clusters = (int)(tiles < slots ? tiles : slots);
-  plan.split = clusters > 1;
+  const int64_t prefix_tiles = sh.groups * ((prefix.s_max + kNp - 1) / kNp);
+  const int64_t own_tiles = own_groups * ((a.c.s_max + kNp - 1) / kNp);
+  // An FP8 prefix becomes bf16 once, and the two kinds of groups take a launch each, where that
+  // saves more than it costs.  us without and with, by tiles of the prefix to a cluster: 6.7 41 / 50, 13.5 56 / 59,
+  // 27 85 / 76, 29 90 / 83, 54 156 / 127, 108 283 / 189, 431 (64 x 32768 x 128 heads) 1000 / 576.
+  const bool expand = f8 && sh.groups > 1 && prefix.s_max <= kExpandRows && prefix_tiles >= 16 * (int64_t)slots;
+
+  bf16* const rows16 = static_cast<bf16*>(a.ws);
   const size_t vectors = (size_t)a.rows * a.H;
   Workspace ws = {};
-  ws.o = static_cast<float*>(a.ws);
-  ws.whole_o = ws.o + (size_t)2 * clusters * kM * DSI_D_LATENT;
+  ws.o = reinterpret_cast<float*>(rows16 + (size_t)kExpandRows * DSI_D_QK);
+  ws.whole_o = ws.o + (size_t)4 * slots * kM * DSI_D_LATENT;
   ws.ml = reinterpret_cast<float2*>(ws.whole_o + 2 * vectors * DSI_D_LATENT);
-  ws.whole_ml = ws.ml + (size_t)2 * clusters * kM;
+  ws.whole_ml = ws.ml + (size_t)4 * slots * kM;
   ws.spans = reinterpret_cast<int2*>(ws.whole_ml + 2 * vectors);
   int box;
   CUtensorMap map, rmap, qmap;
-  if (!map_rows(a.c, f8, &map, &rmap, &box) || !map_rows(prefix, f8, &sh.lmap, &sh.rmap, &sh.box) ||
-      !map_queries(a, &qmap))
-    return cudaErrorInvalidValue;
-  cudaError_t e = f8 ? launch<true, true>(map, rmap, qmap, a, plan, ws, box, sh, clusters, st)
-                     : launch<false, true>(map, rmap, qmap, a, plan, ws, box, sh, clusters, st);
+  if (!map_rows(a.c, f8, &map, &rmap, &box) || !map_queries(a, &qmap)) return cudaErrorInvalidValue;
+  if (expand) {
+    sh.c.latent = rows16;
+    sh.c.block_table = nullptr;
+  }
+  if (!map_rows(sh.c, f8 && !expand, &sh.lmap, &sh.rmap, &sh.box)) return cudaErrorInvalidValue;
+  plan.live = (sh.tokens * a.H + 31) / 32;
+  // at most a cluster a tile
+  auto clusters_for = [&](int64_t tiles) { return (int)(tiles < slots ? tiles : slots); };
+  cudaError_t e;
+  if (expand) {
+    const int64_t blocks = (prefix.s_max + 7) / 8, wave = 16 * (int64_t)slots;
+    e = launch_overlapped(prefix_expand, dim3((unsigned)(blocks < wave ? blocks : wave)), dim3(256), 0, st, prefix,
+                          prefix_scale, rows16, a.err);
+    note_launch();
+    if (e != cudaSuccess) return e;
+    plan.groups = sh.groups;
+    int clusters = clusters_for(prefix_tiles);
+    plan.split = clusters > 1;
+    e = launch<false, true>(sh.lmap, sh.rmap, qmap, a, plan, ws, sh.box, sh, clusters, st);
+    if (e != cudaSuccess) return e;
+    Prefix<true> none = sh;
+    none.groups = 0;
+    Workspace own = ws;
+    own.o += (size_t)2 * slots * kM * DSI_D_LATENT;
+    own.ml += (size_t)2 * slots * kM;
+    own.spans += sh.groups;
+    Plan own_plan = plan;
+    own_plan.groups = own_groups;
+    own_plan.live = (plan.tokens * a.H + 31) / 32;
+    clusters = clusters_for(own_tiles);
+    own_plan.split = clusters > 1;
+    e = launch<true, true>(map, rmap, qmap, a, own_plan, own, box, none, clusters, st);
+  } else {
+    plan.groups = sh.groups + own_groups;        // <= 2 * rows
+    const int clusters = clusters_for(prefix_tiles + own_tiles);
+    plan.split = clusters > 1;
+    e = f8 ? launch<true, true>(map, rmap, qmap, a, plan, ws, box, sh, clusters, st)
+           : launch<false, true>(map, rmap, qmap, a, plan, ws, box, sh, clusters, st);
+  }
   if (e != cudaSuccess) return e;
-  const int64_t wave = 32 * clusters;
+  const int64_t wave = 32 * (int64_t)slots;
   e = launch_overlapped(prefix_mla_join, dim3((unsigned)((int64_t)vectors < wave ? (int64_t)vectors : wave)),
-                        dim3(kJoinThreads), 0, st, a, plan, ws, sh.tokens, sh.groups);
+                        dim3(kJoinThreads), 0, st, a, plan, ws, sh.tokens, sh.groups, expand ? 2 * slots : 0);
   note_launch();
   return e;
 }

@@ -54,7 +54,7 @@ constexpr int kMarks = 5;                      // (the place of V t + 5 is free 
 constexpr int oBad = oS + kTile;               // [kMarks][8] a warp's part of V holds something not finite
 constexpr int oFirst = oBad + kMarks * 8 * 4;  // [kMarks][8][32] the first such row of a column
 constexpr int oBar = oFirst + kMarks * 8 * 32;
-constexpr int kBars = 4 * kQk + 3 * kV + 4 * 2 + 5;
+constexpr int kBars = 4 * kQk + 3 * kV + 4 * 2 + 4 + 4;
 constexpr int oSlot = oBar + kBars * 8;
 constexpr int oTable = oSlot + 8;              // next_item's
 constexpr int kSmem = oTable + 264;
@@ -225,11 +225,12 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
   uint64_t* p_full = s_full + 2;               // [2] P in TMEM
   uint64_t* o_full = p_full + 2;               // [2] OI and OX done
   uint64_t* o_empty = o_full + 2;              // [2] ... read out: P's tile and OX's are free
-  uint64_t* v_ready = o_empty + 2;             // V' and K^T written
-  uint64_t* st_ready = v_ready + 1;            // the state's bf16 form written
-  uint64_t* st_taken = v_ready + 2;            // Q S done
-  uint64_t* d_full = v_ready + 3;              // K^T V' done
-  uint64_t* d_empty = v_ready + 4;             // ... added to the state
+  uint64_t* v_ready = o_empty + 2;             // [2] V' and K^T of half the tokens written
+  uint64_t* v_taken = v_ready + 2;             // [2] ... multiplied
+  uint64_t* st_ready = v_taken + 2;            // the state's bf16 form written
+  uint64_t* st_taken = st_ready + 1;           // Q S done
+  uint64_t* d_full = st_ready + 2;             // K^T V' done
+  uint64_t* d_empty = st_ready + 3;            // ... added to the state
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + oSlot);
   const dsi_linear& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -252,7 +253,10 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       mbar_init(&o_full[i], 2);
       mbar_init(&o_empty[i], 4);
     }
-    mbar_init(v_ready, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&v_ready[i], 4);
+      mbar_init(&v_taken[i], 1);
+    }
     mbar_init(st_ready, 8);
     mbar_init(st_taken, 1);
     mbar_init(d_full, 1);
@@ -354,12 +358,20 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
 #pragma unroll 1
         for (int c = it.c0; c < it.c1; ++c, ++t) {
           const uint32_t ph = (uint32_t)t & 1u;
-          if (!(ok = wait32(v_ready, ph) && wait32(d_empty, ph ^ 1u))) break;
-          tc_fence_after();
+          if (!(ok = wait32(d_empty, ph ^ 1u))) break;
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) {     // 64 tokens at a time: the next chunk's go where they were
+            if (!(ok = wait32(&v_ready[hf], ph))) break;
+            tc_fence_after();
 #pragma unroll 4
-          for (int x = 0; x < kSplit * (kC / 16); ++x)
-            e_mma_ta(tmem + TM_D, tmem + TM_KT + (x & 7) * 8,
-                            d_vp + (uint64_t)(((x >> 3) * kTile + (x & 7) * 2048) >> 4), IDESC_O, x > 0 ? 1u : 0u);
+            for (int x = 0; x < kSplit * 4; ++x) {
+              const int step = hf * 4 + (x & 3);
+              e_mma_ta(tmem + TM_D, tmem + TM_KT + step * 8, d_vp + (uint64_t)(((x >> 2) * kTile + step * 2048) >> 4), IDESC_O,
+                       hf + x > 0 ? 1u : 0u);
+            }
+            e_commit(&v_taken[hf]);
+          }
+          if (!ok) break;
           e_commit(d_full);
         }
       }
@@ -491,10 +503,11 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     }
   } else if (warp >= 8 && warp < 16) {
     // ======================= V' and K^T ==========================================
-    // V': thread = half a row of V, its parts held in registers until the products with the
-    // V' before are done.  K^T: a warp turns 32 dims of 64 tokens, 8 x 8 at a time.
-    const int w = warp - 8, u0 = (w >> 2) * 4, quarter = w & 3;
-    const uint32_t k_lane = (uint32_t)((w >> 2) * 64 + ((lane >> 4) & 1) * 8 + (lane & 7));   // token whose address this lane gives
+    // Four warps to half the tokens.  V': thread = half a row of V, its parts held in registers until
+    // the products with the V' before are done.  K^T: a warp turns 32 dims, 8 x 8 at a time.
+    const int w = warp - 8, hf = w >> 2, u0 = (w & 1) * 4, quarter = w & 3;
+    const int v_row0 = hf * 64 + ((w >> 1) & 1) * 32, v_row = v_row0 + lane;
+    const uint32_t k_lane = (uint32_t)(hf * 64 + ((lane >> 4) & 1) * 8 + (lane & 7));        // token whose address this lane gives
     const uint32_t k_u = (uint32_t)((quarter & 1) * 4 + ((lane >> 3) & 1));                  // ... and 8 dims
 #pragma unroll 1
     while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
@@ -504,13 +517,13 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       for (int c = it.c0; c < it.c1; ++c, ++t) {
         const int s = t % kQk, sv = t % kV, r = min(kC, it.n - c * kC);
         uint8_t* st = smem + oV + sv * kTile;
-        if (c == it.c0 || r < kC) f = row < r ? power(g, r - 1 - row) : 0.f;
+        if (c == it.c0 || r < kC) f = v_row < r ? power(g, r - 1 - v_row) : 0.f;
         if (!(ok = wait32(&v_full[sv], (uint32_t)(t / kV) & 1u))) break;
         uint32_t part[kSplit][16];
         float2 all = make_float2(0.f, 0.f);    // not finite if one of the values is not
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const uint4 v4 = *reinterpret_cast<const uint4*>(st + sw128_offset((uint32_t)row, (uint32_t)(u0 + u)));
+          const uint4 v4 = *reinterpret_cast<const uint4*>(st + sw128_offset((uint32_t)v_row, (uint32_t)(u0 + u)));
           const uint32_t x[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -525,15 +538,15 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
             }
           }
         }
-        const bool bad = row < r && !(fabsf(all.x) + fabsf(all.y) < INFINITY);   // (or their sum)
-        if (row >= r) {                        // behind the sequence: what K and V hold must not meet weights of 0
+        const bool bad = v_row < r && !(fabsf(all.x) + fabsf(all.y) < INFINITY);   // (or their sum)
+        if (v_row >= r) {                        // behind the sequence: what K and V hold must not meet weights of 0
 #pragma unroll
           for (int i = 0; i < kSplit; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) part[i][e] = 0u;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const uint32_t off = sw128_offset((uint32_t)row, (uint32_t)(u0 + u));
+            const uint32_t off = sw128_offset((uint32_t)v_row, (uint32_t)(u0 + u));
             *reinterpret_cast<uint4*>(st + off) = make_uint4(0, 0, 0, 0);
           }
         }
@@ -543,22 +556,22 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
           uint8_t* first = smem + oFirst + (t % kMarks * 8 + w) * 32;
 #pragma unroll 1
           for (int x = 0; x < 32; ++x) {
-            uint16_t* e = reinterpret_cast<uint16_t*>(st + sw128_offset((uint32_t)row, (uint32_t)(u0 + (x >> 3)))) + (x & 7);
-            const bool out = row < r && (*e & 0x7F80u) == 0x7F80u;
+            uint16_t* e = reinterpret_cast<uint16_t*>(st + sw128_offset((uint32_t)v_row, (uint32_t)(u0 + (x >> 3)))) + (x & 7);
+            const bool out = v_row < r && (*e & 0x7F80u) == 0x7F80u;
             const uint32_t who = __ballot_sync(0xffffffffu, out);
             if (out) *e = 0;
-            if (lane == 0) first[x] = who ? (uint8_t)((w & 3) * 32 + __ffs(who) - 1) : (uint8_t)kC;
+            if (lane == 0) first[x] = who ? (uint8_t)(v_row0 + __ffs(who) - 1) : (uint8_t)kC;
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(LOCAL ? &v_empty[sv] : &v_clean[sv]);   // (nobody else reads it, or P V does)
-        if (t > 0 && !(ok = wait32(d_full, (uint32_t)(t - 1) & 1u))) break;
+        if (t > 0 && !(ok = wait32(&v_taken[hf], (uint32_t)(t - 1) & 1u))) break;
 #pragma unroll
         for (int i = 0; i < kSplit; ++i)
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<uint4*>(smem + oVp + i * kTile + sw128_offset((uint32_t)row, (uint32_t)(u0 + u))) =
+            *reinterpret_cast<uint4*>(smem + oVp + i * kTile + sw128_offset((uint32_t)v_row, (uint32_t)(u0 + u))) =
                 make_uint4(part[i][4 * u], part[i][4 * u + 1], part[i][4 * u + 2], part[i][4 * u + 3]);
         fence_proxy_async_smem();
         if (!(ok = wait32(&k_full[s], (uint32_t)(t / kQk) & 1u))) break;
@@ -574,11 +587,11 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
             if (r < kC) {                      // behind the sequence: zeros
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const int j = (w >> 2) * 64 + (i >> 1) * 8 + (lane & 3) * 2;
+                const int j = hf * 64 + (i >> 1) * 8 + (lane & 3) * 2;
                 x[i] &= (j < r ? 0xFFFFu : 0u) | (j + 1 < r ? 0xFFFF0000u : 0u);
               }
             }
-            tmem_st_16x128b_x8(tmem + ((uint32_t)(quarter * 32 + m * 16) << 16) + TM_KT + (w >> 2) * 32, x);
+            tmem_st_16x128b_x8(tmem + ((uint32_t)(quarter * 32 + m * 16) << 16) + TM_KT + hf * 32, x);
           }
           tmem_st_wait();
         }
@@ -586,7 +599,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&k_empty[s]);
-          mbar_arrive(v_ready);
+          mbar_arrive(&v_ready[hf]);
         }
       }
     }
@@ -708,10 +721,9 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
           const uint8_t* first = smem + oFirst + t % kMarks * 8 * 32;
 #pragma unroll 1
           for (int x = 0; x < (live ? cols : 0); ++x) {
-            const int part = (x >> 5) * 4;     // the warps that had this column
             int from = kC;
 #pragma unroll 1
-            for (int i = part; i < part + 4; ++i)
+            for (int i = x >> 5; i < 8; i += 2)          // the warps that had this column
               if (reinterpret_cast<const int*>(smem + oBad)[t % kMarks * 8 + i]) from = min(from, (int)first[i * 32 + (x & 31)]);
             if (row >= from) to[x] = __float2bfloat16(__int_as_float(0x7fc00000));
           }

@@ -94,6 +94,10 @@ CASES = {
     "fp8": (500, [300, 64, 1, 0, 900], 1, 128, 64, True, None),
     "fp8_heads_16": (3000, [100, 64, 1, 0, 300] * 5, 1, 16, 64, True, None),
     "fp8_tokens": (513, [70, 300, 2], 3, 20, 0, True, 24),
+    # (long enough for the prefix to be converted once)
+    "fp8_converted": (4005, [37 * i % 200 for i in range(20)], 1, 128, 64, True, None),
+    "fp8_converted_tokens": (4700, [53 * i % 90 for i in range(18)], 2, 64, 24, True, 0),
+    "fp8_converted_heads_20": (6001, [0, 1, 2] * 26, 1, 20, 0, True, 16),
 }
 
 
@@ -320,3 +324,30 @@ def test_checked_library():
     again = case.run(checked=True)
     torch.cuda.synchronize()
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and binding.device_status(checked=True) == 0
+
+
+def test_converted_fp8_prefix_edges():
+    """A prefix that is converted once: its length on the device shorter than its table, bad pages, a NaN code, and
+    what stays in the workspace from the call before."""
+    H, B, page = 128, 24, 64
+    case = Shared(3001, [5] * B, 1, H, page, True, seed=40, prefix_max=4096, garbage=False)
+    case.first.latent.view(torch.uint8)[case.first.table[0, 20].item(), 3, 17] = 0x7F      # NaN at position 1283
+    wsp = binding.alloc_workspace(binding.prefix_mla_workspace_size(B, H), DEV).fill_(0xFF)
+    out, lse = case.device().run(workspace=wsp)
+    torch.cuda.synchronize()
+    assert bool(out.isnan().all()) and bool(lse.isnan().all()) and binding.device_status() == 0
+    case.P = 1283                                     # up to that position
+    case.first.seq_lens.fill_(1283)
+    out, lse = case.run(workspace=wsp)
+    torch.cuda.synchronize()
+    case.check(out, lse, range(0, B, 5))
+    good = out.clone()
+    kept = int(case.first.d_table[0, 7])
+    case.first.d_table[0, 7] = 1 << 29
+    out, _ = case.run(workspace=wsp)
+    torch.cuda.synchronize()
+    assert binding.device_status() == binding.DSI_ERR_BOUNDS and bool(out.isfinite().all())
+    case.first.d_table[0, 7] = kept
+    out, _ = case.run(workspace=wsp)
+    torch.cuda.synchronize()
+    assert binding.device_status() == 0 and torch.equal(out, good)
