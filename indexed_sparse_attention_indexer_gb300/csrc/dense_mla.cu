@@ -41,16 +41,22 @@
 // once: what the tensor core computes there is never read.
 // Every wait is bounded; the cluster syncs after set-up and before exit.
 //
-// What bounds it.  64 sequences of 32768 positions, 128 heads, bf16 rows: 580 us at 2070
-// MHz, 4.2 TB/s (62 % of the measured copy rate) and 1007 TFLOP/s (53 % of the library
-// GEMM's); 605 to 622 us where the power cap holds the clock near 1950 MHz.  A tile takes
-// a cluster about 2750 cycles (the time's cycles over its 431 tiles).  Its bytes take
-// 1700, its MMAs 1340 (64 columns
+// What bounds it.  64 sequences of 32768 positions, 128 heads, bf16 rows: 601 us where the power cap
+// holds the clock near 1950 MHz, 4.0 TB/s (61 % of the measured copy rate) and 972 TFLOP/s (51 % of the
+// library GEMM's).  A tile takes a cluster about 2700 cycles (the time's cycles over its 431 tiles).  Its
+// bytes take 1700, its MMAs 1340 (64 columns
 // take 46 cycles, not 32; P.V is at its rate), the exchange 1600 (distributed shared
 // memory carries 20 bytes a cycle and SM each way): each is idle for a third to a half of
 // the time, because a stage is held for ~10,000 cycles, from its copy to the end of its
-// P.V, and there is room for four.  4096 tokens of 128 heads over windows of 1024: 1349
-// us, 768 TFLOP/s: the same, and the softmax warps' 2.5 us for each group's output.
+// P.V, and there is room for four.  4096 tokens of 128 heads over windows of 1024: 1309
+// us, 791 TFLOP/s: the same, and the softmax warps' 2.5 us for each group's output.
+// (The issuers' MMAs by a lane in a branch of its own: 618 and 1348 us.)
+// A prefix that a batch shares (PFX) adds groups of another kind: 128 (row, head) pairs of any
+// sequences over the prefix's positions, all of which they see.  They come first in the list that is dealt
+// out, the sequences' own rows after them as above, and prefix_mla_join adds up a row's parts over
+// both in fp32.  64 sequences x 16 heads over a prefix of 32768 and 512 rows of their own: 107 us, 627 by
+// the dense call on the same pages (128 heads, whose groups are the same: 614 and 691, the
+// prefix's bytes).  The tile's time bounds it as above; own rows fill 16 of a group's 128.
 // Three softmax sets (640 threads) took 650 us, 64 positions of a tile in each of two
 // sets in turn 812.
 #include "dense_mla.h"
@@ -807,67 +813,63 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
     }
   } else if (warp == kQkWarp) {
     // ======================= logit issuer =======================================
-    {
-      Piece x;
-      int slot = 0, tg = 0, pieces = 0;
-      bool ok = true;
-      const uint64_t qr = desc_sw64(smem_u32(smem + Y::qr));
+    Piece x;
+    int slot = 0, tg = 0, pieces = 0;
+    bool ok = true;
+    const uint64_t qr = desc_sw64(smem_u32(smem + Y::qr));
 #pragma unroll 1
-      while (ok && next_piece(a, plan, sh, walk, x)) {
-        if (!(ok = wait32(q_ready, (uint32_t)pieces & 1u))) break;
-        ++pieces;
-        slot += 2;                               // the query slice
+    while (ok && next_piece(a, plan, sh, walk, x)) {
+      if (!(ok = wait32(q_ready, (uint32_t)pieces & 1u))) break;
+      ++pieces;
+      slot += 2;                               // the query slice
 #pragma unroll 1
-        for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
-          const int stage = slot % kStages, sb = tg & 1;
-          if (!(ok = wait32(&full[stage], (uint32_t)(slot / kStages) & 1u))) break;
-          if (!(ok = wait32(&s_empty[sb], ((uint32_t)(tg >> 1) & 1u) ^ 1u))) break;
-          tc_fence_after();
-          const uint32_t t_s = tmem + TM_S + sb * kNp;
-          const uint32_t base = smem_u32(smem + Y::c + stage * kStageBytes);
-          const uint64_t d0 = desc_sw128(base);
+      for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
+        const int stage = slot % kStages, sb = tg & 1;
+        if (!(ok = wait32(&full[stage], (uint32_t)(slot / kStages) & 1u))) break;
+        if (!(ok = wait32(&s_empty[sb], ((uint32_t)(tg >> 1) & 1u) ^ 1u))) break;
+        tc_fence_after();
+        const uint32_t t_s = tmem + TM_S + sb * kNp;
+        const uint32_t base = smem_u32(smem + Y::c + stage * kStageBytes);
+        const uint64_t d0 = desc_sw128(base);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            e_mma_ta(t_s, tmem + TM_Q + i * 8,
-                            d0 + (uint64_t)(((i >> 2) * kBlockBytes + (i & 3) * 32) >> 4), IDESC_S,
-                            i > 0 ? 1u : 0u);
-          const uint64_t dr = desc_sw64(base + kRopeOff);
+        for (int i = 0; i < 16; ++i)
+          mma_bf16_tmem_a_elect(t_s, tmem + TM_Q + i * 8,
+                          d0 + (uint64_t)(((i >> 2) * kBlockBytes + (i & 3) * 32) >> 4), IDESC_S,
+                          i > 0 ? 1u : 0u);
+        const uint64_t dr = desc_sw64(base + kRopeOff);
 #pragma unroll
-          for (int i = 0; i < kRopeHalf / 16; ++i)
-            e_mma(t_s, qr + (uint64_t)((i * 32) >> 4), dr + (uint64_t)((i * 32) >> 4), IDESC_S, 1u);
-          e_commit(&s_full[sb]);
-        }
+        for (int i = 0; i < kRopeHalf / 16; ++i)
+          mma_bf16_elect(t_s, qr + (uint64_t)((i * 32) >> 4), dr + (uint64_t)((i * 32) >> 4), IDESC_S, 1u);
+        mma_commit_elect(&s_full[sb]);
       }
     }
     __syncwarp();
   } else if (warp == kPvWarp) {
     // ======================= value issuer =======================================
-    {
-      Piece x;
-      int slot = 0, tg = 0;
-      bool ok = true;
-      const uint64_t pd = desc_sw128(smem_u32(smem + Y::p));
+    Piece x;
+    int slot = 0, tg = 0;
+    bool ok = true;
+    const uint64_t pd = desc_sw128(smem_u32(smem + Y::p));
 #pragma unroll 1
-      while (ok && next_piece(a, plan, sh, walk, x)) {
-        slot += 2;                               // the query slice
+    while (ok && next_piece(a, plan, sh, walk, x)) {
+      slot += 2;                               // the query slice
 #pragma unroll 1
-        for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
-          const int stage = slot % kStages;
-          const uint64_t vd = desc_sw128_mn(smem_u32(smem + Y::c + stage * kStageBytes), kBlockBytes);
+      for (int t = x.t0; t < x.t1; ++t, ++tg, ++slot) {
+        const int stage = slot % kStages;
+        const uint64_t vd = desc_sw128_mn(smem_u32(smem + Y::c + stage * kStageBytes), kBlockBytes);
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            if (!(ok = wait32(&p_full[hf], (uint32_t)tg & 1u))) break;
-            tc_fence_after();
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!(ok = wait32(&p_full[hf], (uint32_t)tg & 1u))) break;
+          tc_fence_after();
 #pragma unroll
-            for (int i = 2 * hf; i < 2 * hf + 2; ++i)
-              e_mma(tmem + TM_O, pd + (uint64_t)((i * 32) >> 4), vd + (uint64_t)((i * 2048) >> 4),
-                       IDESC_O, (t > x.t0 || i > 0) ? 1u : 0u);
-            e_commit(&p_empty[hf]);
-          }
-          if (!ok) break;
-          e_commit(&empty[stage]);
-          if (t + 1 == x.t1) e_commit(o_done);
+          for (int i = 2 * hf; i < 2 * hf + 2; ++i)
+            mma_bf16_elect(tmem + TM_O, pd + (uint64_t)((i * 32) >> 4), vd + (uint64_t)((i * 2048) >> 4),
+                     IDESC_O, (t > x.t0 || i > 0) ? 1u : 0u);
+          mma_commit_elect(&p_empty[hf]);
         }
+        if (!ok) break;
+        mma_commit_elect(&empty[stage]);
+        if (t + 1 == x.t1) mma_commit_elect(o_done);
       }
     }
     __syncwarp();

@@ -13,19 +13,25 @@
 //                                      K^T is turned into TMEM (as an MN-major operand in shared
 //                                      memory a product of 16 tokens takes 130 cycles, not 46)
 // and the state, S <- S + expm1(g r) S + D, stays in the registers of its warps, in fp32, from a
-// sequence's first chunk to its last.  (Summed in TMEM by the products themselves its error
-// was 3e-6 of its norm: the tensor core cuts its sums off.)
+// sequence's first chunk to its last.  Its error against 64 bits is 2.5e-6 of its norm, that of the
+// split; a third part makes it 6.6e-7 and the call 17 % longer.
 //
 // Roles (28 warps), each walking the same list of (sequence, head, columns):
 //   0 products Q S and P V, 1 K^T V', 2 Q K^T, 3 copies (TMA), 4-7 P, 8-15 V' and K^T,
 //   16-23 the state, 24-27 outputs.
-// (A lane that issues products in a branch of its own takes 110 cycles for each, of 16 dims or
-// tokens; an elected lane of a converged warp less, and three warps issue side by side: a
-// chunk took 5100 cycles with one issuer.)
+//
 // A chunk's rows behind the sequence's end (other sequences') are cleared or never
 // stored.  A v that is not finite is taken out of V before P V (its weight
 // of 0 for earlier tokens would give NaN) and the column's later outputs become
 // NaN; in V' it stays, and makes the state's column NaN.
+//
+// What bounds it.  8192 tokens, 64 heads of 128 x 128: 137 us, 3.9 TB/s (59 % of the measured copy
+// rate): 64 chunks in a row on each of 128 CTAs, about 4000 cycles a chunk.  Its bytes take 2400, its 40
+// products 2000.  What is full is the way through the SM to shared and tensor memory: 2600 cycles of the
+// warps' loads and stores (logits, P, outputs, V', S, K^T), 1250 of the products' operands and 640 of
+// copies.  More warps for P or the outputs, three tiles of P, both terms of an output in one
+// accumulator took 3 to 20 % longer; one issuer of products for all four 25 %, its lane in a branch of
+// its own another 15 %; much larger loops (110 KB of code) twice the time.
 #include "kernels.h"
 #include "linear_attn.h"
 #include "tc_waits.cuh"
@@ -150,15 +156,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
       : "r"(taddr));
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void tmem_st16w(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16};\n" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -351,89 +348,84 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     }
   } else if (warp == 1) {
     // ======================= D = K^T V' ==========================================
-    {
-      const uint64_t d_vp = desc_sw128_mn(smem_u32(smem + oVp), kTile);
+    const uint64_t d_vp = desc_sw128_mn(smem_u32(smem + oVp), kTile);
 #pragma unroll 1
-      while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
+    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
 #pragma unroll 1
-        for (int c = it.c0; c < it.c1; ++c, ++t) {
-          const uint32_t ph = (uint32_t)t & 1u;
-          if (!(ok = wait32(d_empty, ph ^ 1u))) break;
+      for (int c = it.c0; c < it.c1; ++c, ++t) {
+        const uint32_t ph = (uint32_t)t & 1u;
+        if (!(ok = wait32(d_empty, ph ^ 1u))) break;
 #pragma unroll 1
-          for (int hf = 0; hf < 2; ++hf) {     // 64 tokens at a time: the next chunk's go where they were
-            if (!(ok = wait32(&v_ready[hf], ph))) break;
-            tc_fence_after();
+        for (int hf = 0; hf < 2; ++hf) {     // 64 tokens at a time: the next chunk's go where they were
+          if (!(ok = wait32(&v_ready[hf], ph))) break;
+          tc_fence_after();
 #pragma unroll 4
-            for (int x = 0; x < kSplit * 4; ++x) {
-              const int step = hf * 4 + (x & 3);
-              e_mma_ta(tmem + TM_D, tmem + TM_KT + step * 8, d_vp + (uint64_t)(((x >> 2) * kTile + step * 2048) >> 4), IDESC_O,
-                       hf + x > 0 ? 1u : 0u);
-            }
-            e_commit(&v_taken[hf]);
+          for (int x = 0; x < kSplit * 4; ++x) {
+            const int step = hf * 4 + (x & 3);
+            mma_bf16_tmem_a_elect(tmem + TM_D, tmem + TM_KT + step * 8, d_vp + (uint64_t)(((x >> 2) * kTile + step * 2048) >> 4), IDESC_O,
+                     hf + x > 0 ? 1u : 0u);
           }
-          if (!ok) break;
-          e_commit(d_full);
+          mma_commit_elect(&v_taken[hf]);
         }
+        if (!ok) break;
+        mma_commit_elect(d_full);
       }
     }
     __syncwarp();
   } else if (!LOCAL && warp == 2) {
     // ======================= Q K^T ===============================================
-    {
 #pragma unroll 1
-      while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
+    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
 #pragma unroll 1
-        for (int c = it.c0; c < it.c1; ++c, ++t) {
-          const int s = t % kQk;
-          const uint32_t ph = (uint32_t)(t / kQk) & 1u;
-          if (!(ok = wait32(&k_full[s], ph) && wait32(&q_full[s], ph) &&
-                     wait32(&o_empty[t & 1], ((uint32_t)(t >> 1) & 1u) ^ 1u)))
-            break;
-          tc_fence_after();
-          const uint64_t q = desc_sw128(smem_u32(smem + oQ + s * 2 * kTile)), k = desc_sw128(smem_u32(smem + oK + s * 2 * kTile));
+      for (int c = it.c0; c < it.c1; ++c, ++t) {
+        const int s = t % kQk;
+        const uint32_t ph = (uint32_t)(t / kQk) & 1u;
+        if (!(ok = wait32(&k_full[s], ph) && wait32(&q_full[s], ph) &&
+                   wait32(&o_empty[t & 1], ((uint32_t)(t >> 1) & 1u) ^ 1u)))
+          break;
+        tc_fence_after();
+        const uint64_t q = desc_sw128(smem_u32(smem + oQ + s * 2 * kTile)), k = desc_sw128(smem_u32(smem + oK + s * 2 * kTile));
 #pragma unroll 4
-          for (int x = 0; x < 4 * KB; ++x) {
-            const uint64_t off = (uint64_t)(((x >> 2) * kTile + (x & 3) * 32) >> 4);
-            e_mma(tmem + TM_P + (t & 1) * kC, q + off, k + off, IDESC_P, x > 0 ? 1u : 0u);
-          }
-          e_commit(&s_full[t & 1]);
-          e_commit(&k_empty[s]);
-          e_commit(&q_empty[s]);
+        for (int x = 0; x < 4 * KB; ++x) {
+          const uint64_t off = (uint64_t)(((x >> 2) * kTile + (x & 3) * 32) >> 4);
+          mma_bf16_elect(tmem + TM_P + (t & 1) * kC, q + off, k + off, IDESC_P, x > 0 ? 1u : 0u);
         }
+        mma_commit_elect(&s_full[t & 1]);
+        mma_commit_elect(&k_empty[s]);
+        mma_commit_elect(&q_empty[s]);
       }
     }
     __syncwarp();
   } else if (!LOCAL && warp == 0) {
     // ======================= Q S, P V ============================================
-    {
-      const uint64_t d_s = desc_sw128_mn(smem_u32(smem + oS), kTile);
+    const uint64_t d_s = desc_sw128_mn(smem_u32(smem + oS), kTile);
 #pragma unroll 1
-      while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
+    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
 #pragma unroll 1
-        for (int c = it.c0; c < it.c1; ++c, ++t) {
-          const int s = t % kQk;
-          const uint32_t ph = (uint32_t)t & 1u;
-          if (!(ok = wait32(st_ready, ph) && wait32(&q_full[s], (uint32_t)(t / kQk) & 1u) &&
-                     wait32(&o_empty[t & 1], ((uint32_t)(t >> 1) & 1u) ^ 1u))) break;
-          tc_fence_after();
-          const uint64_t q = desc_sw128(smem_u32(smem + oQ + s * 2 * kTile));
+      for (int c = it.c0; c < it.c1; ++c, ++t) {
+        const int s = t % kQk;
+        const uint32_t ph = (uint32_t)t & 1u;
+        if (!(ok = wait32(st_ready, ph) && wait32(&q_full[s], (uint32_t)(t / kQk) & 1u) &&
+                   wait32(&o_empty[t & 1], ((uint32_t)(t >> 1) & 1u) ^ 1u)))
+          break;
+        tc_fence_after();
+        const uint64_t q = desc_sw128(smem_u32(smem + oQ + s * 2 * kTile));
 #pragma unroll 4
-          for (int x = 0; x < 4 * KB; ++x)
-            e_mma(tmem + TM_OX + (t & 1) * kCols, q + (uint64_t)(((x >> 2) * kTile + (x & 3) * 32) >> 4), d_s + (uint64_t)((x * 2048) >> 4),
-                     IDESC_O, x > 0 ? 1u : 0u);
-          e_commit(st_taken);
-          e_commit(&q_empty[s]);
-          e_commit(&o_full[t & 1]);
-          if (!(ok = wait32(&v_clean[t % kV], (uint32_t)(t / kV) & 1u) && wait32(&p_full[t & 1], (uint32_t)(t >> 1) & 1u))) break;
-          tc_fence_after();
-          const uint64_t v = desc_sw128_mn(smem_u32(smem + oV + (t % kV) * kTile), kTile);
+        for (int x = 0; x < 4 * KB; ++x)
+          mma_bf16_elect(tmem + TM_OX + (t & 1) * kCols, q + (uint64_t)(((x >> 2) * kTile + (x & 3) * 32) >> 4), d_s + (uint64_t)((x * 2048) >> 4),
+                   IDESC_O, x > 0 ? 1u : 0u);
+        mma_commit_elect(st_taken);
+        mma_commit_elect(&q_empty[s]);
+        mma_commit_elect(&o_full[t & 1]);
+        if (!(ok = wait32(&v_clean[t % kV], (uint32_t)(t / kV) & 1u) && wait32(&p_full[t & 1], (uint32_t)(t >> 1) & 1u))) break;
+        tc_fence_after();
+        const uint64_t v = desc_sw128_mn(smem_u32(smem + oV + (t % kV) * kTile), kTile);
 #pragma unroll 4
-          for (int x = 0; x < kC / 16; ++x)
-            e_mma_ta(tmem + TM_OI + (t & 1) * kC, tmem + TM_P + (t & 1) * kC + x * 8, v + (uint64_t)((x * 2048) >> 4), IDESC_O,
-                            x > 0 ? 1u : 0u);
-          e_commit(&o_full[t & 1]);
-          e_commit(&v_empty[t % kV]);
-        }
+        for (int x = 0; x < kC / 16; ++x)
+          mma_bf16_tmem_a_elect(tmem + TM_OI + (t & 1) * kC, tmem + TM_P + (t & 1) * kC + x * 8, v + (uint64_t)((x * 2048) >> 4), IDESC_O,
+                          x > 0 ? 1u : 0u);
+        mma_commit_elect(&o_full[t & 1]);
+        mma_commit_elect(&v_empty[t % kV]);
       }
     }
     __syncwarp();
