@@ -238,6 +238,7 @@ dsi_status check_linear(const dsi_linear* a, int64_t n_tokens, int batch, Linear
   p->batch = batch;
   p->T = 0;
   p->group = a->n_heads / a->n_kv_heads;
+  p->few = 0;
   p->err = status_ptr();
   return DSI_OK;
 }

@@ -15,6 +15,7 @@ struct LinearArgs {
   int64_t n_tokens;
   int batch, T;              // T: decode, tokens of every sequence
   int group;                 // heads to a key and value head
+  int few;                   // prefill: sequences of so many tokens at most go token by token (-1: none)
   int* err;
 };
 
@@ -63,6 +64,7 @@ inline int sm_count() {
   return sms;
 }
 
+// Token by token: every sequence, or a prefill's of p.few tokens at most.
 cudaError_t launch_linear_recurrent(const LinearArgs& p, cudaStream_t st);
 size_t linear_prefill_workspace(int64_t n_tokens, int batch, int H, int dk, int dv);
 cudaError_t launch_linear_prefill(const LinearArgs& p, void* ws, cudaStream_t st);

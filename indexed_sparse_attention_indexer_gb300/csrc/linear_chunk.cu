@@ -17,8 +17,8 @@
 // split; a third part makes it 6.6e-7 and the call 17 % longer.
 //
 // Roles (28 warps), each walking the same list of (sequence, head, columns):
-//   0 products Q S and P V, 1 K^T V', 2 Q K^T, 3 copies (TMA), 4-7 P, 8-15 V' and K^T,
-//   16-23 the state, 24-27 outputs.
+//   0 products Q S and P V, 1 K^T V', 2 Q K^T, 3 copies (TMA) and the list, 4-7 P,
+//   8-15 V' and K^T, 16-23 the state, 24-27 outputs.
 //
 // A chunk's rows behind the sequence's end (other sequences') are cleared or never
 // stored.  A v that is not finite is taken out of V before P V (its weight
@@ -29,7 +29,8 @@
 // rate): 64 chunks in a row on each of 128 CTAs, about 4000 cycles a chunk.  Its bytes take 2400, its 40
 // products 2000.  What is full is the way through the SM to shared and tensor memory: 2600 cycles of the
 // warps' loads and stores (logits, P, outputs, V', S, K^T), 1250 of the products' operands and 640 of
-// copies.  More warps for P or the outputs, three tiles of P, both terms of an output in one
+// copies.  A sequence's start and end cost about a chunk more (its state, 64 KB a way for a head).
+// More warps for P or the outputs, three tiles of P, both terms of an output in one
 // accumulator took 3 to 20 % longer; one issuer of products for all four 25 %, its lane in a branch of
 // its own another 15 %; much larger loops (110 KB of code) twice the time.
 #include "kernels.h"
@@ -59,13 +60,13 @@ constexpr int kMarks = 5;                      // (the place of V t + 5 is free 
                                                // P's tile was free once the outputs of t were read)
 constexpr int oBad = oS + kTile;               // [kMarks][8] a warp's part of V holds something not finite
 constexpr int oFirst = oBad + kMarks * 8 * 4;  // [kMarks][8][32] the first such row of a column
-constexpr int oBar = oFirst + kMarks * 8 * 32;
-constexpr int kBars = 4 * kQk + 3 * kV + 4 * 2 + 4 + 4;
+constexpr int oRing = oFirst + kMarks * 8 * 32;   // pieces of work
+constexpr int oBar = oRing + 4 * 48;
+constexpr int kBars = 4 * kQk + 3 * kV + 4 * 2 + 4 + 4 + 2 * 4;
 constexpr int oSlot = oBar + kBars * 8;
-constexpr int oTable = oSlot + 8;              // next_item's
-constexpr int kSmem = oTable + 264;
+constexpr int kSmem = oSlot + 8;
 // (static variables take a kilobyte of their own, aligned like the rest)
-static_assert(kSmem <= 226 * 1024 && oBad % 16 == 0 && oBar % 8 == 0, "shared memory");
+static_assert(kSmem <= 226 * 1024 && oBad % 16 == 0 && oBar % 8 == 0 && oRing % 16 == 0, "shared memory");
 
 constexpr uint32_t TM_P = 0;                   // two tiles of 128 columns: q . k, then P in the first half
 constexpr uint32_t TM_OI = 64;                 // ... and OI in the second
@@ -87,11 +88,13 @@ struct Plan {
 // (LOCAL) leaves what each but a sequence's last one adds to a state of zeros, linear_carry turns
 // that into the state that each segment finds, and then all of them run side by side.
 struct Item {
-  int b, h, part, n;                           // n: the sequence's tokens
+  int h, part, n;                              // n: the sequence's tokens; h < 0: the list's end
   int c0, c1;                                  // chunks of the sequence
   int seg;                                     // segment's place in plan.seg, or -1
-  bool last;                                   // of the sequence
-  int64_t first;                               // the sequence's first token
+  int last;                                    // of the sequence
+  int first;                                   // the sequence's first token
+  int64_t src, dst;                            // slots, or -1
+  float g;                                     // log decay
 };
 constexpr int kMaxSplit = 64;                  // sequences of a call that is split
 constexpr int kMaxOrder = 256;                 // ... whose sequences are taken in order of length
@@ -99,39 +102,66 @@ constexpr int kMaxOrder = 256;                 // ... whose sequences are taken 
 // The CTA's next piece of work; `round` counts them.  Rounds go back and forth over the CTAs,
 // whole sequences from the longest to the shortest (table: their order), so that every CTA has about the same
 // to do.  Split: table[b] is the first segment of sequence b.
-// (not inline: the roles' code together has to stay small for the instruction cache)
 template <bool LOCAL>
-__device__ __noinline__ bool next_item(const LinearArgs& p, const Plan& plan, const uint8_t* table_s, int& round, Item& it) {
+__device__ __forceinline__ void look_up(const LinearArgs& p, const Plan& plan, const uint8_t* table_s, int& round, Item& it) {
   for (;;) {
+    it.h = -1;
     const int G = gridDim.x, at = (round & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x;
     const int64_t i64 = (int64_t)round * G + at;
-    if (i64 >= plan.items) return false;
+    if (i64 >= plan.items) return;
     const int i = (int)i64, g = i / (plan.parts * p.a.n_heads), hp = i - g * plan.parts * p.a.n_heads;
+    const int h = hp / plan.parts;
     ++round;
-    it.h = hp / plan.parts;
-    it.part = hp - it.h * plan.parts;
-    if (plan.split) {
-      const int* first = reinterpret_cast<const int*>(table_s);
-      if (g >= first[p.batch]) return false;
-      it.b = 0;
-      while (first[it.b + 1] <= g) ++it.b;
-      tokens_of(p, it.b, it.first, it.n);
-      const int s = g - first[it.b], chunks = (it.n + kC - 1) / kC;
-      it.c0 = s * plan.split;
-      it.c1 = min(chunks, it.c0 + plan.split);
-      it.last = g + 1 == first[it.b + 1];
-      it.seg = first[it.b + 1] - first[it.b] > 1 ? g : -1;
-      if (LOCAL && it.last) continue;
-      return true;
-    }
-    it.b = p.batch <= kMaxOrder ? table_s[g] : g;
-    tokens_of(p, it.b, it.first, it.n);
-    it.c0 = 0;
-    it.c1 = (it.n + kC - 1) / kC;
+    it.part = hp - h * plan.parts;
     it.seg = -1;
-    it.last = true;
-    return true;
+    it.last = 1;
+    it.c0 = 0;
+    int b = plan.split == 0 && p.batch <= kMaxOrder ? table_s[g] : g;
+    const int* first = reinterpret_cast<const int*>(table_s);
+    if (plan.split) {
+      if (g >= first[p.batch]) return;
+      for (b = 0; first[b + 1] <= g;) ++b;
+      it.last = g + 1 == first[b + 1];
+      if (LOCAL && it.last) continue;
+      it.c0 = (g - first[b]) * plan.split;
+      if (first[b + 1] - first[b] > 1) it.seg = g;
+    }
+    int64_t tok;
+    tokens_of(p, b, tok, it.n);
+    if (it.n <= p.few) {                       // and, in their order, all behind it
+      if (plan.split == 0 && p.batch <= kMaxOrder) return;
+      continue;
+    }
+    it.first = (int)tok;
+    it.c1 = (it.n + kC - 1) / kC;
+    if (plan.split) it.c1 = min(it.c1, it.c0 + plan.split);
+    it.src = in_slot(p, b);
+    it.dst = out_slot(p, b);
+    it.g = __ldg(p.a.log_decay + h);
+    it.h = h;
+    return;
   }
+}
+
+// The list passes from the warp that copies to the others through a ring in shared memory: a look-up is several
+// trips to memory, and a copy of it for each role would crowd the instruction cache.
+constexpr int kRing = 4;
+struct Ring {
+  int4 a[kRing], b[kRing], c[kRing];
+};
+__device__ __forceinline__ void publish(Ring* r, int i, const Item& it) {
+  const int s = i % kRing;
+  r->a[s] = make_int4(it.h, it.part | (it.last << 1), it.n, it.first);
+  r->b[s] = make_int4(it.c0, it.c1, it.seg, (int)it.src);
+  r->c[s] = make_int4((int)it.dst, __float_as_int(it.g), 0, 0);
+}
+__device__ __forceinline__ void peek(const Ring* r, int i, Item& it) {
+  const int s = i % kRing;
+  const int4 a = r->a[s], b = r->b[s], c = r->c[s];
+  it.h = a.x; it.part = a.y & 1; it.last = a.y >> 1; it.n = a.z; it.first = a.w;
+  it.c0 = b.x; it.c1 = b.y; it.seg = b.z; it.src = b.w;
+  it.dst = c.x;
+  it.g = __int_as_float(c.y);
 }
 
 // lam^n: 1 for n = 0, whatever lam is.
@@ -202,6 +232,29 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return r;
 }
 
+// Eight floats, a sector: one access where the address allows, else two.
+__device__ __forceinline__ void load8(const float* p, bool wide, float* f) {
+  if (wide) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                 : "l"(p) : "memory");
+  } else {
+    const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+    f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+    f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+  }
+}
+__device__ __forceinline__ void store8(float* p, bool wide, const float* f) {
+  if (wide) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),
+                 "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+}
+
 // KB: blocks of 64 dims that dk takes.  LOCAL: the first pass over segments.
 template <int KB, bool LOCAL>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -209,6 +262,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
              const __grid_constant__ CUtensorMap vmap, const __grid_constant__ LinearArgs p,
              const __grid_constant__ Plan plan) {
   __shared__ __align__(16) float pow_table[5][32];   // P's warps, from 1 on: scale lam^0 .. scale lam^31
+  __shared__ __align__(8) uint8_t table_s[264];       // look_up's
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + oBar);   // [kQk] Q landed
@@ -228,6 +282,9 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
   uint64_t* st_taken = st_ready + 1;           // Q S done
   uint64_t* d_full = st_ready + 2;             // K^T V' done
   uint64_t* d_empty = st_ready + 3;            // ... added to the state
+  uint64_t* i_full = d_empty + 1;              // [kRing] a piece of work is there
+  uint64_t* i_empty = i_full + kRing;          // [kRing] ... taken by all
+  Ring* const ring = reinterpret_cast<Ring*>(smem + oRing);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + oSlot);
   const dsi_linear& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -258,6 +315,10 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     mbar_init(st_taken, 1);
     mbar_init(d_full, 1);
     mbar_init(d_empty, 8);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&i_full[i], 1);
+      mbar_init(&i_empty[i], LOCAL ? 17 : 27);   // the warps that take pieces
+    }
     s_abort = 0;
     s_err = p.err;
     fence_barrier_init();
@@ -280,7 +341,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       n = max(1, ((n + kC - 1) / kC + plan.split - 1) / plan.split);
     }
     const int before = block_exclusive_scan(n, reinterpret_cast<int*>(smem), total);
-    if (tid <= p.batch) reinterpret_cast<int*>(smem + oTable)[tid] = before;
+    if (tid <= p.batch) reinterpret_cast<int*>(table_s)[tid] = before;
     __syncthreads();
   } else if (p.batch <= kMaxOrder) {           // the sequences, longest first
     int* len = reinterpret_cast<int*>(smem);
@@ -292,7 +353,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     if (tid < p.batch) {
       int rank = 0;
       for (int b = 0; b < p.batch; ++b) rank += len[b] > n || (len[b] == n && b < tid);
-      smem[oTable + rank] = (uint8_t)tid;
+      table_s[rank] = (uint8_t)tid;
     }
     __syncthreads();
   }
@@ -302,21 +363,36 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
   const uint32_t tmem = *tmem_slot;
   const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
   const int row = (warp & 3) * 32 + lane;      // of a chunk, or of the state
-  int round = 0;
   Item it;
-  const uint8_t* const table = smem + oTable;
+  int items = 0;                               // taken so far
   int t = 0;                                   // chunks so far
   bool ok = true;
+  // the role's next piece of work; false at the list's end
+  auto next_item = [&]() {
+    if (!(ok = wait32(&i_full[items % kRing], (uint32_t)(items / kRing) & 1u))) return false;
+    peek(ring, items, it);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&i_empty[items % kRing]);
+    ++items;
+    return it.h >= 0;
+  };
 
   if (warp == 3) {
     // ======================= copies ==============================================
     if (lane == 0) {
+      int round = 0;
 #pragma unroll 1
-      while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
+      while (ok) {
+        look_up<LOCAL>(p, plan, table_s, round, it);
+        if (!(ok = wait1(&i_empty[items % kRing], ((uint32_t)(items / kRing) & 1u) ^ 1u))) break;
+        publish(ring, items, it);
+        mbar_arrive(&i_full[items % kRing]);
+        ++items;
+        if (it.h < 0) break;
         const int hk = it.h / p.group;
 #pragma unroll 1
         for (int c = it.c0; c < it.c1; ++c, ++t) {
-          const int s = t % kQk, sv = t % kV, at = (int)it.first + c * kC;
+          const int s = t % kQk, sv = t % kV, at = it.first + c * kC;
           const uint32_t ph = ((uint32_t)(t / kQk) & 1u) ^ 1u;
           if (!(ok = wait1(&k_empty[s], ph))) break;
           mbar_arrive_expect_tx(&k_full[s], KB * kTile);
@@ -350,7 +426,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     // ======================= D = K^T V' ==========================================
     const uint64_t d_vp = desc_sw128_mn(smem_u32(smem + oVp), kTile);
 #pragma unroll 1
-    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
+    while (ok && next_item()) {
 #pragma unroll 1
       for (int c = it.c0; c < it.c1; ++c, ++t) {
         const uint32_t ph = (uint32_t)t & 1u;
@@ -375,7 +451,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
   } else if (!LOCAL && warp == 2) {
     // ======================= Q K^T ===============================================
 #pragma unroll 1
-    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
+    while (ok && next_item()) {
 #pragma unroll 1
       for (int c = it.c0; c < it.c1; ++c, ++t) {
         const int s = t % kQk;
@@ -400,7 +476,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     // ======================= Q S, P V ============================================
     const uint64_t d_s = desc_sw128_mn(smem_u32(smem + oS), kTile);
 #pragma unroll 1
-    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
+    while (ok && next_item()) {
 #pragma unroll 1
       for (int c = it.c0; c < it.c1; ++c, ++t) {
         const int s = t % kQk;
@@ -439,10 +515,10 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     float far_of[3] = {0.f, 0.f, 0.f};         // lam^(i-j31) of the blocks before the warp's own
     int h = -1;
 #pragma unroll 1
-    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
+    while (ok && next_item()) {
       if (it.h != h) {
         h = it.h;
-        const float g = __ldg(a.log_decay + h);
+        const float g = it.g;
         __syncwarp();
         pow_s[lane] = a.scale * power(g, lane);
 #pragma unroll
@@ -502,8 +578,8 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     const uint32_t k_lane = (uint32_t)(hf * 64 + ((lane >> 4) & 1) * 8 + (lane & 7));        // token whose address this lane gives
     const uint32_t k_u = (uint32_t)((quarter & 1) * 4 + ((lane >> 3) & 1));                  // ... and 8 dims
 #pragma unroll 1
-    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
-      const float g = __ldg(a.log_decay + it.h);
+    while (ok && next_item()) {
+      const float g = it.g;
       float f = 0.f;
 #pragma unroll 1
       for (int c = it.c0; c < it.c1; ++c, ++t) {
@@ -600,11 +676,12 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     // Thread = 32 columns of a row of the state; rows from dk on are zeros, and none behind the
     // last block of 64.
     const bool rows = (warp & 3) < 2 * KB, live = row < a.dk;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.state) & 31) == 0;
     const int half = (warp - 16) >> 2;
 #pragma unroll 1
-    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
-      const float g = __ldg(a.log_decay + it.h);
-      const int64_t src = in_slot(p, it.b), dst = out_slot(p, it.b);
+    while (ok && next_item()) {
+      const float g = it.g;
+      const int64_t src = it.src, dst = it.dst;
       const int cols = live ? min(32, a.dv - it.part * kCols - half * 32) : 0;   // a multiple of 8, or none
       const int64_t head = ((int64_t)it.h * a.dk + row) * a.dv + it.part * kCols + half * 32;
       const int64_t slot = (int64_t)a.n_heads * a.dk * a.dv;
@@ -616,10 +693,10 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         to = plan.seg + it.seg * slot + head;
       }
 #pragma unroll
-      for (int x = 0; x < 32; x += 4) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (from && x < cols) y = *reinterpret_cast<const float4*>(from + x);
-        s[x] = y.x; s[x + 1] = y.y; s[x + 2] = y.z; s[x + 3] = y.w;
+      for (int x = 0; x < 32; x += 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[x + i] = 0.f;
+        if (from && x < cols) load8(from + x, wide, s + x);
       }
 #pragma unroll 1
       for (int c = it.c0; c < it.c1; ++c, ++t) {
@@ -663,8 +740,8 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       }
       if (ok && to) {
 #pragma unroll
-        for (int x = 0; x < 32; x += 4)
-          if (x < cols) *reinterpret_cast<float4*>(to + x) = make_float4(s[x], s[x + 1], s[x + 2], s[x + 3]);
+        for (int x = 0; x < 32; x += 8)
+          if (x < cols) store8(to + x, wide, s + x);
       }
       __syncwarp();
     }
@@ -672,15 +749,15 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     // ======================= outputs =============================================
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.ld_out_row % 16 == 0 && a.ld_out_head % 16 == 0;
 #pragma unroll 1
-    while (ok && next_item<LOCAL>(p, plan, table, round, it)) {
-      const float since = a.scale * power(__ldg(a.log_decay + it.h), row + 1);
+    while (ok && next_item()) {
+      const float since = a.scale * power(it.g, row + 1);
       const int cols = min(kCols, a.dv - it.part * kCols);
 #pragma unroll 1
       for (int c = it.c0; c < it.c1; ++c, ++t) {
         if (!(ok = wait32(&o_full[t & 1], (uint32_t)(t >> 1) & 1u))) break;
         tc_fence_after();
         const bool live = row < it.n - c * kC;
-        bf16* to = reinterpret_cast<bf16*>(a.out) + (it.first + c * kC + row) * a.ld_out_row +
+        bf16* to = reinterpret_cast<bf16*>(a.out) + ((int64_t)it.first + c * kC + row) * a.ld_out_row +
                    (int64_t)it.h * a.ld_out_head + it.part * kCols;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {          // 16 columns at a time
@@ -828,8 +905,19 @@ size_t linear_prefill_workspace(int64_t n_tokens, int batch, int H, int dk, int 
   return split ? (size_t)segments(n_tokens, batch, split) * H * dk * dv * sizeof(float) : 256;
 }
 
-cudaError_t launch_linear_prefill(const LinearArgs& p, void* ws, cudaStream_t st) {
-  if (p.n_tokens == 0) return launch_linear_recurrent(p, st);   // (nothing but states to pass on)
+// Sequences of at most so many tokens go token by token, in a launch of their own: decoding rows of a mixed
+// batch, say.  us for 64 sequences x 32 heads of 128 x 128, so and by chunks: 1 token 47 / 116, 4 61 / 118, 8
+// 84 / 118, 16 129 / 119; one sequence 2.7 / 8.4, 8 tokens 4.1 / 8.4, 16 6.4 / 8.4.
+constexpr int kFew = 8;
+
+cudaError_t launch_linear_prefill(const LinearArgs& given, void* ws, cudaStream_t st) {
+  LinearArgs p = given;
+  p.few = -1;
+  if (p.batch > 1 || p.n_tokens <= kFew) {       // (one sequence among more rows than that is hardly as short)
+    p.few = kFew;
+    const cudaError_t e = launch_linear_recurrent(p, st);
+    if (e != cudaSuccess || p.n_tokens <= kFew) return e;
+  }
   const int sms = sm_count();
   Plan plan;
   plan.parts = (p.a.dv + kCols - 1) / kCols;

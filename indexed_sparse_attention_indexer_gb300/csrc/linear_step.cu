@@ -39,6 +39,7 @@ linear_recurrent(const __grid_constant__ LinearArgs p, int parts) {
   int64_t first;
   int n;
   tokens_of(p, b, first, n);
+  if (p.starts && n > p.few) return;             // the chunked kernel's
   const int64_t src = in_slot(p, b), dst = out_slot(p, b);
   const int64_t head = (int64_t)h * a.dk * a.dv, slot = (int64_t)a.n_heads * a.dk * a.dv;
 

@@ -162,6 +162,8 @@ PREFILLS = [
     dict(lens=[200, 31], H=2, dk=64, dv=64), dict(lens=[300], H=2, dk=96, dv=80), dict(lens=[257], H=2, dk=8, dv=8),
     dict(lens=[140], H=3, dk=72, dv=128), dict(lens=[140], H=3, dk=128, dv=24), dict(lens=[390], H=4, Hk=1, dk=40, dv=104),
     dict(lens=[150, 150], H=5, heads_first=True), dict(lens=[130] * 40, H=8), dict(lens=[1500], H=1),
+    dict(lens=[7, 8, 9, 0, 10, 200, 1], H=3), dict(lens=[1] * 30 + [700], H=4, Hk=2, fork=True), dict(lens=[8], H=2), dict(lens=[9], H=2),
+    dict(lens=[3, 9, 8, 2, 1, 0] * 50, H=1, dk=96), dict(lens=[5, 4000, 2], H=1, dv=40),
     dict(lens=[7 * i % 41 for i in range(300)], H=2, dk=64, dv=64), dict(lens=[i % 3 * 100 for i in range(256)], H=1, dk=32, dv=16),
 ]
 
