@@ -25,11 +25,12 @@
 // of 0 for earlier tokens would give NaN) and the column's later outputs become
 // NaN; in V' it stays, and makes the state's column NaN.
 //
-// What bounds it.  8192 tokens, 64 heads of 128 x 128: 137 us, 3.9 TB/s (59 % of the measured copy
+// What bounds it.  8192 tokens, 64 heads of 128 x 128: 139 us, 3.9 TB/s (58 % of the measured copy
 // rate): 64 chunks in a row on each of 128 CTAs, about 4000 cycles a chunk.  Its bytes take 2400, its 40
 // products 2000.  What is full is the way through the SM to shared and tensor memory: 2600 cycles of the
 // warps' loads and stores (logits, P, outputs, V', S, K^T), 1250 of the products' operands and 640 of
-// copies.  A sequence's start and end cost about a chunk more (its state, 64 KB a way for a head).
+// copies.  A sequence's start and end cost 2.5 to 3 us on top, a chunk 2.0 (76 heads: one sequence of 32 chunks
+// 73 us, four of 8 83, 32 of one 157).
 // More warps for P or the outputs, three tiles of P, both terms of an output in one
 // accumulator took 3 to 20 % longer; one issuer of products for all four 25 %, its lane in a branch of
 // its own another 15 %; much larger loops (110 KB of code) twice the time.
@@ -907,7 +908,8 @@ size_t linear_prefill_workspace(int64_t n_tokens, int batch, int H, int dk, int 
 
 // Sequences of at most so many tokens go token by token, in a launch of their own: decoding rows of a mixed
 // batch, say.  us for 64 sequences x 32 heads of 128 x 128, so and by chunks: 1 token 47 / 116, 4 61 / 118, 8
-// 84 / 118, 16 129 / 119; one sequence 2.7 / 8.4, 8 tokens 4.1 / 8.4, 16 6.4 / 8.4.
+// 84 / 118, 16 129 / 119; one sequence 2.7 / 8.4, 8 tokens 4.1 / 8.4, 16 6.4 / 8.4.  The launch costs 2 to 3 %
+// where no sequence is short: 4 x 2048 tokens 77 -> 78.5 us, 64 x 200 179 -> 184.
 constexpr int kFew = 8;
 
 cudaError_t launch_linear_prefill(const LinearArgs& given, void* ws, cudaStream_t st) {

@@ -1,5 +1,5 @@
 // Linear attention with a decay for each head, token by token (the form of a
-// decode step): S = exp(g) S + k v^T, out = scale S^T q.
+// decode step, and of a prefill's sequences of a few tokens): S = exp(g) S + k v^T, out = scale S^T q.
 //
 // A CTA takes one head of one sequence, or some columns of its state: 4 COLS of
 // the dv columns, all dk rows, held in registers (a float4 of columns for every
@@ -125,6 +125,14 @@ linear_recurrent(const __grid_constant__ LinearArgs p, int parts) {
 template <int COLS, int DIMS>
 cudaError_t launch_for(const LinearArgs& p, cudaStream_t st) {
   const int parts = (p.a.dv + 4 * COLS - 1) / (4 * COLS);
+  // Where registers keep it to two CTAs an SM (41 KB of shared memory) the rest is to be L1, through which the states
+  // come: behind a kernel of 226 KB it would find that kernel's split.  256 sequences x 32 heads of 128 x 128: a
+  // prefill of one token each 212 -> 178 us, a step behind a prompt's chunk 171 -> 168, behind itself 167 as before.
+  // The narrower ones hold more CTAs, which a quarter has no room for: 11.7 -> 13.1 us.
+  if (DIMS * COLS == 128 * 32) {
+    const cudaError_t c = cudaFuncSetAttribute(linear_recurrent<COLS, DIMS>, cudaFuncAttributePreferredSharedMemoryCarveout, 25);
+    if (c != cudaSuccess) return c;
+  }
   const cudaError_t e = launch_overlapped(linear_recurrent<COLS, DIMS>, dim3((unsigned)(p.batch * p.a.n_heads * parts)),
                                           dim3(kThreads), 0, st, p, parts);
   note_launch();
