@@ -27,7 +27,7 @@
 //
 // What bounds it.  8192 tokens, 64 heads of 128 x 128: 139 us, 3.9 TB/s (58 % of the measured copy
 // rate): 64 chunks in a row on each of 128 CTAs, about 4000 cycles a chunk.  Its bytes take 2400, its 40
-// products 2000.  What is full is the way through the SM to shared and tensor memory: 2600 cycles of the
+// products 1550 of the tensor pipe (counted over 32 chunks, 33 % of the time).  What is full is the way through the SM to shared and tensor memory: 2600 cycles of the
 // warps' loads and stores (logits, P, outputs, V', S, K^T), 1250 of the products' operands and 640 of
 // copies.  A sequence's start and end cost 2.5 to 3 us on top, a chunk 2.0 (76 heads: one sequence of 32 chunks
 // 73 us, four of 8 83, 32 of one 157).
