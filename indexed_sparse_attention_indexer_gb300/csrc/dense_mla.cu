@@ -64,6 +64,7 @@
 #include <atomic>
 
 #include "kernels.h"
+#include "prefix_parts.h"
 #include "tc_common.cuh"
 #include "tc_waits.cuh"
 #include "tma_host.h"
@@ -1305,7 +1306,8 @@ prefix_expand(CacheView c, const float* scale, bf16* to, int* err) {
 // Joins a row's parts over the prefix and over its sequence's own rows, each of one piece or
 // more: a warp takes 128 dims of a head.  Bound by the parts' 2 KB each, which mostly are in L2.
 __global__ void __launch_bounds__(kJoinThreads)
-prefix_mla_join(DenseArgs a, Plan plan, Workspace ws, int prefix_tokens, int prefix_groups, int own_slot0) {
+prefix_mla_join(DenseArgs a, Plan plan, Workspace ws, int prefix_tokens, int prefix_groups, int prefix_clusters,
+                int own_clusters, int own_slot0) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int vectors = a.rows * a.H;
   grid_dep_wait();     // the parts come from the kernel launched just before
@@ -1313,17 +1315,14 @@ prefix_mla_join(DenseArgs a, Plan plan, Workspace ws, int prefix_tokens, int pre
   for (int at = blockIdx.x; at < vectors; at += gridDim.x) {
     const int row = at / a.H, h = at - row * a.H, b = row / a.T, t = row - b * a.T;
     const int gp = row / prefix_tokens, go = prefix_groups + b * plan.per_seq + t / plan.tokens;
-    const int mp = (row - gp * prefix_tokens) * a.H + h, mo = t % plan.tokens * a.H + h;
+    const int of_group[2] = {(row - gp * prefix_tokens) * a.H + h, t % plan.tokens * a.H + h};
     const int2 sp = ws.spans[gp], so = ws.spans[go];
-    const int np = sp.y - sp.x + 1, n = np + so.y - so.x + 1;
-    // piece j: where it is (an index of the pieces' slots, or of the rows' places, below 0)
-    auto place = [&](int j) {
-      const bool own = j >= np;
-      const int2 s = own ? so : sp;
-      if (own) j -= np;
-      if (s.x == s.y) return -1 - (own ? (int64_t)vectors + at : (int64_t)at);
-      return (int64_t)((own ? own_slot0 : 0) + 2 * (s.x + j) + (j == 0 ? 1 : 0)) * kM + (own ? mo : mp);
-    };
+    // (a wait that ran out leaves spans unwritten: what they hold then is no index)
+    RowParts parts;
+    const bool whole = parts.set(0, sp.x, sp.y, prefix_clusters);
+    if (!parts.set(1, so.x, so.y, own_clusters) || !whole) report(a.err, kErrTimeout);
+    const int n = parts.count();
+    auto place = [&](int j) { return parts.place(j, of_group, at, vectors, own_slot0, kM); };
     auto stats = [&](int64_t p) { return p < 0 ? ws.whole_ml[-1 - p] : ws.ml[p]; };
     float top = -INFINITY;
     for (int j = lane; j < n; j += 32) top = fmaxf(top, stats(place(j)).x);
@@ -1514,6 +1513,8 @@ cudaError_t launch_prefix_mla(const DenseArgs& a, const CacheView& prefix, const
   plan.live = (sh.tokens * a.H + 31) / 32;
   // at most a cluster a tile
   auto clusters_for = [&](int64_t tiles) { return (int)(tiles < slots ? tiles : slots); };
+  const int prefix_clusters = clusters_for(expand ? prefix_tiles : prefix_tiles + own_tiles);
+  const int own_clusters = expand ? clusters_for(own_tiles) : prefix_clusters;
   cudaError_t e;
   if (expand) {
     const int64_t blocks = (prefix.s_max + 7) / 8, wave = 16 * (int64_t)slots;
@@ -1522,9 +1523,8 @@ cudaError_t launch_prefix_mla(const DenseArgs& a, const CacheView& prefix, const
     note_launch();
     if (e != cudaSuccess) return e;
     plan.groups = sh.groups;
-    int clusters = clusters_for(prefix_tiles);
-    plan.split = clusters > 1;
-    e = launch<false, true>(sh.lmap, sh.rmap, qmap, a, plan, ws, sh.box, sh, clusters, st);
+    plan.split = prefix_clusters > 1;
+    e = launch<false, true>(sh.lmap, sh.rmap, qmap, a, plan, ws, sh.box, sh, prefix_clusters, st);
     if (e != cudaSuccess) return e;
     Prefix<true> none = sh;
     none.groups = 0;
@@ -1535,20 +1535,19 @@ cudaError_t launch_prefix_mla(const DenseArgs& a, const CacheView& prefix, const
     Plan own_plan = plan;
     own_plan.groups = own_groups;
     own_plan.live = (plan.tokens * a.H + 31) / 32;
-    clusters = clusters_for(own_tiles);
-    own_plan.split = clusters > 1;
-    e = launch<true, true>(map, rmap, qmap, a, own_plan, own, box, none, clusters, st);
+    own_plan.split = own_clusters > 1;
+    e = launch<true, true>(map, rmap, qmap, a, own_plan, own, box, none, own_clusters, st);
   } else {
     plan.groups = sh.groups + own_groups;        // <= 2 * rows
-    const int clusters = clusters_for(prefix_tiles + own_tiles);
-    plan.split = clusters > 1;
-    e = f8 ? launch<true, true>(map, rmap, qmap, a, plan, ws, box, sh, clusters, st)
-           : launch<false, true>(map, rmap, qmap, a, plan, ws, box, sh, clusters, st);
+    plan.split = prefix_clusters > 1;
+    e = f8 ? launch<true, true>(map, rmap, qmap, a, plan, ws, box, sh, prefix_clusters, st)
+           : launch<false, true>(map, rmap, qmap, a, plan, ws, box, sh, prefix_clusters, st);
   }
   if (e != cudaSuccess) return e;
   const int64_t wave = 32 * (int64_t)slots;
   e = launch_overlapped(prefix_mla_join, dim3((unsigned)((int64_t)vectors < wave ? (int64_t)vectors : wave)),
-                        dim3(kJoinThreads), 0, st, a, plan, ws, sh.tokens, sh.groups, expand ? 2 * slots : 0);
+                        dim3(kJoinThreads), 0, st, a, plan, ws, sh.tokens, sh.groups, prefix_clusters, own_clusters,
+                        expand ? 2 * slots : 0);
   note_launch();
   return e;
 }
