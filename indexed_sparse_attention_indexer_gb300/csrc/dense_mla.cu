@@ -1315,14 +1315,13 @@ prefix_mla_join(DenseArgs a, Plan plan, Workspace ws, int prefix_tokens, int pre
   for (int at = blockIdx.x; at < vectors; at += gridDim.x) {
     const int row = at / a.H, h = at - row * a.H, b = row / a.T, t = row - b * a.T;
     const int gp = row / prefix_tokens, go = prefix_groups + b * plan.per_seq + t / plan.tokens;
-    const int of_group[2] = {(row - gp * prefix_tokens) * a.H + h, t % plan.tokens * a.H + h};
-    const int2 sp = ws.spans[gp], so = ws.spans[go];
+    const int mp = (row - gp * prefix_tokens) * a.H + h, mo = t % plan.tokens * a.H + h;
+    const int2 x = ws.spans[gp], y = ws.spans[go];
     // (a wait that ran out leaves spans unwritten: what they hold then is no index)
-    RowParts parts;
-    const bool whole = parts.set(0, sp.x, sp.y, prefix_clusters);
-    if (!parts.set(1, so.x, so.y, own_clusters) || !whole) report(a.err, kErrTimeout);
-    const int n = parts.count();
-    auto place = [&](int j) { return parts.place(j, of_group, at, vectors, own_slot0, kM); };
+    const Span sp(x.x, x.y, prefix_clusters), so(y.x, y.y, own_clusters);
+    if (sp.pieces == 0 || so.pieces == 0) report(a.err, kErrTimeout);
+    const int n = sp.pieces + so.pieces;
+    auto place = [&](int j) { return part_place(sp, so, j, mp, mo, at, vectors, own_slot0, kM); };
     auto stats = [&](int64_t p) { return p < 0 ? ws.whole_ml[-1 - p] : ws.ml[p]; };
     float top = -INFINITY;
     for (int j = lane; j < n; j += 32) top = fmaxf(top, stats(place(j)).x);

@@ -18,11 +18,11 @@ PROGRAM = r"""
 int main() {
   int x0, y0, x1, y1, c0, c1, r0, r1, at, vectors, slot0;
   while (scanf("%d %d %d %d %d %d %d %d %d %d %d", &x0, &y0, &x1, &y1, &c0, &c1, &r0, &r1, &at, &vectors, &slot0) == 11) {
-    dsi::RowParts p;
-    const bool a = p.set(0, x0, y0, c0), b = p.set(1, x1, y1, c1);
-    const int row[2] = {r0, r1};
-    printf("%d %d", a && b, p.count());
-    for (int j = 0; j < p.count() && j < 600; ++j) printf(" %lld", (long long)p.place(j, row, at, vectors, slot0, 128));
+    const dsi::Span a(x0, y0, c0), b(x1, y1, c1);
+    const int n = a.pieces + b.pieces;
+    printf("%d %d", a.pieces > 0 && b.pieces > 0, n);
+    for (int j = 0; j < n && j < 600; ++j)
+      printf(" %lld", (long long)dsi::part_place(a, b, j, r0, r1, at, vectors, slot0, 128));
     printf("\n");
   }
 }
