@@ -874,14 +874,26 @@ namespace {
 
 // Chunks of a segment, or 0 where sequences stay whole.  Times in chunks of one CTA: whole
 // sequences take their length; a split takes its share of all chunks 1.6 times (the first
-// pass reads K and V again) and three launches, about kSplitCost.
+// pass reads K and V again) and three launches, about kSplitCost.  The host knows no length but the mean.
+// A segment is then no shorter than sequences of that length allow in one round of CTAs: with the bare
+// share a few segments more than there are CTAs doubled the call (4 x 4096 tokens of 8 heads 114 us, so 74).
+// us of heads of 128 x 128, whole and split (those that the rule takes marked *):
+//   tokens x heads  1024 x 1 *22 / 20, 1536 x 1 30 / *21, 4096 x 1 67 / *22, 1536 x 8 30 / *24, 8192 x 8 130 / *45,
+//     1024 x 16 *23 / 25, 1536 x 16 *30 / 28, 2048 x 16 38 / *31, 16384 x 16 260 / *128, 2048 x 32 *39 / 45,
+//     3584 x 32 64 / *66, 8192 x 32 135 / *127, 4096 x 45 *71 / 78, 8192 x 60 *136 / 149
+//   sequences       4 x 1024 x 2 *24 / 24, 4 x 2048 x 2 39 / *28, 4 x 2048 x 8 *40 / 47, 4 x 4096 x 8 73 / *74,
+//     4 x 8192 x 8 136 / *127, 8 x 8192 x 2 135 / *74, 8 x 4096 x 8 *75 / 84
+//   mixed           16000 and 3 of 4000, 8 heads 255 / *205; 6000, 5000, 4000, 3000 102 / *81; where the mean
+//     misleads: 8192 and 7 of 40 *134 / 54
 constexpr int kSplitCost = 8;
 int segment_chunks(int64_t n_tokens, int batch, int H, int dv, int sms) {
   const int64_t chunks = (n_tokens + kC - 1) / kC, columns = (int64_t)H * ((dv + kCols - 1) / kCols);
   if (batch > kMaxSplit || batch * columns >= sms) return 0;
   const int64_t share = ((chunks + batch - 1) * columns + sms - 1) / sms;
   if (10 * (chunks / batch) <= 16 * share + 10 * kSplitCost) return 0;
-  return (int)(share < 2 ? 2 : share);
+  const int64_t mean = (chunks + batch - 1) / batch, pieces = sms / (batch * columns), even = (mean + pieces - 1) / pieces;
+  const int64_t n = share > even ? share : even;
+  return (int)(n < 2 ? 2 : n);
 }
 // At most so many segments (a sequence has one more than it has whole ones).
 int64_t segments(int64_t n_tokens, int batch, int split) {
