@@ -632,6 +632,9 @@ dsi_status dsi_linear_prefill(const dsi_linear* a, int64_t n_tokens, const int32
   const dsi_status s = check_linear(a, n_tokens, batch, &p);
   if (s != DSI_OK) return s;
   if (!seq_starts || !aligned(seq_starts, 4)) return DSI_ERR_INVALID_ARG;
+  // (the copies' maps take strides below 2^40 bytes)
+  for (const int64_t x : {a->ld_q_row, a->ld_q_head, a->ld_k_row, a->ld_k_head, a->ld_v_row, a->ld_v_head})
+    if (n_tokens > 0 && x >= (1ll << 39)) return DSI_ERR_UNSUPPORTED;
   if (workspace) {
     if (!aligned(workspace, 256)) return DSI_ERR_INVALID_ARG;
     if (workspace_bytes < dsi_linear_workspace_size(n_tokens, batch, a->n_heads, a->dk, a->dv))

@@ -927,6 +927,13 @@ constexpr int kFew = 8;
 cudaError_t launch_linear_prefill(const LinearArgs& given, void* ws, cudaStream_t st) {
   LinearArgs p = given;
   p.few = -1;
+  // (whatever can be refused is refused before the first launch)
+  CUtensorMap qmap, kmap, vmap;
+  if (p.n_tokens > kFew &&
+      (!map_heads(&qmap, p.a.q, p.n_tokens, p.a.n_heads, p.a.dk, p.a.ld_q_row, p.a.ld_q_head) ||
+       !map_heads(&kmap, p.a.k, p.n_tokens, p.a.n_kv_heads, p.a.dk, p.a.ld_k_row, p.a.ld_k_head) ||
+       !map_heads(&vmap, p.a.v, p.n_tokens, p.a.n_kv_heads, p.a.dv, p.a.ld_v_row, p.a.ld_v_head)))
+    return cudaErrorInvalidValue;
   if (p.batch > 1 || p.n_tokens <= kFew) {       // (one sequence among more rows than that is hardly as short)
     p.few = kFew;
     const cudaError_t e = launch_linear_recurrent(p, st);
@@ -938,11 +945,6 @@ cudaError_t launch_linear_prefill(const LinearArgs& given, void* ws, cudaStream_
   plan.split = ws ? segment_chunks(p.n_tokens, p.batch, p.a.n_heads, p.a.dv, sms) : 0;
   plan.items = (int)((plan.split ? segments(p.n_tokens, p.batch, plan.split) : p.batch) * p.a.n_heads * plan.parts);
   plan.seg = static_cast<float*>(ws);
-  CUtensorMap qmap, kmap, vmap;
-  if (!map_heads(&qmap, p.a.q, p.n_tokens, p.a.n_heads, p.a.dk, p.a.ld_q_row, p.a.ld_q_head) ||
-      !map_heads(&kmap, p.a.k, p.n_tokens, p.a.n_kv_heads, p.a.dk, p.a.ld_k_row, p.a.ld_k_head) ||
-      !map_heads(&vmap, p.a.v, p.n_tokens, p.a.n_kv_heads, p.a.dv, p.a.ld_v_row, p.a.ld_v_head))
-    return cudaErrorInvalidValue;
   const bool wide = p.a.dk > 64;
   cudaError_t e;
   if (plan.split) {
