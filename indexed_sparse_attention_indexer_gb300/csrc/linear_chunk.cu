@@ -89,7 +89,7 @@ struct Plan {
 // (LOCAL) leaves what each but a sequence's last one adds to a state of zeros, linear_carry turns
 // that into the state that each segment finds, and then all of them run side by side.
 struct Item {
-  int h, part, n;                              // n: the sequence's tokens; h < 0: the list's end
+  int h, part, n;                              // n: the sequence's tokens; h -1: the list's end
   int c0, c1;                                  // chunks of the sequence
   int seg;                                     // segment's place in plan.seg, or -1
   int last;                                    // of the sequence
@@ -99,13 +99,45 @@ struct Item {
 };
 constexpr int kMaxSplit = 64;                  // sequences of a call that is split
 constexpr int kMaxOrder = 256;                 // ... whose sequences are taken in order of length
+constexpr int kBits = 2048;                    // more: a bit for every so many sequences, whether one is long
+
+// Sequences to a bit, as a power of two.
+__device__ __forceinline__ int bit_shift(const LinearArgs& p) { return max(0, 21 - __clz(p.batch - 1)); }
+
+// First sequence from g on of more than p.few tokens, or p.batch.  (Batches of thousands of decoding rows
+// are walked by the bit, a block that has one eight sequences at a time.)
+__device__ __forceinline__ int next_long(const LinearArgs& p, const uint32_t* bits, int g) {
+  const int shift = bit_shift(p);
+  while (g < p.batch) {
+    int w = g >> shift >> 5;
+    uint32_t word = bits[w] & (0xffffffffu << ((g >> shift) & 31));
+    while (word == 0u && ++w < kBits / 32) word = bits[w];
+    if (word == 0u) return p.batch;
+    const int block = w * 32 + __ffs(word) - 1;
+    g = max(g, block << shift);
+    if (shift == 0) return g;
+    for (const int end = min(p.batch, (block + 1) << shift); g < end; g += 8) {
+      int start[9], at = 8;
+#pragma unroll
+      for (int i = 0; i < 9; ++i) start[i] = held_start(p, min(end, g + i));
+#pragma unroll
+      for (int i = 7; i >= 0; --i)
+        if (start[i + 1] - start[i] > p.few) at = i;
+      if (at < 8) return g + at;
+    }
+    g = (block + 1) << shift;
+  }
+  return p.batch;
+}
 
 // The CTA's next piece of work; `round` counts them.  Rounds go back and forth over the CTAs,
-// whole sequences from the longest to the shortest (table: their order), so that every CTA has about the same
-// to do.  Split: table[b] is the first segment of sequence b.
+// whole sequences from the longest to the shortest (table: their order).  Split: table[b] is the
+// first segment of sequence b.  More than kMaxOrder sequences are taken as they come, the short ones left
+// out by the bits in the table.  A search that takes long gives kNothingYet: no wait runs out over it.
+constexpr int kNothingYet = -2, kSteps = 1024;
 template <bool LOCAL>
 __device__ __forceinline__ void look_up(const LinearArgs& p, const Plan& plan, const uint8_t* table_s, int& round, Item& it) {
-  for (;;) {
+  for (int step = 0;; ++step) {
     it.h = -1;
     const int G = gridDim.x, at = (round & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x;
     const int64_t i64 = (int64_t)round * G + at;
@@ -126,6 +158,19 @@ __device__ __forceinline__ void look_up(const LinearArgs& p, const Plan& plan, c
       if (LOCAL && it.last) continue;
       it.c0 = (g - first[b]) * plan.split;
       if (first[b + 1] - first[b] > 1) it.seg = g;
+    }
+    if (!LOCAL && p.batch > kMaxOrder) {
+      const int next = next_long(p, reinterpret_cast<const uint32_t*>(table_s), b);
+      if (next == p.batch) return;
+      if (next > b) {                          // on to the round that it begins in
+        const unsigned lo = (unsigned)(next * plan.parts * p.a.n_heads), r0 = lo / (unsigned)G;
+        round = max(round, (int)r0);
+        // (its first pieces may be this round's behind the CTA's)
+        if (round == (int)r0 && r0 * G + ((r0 & 1) ? G - 1 - blockIdx.x : blockIdx.x) < lo) ++round;
+        if (step < kSteps) continue;
+        it.h = kNothingYet;
+        return;
+      }
     }
     int64_t tok;
     tokens_of(p, b, tok, it.n);
@@ -357,6 +402,25 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       table_s[rank] = (uint8_t)tid;
     }
     __syncthreads();
+  } else {                                     // which of them are long
+    uint32_t* bits = reinterpret_cast<uint32_t*>(table_s);
+    const int shift = bit_shift(p);
+    if (tid < kBits / 32) bits[tid] = 0u;
+    __syncthreads();
+    for (int b0 = tid; b0 < p.batch; b0 += 4 * kThreads) {
+      int n[4] = {};
+      int64_t first;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (b0 + i * kThreads < p.batch) tokens_of(p, b0 + i * kThreads, first, n[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = (b0 + i * kThreads) >> shift;
+        if (n[i] > p.few && !(reinterpret_cast<volatile uint32_t*>(bits)[at >> 5] >> (at & 31) & 1u))
+          atomicOr(bits + (at >> 5), 1u << (at & 31));
+      }
+    }
+    __syncthreads();
   }
   fence_proxy_async_smem();                    // copies land where the lengths were
   __syncthreads();
@@ -370,11 +434,13 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
   bool ok = true;
   // the role's next piece of work; false at the list's end
   auto next_item = [&]() {
-    if (!(ok = wait32(&i_full[items % kRing], (uint32_t)(items / kRing) & 1u))) return false;
-    peek(ring, items, it);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&i_empty[items % kRing]);
-    ++items;
+    do {
+      if (!(ok = wait32(&i_full[items % kRing], (uint32_t)(items / kRing) & 1u))) return false;
+      peek(ring, items, it);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&i_empty[items % kRing]);
+      ++items;
+    } while (it.h == kNothingYet);
     return it.h >= 0;
   };
 
@@ -389,6 +455,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         publish(ring, items, it);
         mbar_arrive(&i_full[items % kRing]);
         ++items;
+        if (it.h == kNothingYet) continue;
         if (it.h < 0) break;
         const int hk = it.h / p.group;
 #pragma unroll 1
