@@ -577,9 +577,11 @@ dsi_status dsi_norm_rope(const dsi_heads* queries, const dsi_heads* keys, int64_
  * Prefill: prompts of any length laid end to end; sequence b has the tokens
  * seq_starts[b] .. seq_starts[b + 1] - 1.  Rows before seq_starts[0] and behind
  * seq_starts[batch] are neither read nor written.  The chunked form: 128 tokens meet
- * each other and the state by matrix products (sequences of up to 8 tokens, decoding rows
- * in a batch of prompts, go as in decode).  Decode: tokens_per_seq (T) tokens of
- * every sequence, rows T to a sequence, in order.
+ * each other and the state by matrix products (sequences of up to 8 tokens go as in decode,
+ * where the call has several sequences, decoding rows in a batch of prompts say, or no more than 8
+ * rows).  Decode: tokens_per_seq (T) tokens of every sequence, rows T to a sequence, in order.
+ * The state left is the one behind the last of them: where tokens of a step may be refused
+ * later, keep the slot that it starts from and leave the step's state in another.
  *
  * States live in slots.  Sequence b starts from slot in_slots[b] (negative: from
  * zeros) and leaves its state in slot out_slots[b] (negative: nowhere); in_slots
