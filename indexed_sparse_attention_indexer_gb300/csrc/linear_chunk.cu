@@ -82,6 +82,7 @@ struct Plan {
   int parts;                                   // 64-column parts of dv
   int items;                                   // (sequence, head, part); with a split an upper bound
   int split;                                   // chunks of a segment, or 0: sequences stay whole
+  int segments;                                // that there is room for (starts that go back may ask for more: whole, too)
   float* seg;                                  // split: [segments][heads][dk][dv] states
 };
 
@@ -97,6 +98,14 @@ struct Item {
   int64_t src, dst;                            // slots, or -1
   float g;                                     // log decay
 };
+// Segments of sequence b where the call is split.
+__device__ __forceinline__ int segments_of(const LinearArgs& p, const Plan& plan, int b) {
+  int64_t first;
+  int n;
+  tokens_of(p, b, first, n);
+  return max(1, ((n + kC - 1) / kC + plan.split - 1) / plan.split);
+}
+
 constexpr int kMaxSplit = 64;                  // sequences of a call that is split
 constexpr int kMaxOrder = 256;                 // ... whose sequences are taken in order of length
 constexpr int kBits = 2048;                    // more: a bit for every so many sequences, whether one is long
@@ -180,7 +189,7 @@ __device__ __forceinline__ void look_up(const LinearArgs& p, const Plan& plan, c
     }
     it.first = (int)tok;
     it.c1 = (it.n + kC - 1) / kC;
-    if (plan.split) it.c1 = min(it.c1, it.c0 + plan.split);
+    if (it.seg >= 0) it.c1 = min(it.c1, it.c0 + plan.split);
     it.src = in_slot(p, b);
     it.dst = out_slot(p, b);
     it.g = __ldg(p.a.log_decay + h);
@@ -380,14 +389,10 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
   __syncthreads();
   tc_fence_after();
   if (plan.split) {                            // the sequences' first segments
-    int n = 0, total;
-    if (tid < p.batch) {
-      int64_t first;
-      tokens_of(p, tid, first, n);
-      n = max(1, ((n + kC - 1) / kC + plan.split - 1) / plan.split);
-    }
+    int total;
+    const int n = tid < p.batch ? segments_of(p, plan, tid) : 0;
     const int before = block_exclusive_scan(n, reinterpret_cast<int*>(smem), total);
-    if (tid <= p.batch) reinterpret_cast<int*>(table_s)[tid] = before;
+    if (tid <= p.batch) reinterpret_cast<int*>(table_s)[tid] = total > plan.segments ? tid : before;
     __syncthreads();
   } else if (p.batch <= kMaxOrder) {           // the sequences, longest first
     int* len = reinterpret_cast<int*>(smem);
@@ -882,26 +887,22 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
 constexpr int kCarryThreads = 256;
 __global__ void __launch_bounds__(kCarryThreads)
 linear_carry(const __grid_constant__ LinearArgs p, const __grid_constant__ Plan plan) {
-  __shared__ int first_s;
+  __shared__ int first_s, total_s;
   const int per = p.a.dk * p.a.dv / 4, heads = p.a.n_heads;     // float4s of a head's state
   const int blocks = (heads * per + kCarryThreads - 1) / kCarryThreads;
   const int b = blockIdx.x / blocks, e = (blockIdx.x - b * blocks) * kCarryThreads + threadIdx.x;
   grid_dep_wait();
   grid_dep_launch();
-  if (threadIdx.x == 0) first_s = 0;
+  if (threadIdx.x == 0) first_s = total_s = 0;
   __syncthreads();
-  int64_t tok;
-  int n;
-  for (int i = threadIdx.x; i < b; i += kCarryThreads) {        // segments of the sequences before
-    tokens_of(p, i, tok, n);
-    atomicAdd(&first_s, max(1, ((n + kC - 1) / kC + plan.split - 1) / plan.split));
+  for (int i = threadIdx.x; i < p.batch; i += kCarryThreads) {
+    const int m = segments_of(p, plan, i);
+    if (i < b) atomicAdd(&first_s, m);         // those of the sequences before
+    atomicAdd(&total_s, m);
   }
   __syncthreads();
-  tokens_of(p, b, tok, n);
-  // (starts that go back could ask for more segments than there is room for)
-  const int segs = min(max(1, ((n + kC - 1) / kC + plan.split - 1) / plan.split),
-                       plan.items / (heads * plan.parts) - first_s);
-  if (segs <= 1 || e >= heads * per) return;
+  const int segs = segments_of(p, plan, b);
+  if (segs <= 1 || total_s > plan.segments || e >= heads * per) return;
   const int64_t slot = (int64_t)heads * per, src = in_slot(p, b);
   float4* at = reinterpret_cast<float4*>(plan.seg) + first_s * slot + e;
   const float d1 = expm1f(__ldg(p.a.log_decay + e / per) * (float)(plan.split * kC));
@@ -1010,7 +1011,8 @@ cudaError_t launch_linear_prefill(const LinearArgs& given, void* ws, cudaStream_
   Plan plan;
   plan.parts = (p.a.dv + kCols - 1) / kCols;
   plan.split = ws ? segment_chunks(p.n_tokens, p.batch, p.a.n_heads, p.a.dv, sms) : 0;
-  plan.items = (int)((plan.split ? segments(p.n_tokens, p.batch, plan.split) : p.batch) * p.a.n_heads * plan.parts);
+  plan.segments = plan.split ? (int)segments(p.n_tokens, p.batch, plan.split) : 0;
+  plan.items = (plan.split ? plan.segments : p.batch) * p.a.n_heads * plan.parts;
   plan.seg = static_cast<float*>(ws);
   const bool wide = p.a.dk > 64;
   cudaError_t e;

@@ -1,12 +1,11 @@
 """Linear attention prefills at the edges of what their description promises: one short sequence in a
 longer buffer, starts that go back in a call that is cut into segments."""
-import math
-
 import pytest
 import torch
 
 from indexed_sparse_attention_indexer_gb300 import binding
 from tests.test_gpu_linear import DEV, Case
+from tests.test_gpu_linear_split import Prompts
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +30,26 @@ def test_short_sequences_beside_others(n):
         assert bool(((out[at:at + n].double() - ref).abs() <= tol["decode"]).all())
         slot = int(c.out_slots[b])
         assert bool(((state[slot].double() - new).abs() <= tol_s["decode"]).all())
+
+
+@pytest.mark.parametrize("H,B", [(1, 3), (2, 5), (1, 9)])
+def test_starts_that_go_back_over_a_cut_prompt(H, B):
+    """Every other sequence has all the tokens, which is more segments than the workspace is meant for: the
+    call reports it, writes nothing beyond the workspace, and every sequence has its outputs and its state,
+    those of a call that leaves it whole."""
+    n, d = 30000, 64
+    p = Prompts([n], H, d)
+    p.call(False)
+    size = binding.linear_workspace_size(n, B, H, d, d)
+    assert size > 256
+    ws = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+    starts = torch.tensor([b % 2 * n for b in range(B + 1)], dtype=torch.int32, device=DEV)
+    state = torch.full((B, H, d, d), 3.0, device=DEV)
+    slots = torch.arange(B, dtype=torch.int32, device=DEV)
+    out = binding.linear_prefill(p.q, p.k, p.v, p.decay, d ** -0.5, starts, state, torch.full_like(slots, -1), slots,
+                                 workspace=ws[:size])
+    assert binding.device_status() == binding.DSI_ERR_BOUNDS
+    assert bool((ws[size:] == 0x5A).all())
+    assert torch.equal(out, p.out)
+    for b in range(B):
+        assert torch.equal(state[b], p.state[0] if b % 2 == 0 else torch.zeros_like(state[b])), b
