@@ -596,8 +596,8 @@ dsi_status dsi_norm_rope(const dsi_heads* queries, const dsi_heads* keys, int64_
  * that a decay near one keeps its distance from one.  Decode computes in fp32 with one
  * rounding to bf16 at the end.  Prefill multiplies on the tensor cores: the weights
  * exp(g (i - j)) q_i . k_j and the state that a chunk's queries meet are rounded to
- * bf16 (off by at most 2^-8 of a value), the decayed values that enter the state are
- * split in two bf16 parts (2^-16).
+ * bf16 (off by at most 2^-8 of a value); what enters the state is multiplied in
+ * parts that hold a decayed value to an fp32's last bit, and summed in fp32.
  * A token whose q is not finite gives an out of that kind by itself; a k or
  * v that is not reaches the outputs of that head from its token on and its state, as NaN or by
  * the formula's arithmetic, and nothing else.  log_decay is at most 0 in use; -inf (no

@@ -9,12 +9,12 @@
 //   P  = Q K^T     [tokens x tokens]   decayed, masked, to bf16 in place (TMEM)
 //   OI = P V       [tokens x 64]
 //   OX = Q S       [tokens x 64]       S rounded to bf16
-//   D  = K^T V'    [dk x 64]           V' = decayed V in two bf16 parts, exact to 2^-16;
+//   D  = K^T V'    [dk x 64]           V' = decayed V in three bf16 parts, which hold it to its last bit;
 //                                      K^T is turned into TMEM (as an MN-major operand in shared
 //                                      memory a product of 16 tokens takes 130 cycles, not 46)
 // and the state, S <- S + expm1(g r) S + D, stays in the registers of its warps, in fp32, from a
-// sequence's first chunk to its last.  Its error against 64 bits is 2.5e-6 of its norm, that of the
-// split; a third part makes it 6.6e-7 and the call 17 % longer.
+// sequence's first chunk to its last.  Its error against 64 bits is 6.5e-7 of its norm (two parts of V'
+// made it 2.5e-6 and calls 1 to 7 % shorter).
 //
 // Roles (28 warps), each walking the same list of (sequence, head, columns):
 //   0 products Q S and P V, 1 K^T V', 2 Q K^T, 3 copies (TMA) and the list, 4-7 P,
@@ -48,8 +48,8 @@ constexpr int kC = 128;                        // tokens of a chunk
 constexpr int kCols = 64;                      // columns of the state that a CTA takes
 constexpr int kTile = kC * 128;                // 64 dims of a chunk, 16 KB
 constexpr int kQk = 2;                         // chunks of Q and of K in shared memory
-constexpr int kV = 3;                          // of V
-constexpr int kSplit = 2;                      // bf16 parts of V'
+constexpr int kV = 2;                          // of V (a third, without a part of V', gains 1 to 2 %)
+constexpr int kSplit = 3;                      // bf16 parts of V': 8 bits each of an fp32's 24
 constexpr int kThreads = 896;
 
 constexpr int oQ = 0;                          // [kQk][2] tiles
@@ -57,7 +57,7 @@ constexpr int oK = oQ + kQk * 2 * kTile;       // [kQk][2]
 constexpr int oV = oK + kQk * 2 * kTile;       // [kV]
 constexpr int oVp = oV + kV * kTile;           // V', its parts
 constexpr int oS = oVp + kSplit * kTile;       // the state in bf16: [dk][64]
-constexpr int kMarks = 5;                      // (the place of V t + 5 is free once P V of t + 2 is done, whose
+constexpr int kMarks = 4;                      // (the place of V t + 4 is free once P V of t + 2 is done, whose
                                                // P's tile was free once the outputs of t were read)
 constexpr int oBad = oS + kTile;               // [kMarks][8] a warp's part of V holds something not finite
 constexpr int oFirst = oBad + kMarks * 8 * 4;  // [kMarks][8][32] the first such row of a column
@@ -644,7 +644,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
     }
   } else if (warp >= 8 && warp < 16) {
     // ======================= V' and K^T ==========================================
-    // Four warps to half the tokens.  V': thread = half a row of V, its parts held in registers until
+    // Four warps to half the tokens.  V': thread = half a row of V, decayed and cut into parts once
     // the products with the V' before are done.  K^T: a warp turns 32 dims, 8 x 8 at a time.
     const int w = warp - 8, hf = w >> 2, u0 = (w & 1) * 4, quarter = w & 3;
     const int v_row0 = hf * 64 + ((w >> 1) & 1) * 32, v_row = v_row0 + lane;
@@ -660,35 +660,21 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         uint8_t* st = smem + oV + sv * kTile;
         if (c == it.c0 || r < kC) f = v_row < r ? power(g, r - 1 - v_row) : 0.f;
         if (!(ok = wait32(&v_full[sv], (uint32_t)(t / kV) & 1u))) break;
-        uint32_t part[kSplit][16];
+        uint4 v[4];                              // (as they are: three parts of each would be 48 registers)
         float2 all = make_float2(0.f, 0.f);    // not finite if one of the values is not
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const uint4 v4 = *reinterpret_cast<const uint4*>(st + sw128_offset((uint32_t)v_row, (uint32_t)(u0 + u)));
-          const uint32_t x[4] = {v4.x, v4.y, v4.z, v4.w};
+          v[u] = *reinterpret_cast<const uint4*>(st + sw128_offset((uint32_t)v_row, (uint32_t)(u0 + u)));
+          const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[e]));
-            all = add2(all, v);
-            float2 y = mul2(v, make_float2(f, f));
-#pragma unroll
-            for (int i = 0; i < kSplit; ++i) {
-              part[i][4 * u + e] = pack_bf16(y.x, y.y);
-              const float2 z = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&part[i][4 * u + e]));
-              if (i + 1 < kSplit) y = fma2(z, make_float2(-1.f, -1.f), y);
-            }
-          }
+          for (int e = 0; e < 4; ++e) all = add2(all, __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[e])));
         }
         const bool bad = v_row < r && !(fabsf(all.x) + fabsf(all.y) < INFINITY);   // (or their sum)
         if (v_row >= r) {                        // behind the sequence: what K and V hold must not meet weights of 0
 #pragma unroll
-          for (int i = 0; i < kSplit; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) part[i][e] = 0u;
-#pragma unroll
           for (int u = 0; u < 4; ++u) {
             const uint32_t off = sw128_offset((uint32_t)v_row, (uint32_t)(u0 + u));
-            *reinterpret_cast<uint4*>(st + off) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(st + off) = v[u] = make_uint4(0, 0, 0, 0);
           }
         }
         const bool any = __any_sync(0xffffffffu, bad);
@@ -709,11 +695,24 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
         if (lane == 0) mbar_arrive(LOCAL ? &v_empty[sv] : &v_clean[sv]);   // (nobody else reads it, or P V does)
         if (t > 0 && !(ok = wait32(&v_taken[hf], (uint32_t)(t - 1) & 1u))) break;
 #pragma unroll
-        for (int i = 0; i < kSplit; ++i)
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          uint32_t part[kSplit][4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
+          for (int e = 0; e < 4; ++e) {
+            float2 y = mul2(__bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[e])), make_float2(f, f));
+#pragma unroll
+            for (int i = 0; i < kSplit; ++i) {   // the upper 16 bits (8 of the value), and what they leave
+              const uint32_t lo = __float_as_uint(y.x), hi = __float_as_uint(y.y);
+              part[i][e] = __byte_perm(lo, hi, 0x7632);
+              y = add2(y, make_float2(-__uint_as_float(lo & 0xFFFF0000u), -__uint_as_float(hi & 0xFFFF0000u)));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kSplit; ++i)
             *reinterpret_cast<uint4*>(smem + oVp + i * kTile + sw128_offset((uint32_t)v_row, (uint32_t)(u0 + u))) =
-                make_uint4(part[i][4 * u], part[i][4 * u + 1], part[i][4 * u + 2], part[i][4 * u + 3]);
+                make_uint4(part[i][0], part[i][1], part[i][2], part[i][3]);
+        }
         fence_proxy_async_smem();
         if (!(ok = wait32(&k_full[s], (uint32_t)(t / kQk) & 1u))) break;
         tc_fence_after();
