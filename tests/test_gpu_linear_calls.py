@@ -53,3 +53,12 @@ def test_starts_that_go_back_over_a_cut_prompt(H, B):
     assert torch.equal(out, p.out)
     for b in range(B):
         assert torch.equal(state[b], p.state[0] if b % 2 == 0 else torch.zeros_like(state[b])), b
+
+
+@pytest.mark.parametrize("lens,H", [([5000] + [1] * 3, 2), ([1] * 20 + [5000] + [3] * 20, 2), ([40] * 7 + [6000], 1),
+                                    ([2, 3000] * 4, 4), ([1] * 63 + [4000], 1), ([1] * 64 + [4000], 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_long_prompt_beside_short_rows(lens, H, d):
+    """Cut, or left whole for its neighbours' sake: against the formula either way."""
+    c = Case(lens, H=H, dk=d, dv=d, seed=len(lens))
+    c.check(*c.prefill())
