@@ -471,8 +471,11 @@ size_t dsi_dense_mla_workspace_size(int32_t rows, int32_t n_heads);
  *   cache   the sequences' own rows.  Both have latent_dtype in common; they may be pages
  *           of one pool, of one or of different sizes, or separate tensors
  *   workspace  256-byte aligned, at least dsi_prefix_mla_workspace_size() bytes: the prefix's
- *           and the sequences' parts are joined from there, and a long FP8 prefix of up to
- *           65536 positions is converted into it.  Calls that may run at once need one each.
+ *           and the sequences' parts are joined from there, and the rows of an FP8 prefix that
+ *           several groups of 128 pairs read are converted into it, once for all, where its
+ *           cache has room for many positions but for no more than 65536 (s_max: the host knows no
+ *           lengths).  Most of it is for that and for the parts, 155 MB for the smallest call on a GB300.
+ *           Calls that may run at once need one each.
  * Numbers, rows outside the visible range, rows that are not finite, page ids and errors as for
  * dsi_dense_mla_decode; DSI_ERR_INVALID_ARG also for a prefix of other than
  * one sequence, DSI_ERR_UNSUPPORTED for different latent dtypes and
@@ -616,7 +619,8 @@ dsi_status dsi_norm_rope(const dsi_heads* queries, const dsi_heads* keys, int64_
  *   workspace / workspace_bytes (prefill): NULL and 0, or 256-byte aligned with
  *          dsi_linear_workspace_size() bytes: then calls of few heads and sequences
  *          are split along the sequences.  Calls that may run at once need one each.
- * Results are the same from one call to the next.
+ * Results are the same from one call to the next.  A sequence beside others may differ in rounding
+ * from itself alone: whether it goes as in decode and whether it is split depends on the call's sizes.
  * Errors: DSI_ERR_INVALID_ARG (null pointer, negative size, misalignment, a pitch
  * below the vector's width, n_heads not a multiple of n_kv_heads, slots without a
  * state, fewer slots than sequences without in_slots, NaN scale, T < 1, out at q, k or v),

@@ -635,7 +635,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
           if (!(ok = wait32(F8 ? &raw_empty[stage] : &empty[stage], ph ^ 1))) break;
           constexpr int kBlks = F8 ? 3 : 5;      // blocks of 128 bytes a row, the last the rope half
           const int boxes = kNp / rows_box;
-          const int pb = p0 + lane * rows_box;        // lane's rows_box, if it has one
+          const int pb = p0 + lane * rows_box;        // lane's box, if it has one
           const bool seen = lane < boxes && pb < x.grp.n_last && (pb + rows_box > x.grp.lo || pb < (int)a.n_sink);
           const int n = __popc(__ballot_sync(0xffffffffu, seen));
           if (lane == 0) {
@@ -653,7 +653,7 @@ dense_mla_tc(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ C
             const int bx = i / kBlks, blk = i - bx * kBlks, p = p0 + bx * rows_box;
             if (!(p < x.grp.n_last && (p + rows_box > x.grp.lo || p < (int)a.n_sink))) continue;
             const int row = row_of(c, x.grp.b, p, err);
-            // a bad page id: the rows_box past the tensor's last row, which reads as zeros
+            // a bad page id: the box past the tensor's last row, which reads as zeros
             const int y = row < 0 ? (int)c.num_pages * c.page_size : row;
             if (blk < kBlks - 1)
               tma_load_2d(st + blk * kBlockBytes + bx * rows_box * 128, rows_map,
@@ -1490,7 +1490,9 @@ cudaError_t launch_prefix_mla(const DenseArgs& a, const CacheView& prefix, const
   const int64_t own_tiles = own_groups * ((a.c.s_max + kNp - 1) / kNp);
   // An FP8 prefix becomes bf16 once, and the two kinds of groups take a launch each, where that
   // saves more than it costs.  us without and with, by tiles of the prefix to a cluster: 6.7 41 / 50, 13.5 56 / 59,
-  // 27 85 / 76, 29 90 / 83, 54 156 / 127, 108 283 / 189, 431 (64 x 32768 x 128 heads) 1000 / 576.
+  // 27 85 / 76, 29 90 / 83, 54 156 / 127, 108 283 / 189, 431 (64 x 32768 x 128 heads) 1000 / 576.  (The tiles that
+  // the cache has room for, since the host knows no length: 512 positions x 16 heads 33.4 us, 36.0 in a cache of
+  // 65536; 32768 x 128 heads in one of more than 65536, for which the workspace has no room, 894, 551 in a smaller one.)
   const bool expand = f8 && sh.groups > 1 && prefix.s_max <= kExpandRows && prefix_tiles >= 16 * (int64_t)slots;
 
   bf16* const rows16 = static_cast<bf16*>(a.ws);

@@ -25,12 +25,14 @@
 // of 0 for earlier tokens would give NaN) and the column's later outputs become
 // NaN; in V' it stays, and makes the state's column NaN.
 //
-// What bounds it.  8192 tokens, 64 heads of 128 x 128: 139 us, 3.9 TB/s (58 % of the measured copy
-// rate): 64 chunks in a row on each of 128 CTAs, about 4000 cycles a chunk.  Its bytes take 2400, its 40
-// products 1550 of the tensor pipe (counted over 32 chunks, 33 % of the time).  What is full is the way through the SM to shared and tensor memory: 2600 cycles of the
-// warps' loads and stores (logits, P, outputs, V', S, K^T), 1250 of the products' operands and 640 of
-// copies.  A sequence's start and end cost 2.5 to 3 us on top, a chunk 2.0 (76 heads: one sequence of 32 chunks
-// 73 us, four of 8 83, 32 of one 157).
+// What bounds it.  8192 tokens, 64 heads of 128 x 128: 147 us, 3.7 TB/s (55 % of the measured copy
+// rate): 64 chunks in a row on each of 128 CTAs, about 4500 cycles a chunk, 2.3 us; its bytes at the copy rate
+// would take 2450.  Counted over 32 chunks (4800 cycles each with start and end): 2580 cycles of the warps' loads
+// and stores to shared memory (logits, P, outputs, V', S, K^T), 1790 of the tensor pipe for 48 products, issue
+// slots half full.  So no pipe is full; the products' operands and the copies, which the first count leaves
+// out, are about 1400 and 640 cycles of that memory by their bytes, and whether they or the roles' waits for one another
+// set the pace has not been told apart.  A sequence's start and end cost about 3 us on top (76 heads: one
+// sequence of 32 chunks 79 us, four of 8 90, 32 of one 166).
 // More warps for P or the outputs, three tiles of P, both terms of an output in one
 // accumulator took 3 to 20 % longer; one issuer of products for all four 25 %, its lane in a branch of
 // its own another 15 %; much larger loops (110 KB of code) twice the time.
@@ -143,6 +145,8 @@ __device__ __forceinline__ int next_long(const LinearArgs& p, const uint32_t* bi
 // whole sequences from the longest to the shortest (table: their order).  Split: table[b] is the
 // first segment of sequence b.  More than kMaxOrder sequences are taken as they come, the short ones left
 // out by the bits in the table.  A search that takes long gives kNothingYet: no wait runs out over it.
+// (Every CTA gets as many pieces as the others, not as much work: of a ragged batch the CTAs with the longest
+// sequences end last.)
 constexpr int kNothingYet = -2, kSteps = 1024;
 template <bool LOCAL>
 __device__ __forceinline__ void look_up(const LinearArgs& p, const Plan& plan, const uint8_t* table_s, int& round, Item& it) {
@@ -986,9 +990,9 @@ size_t linear_prefill_workspace(int64_t n_tokens, int batch, int H, int dk, int 
 }
 
 // Sequences of at most so many tokens go token by token, in a launch of their own: decoding rows of a mixed
-// batch, say.  us for 64 sequences x 32 heads of 128 x 128, so and by chunks: 1 token 47 / 116, 4 61 / 118, 8
-// 84 / 118, 16 129 / 119; one sequence 2.7 / 8.4, 8 tokens 4.1 / 8.4, 16 6.4 / 8.4.  The launch costs 2 to 3 %
-// where no sequence is short: 4 x 2048 tokens 77 -> 78.5 us, 64 x 200 179 -> 184.
+// batch, say.  us for 64 sequences x 32 heads of 128 x 128, so and by chunks: 1 token 48 / 133, 4 62 / 134, 8
+// 85 / 135, 16 129 / 135; one sequence 3.6 / 9.3, 8 tokens 5.2 / 9.3, 16 7.3 / 9.3.  The launch costs 1 to 2 %
+// where no sequence is short: 4 x 2048 tokens 82.7 -> 83.3 us, 64 x 200 192 -> 195.
 constexpr int kFew = 8;
 
 cudaError_t launch_linear_prefill(const LinearArgs& given, void* ws, cudaStream_t st) {
