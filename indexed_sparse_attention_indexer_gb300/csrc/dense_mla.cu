@@ -67,6 +67,7 @@
 #include "prefix_parts.h"
 #include "tc_common.cuh"
 #include "tc_waits.cuh"
+#include "tc_warp.cuh"
 #include "tma_host.h"
 
 namespace dsi {

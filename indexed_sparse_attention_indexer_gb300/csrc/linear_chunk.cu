@@ -39,6 +39,7 @@
 #include "kernels.h"
 #include "linear_attn.h"
 #include "tc_waits.cuh"
+#include "tc_warp.cuh"
 #include "tma_host.h"
 
 namespace dsi {
