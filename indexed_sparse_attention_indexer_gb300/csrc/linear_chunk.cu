@@ -457,7 +457,7 @@ linear_chunk(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
       // under way: a wait that nothing ends is bounded)
       if (s_abort) {
         volatile int no_abort = 0;
-        for (int i = max(0, t + 1 - kV); i <= t; ++i) {
+        for (int i = max(0, t - max(kQk, kV)); i <= t; ++i) {
           if (!LOCAL) mbar_wait(&q_full[i % kQk], (uint32_t)(i / kQk) & 1u, &no_abort, p.err, 1000000ull);
           mbar_wait(&k_full[i % kQk], (uint32_t)(i / kQk) & 1u, &no_abort, p.err, 1000000ull);
           mbar_wait(&v_full[i % kV], (uint32_t)(i / kV) & 1u, &no_abort, p.err, 1000000ull);
