@@ -624,8 +624,8 @@ dsi_status dsi_norm_rope(const dsi_heads* queries, const dsi_heads* keys, int64_
  * Errors: DSI_ERR_INVALID_ARG (null pointer, negative size, misalignment, a pitch
  * below the vector's width, n_heads not a multiple of n_kv_heads, slots without a
  * state, fewer slots than sequences without in_slots, NaN scale, T < 1, out at q, k or v),
- * DSI_ERR_UNSUPPORTED (dk or dv, n_tokens or batch * n_heads * 4 of 2^31 or more; prefill: a pitch
- * of q, k or v of 2^39 or more),
+ * DSI_ERR_UNSUPPORTED (dk or dv; n_tokens, or batch * T, above 2^31 - 1024; batch * n_heads of 2^29
+ * or more; prefill: a pitch of q, k or v of 2^39 or more),
  * DSI_ERR_WORKSPACE (workspace too small).
  */
 typedef struct dsi_linear {

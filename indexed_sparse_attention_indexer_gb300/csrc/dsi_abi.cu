@@ -216,8 +216,8 @@ dsi_status check_linear(const dsi_linear* a, int64_t n_tokens, int batch, Linear
   if (a->dk < 8 || a->dk > 128 || a->dk % 8 != 0 || a->dv < 8 || a->dv > 128 || a->dv % 8 != 0)
     return DSI_ERR_UNSUPPORTED;
   if (a->n_heads % a->n_kv_heads != 0) return DSI_ERR_INVALID_ARG;
-  // (blocks and tokens are counted in 32 bits)
-  if (n_tokens >= (1ll << 31) || (int64_t)batch * a->n_heads >= (1ll << 29)) return DSI_ERR_UNSUPPORTED;
+  // (blocks and tokens are counted in 32 bits, up to a chunk past the last one)
+  if (n_tokens > (1ll << 31) - 1024 || (int64_t)batch * a->n_heads >= (1ll << 29)) return DSI_ERR_UNSUPPORTED;
   if (n_tokens > 0) {
     if (!a->q || !a->k || !a->v || !a->out || a->out == a->q || a->out == a->k || a->out == a->v)
       return DSI_ERR_INVALID_ARG;
