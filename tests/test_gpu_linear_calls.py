@@ -62,3 +62,23 @@ def test_a_long_prompt_beside_short_rows(lens, H, d):
     """Cut, or left whole for its neighbours' sake: against the formula either way."""
     c = Case(lens, H=H, dk=d, dv=d, seed=len(lens))
     c.check(*c.prefill())
+
+
+@pytest.mark.parametrize("where", ["q", "k", "v"])
+@pytest.mark.parametrize("at", [0, 100, 200])
+def test_what_a_bad_value_does_not_reach_follows_the_formula(where, at):
+    """Tokens before it, other heads and the next sequence, in outputs and states."""
+    c = Case([260, 90], H=3, lead=0, tail=0, seed=31)
+    {"q": c.dq, "k": c.dk_, "v": c.dv_}[where][at, 1, 7] = float("nan")
+    out, state = c.prefill()
+    assert binding.device_status() == 0
+    for b, (lo, hi) in enumerate(((0, 260), (260, 350))):
+        ref, tol, new, tol_s = c.reference(b)
+        ok = torch.ones(ref.shape, dtype=torch.bool, device=DEV)
+        heads = [0, 1, 2]
+        if b == 0:
+            ok[at:at + 1 if where == "q" else 260, 1] = False
+            heads = [0, 1, 2] if where == "q" else [0, 2]
+        assert bool((((out[lo:hi].double() - ref).abs() <= tol["prefill"]) | ~ok).all())
+        slot = int(c.out_slots[b])
+        assert bool(((state[slot].double() - new).abs() <= tol_s["prefill"])[heads].all())
