@@ -912,15 +912,15 @@ namespace {
 // sequences take their length; a split takes its share of all chunks 1.6 times (the first
 // pass reads K and V again) and three launches, about kSplitCost.  The host knows no length but the mean.
 // A segment is then no shorter than sequences of that length allow in one round of CTAs: with the bare
-// share a few segments more than there are CTAs doubled the call (4 x 4096 tokens of 8 heads 114 us, so 74).
+// share a few segments more than there are CTAs doubled the last two launches (4 x 4096 tokens of 8 heads 114 us, so 77).
 // us of heads of 128 x 128, whole and split (those that the rule takes marked *):
-//   tokens x heads  1024 x 1 *22 / 20, 1536 x 1 30 / *21, 4096 x 1 67 / *22, 1536 x 8 30 / *24, 8192 x 8 130 / *45,
-//     1024 x 16 *23 / 25, 1536 x 16 *30 / 28, 2048 x 16 38 / *31, 16384 x 16 260 / *128, 2048 x 32 *39 / 45,
-//     3584 x 32 64 / *66, 8192 x 32 135 / *127, 4096 x 45 *71 / 78, 8192 x 60 *136 / 149
-//   sequences       4 x 1024 x 2 *24 / 24, 4 x 2048 x 2 39 / *28, 4 x 2048 x 8 *40 / 47, 4 x 4096 x 8 73 / *74,
-//     4 x 8192 x 8 136 / *127, 8 x 8192 x 2 135 / *74, 8 x 4096 x 8 *75 / 84
-//   mixed           16000 and 3 of 4000, 8 heads 255 / *205; 6000, 5000, 4000, 3000 102 / *81; where the mean
-//     misleads: 8192 and 7 of 40 *134 / 54
+//   tokens x heads  1024 x 1 *23 / 21, 1536 x 1 31 / *22, 4096 x 1 72 / *23, 1536 x 8 32 / *24, 8192 x 8 137 / *46,
+//     1024 x 16 *24 / 26, 1536 x 16 *32 / 29, 2048 x 16 40 / *33, 16384 x 16 265 / *132, 2048 x 32 *40 / 47,
+//     3584 x 32 65 / *69, 8192 x 32 138 / *132, 4096 x 45 *74 / 82, 8192 x 60 *142 / 152
+//   sequences       4 x 1024 x 2 *25 / 25, 4 x 2048 x 2 41 / *28, 4 x 2048 x 8 *42 / 48, 4 x 4096 x 8 75 / *77,
+//     4 x 8192 x 8 139 / *132, 8 x 8192 x 2 138 / *77, 8 x 4096 x 8 *78 / 87
+//   mixed           16000 and 3 of 4000, 8 heads 261 / *214; 6000, 5000, 4000, 3000 105 / *85; where the mean
+//     misleads: 8192 and 7 of 40 *138 / 56
 constexpr int kSplitCost = 8;
 int segment_chunks(int64_t n_tokens, int batch, int H, int dv, int sms) {
   const int64_t chunks = (n_tokens + kC - 1) / kC, columns = (int64_t)H * ((dv + kCols - 1) / kCols);
